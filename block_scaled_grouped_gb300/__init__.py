@@ -28,7 +28,10 @@ SYMBOLS = ("bsgg_create", "bsgg_run", "bsgg_run_host", "bsgg_run_host_async", "b
            "bsgg_status_string", "bsgg_sf_bytes", "bsgg_sf_offset", "bsgg_pack_sf", "bsgg_run_noalloc",
            "bsgg_measure_mma_peak", "bsgg_measure_mma_peak_tile", "bsgg_debug_force_timeout",
            "bsgg_launches_per_run", "bsgg_debug_bounds_checked", "bsgg_debug_bounds_margin",
-           "bsgg_debug_bounds_violation")
+           "bsgg_debug_bounds_violation",
+           "bsgg_route", "bsgg_route_backward", "bsgg_sort_rows", "bsgg_sort_workspace_bytes", "bsgg_sort_tokens",
+           "bsgg_dispatch", "bsgg_combine", "bsgg_combine_backward", "bsgg_linear", "bsgg_linear_backward",
+           "bsgg_query_status_word")
 
 
 class BsggError(RuntimeError):
@@ -152,6 +155,7 @@ def lib(debug_bounds: bool = False):
         L.bsgg_debug_bounds_margin.argtypes = [ctypes.c_void_p, ctypes.c_int32]
         L.bsgg_debug_bounds_violation.restype = ctypes.c_int
         L.bsgg_debug_bounds_violation.argtypes = [ctypes.c_void_p] + [ctypes.POINTER(ctypes.c_uint32)] * 3
+        operators.bind(L)
         _libs[debug_bounds] = L
     return L
 
@@ -356,3 +360,8 @@ def run_noalloc(*, stream=None, wait_status: bool = True, **kw) -> int:
     args = Args(*[_ptr(tensors.get(name)) for name, _ in Args._fields_])
     return int(lib().bsgg_run_noalloc(ctypes.byref(desc), ctypes.byref(args), _stream(stream),
                                       int(bool(wait_status))))
+
+
+from . import operators  # noqa: E402  (needs the names above)
+from .operators import (TokenMap, combine, combine_backward, dispatch, linear, linear_backward,  # noqa: E402,F401
+                        operators_status, route, route_backward, sort_rows, sort_tokens)

@@ -1,0 +1,171 @@
+// bsgg_ops.cuh -- what the operators around the grouped GEMM share: formats,
+// 8-value vector loads and stores, and the block quantizer.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/bsgg.h"
+#include "bsgg_kernel.cuh"
+
+namespace bsgg {
+
+inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline bool is_float_format(int f) { return f == BSGG_OUT_BF16 || f == BSGG_OUT_F16 || f == BSGG_OUT_F32; }
+inline int float_bytes(int f) { return f == BSGG_OUT_F32 ? 4 : 2; }
+
+// One element of a bf16, f16 or f32 tensor (KIND: OK_BF16, OK_F16, OK_F32).
+template <int KIND>
+__device__ __forceinline__ float load1(const void* base, int64_t i) {
+  if (KIND == OK_F32) return static_cast<const float*>(base)[i];
+  if (KIND == OK_F16) return __half2float(static_cast<const __half*>(base)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
+}
+__device__ __forceinline__ float load1(int kind, const void* base, int64_t i) {
+  if (kind == OK_F32) return load1<OK_F32>(base, i);
+  return kind == OK_F16 ? load1<OK_F16>(base, i) : load1<OK_BF16>(base, i);
+}
+template <int KIND>
+__device__ __forceinline__ void store1(void* base, int64_t i, float v) {
+  if (KIND == OK_F32) static_cast<float*>(base)[i] = v;
+  else if (KIND == OK_F16) static_cast<__half*>(base)[i] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ void store1(int kind, void* base, int64_t i, float v) {
+  if (kind == OK_F32) store1<OK_F32>(base, i, v);
+  else if (kind == OK_F16) store1<OK_F16>(base, i, v);
+  else store1<OK_BF16>(base, i, v);
+}
+
+template <int KIND>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  if (KIND == OK_F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+}
+template <int KIND>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (KIND == OK_F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight consecutive values from element i (16-byte aligned pieces).
+template <int KIND>
+__device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]) {
+  if constexpr (KIND == OK_F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack2<KIND>(w[k]);
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+    }
+  }
+}
+template <int KIND>
+__device__ __forceinline__ void store8(void* base, int64_t i, const float (&v)[8]) {
+  if constexpr (KIND == OK_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =
+        make_uint4(pack2<KIND>(v[0], v[1]), pack2<KIND>(v[2], v[3]), pack2<KIND>(v[4], v[5]), pack2<KIND>(v[6], v[7]));
+  }
+}
+
+// ---------------------------------------------------------------- quantizer
+// Row formats by their bsgg_in_format: bits per value, values per scale.
+__host__ __device__ constexpr bool rf_scaled(int f) { return f != BSGG_IN_BF16 && f != BSGG_ROW_F16; }
+__host__ __device__ constexpr bool rf_fp4(int f) {
+  return f == BSGG_IN_NVFP4 || f == BSGG_IN_FP4_UE8M0_16 || f == BSGG_IN_MXFP4;
+}
+__host__ __device__ constexpr int rf_vec(int f) { return f == BSGG_IN_NVFP4 || f == BSGG_IN_FP4_UE8M0_16 ? 16 : 32; }
+__host__ __device__ constexpr int rf_bits(int f) { return !rf_scaled(f) ? 16 : rf_fp4(f) ? 4 : 8; }
+// the code of scale 1
+__host__ __device__ constexpr uint32_t rf_one(int f) { return f == BSGG_IN_NVFP4 ? 0x38u : 127u; }
+
+// The scale code of a block whose largest magnitude has the bits `amax`.
+// UE8M0: e = ceil(log2(amax / q_max)) read off the bits: q_max = m_q 2^p with
+// m_q = 1.75 (E4M3, E5M2) or 1.5 (E2M1), so e is amax's exponent - p, and one
+// more when its significand is above m_q.  No quotient is formed, so no rounding
+// can move a block's exponent.
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
+  if (FMT == BSGG_IN_NVFP4) {
+    if (amax >= 0x7F800000u) return 0x7Fu;
+    const uint32_t c = cvt_e4m3x2(__fdiv_rn(__uint_as_float(amax), 6.0f), 0.0f) & 0xFFu;
+    return c == 0u ? rf_one(FMT) : c;
+  }
+  if (amax >= 0x7F800000u) return 0xFFu;
+  if (amax == 0u) return rf_one(FMT);
+  constexpr int p = FMT == BSGG_IN_MXFP8_E4M3 ? 8 : FMT == BSGG_IN_MXFP8_E5M2 ? 15 : 2;
+  constexpr uint32_t mq = rf_fp4(FMT) ? 0x400000u : 0x600000u;
+  const int e = static_cast<int>(amax >> 23) - p + ((amax & 0x7FFFFFu) > mq ? 1 : 0);
+  return static_cast<uint32_t>(e < 0 ? 0 : e);   // biased by 127; 2^-127 at the least
+}
+
+// Eight values over the scale of `code`, as packed codes: 2 words (FP8), 1 word
+// (FP4), 4 words (bf16 and f16, no scale).  UE8M0: times 2^-e, exact.  E4M3 scales: the
+// correctly rounded quotient, whose comparison with E2M1's thresholds is that
+// of the exact one (a value off a tie differs from it by more than a rounding).
+template <int FMT>
+__device__ __forceinline__ void quantize8(const float (&v)[8], uint32_t code, uint32_t (&out)[4]) {
+  if constexpr (!rf_scaled(FMT)) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = pack2<FMT == BSGG_ROW_F16 ? OK_F16 : OK_BF16>(v[2 * k], v[2 * k + 1]);
+  } else {
+    float q[8];
+    const bool nan_block = code == (FMT == BSGG_IN_NVFP4 ? 0x7Fu : 0xFFu);
+    if (FMT == BSGG_IN_NVFP4) {
+      const float s = e4m3_to_float(code);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[k] = nan_block ? 0.0f : __fdiv_rn(v[k], s);
+    } else {
+      // 2^(127 - code): exponent field 254 - code, at code 254 the subnormal 2^-127
+      const float r = code >= 254u ? __uint_as_float(0x400000u) : __uint_as_float((254u - code) << 23);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[k] = nan_block ? 0.0f : v[k] * r;
+    }
+    if (FMT == BSGG_IN_MXFP8_E4M3) {
+      out[0] = cvt_e4m3x2(q[0], q[1]) | (cvt_e4m3x2(q[2], q[3]) << 16);
+      out[1] = cvt_e4m3x2(q[4], q[5]) | (cvt_e4m3x2(q[6], q[7]) << 16);
+    } else if (FMT == BSGG_IN_MXFP8_E5M2) {
+      out[0] = cvt_e5m2x2(q[0], q[1]) | (cvt_e5m2x2(q[2], q[3]) << 16);
+      out[1] = cvt_e5m2x2(q[4], q[5]) | (cvt_e5m2x2(q[6], q[7]) << 16);
+    } else {
+      out[0] = cvt_e2m1x2(q[0], q[1]) | (cvt_e2m1x2(q[2], q[3]) << 8) | (cvt_e2m1x2(q[4], q[5]) << 16) |
+               (cvt_e2m1x2(q[6], q[7]) << 24);
+    }
+  }
+}
+
+// Stores the packed codes of eight values at element i of a row buffer.
+template <int FMT>
+__device__ __forceinline__ void store_codes8(void* base, int64_t i, const uint32_t (&c)[4]) {
+  uint8_t* p = static_cast<uint8_t*>(base) + i * rf_bits(FMT) / 8;
+  if (!rf_scaled(FMT)) *reinterpret_cast<uint4*>(p) = make_uint4(c[0], c[1], c[2], c[3]);
+  else if (rf_fp4(FMT)) *reinterpret_cast<uint32_t*>(p) = c[0];
+  else *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
+}
+
+__device__ __forceinline__ uint32_t max_abs_bits8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+  return m;
+}
+
+}  // namespace bsgg

@@ -440,6 +440,181 @@ BSGG_API bsgg_status bsgg_measure_mma_peak(int32_t in_format, int32_t tile_n, in
 BSGG_API bsgg_status bsgg_measure_mma_peak_tile(int32_t in_format, int32_t tile_m, int32_t tile_n, int64_t mmas,
                                        double* tflops, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the grouped GEMM of an expert layer (the pages start at
+ * its operands; these have no counterpart there): the router's top-k, the sort
+ * of tokens by expert into rows padded to 128 per expert, the quantization of
+ * tokens into A and SFA, the way back to tokens, the dense layers beside the
+ * experts, and their gradients.
+ *
+ * They hold no plan: every call is described by its desc, validated on the
+ * host, enqueued on `stream` and returns (asynchronous, no allocation, graph
+ * capturable).  Formats "f" below are bsgg_out_format values BSGG_OUT_BF16,
+ * BSGG_OUT_F16 or BSGG_OUT_F32.  Pointers are device pointers; rows of
+ * vectors are read in 16-byte pieces, so the tensors of tokens and rows need
+ * 16-byte aligned bases and row pitches (BSGG_ERR_INVALID_ARG otherwise).  No
+ * output may overlap an input unless its entry says so.  Sums, softmax
+ * statistics and products are accumulated in 32 bits and rounded once at the
+ * end; results do not depend on the order in which blocks run.
+ *
+ * A SLOT is one choice of one token: slot = token * topk + j.  A ROW is a row
+ * of the grouped GEMM's A (and D).  row_of_slot (tokens, topk) names a slot's
+ * row and slot_of_row (m_pad) a row's slot; -1 stands for a slot that is not
+ * routed and for a padding row.  Entries outside the ranges count as -1. */
+
+/* Softmax top-k router.  For a row l of logits, m = max l:
+ *   ids     = the topk largest logits, largest first; equal ones by lowest index
+ *   weights = exp(l_id - m) / S,  S = the sum of exp(l - m) over all experts
+ *             (normalize = 0) or over the chosen ones (normalize = 1)
+ * A logit of -inf is never chosen: where fewer than topk are left the id is -1
+ * and its weight 0 (a row of -inf only: every id -1).  A NaN logit counts as the
+ * largest and makes the row's weights NaN. */
+typedef struct {
+  int64_t tokens;         /* >= 0; 0 launches nothing */
+  int64_t ld;             /* row pitch of logits and dlogits in elements, >= num_experts */
+  int32_t num_experts;    /* 1..1024 */
+  int32_t topk;           /* 1..min(32, num_experts) */
+  int32_t logit_format;   /* f: logits, and dlogits of the backward */
+  int32_t normalize;      /* 0 or 1 */
+} bsgg_route_desc;
+
+BSGG_API bsgg_status bsgg_route(const bsgg_route_desc* desc, const void* logits, int32_t* ids, float* weights,
+                                void* stream);
+
+/* Gradient of bsgg_route with respect to the logits, given ids and weights it
+ * returned and g = dweights: inner = sum_j g_j w_j;
+ *   normalize = 1: dlogits_i = w_i (g_i - inner) for the chosen i, 0 elsewhere
+ *   normalize = 0: dlogits_i = p_i (g_i [i chosen] - inner), p = softmax(l)
+ * dweights is (tokens, topk); with row_of_slot given (not NULL) it is instead a
+ * per-row gradient of m_pad floats (the backward GEMM's dprob) and slot s reads
+ * dweights[row_of_slot[s]], 0 for a slot without a row. */
+BSGG_API bsgg_status bsgg_route_backward(const bsgg_route_desc* desc, const void* logits, const int32_t* ids,
+                                         const float* weights, const float* dweights, const int32_t* row_of_slot,
+                                         int64_t m_pad, void* dlogits, void* stream);
+
+/* Tokens sorted by expert: slots in order of expert, then of slot (stable); each
+ * expert's rows padded to a multiple of 128.  An id outside [0, num_experts)
+ * is a slot without a row (-1: a masked choice; ids of another process's
+ * experts).  Outputs:
+ *   padded_offsets (num_experts)  end of each expert's rows; the last one is
+ *                                 m_pad, as bsgg_run wants it (rows past the
+ *                                 sizes' sum are padding rows of the last expert)
+ *   row_of_slot (slots), slot_of_row (m_pad)
+ *   prob (m_pad)                  weights[slot] of each row, 0 for padding rows
+ *                                 (NULL: not wanted; weights NULL = ones)
+ *   rows_used (1)                 the padded sizes' sum, the least m_pad that
+ *                                 holds them (NULL: not wanted)
+ * m_pad: a positive multiple of 128; bsgg_sort_rows gives one that always
+ * suffices.  Where it is too small the slots that do not fit get no row, offsets
+ * are cut at m_pad, and BSGG_ERR_BAD_OFFSETS is reported in `status`.
+ * workspace: bsgg_sort_workspace_bytes(slots, num_experts) bytes (0: may be
+ * NULL).  status: a device word (NULL: not reported) that kernels only ever OR
+ * bits into; see bsgg_query_status_word. */
+BSGG_API int64_t bsgg_sort_rows(int64_t slots, int32_t num_experts);
+BSGG_API uint64_t bsgg_sort_workspace_bytes(int64_t slots, int32_t num_experts);
+BSGG_API bsgg_status bsgg_sort_tokens(int64_t slots, int32_t num_experts, int64_t m_pad, const int32_t* ids,
+                                      const float* weights, int32_t* padded_offsets, int32_t* row_of_slot,
+                                      int32_t* slot_of_row, float* prob, int32_t* rows_used, void* workspace,
+                                      uint32_t* status, void* stream);
+
+/* Format of the rows that dispatch and combine_backward write: a bsgg_in_format
+ * (BSGG_IN_BF16: bfloat16 values, no scale factors), or float16 values. */
+#define BSGG_ROW_F16 6
+
+/* Description of the three operators between tokens and rows. */
+typedef struct {
+  int64_t tokens;         /* >= 0 */
+  int64_t hidden;         /* vector length; a multiple of 8, and of 16 (FP8) or 32 (FP4) for
+                             those row formats */
+  int64_t m_pad;          /* rows: a positive multiple of 128 */
+  int64_t ld_token;       /* row pitch of x, y or dy in elements, >= hidden */
+  int64_t ld_residual;    /* row pitch of the residual (combine), >= hidden; 0 without one */
+  int32_t topk;           /* >= 1; tokens * topk < 2^31 */
+  int32_t token_format;   /* f: x, dy; y and the residual */
+  int32_t row_format;     /* dispatch, combine_backward: format of A / dD, as above */
+  int32_t d_format;       /* f: D (combine, combine_backward) */
+} bsgg_tokens_desc;
+
+/* A[row] = x[token of the row], quantized to row_format with its scale
+ * factors in the swizzled SF(m_pad, hidden) layout; padding rows are 0 with
+ * scale 1.  Scales: UE8M0 2^ceil(log2(amax / q_max)) per 32 (16) values, E4M3
+ * RN(amax / 6) per 16 for NVFP4; an all-zero block (or an E4M3 scale that rounds
+ * to 0) has scale 1; codes are RNE(x / scale), saturating.  A block with an
+ * infinity or a NaN gets the NaN scale (UE8M0 0xFF, E4M3 0x7F) and zero codes.
+ * a: (m_pad, hidden) codes; sfa: bsgg_sf_bytes(m_pad, hidden, v, 1) bytes, every
+ * one written (NULL for bfloat16 and float16 rows).  The gradient of a dispatch is
+ * bsgg_combine without weights. */
+BSGG_API bsgg_status bsgg_dispatch(const bsgg_tokens_desc* desc, const void* x, const int32_t* row_of_slot,
+                                   const int32_t* slot_of_row, void* a, void* sfa, void* stream);
+
+/* y[t] = residual[t] + sum_j weights[t, j] * D[row_of_slot[t, j]] over the slots
+ * that have a row, j ascending.  weights (tokens, topk) float; NULL = ones
+ * (where the GEMM's epilogue already multiplied by prob).  residual may be NULL
+ * and may be y itself. */
+BSGG_API bsgg_status bsgg_combine(const bsgg_tokens_desc* desc, const void* d, const int32_t* row_of_slot,
+                                  const float* weights, const void* residual, void* y, void* stream);
+
+/* Gradient of bsgg_combine (that of the residual is dy itself):
+ *   dD[row]        = weights[slot of the row] * dy[its token], 0 for padding rows,
+ *                    in row_format with scale factors as bsgg_dispatch writes them
+ *   dweights[t, j] = <dy[t], D[row_of_slot[t, j]]>, 0 for a slot without a row
+ * dd (and sfd) NULL: not wanted; dweights NULL: not wanted, d is then not read. */
+BSGG_API bsgg_status bsgg_combine_backward(const bsgg_tokens_desc* desc, const void* dy, const void* d,
+                                           const int32_t* row_of_slot, const int32_t* slot_of_row,
+                                           const float* weights, void* dd, void* sfd, float* dweights,
+                                           void* stream);
+
+/* Activations of the dense layer; gelu is z * Phi(z), srelu max(z, 0)^2. */
+typedef enum {
+  BSGG_ACT_NONE = 0, BSGG_ACT_RELU = 1, BSGG_ACT_SRELU = 2, BSGG_ACT_SILU = 3, BSGG_ACT_GELU = 4
+} bsgg_activation;
+
+/* Dense layer: z = x W^T + bias, y = act(z) + residual.  x (m, k), W (n, k) and
+ * the residual (m, n) are in in_format, bias (n) in bias_format, y (m, n) in
+ * out_format, z (m, n), kept for the backward, in in_format; each rounded once
+ * from the 32-bit accumulator.  Sizes are free (m = 0 launches nothing); x and W
+ * are fetched by TMA: 16-byte aligned bases, pitches ldx, ldw multiples of 8.
+ * The other tensors need only their element's alignment.  residual may be y. */
+typedef struct {
+  int64_t m, n, k;
+  int64_t ldx, ldw, ld_residual, ldy, ldz;   /* row pitches in elements (0 for an absent tensor) */
+  int32_t in_format;      /* BSGG_OUT_BF16 or BSGG_OUT_F16 */
+  int32_t out_format;     /* f */
+  int32_t bias_format;    /* f (when bias) */
+  int32_t activation;     /* bsgg_activation */
+} bsgg_linear_desc;
+
+BSGG_API bsgg_status bsgg_linear(const bsgg_linear_desc* desc, const void* x, const void* w, const void* bias,
+                                 const void* residual, void* y, void* z, uint32_t* status, void* stream);
+
+/* Gradient of the dense layer: dz = dy * act'(z), dbias = sum over rows of dz,
+ *   dx = dz W,   dw = dz^T x  (accumulate_dw = 1: dw += dz^T x, read and
+ * rounded once).  dz is kept in in_format (its rounding enters dx and dw; dbias
+ * sums the unrounded values in 32 bits) in the caller's buffer of m rows of pitch
+ * ld_dz; without an activation dz is dy itself, z and dz are NULL and nothing is
+ * rounded.  dx, dw and dbias (float) may each be NULL: not wanted.  dy, z, dz, x
+ * and w: 16-byte aligned bases, pitches multiples of 8.  The gradient of the
+ * residual is dy. */
+typedef struct {
+  int64_t m, n, k;
+  int64_t ld_dy, ldz, ld_dz, ldx, ldw, ld_dx, ld_dw;
+  int32_t in_format;      /* BSGG_OUT_BF16 or BSGG_OUT_F16: dy, z, dz, x, w */
+  int32_t dx_format;      /* f */
+  int32_t dw_format;      /* f */
+  int32_t activation;
+  int32_t accumulate_dw;  /* 0 or 1 */
+} bsgg_linear_bwd_desc;
+
+BSGG_API bsgg_status bsgg_linear_backward(const bsgg_linear_bwd_desc* desc, const void* dy, const void* x,
+                                          const void* w, const void* z, void* dz, void* dx, void* dw,
+                                          float* dbias, uint32_t* status, void* stream);
+
+/* Synchronize `stream`, then read and clear a status word that the operators
+ * above were given: BSGG_OK, BSGG_ERR_BAD_OFFSETS (m_pad too small for the
+ * sort), BSGG_ERR_DEVICE_TIMEOUT (a wait of bsgg_linear ran out; its outputs are
+ * incomplete), or BSGG_ERR_CUDA. */
+BSGG_API bsgg_status bsgg_query_status_word(uint32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
