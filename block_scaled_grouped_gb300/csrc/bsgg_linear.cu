@@ -1,6 +1,10 @@
 // bsgg_linear.cu -- the dense layer act(x W^T + bias) + residual and its
 // gradient.
-#include "bsgg_ops.cuh"
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "bsgg_linear_kernel.cuh"
 
 namespace {
 
@@ -8,17 +12,6 @@ using namespace bsgg;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// act(z).  silu = z / (1 + e^-z); gelu = z Phi(z) with Phi from normcdff,
-// which keeps its relative accuracy in the lower tail where 1 + erf cancels.
-__device__ __forceinline__ float act_value(int act, float z) {
-  switch (act) {
-    case BSGG_ACT_RELU: return z <= 0.0f ? 0.0f : z;               // a NaN stays
-    case BSGG_ACT_SRELU: return z <= 0.0f ? 0.0f : z * z;
-    case BSGG_ACT_SILU: return z / (1.0f + expf(-z));
-    case BSGG_ACT_GELU: return z * normcdff(z);
-    default: return z;
-  }
-}
 // act'(z).  silu: s + z s (1 - s) with 1 - s = s(-z), no cancellation;
 // gelu: Phi(z) + z phi(z).
 __device__ __forceinline__ float act_slope(int act, float z) {
@@ -32,64 +25,6 @@ __device__ __forceinline__ float act_slope(int act, float z) {
     case BSGG_ACT_GELU: return normcdff(z) + z * 0.398942280401432678f * expf(-0.5f * z * z);
     default: return 1.0f;
   }
-}
-
-// C[i, j] = sum_r A(i, r) B(j, r): operand elements at i * s_i + r * s_r.
-struct MatParams {
-  int64_t rows, cols, depth;
-  const void *a, *b;
-  int64_t a_i, a_r, b_j, b_r;
-  int in_kind, out_kind, bias_kind, act;
-  const void* bias;          // by column
-  const void* residual;
-  int residual_kind;
-  int64_t ld_residual;
-  void* out;
-  int64_t ld_out;
-  void* z;
-  int64_t ldz;
-};
-
-__device__ __forceinline__ void finish(const MatParams& p, int64_t i, int64_t j, float v) {
-  if (p.bias != nullptr) v += load1(p.bias_kind, p.bias, j);
-  if (p.z != nullptr) store1(p.in_kind, p.z, i * p.ldz + j, v);
-  v = act_value(p.act, v);
-  if (p.residual != nullptr) v += load1(p.residual_kind, p.residual, i * p.ld_residual + j);
-  store1(p.out_kind, p.out, i * p.ld_out + j, v);
-}
-
-constexpr int kTile = 64, kDepth = 16;
-
-// A 64 x 64 tile per block of 256 threads, 4 x 4 values each, over depth 16
-// slices in shared memory.
-__global__ void __launch_bounds__(256) mat_kernel(MatParams p) {
-  __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kTile, j0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t r0 = 0; r0 < p.depth; r0 += kDepth) {
-    for (int e = threadIdx.x; e < kTile * kDepth; e += 256) {
-      const int i = e / kDepth, r = e % kDepth;
-      const bool in = r0 + r < p.depth;
-      sa[r][i] = in && i0 + i < p.rows ? load1(p.in_kind, p.a, (i0 + i) * p.a_i + (r0 + r) * p.a_r) : 0.0f;
-      sb[r][i] = in && j0 + i < p.cols ? load1(p.in_kind, p.b, (j0 + i) * p.b_j + (r0 + r) * p.b_r) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kDepth; ++r)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(sa[r][ty + 16 * u], sb[r][tx + 16 * v], acc[u][v]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
-      if (i < p.rows && j < p.cols) finish(p, i, j, acc[u][v]);
-    }
 }
 
 // dz = dy act'(z) and dbias, a warp's lanes over 32 columns, the block's 8
@@ -120,10 +55,139 @@ __global__ void __launch_bounds__(256) dz_kernel(int64_t m, int64_t n, int64_t l
 
 bsgg_status launch_status() { return cudaGetLastError() == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA; }
 
-bsgg_status launch_mat(const MatParams& p, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(p.cols, kTile)), static_cast<unsigned>(ceil_div(p.rows, kTile)));
-  mat_kernel<<<grid, 256, 0, s>>>(p);
-  return launch_status();
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return nullptr;
+  }();
+  return fn;
+}
+
+// An operand of a product: `rows` indices and `depth` reduction indices; mn: the
+// row index is the contiguous one.
+struct Operand {
+  const void* base;
+  int64_t rows, depth, ld;
+  bool mn;
+};
+
+// Boxes of 64 reduction indices: (64, tile_rows) K-major, (64, 64) MN-major.
+bool encode_operand(CUtensorMap* map, const Operand& o, int tile_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(o.mn ? o.rows : o.depth), cuuint64_t(o.mn ? o.depth : o.rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(2 * o.ld)};
+  const cuuint32_t box[2] = {64, cuuint32_t(o.mn ? 64 : tile_rows)};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(o.base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Device {
+  int sms = 0;
+  bool ok = false;
+};
+
+template <typename K>
+bool allow_smem(K kern, int bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+// SM count and the kernels' shared-memory limits, once per device.
+const Device* device_state() {
+  static Device state[64];
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  std::lock_guard<std::mutex> lk(mu);
+  Device& d = state[dev];
+  if (!d.ok) {
+    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return nullptr;
+    if (!allow_smem(linear_pair_kernel, LinPair::kSmem) || !allow_smem(linear_tile_kernel<32>, LinTile<32>::kSmem) ||
+        !allow_smem(linear_tile_kernel<64>, LinTile<64>::kSmem) || !allow_smem(linear_tile_kernel<128>, LinTile<128>::kSmem))
+      return nullptr;
+    d.ok = true;
+  }
+  return &d;
+}
+
+uint32_t lin_idesc(int in_format, bool p_mn, bool q_mn, int m, int n) {
+  // kind::f16: F32 accumulator (bits 4-5 = 1), F16 (0) or BF16 (1) operands, majorness (1 = MN)
+  const uint32_t fmt = in_format == BSGG_OUT_BF16 ? 1u : 0u;
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (p_mn ? 1u << 15 : 0u) | (q_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+template <int BN>
+cudaError_t launch_tile(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.p_tiles) * p.q_tiles * split), 1, 1);
+  cfg.blockDim = dim3(kLinThreads, 1, 1);
+  cfg.dynamicSmemBytes = LinTile<BN>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_tile_kernel<BN>, tp, tq, p, split);
+}
+
+bsgg_status launch_product(const Operand& P, const Operand& Q, int in_format, LinParams p, cudaStream_t s) {
+  const Device* dev = device_state();
+  if (!dev) return BSGG_ERR_CUDA;
+  p.cols = static_cast<int32_t>(P.rows);
+  p.rows = static_cast<int32_t>(Q.rows);
+  p.k_blocks = static_cast<int32_t>(ceil_div(P.depth, kLinDepth));
+  p.p_mn = P.mn;
+  p.q_mn = Q.mn;
+  p.in_kind = in_format;
+  p.wait_limit_ns = kWaitLimitNs;
+  CUtensorMap tp, tq;
+  const int64_t pair_tiles = ceil_div(P.rows, 256) * ceil_div(Q.rows, 256);
+  cudaError_t e;
+  if (pair_tiles >= dev->sms / 2 && Q.rows > 128) {
+    p.p_tiles = static_cast<int32_t>(ceil_div(P.rows, 256));
+    p.q_tiles = static_cast<int32_t>(ceil_div(Q.rows, 256));
+    p.idesc = lin_idesc(in_format, P.mn, Q.mn, 256, 256);
+    if (!encode_operand(&tp, P, 128) || !encode_operand(&tq, Q, 128)) return BSGG_ERR_CUDA;
+    const int64_t units = pair_tiles < dev->sms / 2 ? pair_tiles : dev->sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * units), 1, 1);
+    cfg.blockDim = dim3(kLinThreads, 1, 1);
+    cfg.dynamicSmemBytes = LinPair::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, linear_pair_kernel, tp, tq, p);
+  } else {
+    // the instruction's N: the least that holds the output rows (MN-major boxes are 64 wide)
+    const int bn = Q.rows <= 32 && !Q.mn ? 32 : Q.rows <= 64 ? 64 : 128;
+    p.p_tiles = static_cast<int32_t>(ceil_div(P.rows, 128));
+    p.q_tiles = static_cast<int32_t>(ceil_div(Q.rows, bn));
+    p.idesc = lin_idesc(in_format, P.mn, Q.mn, 128, bn);
+    // split the reduction while the tiles leave SMs idle and every part keeps four blocks
+    const int64_t tiles = int64_t(p.p_tiles) * p.q_tiles;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 2 * dev->sms && p.k_blocks >= 8 * split) split *= 2;
+    if (!encode_operand(&tp, P, 128) || !encode_operand(&tq, Q, bn)) return BSGG_ERR_CUDA;
+    e = bn == 32   ? launch_tile<32>(tp, tq, p, split, s)
+        : bn == 64 ? launch_tile<64>(tp, tq, p, split, s)
+                   : launch_tile<128>(tp, tq, p, split, s);
+  }
+  return e == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA;
 }
 
 bool is_half_format(int f) { return f == BSGG_OUT_BF16 || f == BSGG_OUT_F16; }
@@ -150,14 +214,12 @@ bsgg_status bsgg_linear(const bsgg_linear_desc* d, const void* x, const void* w,
       !aligned_to(residual, 2) || !aligned_to(z, 2) || (bias && !aligned_to(bias, float_bytes(d->bias_format))) ||
       !aligned_to(status, 4))
     return BSGG_ERR_INVALID_ARG;
-  MatParams p = {};
-  p.rows = d->m; p.cols = d->n; p.depth = d->k;
-  p.a = x; p.a_i = d->ldx; p.a_r = 1;
-  p.b = w; p.b_j = d->ldw; p.b_r = 1;
-  p.in_kind = d->in_format; p.out_kind = d->out_format; p.bias_kind = d->bias_format; p.act = d->activation;
-  p.bias = bias; p.residual = residual; p.residual_kind = d->in_format; p.ld_residual = d->ld_residual;
-  p.out = y; p.ld_out = d->ldy; p.z = z; p.ldz = d->ldz;
-  return launch_mat(p, static_cast<cudaStream_t>(stream));
+  LinParams p = {};
+  p.act = d->activation; p.out_kind = d->out_format; p.bias_kind = d->bias_format; p.residual_kind = d->in_format;
+  p.bias = bias; p.residual = residual; p.ld_residual = d->ld_residual;
+  p.out = y; p.ld_out = d->ldy; p.z = z; p.ldz = d->ldz; p.status = status;
+  return launch_product({w, d->n, d->k, d->ldw, false}, {x, d->m, d->k, d->ldx, false}, d->in_format, p,
+                        static_cast<cudaStream_t>(stream));
 }
 
 bsgg_status bsgg_linear_backward(const bsgg_linear_bwd_desc* d, const void* dy, const void* x, const void* w,
@@ -197,23 +259,17 @@ bsgg_status bsgg_linear_backward(const bsgg_linear_bwd_desc* d, const void* dy, 
   const void* g = has_act ? dz : dy;
   const int64_t ldg = has_act ? d->ld_dz : d->ld_dy;
   if (dx) {
-    MatParams p = {};
-    p.rows = d->m; p.cols = d->k; p.depth = d->n;
-    p.a = g; p.a_i = ldg; p.a_r = 1;
-    p.b = w; p.b_j = 1; p.b_r = d->ldw;
-    p.in_kind = d->in_format; p.out_kind = d->dx_format;
-    p.out = dx; p.ld_out = d->ld_dx;
-    if (launch_mat(p, s) != BSGG_OK) return BSGG_ERR_CUDA;
+    LinParams p = {};
+    p.out_kind = d->dx_format; p.out = dx; p.ld_out = d->ld_dx; p.status = status;
+    const bsgg_status st = launch_product({w, d->k, d->n, d->ldw, true}, {g, d->m, d->n, ldg, false}, d->in_format, p, s);
+    if (st != BSGG_OK) return st;
   }
   if (dw) {
-    MatParams p = {};
-    p.rows = d->n; p.cols = d->k; p.depth = d->m;
-    p.a = g; p.a_i = 1; p.a_r = ldg;
-    p.b = x; p.b_j = 1; p.b_r = d->ldx;
-    p.in_kind = d->in_format; p.out_kind = d->dw_format;
-    p.out = dw; p.ld_out = d->ld_dw;
+    LinParams p = {};
+    p.out_kind = d->dw_format; p.out = dw; p.ld_out = d->ld_dw; p.status = status;
     if (d->accumulate_dw) { p.residual = dw; p.residual_kind = d->dw_format; p.ld_residual = d->ld_dw; }
-    if (launch_mat(p, s) != BSGG_OK) return BSGG_ERR_CUDA;
+    const bsgg_status st = launch_product({x, d->k, d->m, d->ldx, true}, {g, d->n, d->m, ldg, true}, d->in_format, p, s);
+    if (st != BSGG_OK) return st;
   }
   return BSGG_OK;
 }

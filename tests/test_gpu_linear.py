@@ -76,6 +76,16 @@ def test_linear_sizes(M, N, K, dtype):
     assert bsgg.operators_status() == 0
 
 
+@pytest.mark.parametrize("dtype,act", [("bf16", "gelu"), ("f16", "silu")])
+def test_linear_many_tiles(dtype, act):
+    """Enough 256 x 256 tiles for CTA pairs to walk several each, ragged both ways."""
+    M, N, K = 2500, 5001, 328
+    x, w, b, r = problem(M, N, K, dtype, 77)
+    y, z = bsgg.linear(x.cuda(), w.cuda(), bias=b.cuda(), residual=r.cuda(), activation=act, want_z=True)
+    check_forward(x, w, b, r, act, y, z, True)
+    assert bsgg.operators_status() == 0
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "srelu", "silu", "gelu"])
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("M,N,K", [(3, 70, 264), (150, 300, 328), (260, 520, 200)])
@@ -168,6 +178,15 @@ def test_linear_backward_sizes(M, N, K, act):
     dx, dw, db = bsgg.linear_backward(pitched(dy, 8, 8), pitched(x, 8), pitched(w, 8, 8), z=pitched(z, 8) if act != "none" else None,
                                       activation=act, want_dbias=True)
     check_backward(dy, x, w, z, act, dx, dw, db)
+    assert bsgg.operators_status() == 0
+
+
+def test_linear_backward_many_tiles():
+    M, N, K = 2310, 2408, 2504
+    x, w, _, z = problem(M, N, K, "bf16", 78)
+    dy = torch.randn(M, N, generator=gen(9)).bfloat16()
+    dx, dw, db = bsgg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), z=z.cuda(), activation="silu", want_dbias=True)
+    check_backward(dy, x, w, z, "silu", dx, dw, db)
     assert bsgg.operators_status() == 0
 
 
