@@ -14,46 +14,77 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // act'(z).  silu: s + z s (1 - s) with 1 - s = s(-z), no cancellation;
 // gelu: Phi(z) + z phi(z).
-__device__ __forceinline__ float act_slope(int act, float z) {
-  switch (act) {
-    case BSGG_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case BSGG_ACT_SRELU: return 2.0f * fmaxf(z, 0.0f);
-    case BSGG_ACT_SILU: {
-      const float s = 1.0f / (1.0f + expf(-z)), c = 1.0f / (1.0f + expf(z));
-      return s * (1.0f + z * c);
-    }
-    case BSGG_ACT_GELU: return normcdff(z) + z * 0.398942280401432678f * expf(-0.5f * z * z);
-    default: return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if (ACT == BSGG_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if (ACT == BSGG_ACT_SRELU) return z > 0.0f ? 2.0f * z : 0.0f;
+  if (ACT == BSGG_ACT_SILU) {
+    const float s = __fdividef(1.0f, 1.0f + __expf(-z)), c = __fdividef(1.0f, 1.0f + __expf(z));
+    return s * (1.0f + z * c);
   }
+  if (ACT == BSGG_ACT_GELU) return normcdff(z) + z * 0.398942280401432678f * __expf(-0.5f * z * z);
+  return 1.0f;
 }
 
-// dz = dy act'(z) and dbias, a warp's lanes over 32 columns, the block's 8
-// warps over the rows; the 8 partial sums are added in order.
-__global__ void __launch_bounds__(256) dz_kernel(int64_t m, int64_t n, int64_t ld_dy, int64_t ldz, int64_t ld_dz, int kind,
-                                                 int act, const void* dy, const void* z, void* dz, float* dbias) {
-  __shared__ float part[8][32];
+// dz = dy act'(z) and dbias.  A block owns 64 columns (a lane eight of them, so
+// that a warp reads four 128-byte pieces of rows at a time) and one of the
+// cluster's runs of rows; its sums join through shared memory and, between the
+// cluster's blocks, through distributed shared memory, in a fixed order.
+constexpr int kDzThreads = 256, kDzCols = 64, kDzSplit = 8;
+
+template <int KIND, int ACT>
+__global__ void __launch_bounds__(kDzThreads) dz_kernel(int64_t m, int64_t n, int64_t ld_dy, int64_t ldz, int64_t ld_dz,
+                                                        const void* dy, const void* z, void* dz, float* dbias) {
+  __shared__ float part[kDzThreads / 32][kDzCols];
+  __shared__ float block_sum[kDzCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float sum = 0.0f;
-  if (j < n)
-    for (int64_t i = warp; i < m; i += 8) {
-      float v = load1(kind, dy, i * ld_dy + j);
-      if (z != nullptr) {
-        v *= act_slope(act, load1(kind, z, i * ldz + j));
-        store1(kind, dz, i * ld_dz + j, v);
+  const int64_t j = static_cast<int64_t>(blockIdx.y) * kDzCols + (lane & 7) * 8;
+  // rows [i0, i1), a warp four at a time
+  const int64_t i0 = m * blockIdx.x / gridDim.x, i1 = m * (blockIdx.x + 1) / gridDim.x;
+  // n need not be a multiple of 8, the pitches are: whole pieces are read, the
+  // padding columns' sums are not used and their dz is written as the pitch allows
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (j < n) {
+#pragma unroll 2
+    for (int64_t i = i0 + warp * 4 + (lane >> 3); i < i1; i += kDzThreads / 8) {
+      float g[8];
+      load8<KIND>(dy, i * ld_dy + j, g);
+      if (ACT != BSGG_ACT_NONE) {
+        float v[8];
+        load8<KIND>(z, i * ldz + j, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] *= act_slope<ACT>(v[k]);
+        store8<KIND>(dz, i * ld_dz + j, g);
       }
-      sum += v;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += g[k];
     }
-  part[warp][lane] = sum;
-  __syncthreads();
-  if (dbias != nullptr && warp == 0 && j < n) {
-    float s = 0.0f;
-    for (int w = 0; w < 8; ++w) s += part[w][lane];
-    dbias[j] = s;
   }
+  if (dbias == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], 8);
+    sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], 16);
+  }
+  if (lane < 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[warp][lane * 8 + k] = sum[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < kDzCols) {
+    float s = 0.0f;
+    for (int w = 0; w < kDzThreads / 32; ++w) s += part[w][threadIdx.x];
+    block_sum[threadIdx.x] = s;
+  }
+  cluster_sync();
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * kDzCols + threadIdx.x;
+  if (blockIdx.x == 0 && threadIdx.x < kDzCols && c < n) {
+    float s = 0.0f;
+    for (unsigned r = 0; r < gridDim.x; ++r) s += ld_shared_cluster(mapa_shared(smem_u32(&block_sum[threadIdx.x]), r));
+    dbias[c] = s;
+  }
+  cluster_sync();          // the sums stay until block 0 has read them
 }
-
-bsgg_status launch_status() { return cudaGetLastError() == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA; }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
@@ -88,17 +119,63 @@ bool encode_operand(CUtensorMap* map, const Operand& o, int tile_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+uint32_t lin_idesc(int in_format, bool p_mn, bool q_mn, int m, int n) {
+  // kind::f16: F32 accumulator (bits 4-5 = 1), F16 (0) or BF16 (1) operands, majorness (1 = MN)
+  const uint32_t fmt = in_format == BSGG_OUT_BF16 ? 1u : 0u;
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (p_mn ? 1u << 15 : 0u) | (q_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// A launch of `ctas` CTAs in clusters of `cluster`; attr holds the attribute.
+cudaLaunchConfig_t lin_config(int64_t ctas, int cluster, int smem, cudaStream_t s, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(kLinThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+template <typename K>
+cudaError_t launch_lin(K kern, int64_t ctas, int cluster, int smem, const CUtensorMap& tp, const CUtensorMap& tq,
+                       const LinParams& p, int split, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = lin_config(ctas, cluster, smem, s, attr);
+  return cudaLaunchKernelEx(&cfg, kern, tp, tq, p, split);
+}
+
+// What a device holds of the products' kernels: SMs, and for each kernel and
+// cluster size the clusters resident at once (a GPC's SMs are shared out in whole
+// clusters, so that 16 clusters of 8 CTAs with an SM each do not fit 152 SMs).
 struct Device {
-  int sms = 0;
   bool ok = false;
+  int sms = 0;
+  int pair_clusters[2][3];        // [bn 256, 128][split 1, 2, 4]
+  int tile_clusters[3][2][4];     // [bn 32, 64, 128][shared, alone][split 1, 2, 4, 8]
 };
 
 template <typename K>
-bool allow_smem(K kern, int bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+bool prepare_kernel(K kern, int smem, int ctas, int clusters, int* resident) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+  for (int i = 0; i < clusters; ++i) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = lin_config(int64_t(ctas) << i, ctas << i, smem, nullptr, attr);
+    if (cudaOccupancyMaxActiveClusters(&resident[i], kern, &cfg) != cudaSuccess || resident[i] < 1) return false;
+  }
+  return true;
+}
+template <int BN>
+bool prepare_tile(int (*resident)[4]) {
+  return prepare_kernel(linear_tile_kernel<BN, false>, LinTile<BN, false>::kSmem, 1, 4, resident[0]) &&
+         prepare_kernel(linear_tile_kernel<BN, true>, LinTile<BN, true>::kSmem, 1, 4, resident[1]);
 }
 
-// SM count and the kernels' shared-memory limits, once per device.
+// The current device's state, set up at its first call.
 const Device* device_state() {
   static Device state[64];
   static std::mutex mu;
@@ -108,36 +185,86 @@ const Device* device_state() {
   Device& d = state[dev];
   if (!d.ok) {
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return nullptr;
-    if (!allow_smem(linear_pair_kernel, LinPair::kSmem) || !allow_smem(linear_tile_kernel<32>, LinTile<32>::kSmem) ||
-        !allow_smem(linear_tile_kernel<64>, LinTile<64>::kSmem) || !allow_smem(linear_tile_kernel<128>, LinTile<128>::kSmem))
+    if (!prepare_kernel(linear_pair_kernel<256>, LinPair<256>::kSmem, 2, 3, d.pair_clusters[0]) ||
+        !prepare_kernel(linear_pair_kernel<128>, LinPair<128>::kSmem, 2, 3, d.pair_clusters[1]) ||
+        !prepare_tile<32>(d.tile_clusters[0]) || !prepare_tile<64>(d.tile_clusters[1]) ||
+        !prepare_tile<128>(d.tile_clusters[2]))
       return nullptr;
     d.ok = true;
   }
   return &d;
 }
 
-uint32_t lin_idesc(int in_format, bool p_mn, bool q_mn, int m, int n) {
-  // kind::f16: F32 accumulator (bits 4-5 = 1), F16 (0) or BF16 (1) operands, majorness (1 = MN)
-  const uint32_t fmt = in_format == BSGG_OUT_BF16 ? 1u : 0u;
-  return (1u << 4) | (fmt << 7) | (fmt << 10) | (p_mn ? 1u << 15 : 0u) | (q_mn ? 1u << 16 : 0u) |
-         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+template <int BN>
+cudaError_t launch_tile(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, int sms, cudaStream_t s) {
+  const int64_t ctas = int64_t(p.p_tiles) * p.q_tiles * split;
+  return ctas <= sms ? launch_lin(linear_tile_kernel<BN, true>, ctas, split, LinTile<BN, true>::kSmem, tp, tq, p, split, s)
+                     : launch_lin(linear_tile_kernel<BN, false>, ctas, split, LinTile<BN, false>::kSmem, tp, tq, p, split, s);
+}
+template <int BN>
+cudaError_t launch_pair(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, const Device& dev,
+                        cudaStream_t s) {
+  const int64_t tiles = int64_t(p.p_tiles) * p.q_tiles, resident = dev.pair_clusters[BN == 256 ? 0 : 1][0];
+  const int64_t units = split > 1 || tiles < resident ? tiles : resident;
+  return launch_lin(linear_pair_kernel<BN>, 2 * split * units, 2 * split, LinPair<BN>::kSmem, tp, tq, p, split, s);
 }
 
-template <int BN>
-cudaError_t launch_tile(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.p_tiles) * p.q_tiles * split), 1, 1);
-  cfg.blockDim = dim3(kLinThreads, 1, 1);
-  cfg.dynamicSmemBytes = LinTile<BN>::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_tile_kernel<BN>, tp, tq, p, split);
+// How a product is tiled: 256 x bn on CTA pairs, or 128 x bn on single CTAs, with
+// the reduction in `split` parts.
+struct Choice {
+  bool pair;
+  int bn, split;
+};
+
+// Microseconds of a choice, from what a block of 64 of the reduction took on GB300
+// (bf16 operands out of DRAM) and what is paid once:
+//   start, tensor-memory allocation, first load, epilogue      5, pairs of 256 6.5
+//   256 x 256 pair block 0.33, 256 x 128 pair block 0.21
+//   128 x 32 / 64 / 128 block, a CTA per SM   0.155 / 0.165 / 0.24
+//   the same, several CTAs per SM, per block of each SM   0.15 / 0.173 / 0.256
+//   joining a split reduction                 1.5 and 4 MB of partial tiles per us
+// Measured both ways: 512 x 4096 x 4096 takes 19.8 us on 64 pairs of 256 x 128 and
+// 27.3 on 32 of 256 x 256; 2048 x 4096 x 4096 45.3 on 256 x 256, 56.2 on 256 x 128,
+// 60.5 on 128 x 128; 128 x 4096 x 7168 17.5 on 64-wide tiles in two parts, 24.0 whole;
+// one row x 14336 -> 4096 22.2 in four parts, 40.0 whole.
+// Clusters beyond those resident at once wait for a second round.
+double cost_us(const Choice& c, int64_t p_rows, int64_t q_rows, int64_t k_blocks, const Device& dev) {
+  const int side = c.pair ? 256 : 128, log2 = c.split == 1 ? 0 : c.split == 2 ? 1 : c.split == 4 ? 2 : 3;
+  const int64_t tiles = ceil_div(p_rows, side) * ceil_div(q_rows, c.bn);
+  const double blocks = double(ceil_div(k_blocks, c.split));
+  double run, fixed = 5.0;
+  if (c.pair) {
+    run = double(ceil_div(tiles, dev.pair_clusters[c.bn == 256 ? 0 : 1][log2])) * blocks * (c.bn == 256 ? 0.33 : 0.21);
+    if (c.bn == 256) fixed = 6.5;
+  } else {
+    const int w = c.bn == 32 ? 0 : c.bn == 64 ? 1 : 2;
+    const double alone[3] = {0.155, 0.165, 0.24}, shared[3] = {0.15, 0.173, 0.256};
+    const int64_t ctas = tiles * c.split;
+    if (ctas <= dev.sms) {
+      run = double(ceil_div(tiles, dev.tile_clusters[w][1][log2])) * blocks * alone[w];
+    } else {
+      const double rounds = double(tiles) / dev.tile_clusters[w][0][log2];
+      run = blocks * shared[w] * (rounds > 1.0 ? 2.0 * rounds : double(ctas) / dev.sms);
+    }
+  }
+  const double join = c.split > 1 ? 1.5 + double(tiles) * c.split * side * c.bn * 4.0 / 4e6 : 0.0;
+  return fixed + run + join;
+}
+
+Choice choose(const Operand& P, const Operand& Q, int k_blocks, const Device& dev) {
+  Choice best = {true, 256, 1};
+  double least = cost_us(best, P.rows, Q.rows, k_blocks, dev);
+  for (const int pair : {1, 0})
+    for (const int bn : {256, 128, 64, 32}) {
+      if (pair ? bn < 128 : bn > 128) continue;
+      if (bn == 32 && Q.mn) continue;                        // MN-major boxes are 64 wide
+      for (int split = 1; split <= (pair ? kLinMaxSplit / 2 : kLinMaxSplit) && k_blocks >= 2 * split; split *= 2) {
+        const Choice c = {pair != 0, bn, split};
+        const double t = cost_us(c, P.rows, Q.rows, k_blocks, dev);
+        if (t < least) { least = t; best = c; }
+      }
+    }
+  return best;
 }
 
 bsgg_status launch_product(const Operand& P, const Operand& Q, int in_format, LinParams p, cudaStream_t s) {
@@ -151,42 +278,52 @@ bsgg_status launch_product(const Operand& P, const Operand& Q, int in_format, Li
   p.in_kind = in_format;
   p.wait_limit_ns = kWaitLimitNs;
   CUtensorMap tp, tq;
-  const int64_t pair_tiles = ceil_div(P.rows, 256) * ceil_div(Q.rows, 256);
+  const Choice c = choose(P, Q, p.k_blocks, *dev);
+  const int side = c.pair ? 256 : 128;
+  p.p_tiles = static_cast<int32_t>(ceil_div(P.rows, side));
+  p.q_tiles = static_cast<int32_t>(ceil_div(Q.rows, c.bn));
+  p.idesc = lin_idesc(in_format, P.mn, Q.mn, side, c.bn);
+  if (!encode_operand(&tp, P, 128) || !encode_operand(&tq, Q, c.pair ? c.bn / 2 : c.bn)) return BSGG_ERR_CUDA;
   cudaError_t e;
-  if (pair_tiles >= dev->sms / 2 && Q.rows > 128) {
-    p.p_tiles = static_cast<int32_t>(ceil_div(P.rows, 256));
-    p.q_tiles = static_cast<int32_t>(ceil_div(Q.rows, 256));
-    p.idesc = lin_idesc(in_format, P.mn, Q.mn, 256, 256);
-    if (!encode_operand(&tp, P, 128) || !encode_operand(&tq, Q, 128)) return BSGG_ERR_CUDA;
-    const int64_t units = pair_tiles < dev->sms / 2 ? pair_tiles : dev->sms / 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * units), 1, 1);
-    cfg.blockDim = dim3(kLinThreads, 1, 1);
-    cfg.dynamicSmemBytes = LinPair::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, linear_pair_kernel, tp, tq, p);
-  } else {
-    // the instruction's N: the least that holds the output rows (MN-major boxes are 64 wide)
-    const int bn = Q.rows <= 32 && !Q.mn ? 32 : Q.rows <= 64 ? 64 : 128;
-    p.p_tiles = static_cast<int32_t>(ceil_div(P.rows, 128));
-    p.q_tiles = static_cast<int32_t>(ceil_div(Q.rows, bn));
-    p.idesc = lin_idesc(in_format, P.mn, Q.mn, 128, bn);
-    // split the reduction while the tiles leave SMs idle and every part keeps four blocks
-    const int64_t tiles = int64_t(p.p_tiles) * p.q_tiles;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * dev->sms && p.k_blocks >= 8 * split) split *= 2;
-    if (!encode_operand(&tp, P, 128) || !encode_operand(&tq, Q, bn)) return BSGG_ERR_CUDA;
-    e = bn == 32   ? launch_tile<32>(tp, tq, p, split, s)
-        : bn == 64 ? launch_tile<64>(tp, tq, p, split, s)
-                   : launch_tile<128>(tp, tq, p, split, s);
+  if (c.pair) e = c.bn == 256 ? launch_pair<256>(tp, tq, p, c.split, *dev, s) : launch_pair<128>(tp, tq, p, c.split, *dev, s);
+  else if (c.bn == 128) e = launch_tile<128>(tp, tq, p, c.split, dev->sms, s);
+  else if (c.bn == 64) e = launch_tile<64>(tp, tq, p, c.split, dev->sms, s);
+  else e = launch_tile<32>(tp, tq, p, c.split, dev->sms, s);
+  return e == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA;
+}
+
+template <int KIND, int ACT>
+cudaError_t launch_dz_one(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias,
+                          cudaStream_t s) {
+  // runs of at least 32 rows, at most the portable cluster's eight
+  const int64_t runs = ceil_div(d->m, 32);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(runs < kDzSplit ? runs : kDzSplit), static_cast<unsigned>(ceil_div(d->n, kDzCols)), 1);
+  cfg.blockDim = dim3(kDzThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cfg.gridDim.x;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dz_kernel<KIND, ACT>, d->m, d->n, d->ld_dy, d->ldz, d->ld_dz, dy, z, dz, dbias);
+}
+template <int KIND>
+cudaError_t launch_dz_kind(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias,
+                           cudaStream_t s) {
+  switch (d->activation) {
+    case BSGG_ACT_RELU: return launch_dz_one<KIND, BSGG_ACT_RELU>(d, dy, z, dz, dbias, s);
+    case BSGG_ACT_SRELU: return launch_dz_one<KIND, BSGG_ACT_SRELU>(d, dy, z, dz, dbias, s);
+    case BSGG_ACT_SILU: return launch_dz_one<KIND, BSGG_ACT_SILU>(d, dy, z, dz, dbias, s);
+    case BSGG_ACT_GELU: return launch_dz_one<KIND, BSGG_ACT_GELU>(d, dy, z, dz, dbias, s);
+    default: return launch_dz_one<KIND, BSGG_ACT_NONE>(d, dy, z, dz, dbias, s);
   }
+}
+bsgg_status launch_dz(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias, cudaStream_t s) {
+  const cudaError_t e = d->in_format == BSGG_OUT_BF16 ? launch_dz_kind<OK_BF16>(d, dy, z, dz, dbias, s)
+                                                      : launch_dz_kind<OK_F16>(d, dy, z, dz, dbias, s);
   return e == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA;
 }
 
@@ -252,9 +389,8 @@ bsgg_status bsgg_linear_backward(const bsgg_linear_bwd_desc* d, const void* dy, 
     return BSGG_OK;
   }
   if (has_act || dbias) {
-    dz_kernel<<<static_cast<unsigned>(ceil_div(d->n, 32)), 256, 0, s>>>(d->m, d->n, d->ld_dy, d->ldz, d->ld_dz, d->in_format,
-                                                                       d->activation, dy, z, dz, dbias);
-    if (launch_status() != BSGG_OK) return BSGG_ERR_CUDA;
+    const bsgg_status st = launch_dz(d, dy, z, dz, dbias, s);
+    if (st != BSGG_OK) return st;
   }
   const void* g = has_act ? dz : dy;
   const int64_t ldg = has_act ? d->ld_dz : d->ld_dy;

@@ -22,6 +22,7 @@ namespace bsgg {
 
 constexpr int kLinDepth = 64;                 // reduction length of a stage: 128 bytes
 constexpr int kLinEpiWarps = 8;
+constexpr int kLinMaxSplit = 8;                // CTAs (or with pairs, twice the pairs) that share a tile's reduction
 constexpr int kLinChunk = 16;                 // output rows an epilogue warp finishes at a time
 constexpr int kLinThreads = 32 * (2 + kLinEpiWarps);
 
@@ -41,13 +42,16 @@ struct LinParams {
   uint64_t wait_limit_ns;
 };
 
-// act(z).  silu = z / (1 + e^-z); gelu = z Phi(z) with Phi from normcdff,
-// which keeps its relative accuracy in the lower tail where 1 + erf cancels.
+// act(z).  silu = z / (1 + e^-z) with the hardware's exponential and quotient
+// (a few units of 2^-23, as in the grouped GEMM's epilogues; a quarter of the
+// instructions of expf and an IEEE division); gelu = z Phi(z) with Phi from
+// normcdff, which keeps its relative accuracy in the lower tail where 1 + erf
+// cancels.
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if (ACT == BSGG_ACT_RELU) return z <= 0.0f ? 0.0f : z;               // a NaN stays
   if (ACT == BSGG_ACT_SRELU) return z <= 0.0f ? 0.0f : z * z;
-  if (ACT == BSGG_ACT_SILU) return z / (1.0f + expf(-z));
+  if (ACT == BSGG_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
   if (ACT == BSGG_ACT_GELU) return z * normcdff(z);
   return z;
 }
@@ -73,51 +77,164 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+__device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 
-// CH values of output column i, rows j0 .. j0 + CH - 1.
-template <int CH, int ACT>
-__device__ __forceinline__ void lin_finish_act(const LinParams& p, float (&v)[CH], int i, int j0, int nj, float bias) {
-  float r[CH];
-  if (p.residual != nullptr) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-      r[c] = c < nj ? load1(p.residual_kind, p.residual, (j0 + c) * p.ld_residual + i) : 0.0f;
-  }
-#pragma unroll
-  for (int c = 0; c < CH; ++c) v[c] += bias;
-  if (p.z != nullptr) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if (c < nj) store1(p.in_kind, p.z, (j0 + c) * p.ldz + i, v[c]);
-  }
+// CH values of output column i, rows j0 .. j0 + CH - 1 (FULL: all of them exist).
+// Every choice of type and function is made once for the chunk, around a loop
+// whose accesses step by the row pitch: with the choices inside the loop the
+// epilogue took 72 thousand cycles per 256 x 256 tile, twice the products of a
+// reduction of 4096.
+template <int KIND, int CH, bool FULL>
+__device__ __forceinline__ void lin_load_rows(const void* base, int64_t at, int64_t ld, int nj, float (&r)[CH]) {
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    v[c] = act_value<ACT>(v[c]);
-    if (p.residual != nullptr) v[c] += r[c];
+    r[c] = (FULL || c < nj) ? load1<KIND>(base, at) : 0.0f;
+    at += ld;
   }
+}
+template <int KIND, int CH, bool FULL>
+__device__ __forceinline__ void lin_store_rows(void* base, int64_t at, int64_t ld, int nj, const float (&v)[CH]) {
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-    if (c < nj) store1(p.out_kind, p.out, (j0 + c) * p.ld_out + i, v[c]);
+  for (int c = 0; c < CH; ++c) {
+    if (FULL || c < nj) store1<KIND>(base, at, v[c]);
+    at += ld;
+  }
+}
+template <int ACT, int CH>
+__device__ __forceinline__ void lin_act(float (&v)[CH]) {
+#pragma unroll
+  for (int c = 0; c < CH; ++c) v[c] = act_value<ACT>(v[c]);
+}
+template <int CH, bool FULL>
+__device__ __forceinline__ void lin_finish_rows(const LinParams& p, float (&v)[CH], int i, int j0, int nj, float bias) {
+  float r[CH];
+  if (p.residual != nullptr) {
+    const int64_t at = static_cast<int64_t>(j0) * p.ld_residual + i;
+    if (p.residual_kind == OK_BF16) lin_load_rows<OK_BF16, CH, FULL>(p.residual, at, p.ld_residual, nj, r);
+    else if (p.residual_kind == OK_F16) lin_load_rows<OK_F16, CH, FULL>(p.residual, at, p.ld_residual, nj, r);
+    else lin_load_rows<OK_F32, CH, FULL>(p.residual, at, p.ld_residual, nj, r);
+  }
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) v[c] += bias;
+  }
+  if (p.z != nullptr) {
+    const int64_t at = static_cast<int64_t>(j0) * p.ldz + i;
+    if (p.in_kind == OK_BF16) lin_store_rows<OK_BF16, CH, FULL>(p.z, at, p.ldz, nj, v);
+    else lin_store_rows<OK_F16, CH, FULL>(p.z, at, p.ldz, nj, v);
+  }
+  switch (p.act) {
+    case BSGG_ACT_RELU: lin_act<BSGG_ACT_RELU>(v); break;
+    case BSGG_ACT_SRELU: lin_act<BSGG_ACT_SRELU>(v); break;
+    case BSGG_ACT_SILU: lin_act<BSGG_ACT_SILU>(v); break;
+    case BSGG_ACT_GELU: lin_act<BSGG_ACT_GELU>(v); break;
+  }
+  if (p.residual != nullptr) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) v[c] += r[c];
+  }
+  const int64_t at = static_cast<int64_t>(j0) * p.ld_out + i;
+  if (p.out_kind == OK_BF16) lin_store_rows<OK_BF16, CH, FULL>(p.out, at, p.ld_out, nj, v);
+  else if (p.out_kind == OK_F16) lin_store_rows<OK_F16, CH, FULL>(p.out, at, p.ld_out, nj, v);
+  else lin_store_rows<OK_F32, CH, FULL>(p.out, at, p.ld_out, nj, v);
 }
 template <int CH>
 __device__ __forceinline__ void lin_finish(const LinParams& p, float (&v)[CH], int i, int j0, float bias) {
   const int nj = p.rows - j0;
   if (i >= p.cols || nj <= 0) return;
-  switch (p.act) {
-    case BSGG_ACT_RELU: lin_finish_act<CH, BSGG_ACT_RELU>(p, v, i, j0, nj, bias); break;
-    case BSGG_ACT_SRELU: lin_finish_act<CH, BSGG_ACT_SRELU>(p, v, i, j0, nj, bias); break;
-    case BSGG_ACT_SILU: lin_finish_act<CH, BSGG_ACT_SILU>(p, v, i, j0, nj, bias); break;
-    case BSGG_ACT_GELU: lin_finish_act<CH, BSGG_ACT_GELU>(p, v, i, j0, nj, bias); break;
-    default: lin_finish_act<CH, BSGG_ACT_NONE>(p, v, i, j0, nj, bias); break;
-  }
+  if (nj >= CH) lin_finish_rows<CH, true>(p, v, i, j0, nj, bias);
+  else lin_finish_rows<CH, false>(p, v, i, j0, nj, bias);
 }
 __device__ __forceinline__ float lin_bias(const LinParams& p, int i) {
   return p.bias != nullptr && i < p.cols ? load1(p.bias_kind, p.bias, i) : 0.0f;
+}
+
+// Partial tiles of a split reduction: CH output rows from row r of the tile, this
+// lane's column, 128 columns per row; the stages' memory takes them, once every
+// load has landed and every MMA completed.
+template <int CH>
+__device__ __forceinline__ void lin_put_part(uint8_t* smem, const float (&v)[CH], int r, int col) {
+  float* at = reinterpret_cast<float*>(smem) + r * 128 + col;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) at[k * 128] = v[k];
+}
+
+// Adds the partial tiles of SPLIT CTAs (ranks first, first + stride, ...) in
+// order of rank, so the sum does not depend on timing, into this CTA's own tile:
+// part p takes rows [p BN / SPLIT, ...), which nobody else reads here.  A warp
+// reads a whole row of 128 columns per load, 16 bytes a lane, and has eight such
+// loads in flight: distributed shared memory answers in about a microsecond, and
+// 4-byte loads moved 2.2 MB/us over the whole chip, more time than the products.
+template <int SPLIT>
+__device__ __forceinline__ void lin_sum_parts(uint32_t part_base, int r0, int r1, uint32_t stride, uint32_t first) {
+  constexpr int kRows = 8 / SPLIT;
+  const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+  for (int r = r0 + warp * kRows; r < r1; r += kLinEpiWarps * kRows) {
+    const uint32_t at = part_base + static_cast<uint32_t>((r * 128 + lane * 4) * 4);
+    float4 u[SPLIT][kRows];
+#pragma unroll
+    for (int s = 0; s < SPLIT; ++s) {
+      const uint32_t from = mapa_shared(at, first + stride * s);
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (r + k < r1) u[s][k] = ld_shared_cluster4(from + 512u * k);
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (r + k >= r1) break;
+      float4 v = u[0][k];
+#pragma unroll
+      for (int s = 1; s < SPLIT; ++s) { v.x += u[s][k].x; v.y += u[s][k].y; v.z += u[s][k].z; v.w += u[s][k].w; }
+      st_shared_v4(at + 512u * k, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w));
+    }
+  }
+}
+// Then this part's rows go out, lanes along the columns as everywhere else.
+template <int RUN>
+__device__ __forceinline__ void lin_finish_part(const LinParams& p, const uint8_t* smem, int r0, int r1, int i0, int j0) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = warp & 3, half = (warp - 2) >> 2, i = i0 + q * 32 + lane;
+  const float bias = lin_bias(p, i);
+  for (int r = r0 + half * RUN; r < r1; r += 2 * RUN) {
+    const float* at = reinterpret_cast<const float*>(smem) + r * 128 + q * 32 + lane;
+    float v[RUN];
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) v[k] = at[k * 128];
+    lin_finish<RUN>(p, v, i, j0 + r, bias);
+  }
+}
+// Only the epilogue's warps come here.
+template <int BN>
+__device__ __forceinline__ void lin_join(const LinParams& p, uint8_t* smem, int split, int part, uint32_t stride,
+                                         uint32_t first, int i0, int j0) {
+  const int per = BN / split, r0 = part * per;
+  const uint32_t base = smem_u32(smem);
+  if (split == 2) lin_sum_parts<2>(base, r0, r0 + per, stride, first);
+  else if (split == 4) lin_sum_parts<4>(base, r0, r0 + per, stride, first);
+  else lin_sum_parts<8>(base, r0, r0 + per, stride, first);
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kLinEpiWarps) : "memory");
+  if (per >= 32) lin_finish_part<16>(p, smem, r0, r0 + per, i0, j0);
+  else lin_finish_part<4>(p, smem, r0, r0 + per, i0, j0);
+}
+
+// True in one lane of a converged warp.  The matrix instructions are issued
+// under it by a warp whose every lane runs the loop: issued by a lane chosen with
+// an ordinary branch, each cost about 85 cycles of the issuing thread (a 128 x 32
+// block of 64 took 0.22 us whatever its width), under elect.sync about 33.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
 }
 
 // One stage's box loads of an operand tile of ROWS rows from row r0 at
@@ -137,17 +254,27 @@ __device__ __forceinline__ void lin_load(uint32_t dst, const CUtensorMap* map, u
 }
 
 // ---------------------------------------------------------------- CTA pairs
-// 256 x 256 tiles, persistent, two accumulators: the epilogue of one tile runs
-// under the products of the next.
+// 256 x BN tiles (BN 256 or 128), persistent, two accumulators: the epilogue of one tile runs
+// under the products of the next.  Where there are too few tiles for the SMs,
+// clusters of `split` pairs share a tile's reduction instead, one tile each.
+template <int BN>
 struct LinPair {
-  static constexpr int kStages = 6;
-  static constexpr int kOpBytes = 128 * 128;               // this CTA's 128 rows of either operand
-  static constexpr int kOffP = 0, kOffQ = kStages * kOpBytes;
-  static constexpr int kOffBars = 2 * kStages * kOpBytes;
+  // 64-blocks of the reduction per stage.  Handing a stage over costs its threads
+  // about 230 cycles; a block's products take 512 at BN = 256, where they hide it,
+  // and 256 at BN = 128
+  static constexpr int kBlocks = BN == 256 ? 1 : 2;
+  static constexpr int kPBlock = 128 * 128, kQBlock = BN / 2 * 128;   // this CTA's 128 and BN / 2 rows
+  static constexpr int kPBytes = kBlocks * kPBlock, kQBytes = kBlocks * kQBlock;
+  static constexpr int kStageBytes = kPBytes + kQBytes;
+  static constexpr int kStages = 196608 / kStageBytes;
+  static constexpr int kOffP = 0, kOffQ = kStages * kPBytes;
+  static constexpr int kOffBars = kStages * kStageBytes;
   static constexpr int kNumBars = 2 * kStages + 4 + 1;
   static constexpr int kOffHolder = kOffBars + 8 * kNumBars;
   static constexpr int kOffAbort = kOffHolder + 4;
   static constexpr int kSmem = kOffAbort + 4 + 1024;
+  static constexpr uint32_t kCols = 2 * BN;                           // two accumulators
+  static_assert(kOffBars >= 128 * BN * 4, "the partial tile reuses the stages");
 };
 
 // Tile order: bands of 8 tiles along q, every p of a band before the next, so
@@ -161,10 +288,11 @@ __device__ __forceinline__ void lin_tile(int t, int p_tiles, int q_tiles, int& t
   tq = band * kBand + in % w;
 }
 
-static __global__ void __launch_bounds__(kLinThreads, 1)
+template <int BN>
+__global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                       const __grid_constant__ LinParams p) {
-  using Ly = LinPair;
+                       const __grid_constant__ LinParams p, int split) {
+  using Ly = LinPair<BN>;
   constexpr int S = Ly::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -178,10 +306,15 @@ static __global__ void __launch_bounds__(kLinThreads, 1)
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + Ly::kOffHolder);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kOffAbort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const bool leader = rank == 0;
-  const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
+  // ranks 2 s and 2 s + 1 are the pair that sums run s of the reduction
+  const uint32_t rank = cluster_ctarank(), prank = rank & 1u, even = rank & ~1u;
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
+  const int part = static_cast<int>(rank >> 1);
+  const bool leader = prank == 0;
+  const int unit = blockIdx.x / (2 * split), units = gridDim.x / (2 * split);
   const int tiles = p.p_tiles * p.q_tiles;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * part / split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (part + 1) / split);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(full_bar(s), 1); mbar_init(empty_bar(s), 1); }
@@ -192,7 +325,7 @@ static __global__ void __launch_bounds__(kLinThreads, 1)
     prefetch_tmap(&tmP);
     prefetch_tmap(&tmQ);
   }
-  if (warp == 1) { tmem_alloc_pair(smem_u32(holder), 512); tmem_relinquish_pair(); }
+  if (warp == 1) { tmem_alloc_pair(smem_u32(holder), Ly::kCols); tmem_relinquish_pair(); }
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -207,14 +340,17 @@ static __global__ void __launch_bounds__(kLinThreads, 1)
       for (int t = unit; t < tiles && ok; t += units) {
         int tp, tq;
         lin_tile(t, p.p_tiles, p.q_tiles, tp, tq);
-        const int p0 = tp * 256 + static_cast<int>(rank) * 128, q0 = tq * 256 + static_cast<int>(rank) * 128;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        const int p0 = tp * 256 + static_cast<int>(prank) * 128, q0 = tq * BN + static_cast<int>(prank) * (BN / 2);
+        for (int kb = kb0; kb < kb1; kb += Ly::kBlocks) {
           if (!mbar_wait(empty_bar(st), phase ^ 1u, abort_flag, p.wait_limit_ns)) { ok = false; break; }
           // both CTAs' bytes complete the even CTA's barrier
-          const uint32_t fb = full_bar(st), fbl = mapa_shared(fb, 0);
-          if (leader) mbar_expect_tx(fb, 4u * Ly::kOpBytes);
-          lin_load<128, true>(sbase + Ly::kOffP + st * Ly::kOpBytes, &tmP, fbl, p.p_mn, p0, kb);
-          lin_load<128, true>(sbase + Ly::kOffQ + st * Ly::kOpBytes, &tmQ, fbl, p.q_mn, q0, kb);
+          const uint32_t fb = full_bar(st), fbl = mapa_shared(fb, even);
+          const int nb = min(Ly::kBlocks, kb1 - kb);
+          if (leader) mbar_expect_tx(fb, 2u * nb * (Ly::kPBlock + Ly::kQBlock));
+          for (int b = 0; b < nb; ++b) {
+            lin_load<128, true>(sbase + Ly::kOffP + st * Ly::kPBytes + b * Ly::kPBlock, &tmP, fbl, p.p_mn, p0, kb + b);
+            lin_load<BN / 2, true>(sbase + Ly::kOffQ + st * Ly::kQBytes + b * Ly::kQBlock, &tmQ, fbl, p.q_mn, q0, kb + b);
+          }
           any = true;
           if (++st == S) { st = 0; phase ^= 1u; }
         }
@@ -234,7 +370,7 @@ static __global__ void __launch_bounds__(kLinThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0 && leader) {
+    if (leader) {
       int st = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -243,107 +379,131 @@ static __global__ void __launch_bounds__(kLinThreads, 1)
       // 16 reduction indices: 32 bytes inside a K-major row, 16 rows of 128 bytes MN-major
       const uint64_t pstep = p.p_mn ? 2048 >> 4 : 32 >> 4, qstep = p.q_mn ? 2048 >> 4 : 32 >> 4;
       for (int t = unit; t < tiles && ok; t += units) {
-        if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.wait_limit_ns)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.wait_limit_ns))) { ok = false; break; }
         tc_fence_after();
-        const uint32_t d = tmem + acc * 256;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-          if (!mbar_wait(full_bar(st), phase, abort_flag, p.wait_limit_ns)) { ok = false; break; }
+        const uint32_t d = tmem + acc * BN;
+        for (int kb = kb0; kb < kb1; kb += Ly::kBlocks) {
+          if (!__all_sync(0xffffffffu, mbar_wait(full_bar(st), phase, abort_flag, p.wait_limit_ns))) { ok = false; break; }
           tc_fence_after();
-          const uint64_t pd = pd0 + static_cast<uint64_t>((st * Ly::kOpBytes) >> 4);
-          const uint64_t qd = qd0 + static_cast<uint64_t>((st * Ly::kOpBytes) >> 4);
+          const uint64_t pd = pd0 + static_cast<uint64_t>((st * Ly::kPBytes) >> 4);
+          const uint64_t qd = qd0 + static_cast<uint64_t>((st * Ly::kQBytes) >> 4);
+          const bool whole = Ly::kBlocks == 1 || kb + 1 < kb1;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16_pair(d, pd + kk * pstep, qd + kk * qstep, p.idesc, (kb | kk) != 0 ? 1u : 0u);
-          tc_commit_pair(empty_bar(st), 3);
+            for (int kk = 0; kk < 4 * Ly::kBlocks; ++kk) {
+              if (kk >= 4 && !whole) break;
+              tc_mma_bf16_pair(d, pd + (kk / 4) * (Ly::kPBlock >> 4) + (kk % 4) * pstep,
+                               qd + (kk / 4) * (Ly::kQBlock >> 4) + (kk % 4) * qstep, p.idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+            }
+            tc_commit_pair(empty_bar(st), pair_mask);
+          }
+          __syncwarp();
           if (++st == S) { st = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        tc_commit_pair(accf_bar(acc), 3);
+        if (elect_one()) tc_commit_pair(accf_bar(acc), pair_mask);
+        __syncwarp();
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
-      if (!ok) {
+      if (!ok && elect_one()) {
         if (p.status != nullptr) atomicOr(p.status, kStatusTimeout);
-        tc_commit_pair(drain_bar, 1);
+        tc_commit_pair(drain_bar, static_cast<uint16_t>(1u << even));
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < kDrainLimitNs) {}
       }
     }
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3, half = (warp - 2) >> 2;         // lane quadrant, columns [128 half, + 128)
+    const int q = warp & 3, half = (warp - 2) >> 2;         // lane quadrant, half of the columns
+    constexpr int kHalf = BN / 2;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = unit; t < tiles; t += units) {
       int tp, tq;
       lin_tile(t, p.p_tiles, p.q_tiles, tp, tq);
-      const int i = tp * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const int i = tp * 256 + static_cast<int>(prank) * 128 + q * 32 + lane;
       const float bias = lin_bias(p, i);
       if (!__all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag, p.wait_limit_ns))) {
         if (lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusTimeout);
         break;
       }
       tc_fence_after();
-      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256 + half * 128;
+      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + half * kHalf;
 #pragma unroll 1
-      for (int c = 0; c < 128; c += kLinChunk) {
+      for (int c = 0; c < kHalf; c += kLinChunk) {
         float v[kLinChunk];
         tmem_ld16(ta + c, reinterpret_cast<uint32_t*>(v));
         tmem_wait_ld();
-        if (c == 128 - kLinChunk) {
+        if (c == kHalf - kLinChunk) {
           // every column is in registers or stored: hand the accumulator back
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(acce_bar(acc), 0));
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(acce_bar(acc), even));
         }
-        lin_finish<kLinChunk>(p, v, i, tq * 256 + half * 128 + c, bias);
+        if (split == 1) lin_finish<kLinChunk>(p, v, i, tq * BN + half * kHalf + c, bias);
+        else lin_put_part(smem, v, half * kHalf + c, q * 32 + lane);
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
   }
   __syncwarp();
+  if (split > 1) {
+    cluster_sync();
+    if (warp >= 2) {
+      // the pairs' CTAs of this half of p
+      int tp, tq;
+      lin_tile(unit, p.p_tiles, p.q_tiles, tp, tq);
+      lin_join<BN>(p, smem, split, part, 2, prank, tp * 256 + static_cast<int>(prank) * 128, tq * BN);
+    }
+  }
   tc_fence_before();
   cluster_sync();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, Ly::kCols);
   }
 }
 
 // ---------------------------------------------------------------- single CTAs
-// One 128 x BN tile per CTA, two CTAs per SM; with a cluster of S CTAs the
-// reduction is split into S runs of blocks, whose partial tiles are added in
-// order of rank through distributed shared memory, every CTA finishing BN / S of
-// the output rows.
-template <int BN>
+// One 128 x BN tile per CTA; with a cluster of S CTAs the reduction is split into
+// S runs of blocks, whose partial tiles are added in order of rank through
+// distributed shared memory, every CTA finishing BN / S of the output rows.
+// Where every CTA has an SM to itself (ALONE) the ring takes the whole of its shared
+// memory in stages of two 64-blocks: operands that come from DRAM want the depth
+// (three 32 KB stages: 0.36 us a block, six: 0.22), and handing a stage over costs
+// its threads about 230 cycles, which the products of one block do not hide
+// (BN = 32: 0.19 us a block with one block per stage, 0.146 with two).  Two CTAs
+// on an SM hide each other's.
+template <int BN, bool ALONE>
 struct LinTile {
-  static constexpr int kPBytes = 128 * 128, kQBytes = BN * 128;
+  static constexpr int kBlocks = ALONE ? 2 : 1;            // 64-blocks of the reduction per stage
+  static constexpr int kPBlock = 128 * 128, kQBlock = BN * 128;
+  static constexpr int kPBytes = kBlocks * kPBlock, kQBytes = kBlocks * kQBlock;
   static constexpr int kStageBytes = kPBytes + kQBytes;
-  static constexpr int kStages = 110 * 1024 / kStageBytes;
-  static constexpr int kOffP = 0, kOffQ = kStages * kPBytes;
-  static constexpr int kOffBars = kStages * kStageBytes;
-  static constexpr int kOffHolder = kOffBars + 8 * (2 * kStages + 1);
-  static constexpr int kOffAbort = kOffHolder + 4;
-  static constexpr int kSmem = kOffAbort + 4 + 1024;
+  static constexpr int kStages = (ALONE ? 220 : 110) * 1024 / kStageBytes;
+  static constexpr int kHead = 1024;                       // barriers, holder, flag; the ring follows
+  static_assert(8 * (2 * kStages + 1) + 8 <= kHead, "barriers");
   static_assert(kStages * kStageBytes >= 128 * BN * 4, "the partial tile reuses the stages");
+  static constexpr int kSmem = kStages * kStageBytes + kHead + 1024;
 };
 
-template <int BN>
-__global__ void __launch_bounds__(kLinThreads, 2)
+template <int BN, bool ALONE>
+__global__ void __launch_bounds__(kLinThreads, ALONE ? 1 : 2)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ LinParams p, int split) {
-  using Ly = LinTile<BN>;
+  using Ly = LinTile<BN, ALONE>;
   constexpr int S = Ly::kStages;
   constexpr uint32_t kCols = BN;                     // tensor-memory columns, a power of two >= 32
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t bar0 = sbase + Ly::kOffBars;
+  const uint32_t bar0 = smem_u32(smem);
+  const uint32_t ring = bar0 + Ly::kHead;                  // stages of P, then of Q
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
   const uint32_t accf_bar = bar0 + 8u * (2 * S);
-  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + Ly::kOffHolder);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kOffAbort);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + 8 * (2 * S + 1));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 8 * (2 * S + 1) + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = blockIdx.x / split;
@@ -372,18 +532,21 @@ __global__ void __launch_bounds__(kLinThreads, 2)
       uint32_t phase = 0;
       bool ok = true;
       int kb = kb0;
-      for (; kb < kb1; ++kb) {
+      for (; kb < kb1; kb += Ly::kBlocks) {
         if (!mbar_wait(empty_bar(st), phase ^ 1u, abort_flag, p.wait_limit_ns)) { ok = false; break; }
         const uint32_t fb = full_bar(st);
-        mbar_expect_tx(fb, Ly::kStageBytes);
-        lin_load<128, false>(sbase + Ly::kOffP + st * Ly::kPBytes, &tmP, fb, p.p_mn, tp * 128, kb);
-        lin_load<BN, false>(sbase + Ly::kOffQ + st * Ly::kQBytes, &tmQ, fb, p.q_mn, tq * BN, kb);
+        const int nb = min(Ly::kBlocks, kb1 - kb);
+        mbar_expect_tx(fb, nb * (Ly::kPBlock + Ly::kQBlock));
+        for (int b = 0; b < nb; ++b) {
+          lin_load<128, false>(ring + st * Ly::kPBytes + b * Ly::kPBlock, &tmP, fb, p.p_mn, tp * 128, kb + b);
+          lin_load<BN, false>(ring + S * Ly::kPBytes + st * Ly::kQBytes + b * Ly::kQBlock, &tmQ, fb, p.q_mn, tq * BN, kb + b);
+        }
         if (++st == S) { st = 0; phase ^= 1u; }
       }
       if (!ok) {
         if (p.status != nullptr) atomicOr(p.status, kStatusTimeout);
         // the loads in flight, one per stage at most: wait (bounded) for each
-        const int issued = kb - kb0;
+        const int issued = (kb - kb0 + Ly::kBlocks - 1) / Ly::kBlocks;
         for (int u = max(0, issued - S); u < issued; ++u) {
           const uint64_t t0 = globaltimer_ns();
           while (!mbar_try_wait(full_bar(u % S), (u / S) & 1) && globaltimer_ns() - t0 < kDrainLimitNs) {}
@@ -391,24 +554,32 @@ __global__ void __launch_bounds__(kLinThreads, 2)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int st = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      const uint64_t pd0 = p.p_mn ? sdesc_mnmajor_sw128(sbase + Ly::kOffP) : sdesc_kmajor_sw128(sbase + Ly::kOffP);
-      const uint64_t qd0 = p.q_mn ? sdesc_mnmajor_sw128(sbase + Ly::kOffQ) : sdesc_kmajor_sw128(sbase + Ly::kOffQ);
-      const uint64_t pstep = p.p_mn ? 2048 >> 4 : 32 >> 4, qstep = p.q_mn ? 2048 >> 4 : 32 >> 4;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(full_bar(st), phase, abort_flag, p.wait_limit_ns)) { ok = false; break; }
-        tc_fence_after();
-        const uint64_t pd = pd0 + static_cast<uint64_t>((st * Ly::kPBytes) >> 4);
-        const uint64_t qd = qd0 + static_cast<uint64_t>((st * Ly::kQBytes) >> 4);
+    int st = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint32_t ring_q = ring + S * Ly::kPBytes;
+    const uint64_t pd0 = p.p_mn ? sdesc_mnmajor_sw128(ring) : sdesc_kmajor_sw128(ring);
+    const uint64_t qd0 = p.q_mn ? sdesc_mnmajor_sw128(ring_q) : sdesc_kmajor_sw128(ring_q);
+    const uint64_t pstep = p.p_mn ? 2048 >> 4 : 32 >> 4, qstep = p.q_mn ? 2048 >> 4 : 32 >> 4;
+    for (int kb = kb0; kb < kb1; kb += Ly::kBlocks) {
+      if (!__all_sync(0xffffffffu, mbar_wait(full_bar(st), phase, abort_flag, p.wait_limit_ns))) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t pd = pd0 + static_cast<uint64_t>((st * Ly::kPBytes) >> 4);
+      const uint64_t qd = qd0 + static_cast<uint64_t>((st * Ly::kQBytes) >> 4);
+      const bool whole = Ly::kBlocks == 1 || kb + 1 < kb1;
+      if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_bf16(tmem, pd + kk * pstep, qd + kk * qstep, p.idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 4 * Ly::kBlocks; ++kk) {
+          if (kk >= 4 && !whole) break;
+          tc_mma_bf16(tmem, pd + (kk / 4) * (Ly::kPBlock >> 4) + (kk % 4) * pstep,
+                      qd + (kk / 4) * (Ly::kQBlock >> 4) + (kk % 4) * qstep, p.idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+        }
         tc_commit(empty_bar(st));
-        if (++st == S) { st = 0; phase ^= 1u; }
       }
+      __syncwarp();
+      if (++st == S) { st = 0; phase ^= 1u; }
+    }
+    if (elect_one()) {
       // also the drain when a wait ran out: every issued MMA has completed
       tc_commit(accf_bar);
       if (!ok) {
@@ -438,28 +609,14 @@ __global__ void __launch_bounds__(kLinThreads, 2)
         if (split == 1) {
           lin_finish<kLinChunk>(p, v, i, tq * BN + half * kHalf + c, bias);
         } else {
-          // every load has landed and every MMA has completed: the stages' memory
-          // takes the partial tile, a row of 128 columns per output row
-          float* part = reinterpret_cast<float*>(smem) + (half * kHalf + c) * 128 + q * 32 + lane;
-#pragma unroll
-          for (int k = 0; k < kLinChunk; ++k) part[k * 128] = v[k];
+          lin_put_part(smem + Ly::kHead, v, half * kHalf + c, q * 32 + lane);
         }
       }
     }
   }
   if (split > 1) {
     cluster_sync();
-    if (warp >= 2) {
-      // this CTA's BN / split rows, shared between the two halves of the warps
-      const float bias = lin_bias(p, i);
-      const int per = BN / split, r0 = rank * per;
-      for (int r = r0 + half; r < r0 + per; r += 2) {
-        const uint32_t at = sbase + static_cast<uint32_t>((r * 128 + q * 32 + lane) * 4);
-        float v[1] = {0.0f};
-        for (int s = 0; s < split; ++s) v[0] += ld_shared_cluster(mapa_shared(at, s));
-        lin_finish<1>(p, v, i, tq * BN + r, bias);
-      }
-    }
+    if (warp >= 2) lin_join<BN>(p, smem + Ly::kHead, split, rank, 1, 0, tp * 128, tq * BN);
   }
   tc_fence_before();
   if (split > 1) cluster_sync();          // the partial tiles stay until every CTA has read them

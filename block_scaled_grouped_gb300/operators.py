@@ -13,11 +13,13 @@ dimension is contiguous; a row pitch is taken from their strides.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+from ctypes import byref
 from typing import NamedTuple, Optional
 
-from . import BsggError, IN_FORMATS, OUT_FORMATS, _check, _ptr, _stream, lib, sf_bytes
+import torch
+
+from . import BsggError, IN_FORMATS, _check, _stream, lib, sf_bytes
 
 ROW_FORMATS = {**IN_FORMATS, "f16": 6}
 ACTIVATIONS = {"none": 0, "relu": 1, "srelu": 2, "silu": 3, "gelu": 4}
@@ -74,24 +76,23 @@ def bind(L) -> None:
 
 
 # ---------------------------------------------------------------- arguments
-_formats = None
+# A decode step's kernels take a few microseconds, so the host's share of a call
+# counts: types and shapes are looked at once, through the cheapest calls torch has.
+_FORMATS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
 def _format(t, what: str) -> int:
     """The ABI's code of a tensor's type."""
-    global _formats
-    if _formats is None:
-        import torch
-        _formats = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    code = _formats.get(t.dtype)
+    code = _FORMATS.get(t.dtype)
     if code is None:
         raise ValueError(f"{what}: bfloat16, float16 or float32 expected, got {t.dtype}")
     return code
 
 
 def _dtype(name: str):
-    import torch
-    d = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}.get(name)
+    d = _DTYPES.get(name)
     if d is None:
         raise ValueError(f"format: bf16, f16 or f32 expected, got {name!r}")
     return d
@@ -99,82 +100,106 @@ def _dtype(name: str):
 
 def _matrix(t, what: str, rows=None, cols=None, dtype=None):
     """A CUDA matrix with contiguous rows of the given shape; its row pitch."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{what}: a CUDA matrix expected, got {tuple(t.shape)} on {t.device}")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{what}: ({rows}, {cols}) expected, got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA matrix expected, got {tuple(shape)} on {t.device}")
+    r, c = shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{what}: ({rows}, {cols}) expected, got {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    pitch, step = t.stride()
+    if c > 1 and step != 1:
         raise ValueError(f"{what}: rows must be contiguous (strides {t.stride()})")
-    if t.shape[0] <= 1:
-        return -(-t.shape[1] // 8) * 8       # no second row: any pitch will do
-    if t.stride(0) < t.shape[1]:
+    if r <= 1:
+        return (c + 7) // 8 * 8              # no second row: any pitch will do
+    if pitch < c:
         raise ValueError(f"{what}: rows must not overlap (strides {t.stride()})")
-    return t.stride(0)
+    return pitch
 
 
-def _flat(t, what: str, numel: int, dtype_name: str):
-    """A contiguous CUDA tensor of int32 or float32 values (None passes)."""
-    import torch
+def _flat(t, what: str, numel: int, dtype):
+    """The address of a contiguous CUDA tensor of `numel` int32 or float32
+    values (None passes)."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != getattr(torch, dtype_name) or t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{what}: {numel} contiguous {dtype_name} values on the GPU expected, got "
+    if t.dtype != dtype or t.numel() != numel or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: {numel} contiguous {dtype} values on the GPU expected, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    return t
+    return t.data_ptr()
 
 
-def _on(stream):
-    """Allocations of the body belong to `stream` (None: torch's current one)."""
-    import torch
+_empty = torch.empty
+
+
+def _empty_on(stream):
+    """torch.empty whose memory belongs to `stream` (None: torch's current one)."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _empty
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
+
+    def empty(*shape, **kw):
+        with torch.cuda.stream(stream):
+            return _empty(*shape, **kw)
+    return empty
+
+
+def _handle(t, stream):
+    """The stream's handle; t's device has to be the current one."""
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{dev}, but cuda:{torch._C._cuda_getDevice()} is the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 _status_words = {}
 
 
-def _status(device):
-    """The device's status word that calls without one of their own share."""
-    import torch
-    w = _status_words.get(device)
+def _status_of(t, status):
+    """The address of the given status word, or of the one that calls without one
+    share on t's device."""
+    if status is not None:
+        return _flat(status, "status", 1, _I32)
+    dev = t.get_device()
+    w = _status_words.get(dev)
     if w is None:
-        w = _status_words[device] = torch.zeros(1, dtype=torch.int32, device=device)
-        torch.cuda.synchronize(device)
-    return w
+        w = torch.zeros(1, dtype=_I32, device=t.device)
+        torch.cuda.synchronize(t.device)
+        w = _status_words[dev] = (w, w.data_ptr())
+    return w[1]
 
 
 def operators_status(stream=None, status=None) -> int:
     """Synchronize and read/clear the status word of sort_tokens, linear and
     linear_backward on the current device (0 = ok)."""
-    import torch
-    w = status if status is not None else _status(torch.device("cuda", torch.cuda.current_device()))
-    return int(lib().bsgg_query_status_word(_ptr(w), _stream(stream)))
+    if status is None:
+        w = _status_words.get(torch.cuda.current_device())
+        if w is None:                        # nothing has run here
+            return 0
+        status = w[0]
+    return int(lib().bsgg_query_status_word(status.data_ptr(), _stream(stream)))
 
 
 # ---------------------------------------------------------------- routing
-def _route_desc(logits, topk: int, normalize: bool):
-    ld = _matrix(logits, "logits")
-    return RouteDesc(logits.shape[0], ld, logits.shape[1], int(topk), _format(logits, "logits"), int(bool(normalize)))
-
-
 def route(logits, topk: int, normalize: bool = True, ids=None, weights=None, stream=None):
     """Softmax top-k of (tokens, experts) logits: (ids int32, weights float32),
     each (tokens, topk)."""
-    import torch
-    desc = _route_desc(logits, topk, normalize)
-    n = logits.shape[0] * int(topk)
-    with _on(stream):
+    ld = _matrix(logits, "logits")
+    T, L = logits.shape
+    k = int(topk)
+    desc = RouteDesc(T, ld, L, k, _format(logits, "logits"), 1 if normalize else 0)
+    handle = _handle(logits, stream)
+    if ids is None or weights is None:
+        empty, dev = _empty_on(stream), logits.device
         if ids is None:
-            ids = torch.empty(logits.shape[0], int(topk), dtype=torch.int32, device=logits.device)
+            ids = empty((T, max(k, 0)), dtype=_I32, device=dev)
         if weights is None:
-            weights = torch.empty(logits.shape[0], int(topk), dtype=torch.float32, device=logits.device)
-    _flat(ids, "ids", n, "int32"), _flat(weights, "weights", n, "float32")
-    _check(lib().bsgg_route(ctypes.byref(desc), _ptr(logits), _ptr(ids), _ptr(weights), _stream(stream)), "bsgg_route")
+            weights = empty((T, max(k, 0)), dtype=_F32, device=dev)
+    _check(lib().bsgg_route(byref(desc), logits.data_ptr(), _flat(ids, "ids", T * k, _I32),
+                            _flat(weights, "weights", T * k, _F32), handle), "bsgg_route")
     return ids, weights
 
 
@@ -182,23 +207,25 @@ def route_backward(logits, ids, weights, dweights, normalize: bool = True, row_o
     """Gradient of route with respect to the logits, in their type.  dweights is
     (tokens, topk), or with row_of_slot a per-row gradient (the backward GEMM's
     dprob)."""
-    import torch
-    if ids.dim() != 2 or ids.shape[0] != logits.shape[0]:
-        raise ValueError(f"ids: (tokens, topk) expected, got {tuple(ids.shape)}")
-    desc = _route_desc(logits, ids.shape[1], normalize)
+    ld = _matrix(logits, "logits")
+    T, L = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids: ({T}, topk) expected, got {tuple(ids.shape)}")
     n = ids.numel()
-    _flat(ids, "ids", n, "int32"), _flat(weights, "weights", n, "float32")
-    _flat(row_of_slot, "row_of_slot", n, "int32")
-    _flat(dweights, "dweights", dweights.numel() if row_of_slot is not None else n, "float32")
-    with _on(stream):
-        if dlogits is None:
-            # the logits' pitch, so that one desc serves both
-            dlogits = torch.empty(logits.shape[0], desc.ld, dtype=logits.dtype, device=logits.device)[:, :logits.shape[1]]
-    if _matrix(dlogits, "dlogits", *logits.shape, dtype=logits.dtype) != desc.ld:
+    rows = 0 if row_of_slot is None else dweights.numel()
+    desc = RouteDesc(T, ld, L, ids.shape[1], _format(logits, "logits"), 1 if normalize else 0)
+    handle = _handle(logits, stream)
+    if dlogits is None:
+        # the logits' pitch, so that one desc serves both
+        dlogits = _empty_on(stream)((T, ld), dtype=logits.dtype, device=logits.device)
+        if ld != L:
+            dlogits = dlogits[:, :L]
+    elif _matrix(dlogits, "dlogits", T, L, logits.dtype) != ld:
         raise ValueError("dlogits: the logits' row pitch expected")
-    _check(lib().bsgg_route_backward(ctypes.byref(desc), _ptr(logits), _ptr(ids), _ptr(weights), _ptr(dweights),
-                                     _ptr(row_of_slot), dweights.numel() if row_of_slot is not None else 0, _ptr(dlogits),
-                                     _stream(stream)), "bsgg_route_backward")
+    _check(lib().bsgg_route_backward(byref(desc), logits.data_ptr(), _flat(ids, "ids", n, _I32),
+                                     _flat(weights, "weights", n, _F32), _flat(dweights, "dweights", rows or n, _F32),
+                                     _flat(row_of_slot, "row_of_slot", n, _I32), rows, dlogits.data_ptr(), handle),
+           "bsgg_route_backward")
     return dlogits
 
 
@@ -215,51 +242,60 @@ def sort_tokens(ids, num_experts: int, m_pad: Optional[int] = None, weights=None
     """Tokens by expert: ids (tokens, topk) int32 -> TokenMap.  m_pad: rows to lay
     out, by default sort_rows(ids.numel(), num_experts); pass the value of
     rows_used read back to the host for the least."""
-    import torch
     n = ids.numel()
     if ids.dim() != 2:
         raise ValueError(f"ids: (tokens, topk) expected, got {tuple(ids.shape)}")
-    _flat(ids, "ids", n, "int32"), _flat(weights, "weights", n, "float32")
+    p_ids, p_weights = _flat(ids, "ids", n, _I32), _flat(weights, "weights", n, _F32)
     if m_pad is None:
         m_pad = sort_rows(n, num_experts)
     L = lib()
-    nws = int(L.bsgg_sort_workspace_bytes(n, num_experts))
-    with _on(stream):
-        i32 = dict(dtype=torch.int32, device=ids.device)
-        # one allocation: offsets, rows_used, slots, rows, workspace
-        buf = torch.empty(num_experts + 1 + n + max(m_pad, 0) + nws // 4, **i32)
-        prob = torch.empty(max(m_pad, 0), dtype=torch.float32, device=ids.device)
-    offsets, used, row_of_slot, slot_of_row, ws = buf.split([num_experts, 1, n, max(m_pad, 0), nws // 4])
-    status = _status(ids.device) if status is None else status
-    _check(L.bsgg_sort_tokens(n, num_experts, m_pad, _ptr(ids), _ptr(weights), _ptr(offsets), _ptr(row_of_slot),
-                              _ptr(slot_of_row), _ptr(prob), _ptr(used), _ptr(ws) if nws else None, _ptr(status),
-                              _stream(stream)), "bsgg_sort_tokens")
+    nws = L.bsgg_sort_workspace_bytes(n, num_experts) // 4
+    handle = _handle(ids, stream)
+    empty, dev = _empty_on(stream), ids.device
+    m, e = max(m_pad, 0), max(num_experts, 0)
+    # one allocation for the integers: slots, rows, offsets, rows_used, workspace
+    buf = empty(n + m + e + 1 + nws, dtype=_I32, device=dev)
+    prob = empty(m, dtype=_F32, device=dev)
+    row_of_slot, slot_of_row, offsets, used, _ = buf.split_with_sizes((n, m, e, 1, nws))
+    at = buf.data_ptr()
+    _check(L.bsgg_sort_tokens(n, num_experts, m_pad, p_ids, p_weights, at + 4 * (n + m), at, at + 4 * n, prob.data_ptr(),
+                              at + 4 * (n + m + e), at + 4 * (n + m + e + 1) if nws else None, _status_of(ids, status),
+                              handle), "bsgg_sort_tokens")
     return TokenMap(offsets, row_of_slot.view(ids.shape), slot_of_row, prob, used)
 
 
-def _row_buffers(m_pad: int, hidden: int, row_format: str, device):
+def _row_buffers(m_pad: int, hidden: int, row_format: str, device, empty):
     """Buffers of rows and scale factors: uint8 codes, or 16-bit values."""
-    import torch
     if row_format in ("bf16", "f16"):
-        return torch.empty(m_pad, hidden, dtype=_dtype(row_format), device=device), None
-    fp4 = row_format in ("nvfp4", "fp4_ue8m0_16", "mxfp4")
+        return empty((m_pad, hidden), dtype=_DTYPES[row_format], device=device), None
     v = 16 if row_format in ("nvfp4", "fp4_ue8m0_16") else 32
-    a = torch.empty(m_pad, hidden // 2 if fp4 else hidden, dtype=torch.uint8, device=device)
-    return a, torch.empty(sf_bytes(m_pad, hidden, v), dtype=torch.uint8, device=device)
+    a = empty((m_pad, hidden // 2 if row_format in _FP4 else hidden), dtype=_U8, device=device)
+    return a, empty(sf_bytes(m_pad, hidden, v), dtype=_U8, device=device)
+
+
+_FP4 = ("nvfp4", "fp4_ue8m0_16", "mxfp4")
 
 
 def _row_format(name: str) -> int:
-    if name not in ROW_FORMATS:
+    f = ROW_FORMATS.get(name)
+    if f is None:
         raise ValueError(f"row format: one of {sorted(ROW_FORMATS)} expected, got {name!r}")
-    return ROW_FORMATS[name]
+    return f
 
 
-def _maps(row_of_slot, slot_of_row, tokens: int):
-    if row_of_slot.dim() != 2 or row_of_slot.shape[0] != tokens:
-        raise ValueError(f"row_of_slot: ({tokens}, topk) expected, got {tuple(row_of_slot.shape)}")
-    _flat(row_of_slot, "row_of_slot", row_of_slot.numel(), "int32")
-    if slot_of_row is not None:
-        _flat(slot_of_row, "slot_of_row", slot_of_row.numel(), "int32")
+def _slots_of(row_of_slot, tokens: int):
+    """topk and the address of a (tokens, topk) map."""
+    shape = row_of_slot.shape
+    if len(shape) != 2 or shape[0] != tokens:
+        raise ValueError(f"row_of_slot: ({tokens}, topk) expected, got {tuple(shape)}")
+    k = shape[1]
+    return k, _flat(row_of_slot, "row_of_slot", tokens * k, _I32)
+
+
+def _rows_matrix(d, rows, cols):
+    _matrix(d, "d", rows, cols)
+    if not d.is_contiguous():
+        raise ValueError("d: a contiguous matrix expected")
 
 
 def dispatch(x, row_of_slot, slot_of_row, in_format: str = "mxfp8_e4m3", stream=None):
@@ -268,13 +304,14 @@ def dispatch(x, row_of_slot, slot_of_row, in_format: str = "mxfp8_e4m3", stream=
     sfa, or bfloat16 / float16 values with sfa None."""
     ld = _matrix(x, "x")
     T, H = x.shape
-    _maps(row_of_slot, slot_of_row, T)
+    k, p_rows = _slots_of(row_of_slot, T)
     m_pad = slot_of_row.numel()
-    desc = TokensDesc(T, H, m_pad, ld, 0, row_of_slot.shape[1], _format(x, "x"), _row_format(in_format), 0)
-    with _on(stream):
-        a, sfa = _row_buffers(m_pad, H, in_format, x.device)
-    _check(lib().bsgg_dispatch(ctypes.byref(desc), _ptr(x), _ptr(row_of_slot), _ptr(slot_of_row), _ptr(a), _ptr(sfa),
-                               _stream(stream)), "bsgg_dispatch")
+    p_slots = _flat(slot_of_row, "slot_of_row", m_pad, _I32)
+    desc = TokensDesc(T, H, m_pad, ld, 0, k, _format(x, "x"), _row_format(in_format), 0)
+    handle = _handle(x, stream)
+    a, sfa = _row_buffers(m_pad, H, in_format, x.device, _empty_on(stream))
+    _check(lib().bsgg_dispatch(byref(desc), x.data_ptr(), p_rows, p_slots, a.data_ptr(),
+                               sfa.data_ptr() if sfa is not None else None, handle), "bsgg_dispatch")
     return a, sfa
 
 
@@ -282,22 +319,20 @@ def combine(d, row_of_slot, weights=None, residual=None, out_format: Optional[st
     """Rows d (m_pad, hidden) back to tokens: residual + sum_j weights[t, j] *
     d[row_of_slot[t, j]], (tokens, hidden) in out_format (by default the
     residual's type, or d's)."""
-    import torch
-    _matrix(d, "d")
-    if not d.is_contiguous():
-        raise ValueError("d: a contiguous matrix expected")
+    _rows_matrix(d, None, None)
     m_pad, H = d.shape
     T = row_of_slot.shape[0]
-    _maps(row_of_slot, None, T)
-    _flat(weights, "weights", row_of_slot.numel(), "float32")
+    k, p_rows = _slots_of(row_of_slot, T)
     dt = _dtype(out_format) if out_format is not None else residual.dtype if residual is not None else d.dtype
     ldr = _matrix(residual, "residual", T, H, dt) if residual is not None else 0
-    with _on(stream):
-        y = out if out is not None else torch.empty(T, H, dtype=dt, device=d.device)
-    ldy = _matrix(y, "out", T, H, dt)
-    desc = TokensDesc(T, H, m_pad, ldy, ldr, row_of_slot.shape[1], _format(y, "out"), 0, _format(d, "d"))
-    _check(lib().bsgg_combine(ctypes.byref(desc), _ptr(d), _ptr(row_of_slot), _ptr(weights), _ptr(residual), _ptr(y),
-                              _stream(stream)), "bsgg_combine")
+    handle = _handle(d, stream)
+    if out is None:
+        y, ldy = _empty_on(stream)((T, H), dtype=dt, device=d.device), H
+    else:
+        y, ldy = out, _matrix(out, "out", T, H, dt)
+    desc = TokensDesc(T, H, m_pad, ldy, ldr, k, _format(y, "out"), 0, _format(d, "d"))
+    _check(lib().bsgg_combine(byref(desc), d.data_ptr(), p_rows, _flat(weights, "weights", T * k, _F32),
+                              residual.data_ptr() if residual is not None else None, y.data_ptr(), handle), "bsgg_combine")
     return y
 
 
@@ -305,39 +340,39 @@ def combine_backward(dy, d, row_of_slot, slot_of_row, weights=None, out_format: 
                      stream=None):
     """Gradient of combine: (dd, sfd, dweights); dd (m_pad, hidden) in the row
     format out_format with its scale factors sfd (None for bf16 and f16)."""
-    import torch
     ld = _matrix(dy, "dy")
     T, H = dy.shape
-    _maps(row_of_slot, slot_of_row, T)
+    k, p_rows = _slots_of(row_of_slot, T)
     m_pad = slot_of_row.numel()
-    _flat(weights, "weights", row_of_slot.numel(), "float32")
+    p_slots, p_weights = _flat(slot_of_row, "slot_of_row", m_pad, _I32), _flat(weights, "weights", T * k, _F32)
+    p_d, fd = None, 0
     if want_dweights:
-        _matrix(d, "d", m_pad, H)
-        if not d.is_contiguous():
-            raise ValueError("d: a contiguous matrix expected")
-    desc = TokensDesc(T, H, m_pad, ld, 0, row_of_slot.shape[1], _format(dy, "dy"), _row_format(out_format),
-                      _format(d, "d") if want_dweights else 0)
-    with _on(stream):
-        dd, sfd = _row_buffers(m_pad, H, out_format, dy.device)
-        dw = torch.empty(row_of_slot.shape, dtype=torch.float32, device=dy.device) if want_dweights else None
-    _check(lib().bsgg_combine_backward(ctypes.byref(desc), _ptr(dy), _ptr(d) if want_dweights else None, _ptr(row_of_slot),
-                                       _ptr(slot_of_row), _ptr(weights), _ptr(dd), _ptr(sfd), _ptr(dw), _stream(stream)),
-           "bsgg_combine_backward")
+        _rows_matrix(d, m_pad, H)
+        p_d, fd = d.data_ptr(), _format(d, "d")
+    desc = TokensDesc(T, H, m_pad, ld, 0, k, _format(dy, "dy"), _row_format(out_format), fd)
+    handle = _handle(dy, stream)
+    empty, dev = _empty_on(stream), dy.device
+    dd, sfd = _row_buffers(m_pad, H, out_format, dev, empty)
+    dw = empty((T, k), dtype=_F32, device=dev) if want_dweights else None
+    _check(lib().bsgg_combine_backward(byref(desc), dy.data_ptr(), p_d, p_rows, p_slots, p_weights, dd.data_ptr(),
+                                       sfd.data_ptr() if sfd is not None else None,
+                                       dw.data_ptr() if dw is not None else None, handle), "bsgg_combine_backward")
     return dd, sfd, dw
 
 
 # ---------------------------------------------------------------- dense layer
 def _activation(name: str) -> int:
-    if name not in ACTIVATIONS:
+    a = ACTIVATIONS.get(name)
+    if a is None:
         raise ValueError(f"activation: one of {sorted(ACTIVATIONS)} expected, got {name!r}")
-    return ACTIVATIONS[name]
+    return a
 
 
-def _rows_of(cols: int, rows: int, dtype, device):
-    """An empty matrix whose row pitch is a multiple of 8 elements."""
-    import torch
-    ld = -(-cols // 8) * 8
-    return torch.empty(rows, ld, dtype=dtype, device=device)[:, :cols]
+def _rows_of(rows: int, cols: int, dtype, device, empty):
+    """An empty matrix whose row pitch is a multiple of 8 elements, and that pitch."""
+    ld = (cols + 7) // 8 * 8
+    t = empty((rows, ld), dtype=dtype, device=device)
+    return (t if ld == cols else t[:, :cols]), ld
 
 
 def linear(x, w, bias=None, activation: str = "none", residual=None, want_z: bool = False,
@@ -345,24 +380,31 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, want_z: boo
     """act(x w^T + bias) + residual: x (m, k), w (n, k) bfloat16 or float16,
     bias (n), residual (m, n) in x's type -> (y, z); z, the pre-activation in
     x's type, is None unless want_z."""
-    import torch
+    xt = x.dtype
     ldx = _matrix(x, "x")
     m, k = x.shape
-    ldw = _matrix(w, "w", None, k, x.dtype)
+    ldw = _matrix(w, "w", None, k, xt)
     n = w.shape[0]
-    dt = _dtype(out_format) if out_format is not None else x.dtype
-    if bias is not None and (bias.dim() != 1 or bias.numel() != n or not bias.is_contiguous() or not bias.is_cuda):
-        raise ValueError(f"bias: {n} contiguous values on the GPU expected, got {tuple(bias.shape)}")
-    ldr = _matrix(residual, "residual", m, n, x.dtype) if residual is not None else 0
-    with _on(stream):
-        y = out if out is not None else torch.empty(m, n, dtype=dt, device=x.device)
-        z = _rows_of(n, m, x.dtype, x.device) if want_z else None
-    ldy = _matrix(y, "out", m, n, dt)
-    desc = LinearDesc(m, n, k, ldx, ldw, ldr, ldy, _matrix(z, "z") if want_z else 0, _format(x, "x"), _format(y, "out"),
-                      _format(bias, "bias") if bias is not None else 0, _activation(activation))
-    status = _status(x.device) if status is None else status
-    _check(lib().bsgg_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(z),
-                             _ptr(status), _stream(stream)), "bsgg_linear")
+    p_bias, fb, p_res, ldr, z, p_z, ldz = None, 0, None, 0, None, None, 0
+    if bias is not None:
+        if bias.dim() != 1 or bias.shape[0] != n or not bias.is_contiguous() or not bias.is_cuda:
+            raise ValueError(f"bias: {n} contiguous values on the GPU expected, got {tuple(bias.shape)}")
+        p_bias, fb = bias.data_ptr(), _format(bias, "bias")
+    if residual is not None:
+        p_res, ldr = residual.data_ptr(), _matrix(residual, "residual", m, n, xt)
+    dt = xt if out_format is None else _dtype(out_format)
+    handle = _handle(x, stream)
+    empty = _empty_on(stream)
+    if out is None:
+        y, ldy = empty((m, n), dtype=dt, device=x.device), n
+    else:
+        y, ldy = out, _matrix(out, "out", m, n, dt)
+    if want_z:
+        z, ldz = _rows_of(m, n, xt, x.device, empty)
+        p_z = z.data_ptr()
+    desc = LinearDesc(m, n, k, ldx, ldw, ldr, ldy, ldz, _format(x, "x"), _FORMATS[dt], fb, _activation(activation))
+    _check(lib().bsgg_linear(byref(desc), x.data_ptr(), w.data_ptr(), p_bias, p_res, y.data_ptr(), p_z,
+                             _status_of(x, status), handle), "bsgg_linear")
     return y, z
 
 
@@ -372,31 +414,38 @@ def linear_backward(dy, x, w, z=None, activation: str = "none", want_dx: bool = 
     """Gradient of linear: (dx, dw, dbias), each None where not wanted.  z is the
     pre-activation linear kept (None without an activation).  A given dw is
     added to."""
-    import torch
+    t = dy.dtype
     ld_dy = _matrix(dy, "dy")
     m, n = dy.shape
-    ldx = _matrix(x, "x", m, None, dy.dtype)
+    ldx = _matrix(x, "x", m, None, t)
     k = x.shape[1]
-    ldw = _matrix(w, "w", n, k, dy.dtype)
+    ldw = _matrix(w, "w", n, k, t)
     act = _activation(activation)
-    accumulate = dw is not None
-    with _on(stream):
-        dz = _rows_of(n, m, dy.dtype, dy.device) if act else None
-        dx = torch.empty(m, k, dtype=_dtype(dx_format) if dx_format else dy.dtype, device=dy.device) if want_dx else None
-        if want_dw and dw is None:
-            dw = torch.empty(n, k, dtype=_dtype(dw_format) if dw_format else dy.dtype, device=dy.device)
-        dbias = torch.empty(n, dtype=torch.float32, device=dy.device) if want_dbias else None
+    handle = _handle(dy, stream)
+    empty, dev = _empty_on(stream), dy.device
+    dz = dx = dbias = p_z = None
+    ldz = ld_dz = ld_dx = ld_dw = fx = fw = 0
+    if act:
+        if z is None:
+            raise ValueError("z: the pre-activation is needed for an activation's gradient")
+        p_z, ldz = z.data_ptr(), _matrix(z, "z", m, n, t)
+        dz, ld_dz = _rows_of(m, n, t, dev, empty)
+    if want_dx:
+        dx, ld_dx = empty((m, k), dtype=_dtype(dx_format) if dx_format else t, device=dev), k
+        fx = _format(dx, "dx")
+    accumulate = 0
     if not want_dw:
         dw = None
-    if act and z is None:
-        raise ValueError("z: the pre-activation is needed for an activation's gradient")
-    desc = LinearBwdDesc(m, n, k, ld_dy, _matrix(z, "z", m, n, dy.dtype) if act else 0, _matrix(dz, "dz") if act else 0,
-                         ldx, ldw, _matrix(dx, "dx") if want_dx else 0,
-                         _matrix(dw, "dw", n, k) if dw is not None else 0, _format(dy, "dy"),
-                         _format(dx, "dx") if want_dx else 0, _format(dw, "dw") if dw is not None else 0, act,
-                         int(accumulate and want_dw))
-    status = _status(dy.device) if status is None else status
-    _check(lib().bsgg_linear_backward(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(w), _ptr(z) if act else None, _ptr(dz),
-                                      _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(status), _stream(stream)),
-           "bsgg_linear_backward")
+    else:
+        if dw is None:
+            dw, ld_dw = empty((n, k), dtype=_dtype(dw_format) if dw_format else t, device=dev), k
+        else:
+            accumulate, ld_dw = 1, _matrix(dw, "dw", n, k)
+        fw = _format(dw, "dw")
+    if want_dbias:
+        dbias = empty(n, dtype=_F32, device=dev)
+    desc = LinearBwdDesc(m, n, k, ld_dy, ldz, ld_dz, ldx, ldw, ld_dx, ld_dw, _format(dy, "dy"), fx, fw, act, accumulate)
+    _check(lib().bsgg_linear_backward(byref(desc), dy.data_ptr(), x.data_ptr(), w.data_ptr(), p_z,
+                                      *(v.data_ptr() if v is not None else None for v in (dz, dx, dw, dbias)),
+                                      _status_of(dy, status), handle), "bsgg_linear_backward")
     return dx, dw, dbias
