@@ -148,132 +148,106 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(
 // the runs of its warps in order.  A warp finds the slots of its 32 that name the
 // same expert with one match instruction, so a slot's rank is the count before
 // its run plus the run's own before it: no order depends on timing.
-constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
+//
+// Up to kSortClusterSlots slots one cluster does it all in one launch, its blocks'
+// totals meeting in distributed shared memory; more slots take a launch that
+// counts and one that places, since scattered 4-byte stores want many SMs.
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kSortMaxCluster = 8;
+constexpr int64_t kSortClusterSlots = 2 * kSortThreads * kSortMaxCluster;
 
 struct SortParams {
   int64_t slots, m_pad;
-  int L, steps, blocks;          // 32-slot steps per warp
+  int L, steps, blocks;          // 32-slot steps per warp (at most 2047: counts are 16 bits wide)
   const int32_t* ids;
   const float* weights;
   int32_t *offsets, *row_of_slot, *slot_of_row, *rows_used;
   float* prob;
-  int32_t* counts;               // (blocks, L)
+  int32_t* counts;               // (blocks, L), two launches only
   uint32_t* status;
 };
+
+// Shared memory of L experts: total and before (this block's first rank) of each,
+// first row of each and one past the last; a scratch word per warp and expert
+// group; the warps' counts, then their ranks inside the block.
+struct SortShared {
+  int32_t *mine, *total, *before, *first, *scan;
+  uint16_t* warp_count;
+  __device__ SortShared(int32_t* sm, int L)
+      : mine(sm), total(sm + L), before(sm + 2 * L), first(sm + 3 * L), scan(sm + 4 * L + 1),
+        warp_count(reinterpret_cast<uint16_t*>(sm + 4 * L + 1 + kSortWarps)) {}
+};
+constexpr size_t sort_shared_bytes(int L) { return 4 * (4 * size_t(L) + 1 + kSortWarps) + 2 * size_t(L) * kSortWarps; }
 
 __device__ __forceinline__ int sort_id(const SortParams& p, int64_t s) {
   const int32_t e = s < p.slots ? p.ids[s] : -1;
   return (e >= 0 && e < p.L) ? e : -1;
 }
 
-// Per-warp counts of this block's slots into cnt[warp][L] (cleared here).
-__device__ __forceinline__ void sort_count(const SortParams& p, int32_t* cnt, int block) {
+// Counts of this block's slots: per warp (as ranks inside the block) and in all.
+__device__ __forceinline__ void sort_count(const SortParams& p, const SortShared& sh, int block) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * p.L; i += kSortThreads) cnt[i] = 0;
+  for (int i = threadIdx.x; i < kSortWarps * p.L; i += kSortThreads) sh.warp_count[i] = 0;
   __syncthreads();
   const int64_t s0 = (static_cast<int64_t>(block) * kSortWarps + warp) * p.steps * 32;
   for (int k = 0; k < p.steps; ++k) {
     const int e = sort_id(p, s0 + 32 * k + lane);
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) cnt[warp * p.L + e] += __popc(same);
+    if (e >= 0 && lane == __ffs(same) - 1) sh.warp_count[warp * p.L + e] += static_cast<uint16_t>(__popc(same));
     __syncwarp();
   }
   __syncthreads();
-}
-
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortParams p) {
-  extern __shared__ int32_t sm[];
-  sort_count(p, sm, blockIdx.x);
   for (int e = threadIdx.x; e < p.L; e += kSortThreads) {
-    int32_t c = 0;
-    for (int w = 0; w < kSortWarps; ++w) c += sm[w * p.L + e];
-    p.counts[static_cast<int64_t>(blockIdx.x) * p.L + e] = c;
-  }
-}
-
-// Rows of every slot: shared memory holds cnt[warps][L], then total[L] and
-// first[L + 1] (an expert's first row).
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) {
-  extern __shared__ int32_t sm[];
-  int32_t* cnt = sm;
-  int32_t* total = sm + kSortWarps * p.L;
-  int32_t* first = total + p.L;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  sort_count(p, cnt, blockIdx.x);
-  for (int e = threadIdx.x; e < p.L; e += kSortThreads) {
-    int32_t all = 0, before = 0;
-    if (p.blocks == 1) {
-      for (int w = 0; w < kSortWarps; ++w) all += cnt[w * p.L + e];
-    } else {
-      for (int b = 0; b < p.blocks; ++b) {
-        const int32_t c = p.counts[static_cast<int64_t>(b) * p.L + e];
-        all += c;
-        before += b < static_cast<int>(blockIdx.x) ? c : 0;
-      }
-    }
-    total[e] = all;
-    // per-warp starts inside the expert
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int32_t c = cnt[w * p.L + e];
-      cnt[w * p.L + e] = before;
-      before += c;
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    // exclusive prefix of the padded sizes, one contiguous chunk per lane
-    const int chunk = (p.L + 31) / 32, e0 = min(lane * chunk, p.L), e1 = min(e0 + chunk, p.L);
-    int32_t local = 0;
-    for (int e = e0; e < e1; ++e) local += (total[e] + 127) / 128 * 128;
-    int32_t incl = local;
+    int32_t run = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += y;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int32_t c = sh.warp_count[w * p.L + e];
+      sh.warp_count[w * p.L + e] = static_cast<uint16_t>(run);
+      run += c;
     }
-    int32_t run = incl - local;
-    for (int e = e0; e < e1; ++e) {
-      first[e] = run;
-      run += (total[e] + 127) / 128 * 128;
-    }
-    if (lane == 31) first[p.L] = incl;
+    sh.mine[e] = run;
   }
+}
+
+// first[e] from total[e]: exclusive prefix of the padded sizes (L <= 1024: two
+// experts a thread).
+__device__ __forceinline__ void sort_first(const SortParams& p, const SortShared& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = 2 * threadIdx.x;
+  auto padded = [&](int i) { return i < p.L ? (sh.total[i] + 127) / 128 * 128 : 0; };
+  const int32_t a = padded(e), both = a + padded(e + 1);
+  int32_t incl = both;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh.scan[warp] = incl;
   __syncthreads();
+  int32_t base = 0;
+  for (int w = 0; w < warp; ++w) base += sh.scan[w];
+  const int32_t at = base + incl - both;
+  if (e < p.L) sh.first[e] = at;
+  if (e + 1 < p.L) sh.first[e + 1] = at + a;
+  if (e == ((p.L - 1) & ~1)) sh.first[p.L] = at + both;
+  __syncthreads();
+}
+
+// Offsets, padding rows and this block's slots; block of `blocks`.
+__device__ __forceinline__ void sort_place(const SortParams& p, const SortShared& sh, int block, int blocks) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t m_pad = static_cast<int32_t>(p.m_pad);
-  if (blockIdx.x == 0) {
-    for (int e = threadIdx.x; e < p.L; e += kSortThreads)
-      p.offsets[e] = e + 1 == p.L ? m_pad : min(first[e + 1], m_pad);
-    if (threadIdx.x == 0) {
-      if (p.rows_used != nullptr) *p.rows_used = first[p.L];
-      if (first[p.L] > m_pad && p.status != nullptr) atomicOr(p.status, kStatusBadOffsets);
-    }
-  }
-  // padding rows: between an expert's last slot and the next expert, and after
-  // the last expert up to m_pad; a warp per expert, the tail over all threads
-  for (int e = blockIdx.x * kSortWarps + warp; e < p.L; e += gridDim.x * kSortWarps) {
-    for (int32_t r = first[e] + total[e] + lane; r < min(first[e + 1], m_pad); r += 32) {
-      p.slot_of_row[r] = -1;
-      if (p.prob != nullptr) p.prob[r] = 0.0f;
-    }
-  }
-  for (int64_t r = first[p.L] + static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; r < m_pad;
-       r += static_cast<int64_t>(gridDim.x) * kSortThreads) {
-    p.slot_of_row[r] = -1;
-    if (p.prob != nullptr) p.prob[r] = 0.0f;
-  }
-  // the slots
-  const int64_t s0 = (static_cast<int64_t>(blockIdx.x) * kSortWarps + warp) * p.steps * 32;
+  const int64_t s0 = (static_cast<int64_t>(block) * kSortWarps + warp) * p.steps * 32;
   for (int k = 0; k < p.steps; ++k) {
     const int64_t s = s0 + 32 * k + lane;
     const int e = sort_id(p, s);
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
     int32_t r = -1;
     if (e >= 0) {
-      r = first[e] + cnt[warp * p.L + e] + __popc(same & ((1u << lane) - 1u));
+      r = sh.first[e] + sh.before[e] + sh.warp_count[warp * p.L + e] + __popc(same & ((1u << lane) - 1u));
       if (r >= m_pad) r = -1;
     }
     __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) cnt[warp * p.L + e] += __popc(same);
+    if (e >= 0 && lane == __ffs(same) - 1) sh.warp_count[warp * p.L + e] += static_cast<uint16_t>(__popc(same));
     __syncwarp();
     if (s < p.slots) {
       p.row_of_slot[s] = r;
@@ -283,51 +257,254 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) 
       }
     }
   }
+  if (block == 0) {
+    for (int e = threadIdx.x; e < p.L; e += kSortThreads)
+      p.offsets[e] = e + 1 == p.L ? m_pad : min(sh.first[e + 1], m_pad);
+    if (threadIdx.x == 0) {
+      if (p.rows_used != nullptr) *p.rows_used = sh.first[p.L];
+      if (sh.first[p.L] > m_pad && p.status != nullptr) atomicOr(p.status, kStatusBadOffsets);
+    }
+  }
+  // padding rows: between an expert's last slot and the next expert, a warp per
+  // expert; after the last expert up to m_pad, over all threads
+  for (int e = block * kSortWarps + warp; e < p.L; e += blocks * kSortWarps) {
+    for (int32_t r = sh.first[e] + sh.total[e] + lane; r < min(sh.first[e + 1], m_pad); r += 32) {
+      p.slot_of_row[r] = -1;
+      if (p.prob != nullptr) p.prob[r] = 0.0f;
+    }
+  }
+  for (int64_t r = sh.first[p.L] + static_cast<int64_t>(block) * kSortThreads + threadIdx.x; r < m_pad;
+       r += static_cast<int64_t>(blocks) * kSortThreads) {
+    p.slot_of_row[r] = -1;
+    if (p.prob != nullptr) p.prob[r] = 0.0f;
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(SortParams p) {
+  extern __shared__ int32_t sm[];
+  const SortShared sh(sm, p.L);
+  const int rank = blockIdx.x, blocks = p.blocks;
+  sort_count(p, sh, rank);
+  if (blocks > 1) cluster_sync(); else __syncthreads();
+  for (int e = threadIdx.x; e < p.L; e += kSortThreads) {
+    int32_t all = 0, before = 0;
+    for (int r = 0; r < blocks; ++r) {
+      int32_t c;
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(mapa_shared(smem_u32(&sh.mine[e]), r)) : "memory");
+      all += c;
+      before += r < rank ? c : 0;
+    }
+    sh.total[e] = all;
+    sh.before[e] = before;
+  }
+  __syncthreads();
+  sort_first(p, sh);
+  sort_place(p, sh, rank, blocks);
+  if (blocks > 1) cluster_sync();          // the totals stay until every block has read them
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortParams p) {
+  extern __shared__ int32_t sm[];
+  const SortShared sh(sm, p.L);
+  sort_count(p, sh, blockIdx.x);
+  for (int e = threadIdx.x; e < p.L; e += kSortThreads) p.counts[static_cast<int64_t>(blockIdx.x) * p.L + e] = sh.mine[e];
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) {
+  extern __shared__ int32_t sm[];
+  const SortShared sh(sm, p.L);
+  for (int e = threadIdx.x; e < p.L; e += kSortThreads) sh.total[e] = sh.before[e] = 0;
+  sort_count(p, sh, blockIdx.x);
+  // the blocks' counts of an expert: shared out over as many threads as there are
+  // (integer sums: the order of the atomics does not matter)
+  const int per = (p.L + 31) / 32 * 32, groups = max(1, kSortThreads / per);
+  for (int i = threadIdx.x; i < per * groups; i += kSortThreads) {
+    const int e = i % per, g = i / per;
+    if (e >= p.L) continue;
+    int32_t all = 0, before = 0;
+#pragma unroll 4
+    for (int b = g; b < p.blocks; b += groups) {
+      const int32_t c = p.counts[static_cast<int64_t>(b) * p.L + e];
+      all += c;
+      before += b < static_cast<int>(blockIdx.x) ? c : 0;
+    }
+    atomicAdd(&sh.total[e], all);
+    atomicAdd(&sh.before[e], before);
+  }
+  __syncthreads();
+  sort_first(p, sh);
+  sort_place(p, sh, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------- dispatch
 struct RowsParams {
-  int64_t tokens, hidden, m_pad, ld_token, ld_residual;
+  int64_t tokens, hidden, m_pad, ld_token;
   int topk;
   int64_t kq;                       // scale atoms per 128 rows
   const void* x;                    // x or dy
   const int32_t *row_of_slot, *slot_of_row;
-  const float* weights;
   void* a;
   uint8_t* sfa;
+  // the gradient of combine
+  const float* weights;
+  const void* d;
+  int d_kind;
+  float* dweights;
 };
 
-constexpr int kRowThreads = 256;
+// What a kernel of the rows does: dispatch; the gradient of combine, rows (and
+// dweights); dweights alone.
+enum : int { ROWS_DISPATCH = 0, ROWS_GRAD = 1, ROWS_DOT = 2 };
 
-// One block per row of A: gather, scale by the slot's weight, quantize.  Lanes
-// hold eight values each, so a block of v values is v / 8 neighbouring lanes.
-template <int KIND, int FMT>
-__global__ void __launch_bounds__(kRowThreads) dispatch_row_kernel(RowsParams p) {
-  const int64_t r = blockIdx.x;
-  const int32_t s = p.slot_of_row[r];
-  const bool real = s >= 0 && s < p.tokens * p.topk;
-  const int64_t t = real ? s / p.topk : 0;
-  const float w = real && p.weights != nullptr ? p.weights[s] : 1.0f;
-  constexpr int kLanes = rf_vec(FMT) / 8;
+constexpr int kRowThreads = 512, kMaxTopk = 32, kPadRows = 8;
+
+// Values a thread holds: a 16-byte store of codes or 16-bit values (8 bytes FP4).
+__host__ __device__ constexpr int row_values(int fmt) { return rf_scaled(fmt) ? 16 : 8; }
+
+template <int FMT>
+__device__ __forceinline__ void store_row_values(void* base, int64_t i, const float (&v)[row_values(FMT)], uint32_t code) {
+  if constexpr (!rf_scaled(FMT)) {
+    uint32_t c[4];
+    quantize8<FMT>(v, code, c);
+    store_codes8<FMT>(base, i, c);
+  } else {
+    uint32_t lo[4], hi[4];
+    quantize8<FMT>(reinterpret_cast<const float(&)[8]>(v[0]), code, lo);
+    quantize8<FMT>(reinterpret_cast<const float(&)[8]>(v[8]), code, hi);
+    uint8_t* p = static_cast<uint8_t*>(base) + i * rf_bits(FMT) / 8;
+    if (rf_fp4(FMT)) *reinterpret_cast<uint2*>(p) = make_uint2(lo[0], hi[0]);
+    else *reinterpret_cast<uint4*>(p) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
+  }
+}
+
+// The scale code of this thread's block (shared by rf_vec / 16 lanes), and the
+// word of the four blocks it lies in, complete in every lane: their bytes are
+// neighbours in the scale factors' layout.
+template <int FMT>
+__device__ __forceinline__ uint32_t block_code(const float (&v)[16], bool in, uint32_t& word) {
+  constexpr int kLanes = rf_vec(FMT) / 16;
+  uint32_t m = max(max_abs_bits8(reinterpret_cast<const float(&)[8]>(v[0])),
+                   max_abs_bits8(reinterpret_cast<const float(&)[8]>(v[8])));
+  if (kLanes == 2) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  const uint32_t code = scale_code<FMT>(m);
+  word = in ? code << (8 * ((threadIdx.x / kLanes) & 3)) : 0u;
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, kLanes);
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * kLanes);
+  return code;
+}
+
+// Blocks [0, tokens): one token each.  Its values are read once, and (without
+// weights) quantized once, for all of its rows: x is T H elements where the rows
+// are topk times that, and reading and quantizing per row took 276 us for 8192
+// tokens of 7168, top-8, against 98 us of bytes.  The blocks after them write the
+// padding rows, kPadRows each.
+template <int KIND, int FMT, int MODE>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(RowsParams p) {
+  constexpr int V = row_values(FMT), kLanes = rf_scaled(FMT) ? rf_vec(FMT) / 16 : 1;
+  constexpr int kBatch = 32 / V;                      // rows of D in flight
+  __shared__ float part[MODE == ROWS_DISPATCH ? 1 : kMaxTopk][kRowThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  // columns in whole warps, up to the end of the last scale atom
   const int64_t cols = rf_scaled(FMT) ? p.kq * 4 * rf_vec(FMT) : p.hidden;
-  for (int64_t c = threadIdx.x * 8; c < (cols + 255) / 256 * 256; c += kRowThreads * 8) {
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (real && c < p.hidden) load8<KIND>(p.x, t * p.ld_token + c, v);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = p.weights != nullptr ? v[k] * w : v[k];
-    uint32_t code = 0;
-    if (rf_scaled(FMT)) {
-      uint32_t m = max_abs_bits8(v);
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      code = scale_code<FMT>(m);
-      if (threadIdx.x % kLanes == 0 && c < cols)
-        p.sfa[sf_off(r, c / rf_vec(FMT), p.kq)] = static_cast<uint8_t>(c < p.hidden ? code : 0u);
+  const int64_t end = (cols + 32 * V - 1) / (32 * V) * (32 * V);
+  if (blockIdx.x >= p.tokens) {
+    const int64_t r0 = (static_cast<int64_t>(blockIdx.x) - p.tokens) * kPadRows;
+    constexpr uint32_t one = rf_one(FMT) * 0x01010101u;
+    for (int64_t r = r0; r < min(r0 + kPadRows, p.m_pad); ++r) {
+      const int32_t s = p.slot_of_row[r];
+      if (s >= 0 && s < p.tokens * p.topk) continue;
+      const int64_t bytes = p.hidden * rf_bits(FMT) / 8;   // a multiple of 16 (8 for FP4's 16-value tails)
+      uint8_t* row = static_cast<uint8_t*>(p.a) + r * bytes;
+      for (int64_t c = threadIdx.x * 16; c < bytes; c += blockDim.x * 16) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+      if (rf_scaled(FMT)) {
+        const int64_t kb = (p.hidden + rf_vec(FMT) - 1) / rf_vec(FMT);
+        for (int64_t q = threadIdx.x; q < p.kq; q += blockDim.x) {
+          const int64_t left = kb - 4 * q;               // blocks of this word inside hidden
+          *reinterpret_cast<uint32_t*>(p.sfa + sf_off(r, 4 * q, p.kq)) = left >= 4 ? one : one & ((1u << (8 * left)) - 1u);
+        }
+      }
     }
-    if (c < p.hidden) {
-      uint32_t out[4];
-      quantize8<FMT>(v, code, out);
-      store_codes8<FMT>(p.a, r * p.hidden + c, out);
+    return;
+  }
+  const int64_t t = blockIdx.x;
+  const int32_t* rows = p.row_of_slot + t * p.topk;
+  const bool dot = MODE != ROWS_DISPATCH && p.dweights != nullptr;
+  if (dot) {
+    for (int i = threadIdx.x; i < p.topk * warps; i += blockDim.x) part[i / warps][i % warps] = 0.0f;
+    __syncthreads();
+  }
+  for (int64_t c = threadIdx.x * V; c < end; c += static_cast<int64_t>(blockDim.x) * V) {
+    const bool in = c < p.hidden;
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = 0.0f;
+    if (in) {
+#pragma unroll
+      for (int h = 0; h < V; h += 8) load8<KIND>(p.x, t * p.ld_token + c + h, reinterpret_cast<float(&)[8]>(v[h]));
+    }
+    if (dot) {
+      for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+        float u[kBatch][V];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int32_t r = j0 + b < p.topk ? rows[j0 + b] : -1;
+#pragma unroll
+          for (int h = 0; h < V; h += 8) {
+            float(&w)[8] = reinterpret_cast<float(&)[8]>(u[b][h]);
+            if (in && r >= 0 && r < p.m_pad) {
+              const int64_t at = r * p.hidden + c + h;
+              if (p.d_kind == OK_BF16) load8<OK_BF16>(p.d, at, w);
+              else if (p.d_kind == OK_F16) load8<OK_F16>(p.d, at, w);
+              else load8<OK_F32>(p.d, at, w);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = 0.0f;
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          if (j0 + b >= p.topk) break;
+          // a slot without a row has the gradient 0 whatever dy holds
+          const int32_t r = rows[j0 + b];
+          float acc = 0.0f;
+#pragma unroll
+          for (int k = 0; k < V; ++k) acc = fmaf(v[k], u[b][k], acc);
+          acc = warp_sum(r >= 0 && r < p.m_pad ? acc : 0.0f);
+          if (lane == 0) part[j0 + b][warp] += acc;
+        }
+      }
+    }
+    if (MODE == ROWS_DOT) continue;
+    uint32_t code = 0, word = 0;
+    if constexpr (rf_scaled(FMT)) {
+      if (MODE == ROWS_DISPATCH || p.weights == nullptr) code = block_code<FMT>(v, in, word);
+    }
+    for (int j = 0; j < p.topk; ++j) {
+      const int32_t r = rows[j];
+      if (r < 0 || r >= p.m_pad) continue;              // the same for the whole block
+      float w[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) w[k] = v[k];
+      if (MODE == ROWS_GRAD && p.weights != nullptr) {
+        const float f = p.weights[t * p.topk + j];
+#pragma unroll
+        for (int k = 0; k < V; ++k) w[k] = v[k] * f;
+        if constexpr (rf_scaled(FMT)) code = block_code<FMT>(w, in, word);
+      }
+      if constexpr (rf_scaled(FMT)) {
+        const int64_t kb = c / rf_vec(FMT);
+        if (lane % (4 * kLanes) == 0 && c < cols) *reinterpret_cast<uint32_t*>(p.sfa + sf_off(r, kb, p.kq)) = word;
+      }
+      if (in) store_row_values<FMT>(p.a, r * p.hidden + c, w, code);
+    }
+  }
+  if (dot) {
+    __syncthreads();
+    for (int j = threadIdx.x; j < p.topk; j += blockDim.x) {
+      float s = 0.0f;
+      for (int w = 0; w < warps; ++w) s += part[j][w];
+      p.dweights[t * p.topk + j] = s;
     }
   }
 }
@@ -343,49 +520,39 @@ struct CombineParams {
   void* y;
 };
 
+// One token per block of x, a run of columns per block of y; four rows of D are
+// loaded before any is added, so that a thread has 64 bytes of them in flight.
 template <int DK, int KIND>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
+  constexpr int kBatch = 4;
   const int64_t t = blockIdx.x;
-  for (int64_t c = threadIdx.x * 8; c < p.hidden; c += kRowThreads * 8) {
+  const int32_t* rows = p.row_of_slot + t * p.topk;
+  const float* weights = p.weights != nullptr ? p.weights + t * p.topk : nullptr;
+  for (int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * 8; c < p.hidden;
+       c += static_cast<int64_t>(gridDim.y) * blockDim.x * 8) {
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (p.residual != nullptr) load8<KIND>(p.residual, t * p.ld_residual + c, acc);
-    for (int j = 0; j < p.topk; ++j) {
-      const int64_t s = t * p.topk + j;
-      const int32_t r = p.row_of_slot[s];
-      if (r < 0 || r >= p.m_pad) continue;
-      const float w = p.weights != nullptr ? p.weights[s] : 1.0f;
-      float v[8];
-      load8<DK>(p.d, r * p.hidden + c, v);
+    for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+      float v[kBatch][8], w[kBatch];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, v[k], acc[k]);
+      for (int b = 0; b < kBatch; ++b) {
+        const int32_t r = j0 + b < p.topk ? rows[j0 + b] : -1;
+        const bool real = r >= 0 && r < p.m_pad;
+        w[b] = !real ? 0.0f : weights != nullptr ? weights[j0 + b] : 1.0f;
+        if (real) {
+          load8<DK>(p.d, r * p.hidden + c, v[b]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[b][k] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[b], v[b][k], acc[k]);
     }
     store8<KIND>(p.y, t * p.ld_token + c, acc);
   }
-}
-
-// dweights: one warp per slot.
-template <int DK, int KIND>
-__global__ void __launch_bounds__(kRowThreads) dweights_kernel(int64_t tokens, int64_t hidden, int64_t m_pad,
-                                                               int64_t ld_token, int topk, const void* dy,
-                                                               const void* d, const int32_t* row_of_slot,
-                                                               float* dweights) {
-  const int lane = threadIdx.x & 31;
-  const int64_t s = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  if (s >= tokens * topk) return;
-  const int64_t t = s / topk;
-  const int32_t r = row_of_slot[s];
-  float acc = 0.0f;
-  if (r >= 0 && r < m_pad) {
-    for (int64_t c = lane * 8; c < hidden; c += 256) {
-      float u[8], v[8];
-      load8<KIND>(dy, t * ld_token + c, u);
-      load8<DK>(d, r * hidden + c, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc = fmaf(u[k], v[k], acc);
-    }
-  }
-  acc = warp_sum(acc);
-  if (lane == 0) dweights[s] = acc;
 }
 
 // ---------------------------------------------------------------- host
@@ -438,7 +605,7 @@ bsgg_status with_rows(int fmt, F&& f) {
 // What dispatch, combine and combine_backward share.
 bsgg_status check_tokens(const bsgg_tokens_desc* d, bool quantizes, bool reads_d) {
   if (!d || d->tokens < 0 || d->tokens > (int64_t(1) << 30) || d->hidden < 8 || d->hidden % 8 != 0 ||
-      d->hidden > (int64_t(1) << 24) || d->topk < 1 || d->tokens * d->topk >= (int64_t(1) << 31))
+      d->hidden > (int64_t(1) << 24) || d->topk < 1 || d->topk > kMaxTopk || d->tokens * d->topk >= (int64_t(1) << 31))
     return BSGG_ERR_INVALID_ARG;
   if (d->m_pad <= 0 || d->m_pad % 128 != 0 || d->m_pad > (int64_t(1) << 30)) return BSGG_ERR_INVALID_ARG;
   if (!is_float_format(d->token_format)) return BSGG_ERR_INVALID_ARG;
@@ -452,20 +619,47 @@ bsgg_status check_tokens(const bsgg_tokens_desc* d, bool quantizes, bool reads_d
   return BSGG_OK;
 }
 
-bsgg_status launch_rows(const bsgg_tokens_desc* d, const void* x, const int32_t* row_of_slot, const int32_t* slot_of_row,
-                        const float* weights, void* a, void* sfa, cudaStream_t s) {
-  RowsParams p = {};
+// Threads of a block whose threads take `values` of `cols` columns: whole warps.
+int row_threads(int64_t cols, int values) {
+  const int64_t t = ceil_div(ceil_div(cols, values), 32) * 32;
+  return static_cast<int>(t < kRowThreads ? t : kRowThreads);
+}
+
+template <int MODE>
+bsgg_status launch_rows(const bsgg_tokens_desc* d, RowsParams p, cudaStream_t s) {
   p.tokens = d->tokens; p.hidden = d->hidden; p.m_pad = d->m_pad; p.ld_token = d->ld_token; p.topk = d->topk;
-  p.x = x; p.row_of_slot = row_of_slot; p.slot_of_row = slot_of_row; p.weights = weights;
-  p.a = a; p.sfa = static_cast<uint8_t*>(sfa);
   return with_float(d->token_format, [&](auto kind) {
     return with_rows(d->row_format, [&](auto fmt) {
       constexpr int K = decltype(kind)::value, F = decltype(fmt)::value;
       p.kq = rf_scaled(F) ? ceil_div(ceil_div(d->hidden, rf_vec(F)), 4) : 0;
-      dispatch_row_kernel<K, F><<<static_cast<unsigned>(d->m_pad), kRowThreads, 0, s>>>(p);
+      const int64_t grid = d->tokens + ceil_div(d->m_pad, kPadRows);
+      rows_kernel<K, F, MODE><<<static_cast<unsigned>(grid), row_threads(d->hidden, row_values(F)), 0, s>>>(p);
       return launch_status();
     });
   });
+}
+
+// Blocks of the sort and 32-slot steps of their warps.
+void sort_shape(int64_t slots, int64_t* blocks, int64_t* steps) {
+  if (slots <= kSortClusterSlots) {
+    // one cluster: one step while its blocks suffice, then two; powers of two
+    *blocks = 1;
+    while (*blocks < kSortMaxCluster && *blocks * kSortThreads < slots) *blocks *= 2;
+    *steps = slots > *blocks * kSortThreads ? 2 : 1;
+  } else {
+    // two steps, as many blocks as an SM each, then more steps
+    constexpr int64_t kBlocks = 148;
+    *steps = ceil_div(slots, kBlocks * kSortThreads);
+    if (*steps < 2) *steps = 2;
+    *blocks = ceil_div(slots, *steps * kSortThreads);
+  }
+}
+
+// Shared memory beyond the default 48 KB has to be asked for.
+template <typename K>
+bool sort_allowed(K kern, size_t smem) {
+  return smem <= 48 * 1024 ||
+         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess;
 }
 
 }  // namespace
@@ -516,23 +710,12 @@ int64_t bsgg_sort_rows(int64_t slots, int32_t num_experts) {
   return 128 * (blocks > 0 ? blocks : 1);
 }
 
-// Blocks of the sort: one while a block's warps hold the slots in a few steps,
-// else as many as give every warp the same run, at most kSortBlocks.
-static int64_t sort_steps(int64_t slots) {
-  constexpr int64_t kOneBlock = 8, kSortBlocks = 148;
-  const int64_t per_step = 32 * kSortWarps;
-  const int64_t steps = ceil_div(slots, per_step);
-  return steps <= kOneBlock ? (steps > 0 ? steps : 1) : (ceil_div(steps, kSortBlocks) > 4 ? ceil_div(steps, kSortBlocks) : 4);
-}
-static int64_t sort_blocks(int64_t slots) {
-  const int64_t b = ceil_div(slots, sort_steps(slots) * 32 * kSortWarps);
-  return b > 0 ? b : 1;
-}
-
 uint64_t bsgg_sort_workspace_bytes(int64_t slots, int32_t num_experts) {
   if (bsgg_sort_rows(slots, num_experts) < 0) return 0;
-  const int64_t b = sort_blocks(slots);
-  return b > 1 ? uint64_t(4) * b * num_experts : 0;
+  if (slots <= kSortClusterSlots) return 0;
+  int64_t blocks, steps;
+  sort_shape(slots, &blocks, &steps);
+  return uint64_t(4) * blocks * num_experts;
 }
 
 bsgg_status bsgg_sort_tokens(int64_t slots, int32_t num_experts, int64_t m_pad, const int32_t* ids, const float* weights,
@@ -549,17 +732,37 @@ bsgg_status bsgg_sort_tokens(int64_t slots, int32_t num_experts, int64_t m_pad, 
     if (!aligned_to(q, 4)) return BSGG_ERR_INVALID_ARG;
   SortParams p = {};
   p.slots = slots; p.m_pad = m_pad; p.L = num_experts;
-  p.steps = static_cast<int>(sort_steps(slots));
-  p.blocks = static_cast<int>(sort_blocks(slots));
-  if (p.blocks > 1 && !workspace) return BSGG_ERR_INVALID_ARG;
+  int64_t blocks, steps;
+  sort_shape(slots, &blocks, &steps);
+  if (steps > 2047) return BSGG_ERR_UNSUPPORTED;             // 16-bit counts of a warp's run: 155 million slots
+  p.steps = static_cast<int>(steps);
+  p.blocks = static_cast<int>(blocks);
+  const bool one_cluster = slots <= kSortClusterSlots;
+  if (!one_cluster && !workspace) return BSGG_ERR_INVALID_ARG;
   p.ids = ids; p.weights = weights; p.offsets = padded_offsets; p.row_of_slot = row_of_slot; p.slot_of_row = slot_of_row;
   p.rows_used = rows_used; p.prob = prob; p.counts = static_cast<int32_t*>(workspace); p.status = status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.blocks > 1) {
-    sort_count_kernel<<<p.blocks, kSortThreads, sizeof(int32_t) * kSortWarps * p.L, s>>>(p);
-    if (launch_status() != BSGG_OK) return BSGG_ERR_CUDA;
+  const size_t smem = sort_shared_bytes(p.L);                // 49 KB at the most: 1024 experts
+  if (one_cluster) {
+    if (!sort_allowed(sort_cluster_kernel, smem)) return BSGG_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.blocks), 1, 1);
+    cfg.blockDim = dim3(kSortThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cfg.gridDim.x;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sort_cluster_kernel, p) == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA;
   }
-  sort_place_kernel<<<p.blocks, kSortThreads, sizeof(int32_t) * ((kSortWarps + 2) * p.L + 1), s>>>(p);
+  if (!sort_allowed(sort_count_kernel, smem) || !sort_allowed(sort_place_kernel, smem)) return BSGG_ERR_CUDA;
+  sort_count_kernel<<<p.blocks, kSortThreads, smem, s>>>(p);
+  if (launch_status() != BSGG_OK) return BSGG_ERR_CUDA;
+  sort_place_kernel<<<p.blocks, kSortThreads, smem, s>>>(p);
   return launch_status();
 }
 
@@ -572,7 +775,9 @@ bsgg_status bsgg_dispatch(const bsgg_tokens_desc* d, const void* x, const int32_
   if (!aligned_to(x, 16) || !aligned_to(a, 16) || !aligned_to(sfa, 16) || !aligned_to(row_of_slot, 4) ||
       !aligned_to(slot_of_row, 4))
     return BSGG_ERR_INVALID_ARG;
-  return launch_rows(d, x, row_of_slot, slot_of_row, nullptr, a, sfa, static_cast<cudaStream_t>(stream));
+  RowsParams p = {};
+  p.x = x; p.row_of_slot = row_of_slot; p.slot_of_row = slot_of_row; p.a = a; p.sfa = static_cast<uint8_t*>(sfa);
+  return launch_rows<ROWS_DISPATCH>(d, p, static_cast<cudaStream_t>(stream));
 }
 
 bsgg_status bsgg_combine(const bsgg_tokens_desc* d, const void* dd, const int32_t* row_of_slot, const float* weights,
@@ -590,8 +795,12 @@ bsgg_status bsgg_combine(const bsgg_tokens_desc* d, const void* dd, const int32_
                      residual, y};
   return with_float(d->d_format, [&](auto dk) {
     return with_float(d->token_format, [&](auto kind) {
-      combine_kernel<decltype(dk)::value, decltype(kind)::value>
-          <<<static_cast<unsigned>(d->tokens), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+      // few tokens: their columns over several blocks, down to two warps each, so
+      // that the chip has about four blocks an SM
+      int threads = row_threads(d->hidden, 8);
+      while (threads > 64 && d->tokens * ceil_div(d->hidden, threads * 8) < 608) threads = (threads / 2 + 31) / 32 * 32;
+      const dim3 grid(static_cast<unsigned>(d->tokens), static_cast<unsigned>(ceil_div(d->hidden, threads * 8)));
+      combine_kernel<decltype(dk)::value, decltype(kind)::value><<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
       return launch_status();
     });
   });
@@ -610,18 +819,17 @@ bsgg_status bsgg_combine_backward(const bsgg_tokens_desc* d, const void* dy, con
       !aligned_to(row_of_slot, 4) || !aligned_to(slot_of_row, 4) || !aligned_to(weights, 4) || !aligned_to(dweights, 4))
     return BSGG_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dd) {
-    const bsgg_status r = launch_rows(d, dy, row_of_slot, slot_of_row, weights, dd, sfd, s);
-    if (r != BSGG_OK) return r;
-  }
-  if (!dweights || d->tokens == 0) return BSGG_OK;
-  return with_float(d->d_format, [&](auto dk) {
-    return with_float(d->token_format, [&](auto kind) {
-      dweights_kernel<decltype(dk)::value, decltype(kind)::value>
-          <<<static_cast<unsigned>(ceil_div(d->tokens * d->topk, kRowThreads / 32)), kRowThreads, 0, s>>>(
-              d->tokens, d->hidden, d->m_pad, d->ld_token, d->topk, dy, rows, row_of_slot, dweights);
-      return launch_status();
-    });
+  RowsParams p = {};
+  p.x = dy; p.row_of_slot = row_of_slot; p.slot_of_row = slot_of_row; p.a = dd; p.sfa = static_cast<uint8_t*>(sfd);
+  p.weights = weights; p.d = rows; p.d_kind = d->d_format; p.dweights = dweights;
+  if (dd) return launch_rows<ROWS_GRAD>(d, p, s);
+  if (d->tokens == 0) return BSGG_OK;
+  p.tokens = d->tokens; p.hidden = d->hidden; p.m_pad = d->m_pad; p.ld_token = d->ld_token; p.topk = d->topk;
+  return with_float(d->token_format, [&](auto kind) {
+    constexpr int F = BSGG_IN_BF16;
+    rows_kernel<decltype(kind)::value, F, ROWS_DOT>
+        <<<static_cast<unsigned>(d->tokens), row_threads(d->hidden, row_values(F)), 0, s>>>(p);
+    return launch_status();
   });
 }
 

@@ -529,7 +529,7 @@ typedef struct {
   int64_t m_pad;          /* rows: a positive multiple of 128 */
   int64_t ld_token;       /* row pitch of x, y or dy in elements, >= hidden */
   int64_t ld_residual;    /* row pitch of the residual (combine), >= hidden; 0 without one */
-  int32_t topk;           /* >= 1; tokens * topk < 2^31 */
+  int32_t topk;           /* 1..32; tokens * topk < 2^31 */
   int32_t token_format;   /* f: x, dy; y and the residual */
   int32_t row_format;     /* dispatch, combine_backward: format of A / dD, as above */
   int32_t d_format;       /* f: D (combine, combine_backward) */
@@ -542,7 +542,8 @@ typedef struct {
  * to 0) has scale 1; codes are RNE(x / scale), saturating.  A block with an
  * infinity or a NaN gets the NaN scale (UE8M0 0xFF, E4M3 0x7F) and zero codes.
  * a: (m_pad, hidden) codes; sfa: bsgg_sf_bytes(m_pad, hidden, v, 1) bytes, every
- * one written (NULL for bfloat16 and float16 rows).  The gradient of a dispatch is
+ * one written (NULL for bfloat16 and float16 rows).  The two maps are each
+ * other's inverses, as bsgg_sort_tokens writes them.  The gradient of a dispatch is
  * bsgg_combine without weights. */
 BSGG_API bsgg_status bsgg_dispatch(const bsgg_tokens_desc* desc, const void* x, const int32_t* row_of_slot,
                                    const int32_t* slot_of_row, void* a, void* sfa, void* stream);
