@@ -74,6 +74,32 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]
     }
   }
 }
+// Eight values in the registers of their stored form (zeros where absent).
+// STREAM: they are read once and do not fit L2 anyway, so evict them first.
+template <int KIND, bool STREAM>
+struct Raw8 {
+  uint4 q[KIND == OK_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t i, bool present) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * (KIND == OK_F32 ? 4 : 2));
+#pragma unroll
+    for (int k = 0; k < (KIND == OK_F32 ? 2 : 1); ++k) q[k] = !present ? make_uint4(0, 0, 0, 0) : STREAM ? __ldcs(p + k) : p[k];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (KIND == OK_F32) {
+      const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
+    } else {
+      const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2<KIND>(w[k]);
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
+      }
+    }
+  }
+};
 template <int KIND>
 __device__ __forceinline__ void store8(void* base, int64_t i, const float (&v)[8]) {
   if constexpr (KIND == OK_F32) {

@@ -126,18 +126,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(
 #pragma unroll
     for (int i = 0; i < NI; ++i) p[i] *= r;
   }
+  // each expert's gradient: choice by choice, every lane looking for it among its own
+  float gi[NI], wi[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) gi[i] = wi[i] = 0.0f;
+  uint32_t chosen = 0;
+  for (int j = 0; j < topk; ++j) {
+    const int32_t at = __shfl_sync(0xFFFFFFFFu, id, j) - lane;
+    const float gj = __shfl_sync(0xFFFFFFFFu, g, j), wj = __shfl_sync(0xFFFFFFFFu, w, j);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (at == 32 * i) { gi[i] = gj; wi[i] = wj; chosen |= 1u << i; }
+  }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int e = lane + 32 * i;
-    float gi = 0.0f, wi = 0.0f;
-    bool chosen = false;
-    for (int j = 0; j < topk; ++j) {
-      const int32_t idj = __shfl_sync(0xFFFFFFFFu, id, j);
-      const float gj = __shfl_sync(0xFFFFFFFFu, g, j), wj = __shfl_sync(0xFFFFFFFFu, w, j);
-      if (idj == e) { gi = gj; wi = wj; chosen = true; }
-    }
     if (e < L) {
-      const float d = normalize ? (chosen ? wi * (gi - inner) : 0.0f) : p[i] * (gi - inner);
+      const float d = normalize ? ((chosen >> i) & 1u ? wi[i] * (gi[i] - inner) : 0.0f) : p[i] * (gi[i] - inner);
       store1(kind, dlogits, t * ld + e, d);
     }
   }
@@ -358,19 +363,21 @@ enum : int { ROWS_DISPATCH = 0, ROWS_GRAD = 1, ROWS_DOT = 2 };
 
 constexpr int kRowThreads = 512, kMaxTopk = 32, kPadRows = 8;
 
-// Values a thread holds: a 16-byte store of codes or 16-bit values (8 bytes FP4).
-__host__ __device__ constexpr int row_values(int fmt) { return rf_scaled(fmt) ? 16 : 8; }
+// Values a thread holds, in two runs of eight (hidden is a multiple of 8, for rows
+// with scales of 16): with D's two rows of a top-2 token that is 96 bytes a thread
+// in flight.
+constexpr int kRowValues = 16;
 
 template <int FMT>
-__device__ __forceinline__ void store_row_values(void* base, int64_t i, const float (&v)[row_values(FMT)], uint32_t code) {
+__device__ __forceinline__ void store_row_values(void* base, int64_t i, const float (&v)[kRowValues], uint32_t code,
+                                                 bool both) {
+  uint32_t lo[4], hi[4];
+  quantize8<FMT>(reinterpret_cast<const float(&)[8]>(v[0]), code, lo);
+  quantize8<FMT>(reinterpret_cast<const float(&)[8]>(v[8]), code, hi);
   if constexpr (!rf_scaled(FMT)) {
-    uint32_t c[4];
-    quantize8<FMT>(v, code, c);
-    store_codes8<FMT>(base, i, c);
+    store_codes8<FMT>(base, i, lo);
+    if (both) store_codes8<FMT>(base, i + 8, hi);
   } else {
-    uint32_t lo[4], hi[4];
-    quantize8<FMT>(reinterpret_cast<const float(&)[8]>(v[0]), code, lo);
-    quantize8<FMT>(reinterpret_cast<const float(&)[8]>(v[8]), code, hi);
     uint8_t* p = static_cast<uint8_t*>(base) + i * rf_bits(FMT) / 8;
     if (rf_fp4(FMT)) *reinterpret_cast<uint2*>(p) = make_uint2(lo[0], hi[0]);
     else *reinterpret_cast<uint4*>(p) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
@@ -399,9 +406,9 @@ __device__ __forceinline__ uint32_t block_code(const float (&v)[16], bool in, ui
 // tokens of 7168, top-8, against 98 us of bytes.  The blocks after them write the
 // padding rows, kPadRows each.
 template <int KIND, int FMT, int MODE>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(RowsParams p) {
-  constexpr int V = row_values(FMT), kLanes = rf_scaled(FMT) ? rf_vec(FMT) / 16 : 1;
-  constexpr int kBatch = 32 / V;                      // rows of D in flight
+__global__ void __launch_bounds__(kRowThreads, MODE == ROWS_DISPATCH ? 3 : 2) rows_kernel(RowsParams p) {
+  constexpr int V = kRowValues, kLanes = rf_scaled(FMT) ? rf_vec(FMT) / 16 : 1;
+  constexpr int kBatch = 2;                           // rows of D in flight
   __shared__ float part[MODE == ROWS_DISPATCH ? 1 : kMaxTopk][kRowThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   // columns in whole warps, up to the end of the last scale atom
@@ -429,36 +436,62 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(RowsParams p) {
   const int64_t t = blockIdx.x;
   const int32_t* rows = p.row_of_slot + t * p.topk;
   const bool dot = MODE != ROWS_DISPATCH && p.dweights != nullptr;
-  if (dot) {
-    for (int i = threadIdx.x; i < p.topk * warps; i += blockDim.x) part[i / warps][i % warps] = 0.0f;
-    __syncthreads();
-  }
   for (int64_t c = threadIdx.x * V; c < end; c += static_cast<int64_t>(blockDim.x) * V) {
-    const bool in = c < p.hidden;
+    const bool in = c < p.hidden, both = c + 8 < p.hidden;
     float v[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) v[k] = 0.0f;
     if (in) {
 #pragma unroll
-      for (int h = 0; h < V; h += 8) load8<KIND>(p.x, t * p.ld_token + c + h, reinterpret_cast<float(&)[8]>(v[h]));
+      for (int h = 0; h < V; h += 8)
+        if (h == 0 || both) load8<KIND>(p.x, t * p.ld_token + c + h, reinterpret_cast<float(&)[8]>(v[h]));
     }
     if (dot) {
+      // D's rows stay packed until they are used: a batch of 16-bit rows in flight
+      // costs half the registers of its values
+      const bool first = c == static_cast<int64_t>(threadIdx.x) * V;
       for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
-        float u[kBatch][V];
+        int32_t r[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          const int32_t r = j0 + b < p.topk ? rows[j0 + b] : -1;
+          r[b] = j0 + b < p.topk ? rows[j0 + b] : -1;
+          if (r[b] >= p.m_pad) r[b] = -1;
+        }
+        float acc[kBatch];
+        if (p.d_kind == OK_F32) {
 #pragma unroll
-          for (int h = 0; h < V; h += 8) {
-            float(&w)[8] = reinterpret_cast<float(&)[8]>(u[b][h]);
-            if (in && r >= 0 && r < p.m_pad) {
-              const int64_t at = r * p.hidden + c + h;
-              if (p.d_kind == OK_BF16) load8<OK_BF16>(p.d, at, w);
-              else if (p.d_kind == OK_F16) load8<OK_F16>(p.d, at, w);
-              else load8<OK_F32>(p.d, at, w);
-            } else {
+          for (int b = 0; b < kBatch; ++b) {
+            acc[b] = 0.0f;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = 0.0f;
+            for (int h = 0; h < V; h += 8) {
+              float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+              if ((h == 0 ? in : both) && r[b] >= 0) load8<OK_F32>(p.d, r[b] * p.hidden + c + h, w);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) acc[b] = fmaf(v[h + k], w[k], acc[b]);
+            }
+          }
+        } else {
+          uint4 u[kBatch][V / 8];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int h = 0; h < V / 8; ++h) {
+              u[b][h] = make_uint4(0, 0, 0, 0);
+              if ((h == 0 ? in : both) && r[b] >= 0)
+                u[b][h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.d) + r[b] * p.hidden + c + 8 * h);
+            }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            acc[b] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < V / 8; ++h) {
+              const uint32_t q[4] = {u[b][h].x, u[b][h].y, u[b][h].z, u[b][h].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = p.d_kind == OK_F16 ? unpack2<OK_F16>(q[k]) : unpack2<OK_BF16>(q[k]);
+                acc[b] = fmaf(v[8 * h + 2 * k], f.x, acc[b]);
+                acc[b] = fmaf(v[8 * h + 2 * k + 1], f.y, acc[b]);
+              }
             }
           }
         }
@@ -466,12 +499,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(RowsParams p) {
         for (int b = 0; b < kBatch; ++b) {
           if (j0 + b >= p.topk) break;
           // a slot without a row has the gradient 0 whatever dy holds
-          const int32_t r = rows[j0 + b];
-          float acc = 0.0f;
-#pragma unroll
-          for (int k = 0; k < V; ++k) acc = fmaf(v[k], u[b][k], acc);
-          acc = warp_sum(r >= 0 && r < p.m_pad ? acc : 0.0f);
-          if (lane == 0) part[j0 + b][warp] += acc;
+          const float sum = warp_sum(r[b] >= 0 ? acc[b] : 0.0f);
+          if (lane == 0) part[j0 + b][warp] = first ? sum : part[j0 + b][warp] + sum;
         }
       }
     }
@@ -496,15 +525,14 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(RowsParams p) {
         const int64_t kb = c / rf_vec(FMT);
         if (lane % (4 * kLanes) == 0 && c < cols) *reinterpret_cast<uint32_t*>(p.sfa + sf_off(r, kb, p.kq)) = word;
       }
-      if (in) store_row_values<FMT>(p.a, r * p.hidden + c, w, code);
+      if (in) store_row_values<FMT>(p.a, r * p.hidden + c, w, code, both);
     }
   }
   if (dot) {
     __syncthreads();
-    for (int j = threadIdx.x; j < p.topk; j += blockDim.x) {
-      float s = 0.0f;
-      for (int w = 0; w < warps; ++w) s += part[j][w];
-      p.dweights[t * p.topk + j] = s;
+    for (int j = warp; j < p.topk; j += warps) {
+      const float s = warp_sum(lane < warps ? part[j][lane] : 0.0f);
+      if (lane == 0) p.dweights[t * p.topk + j] = s;
     }
   }
 }
@@ -522,7 +550,10 @@ struct CombineParams {
 
 // One token per block of x, a run of columns per block of y; four rows of D are
 // loaded before any is added, so that a thread has 64 bytes of them in flight.
-template <int DK, int KIND>
+// Rows that L2 cannot hold are marked as read once (8192 tokens, top-8, 7168 wide:
+// 206 us without the mark, 198 with it); smaller ones are where the product that
+// wrote them left them (128 tokens: 3.7 us without, 7.2 with).
+template <int DK, int KIND, bool STREAM>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
   constexpr int kBatch = 4;
   const int64_t t = blockIdx.x;
@@ -533,23 +564,22 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (p.residual != nullptr) load8<KIND>(p.residual, t * p.ld_residual + c, acc);
     for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
-      float v[kBatch][8], w[kBatch];
+      Raw8<DK, STREAM> v[kBatch];
+      float w[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         const int32_t r = j0 + b < p.topk ? rows[j0 + b] : -1;
         const bool real = r >= 0 && r < p.m_pad;
         w[b] = !real ? 0.0f : weights != nullptr ? weights[j0 + b] : 1.0f;
-        if (real) {
-          load8<DK>(p.d, r * p.hidden + c, v[b]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[b][k] = 0.0f;
-        }
+        v[b].load(p.d, r * p.hidden + c, real);
       }
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
+      for (int b = 0; b < kBatch; ++b) {
+        float f[8];
+        v[b].values(f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[b], v[b][k], acc[k]);
+        for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[b], f[k], acc[k]);
+      }
     }
     store8<KIND>(p.y, t * p.ld_token + c, acc);
   }
@@ -633,7 +663,7 @@ bsgg_status launch_rows(const bsgg_tokens_desc* d, RowsParams p, cudaStream_t s)
       constexpr int K = decltype(kind)::value, F = decltype(fmt)::value;
       p.kq = rf_scaled(F) ? ceil_div(ceil_div(d->hidden, rf_vec(F)), 4) : 0;
       const int64_t grid = d->tokens + ceil_div(d->m_pad, kPadRows);
-      rows_kernel<K, F, MODE><<<static_cast<unsigned>(grid), row_threads(d->hidden, row_values(F)), 0, s>>>(p);
+      rows_kernel<K, F, MODE><<<static_cast<unsigned>(grid), row_threads(d->hidden, kRowValues), 0, s>>>(p);
       return launch_status();
     });
   });
@@ -791,6 +821,8 @@ bsgg_status bsgg_combine(const bsgg_tokens_desc* d, const void* dd, const int32_
   if (!dd || !row_of_slot || !y || !aligned_to(dd, 16) || !aligned_to(residual, 16) || !aligned_to(y, 16) ||
       !aligned_to(row_of_slot, 4) || !aligned_to(weights, 4))
     return BSGG_ERR_INVALID_ARG;
+  // half of L2's 126 MB
+  const bool large = d->tokens * d->topk * d->hidden * float_bytes(d->d_format) > (int64_t(64) << 20);
   CombineParams p = {d->tokens, d->hidden, d->m_pad, d->ld_token, d->ld_residual, d->topk, dd, row_of_slot, weights,
                      residual, y};
   return with_float(d->d_format, [&](auto dk) {
@@ -800,7 +832,9 @@ bsgg_status bsgg_combine(const bsgg_tokens_desc* d, const void* dd, const int32_
       int threads = row_threads(d->hidden, 8);
       while (threads > 64 && d->tokens * ceil_div(d->hidden, threads * 8) < 608) threads = (threads / 2 + 31) / 32 * 32;
       const dim3 grid(static_cast<unsigned>(d->tokens), static_cast<unsigned>(ceil_div(d->hidden, threads * 8)));
-      combine_kernel<decltype(dk)::value, decltype(kind)::value><<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+      constexpr int D = decltype(dk)::value, K = decltype(kind)::value;
+      if (large) combine_kernel<D, K, true><<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+      else combine_kernel<D, K, false><<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
       return launch_status();
     });
   });
@@ -828,7 +862,7 @@ bsgg_status bsgg_combine_backward(const bsgg_tokens_desc* d, const void* dy, con
   return with_float(d->token_format, [&](auto kind) {
     constexpr int F = BSGG_IN_BF16;
     rows_kernel<decltype(kind)::value, F, ROWS_DOT>
-        <<<static_cast<unsigned>(d->tokens), row_threads(d->hidden, row_values(F)), 0, s>>>(p);
+        <<<static_cast<unsigned>(d->tokens), row_threads(d->hidden, kRowValues), 0, s>>>(p);
     return launch_status();
   });
 }
