@@ -12,15 +12,16 @@ using namespace bsgg;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// act'(z).  silu: s + z s (1 - s) with 1 - s = s(-z), no cancellation;
-// gelu: Phi(z) + z phi(z).
+// act'(z).  silu: s (1 + z (1 - s)) with e = e^-z, s = 1 / (1 + e), 1 - s = e s: no
+// cancellation, one exponential and one reciprocal (the argument is held below 87,
+// where s is 1e-38, so that e s stays a number); gelu: Phi(z) + z phi(z).
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == BSGG_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
   if (ACT == BSGG_ACT_SRELU) return z > 0.0f ? 2.0f * z : 0.0f;
   if (ACT == BSGG_ACT_SILU) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-z)), c = __fdividef(1.0f, 1.0f + __expf(z));
-    return s * (1.0f + z * c);
+    const float e = __expf(fminf(-z, 87.0f)), s = __fdividef(1.0f, 1.0f + e);
+    return s * fmaf(z, e * s, 1.0f);
   }
   if (ACT == BSGG_ACT_GELU) return normcdff(z) + z * 0.398942280401432678f * __expf(-0.5f * z * z);
   return 1.0f;
@@ -29,61 +30,75 @@ __device__ __forceinline__ float act_slope(float z) {
 // dz = dy act'(z) and dbias.  A block owns 64 columns (a lane eight of them, so
 // that a warp reads four 128-byte pieces of rows at a time) and one of the
 // cluster's runs of rows; its sums join through shared memory and, between the
-// cluster's blocks, through distributed shared memory, in a fixed order.
-constexpr int kDzThreads = 256, kDzCols = 64, kDzSplit = 8;
+// cluster's blocks, through distributed shared memory, in a fixed order.  Bound by
+// the loads' latency, so the rows are split no further than fills the chip twice
+// (what a block pays once, its joins above all, cost 4096 x 14336 in eight runs a
+// third of its time: 83 us for 352 MB).
+constexpr int kDzThreads = 512, kDzSplit = 8, kDzRows = 3, kDzLanes = 8;
 
 template <int KIND, int ACT>
-__global__ void __launch_bounds__(kDzThreads) dz_kernel(int64_t m, int64_t n, int64_t ld_dy, int64_t ldz, int64_t ld_dz,
+__global__ void __launch_bounds__(kDzThreads, 2) dz_kernel(int64_t m, int64_t n, int64_t ld_dy, int64_t ldz, int64_t ld_dz,
                                                         const void* dy, const void* z, void* dz, float* dbias) {
-  __shared__ float part[kDzThreads / 32][kDzCols];
-  __shared__ float block_sum[kDzCols];
+  constexpr int kCols = kDzLanes * 8, kWarps = kDzThreads / 32, kStep = kDzThreads / kDzLanes;
+  __shared__ float part[kWarps][kCols];
+  __shared__ float block_sum[kCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t j = static_cast<int64_t>(blockIdx.y) * kDzCols + (lane & 7) * 8;
-  // rows [i0, i1), a warp four at a time
+  const int64_t j = static_cast<int64_t>(blockIdx.y) * kCols + (threadIdx.x % kDzLanes) * 8;
   const int64_t i0 = m * blockIdx.x / gridDim.x, i1 = m * (blockIdx.x + 1) / gridDim.x;
   // n need not be a multiple of 8, the pitches are: whole pieces are read, the
   // padding columns' sums are not used and their dz is written as the pitch allows
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (j < n) {
-#pragma unroll 2
-    for (int64_t i = i0 + warp * 4 + (lane >> 3); i < i1; i += kDzThreads / 8) {
-      float g[8];
-      load8<KIND>(dy, i * ld_dy + j, g);
-      if (ACT != BSGG_ACT_NONE) {
-        float v[8];
-        load8<KIND>(z, i * ldz + j, v);
+    for (int64_t i = i0 + threadIdx.x / kDzLanes; i < i1; i += kStep * kDzRows) {
+      Raw8<KIND, false> g[kDzRows], v[kDzRows];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] *= act_slope<ACT>(v[k]);
-        store8<KIND>(dz, i * ld_dz + j, g);
+      for (int u = 0; u < kDzRows; ++u) {
+        const int64_t r = i + u * kStep;
+        g[u].load(dy, r * ld_dy + j, r < i1);
+        if (ACT != BSGG_ACT_NONE) v[u].load(z, r * ldz + j, r < i1);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] += g[k];
+      for (int u = 0; u < kDzRows; ++u) {
+        const int64_t r = i + u * kStep;
+        if (r >= i1) break;
+        float f[8];
+        g[u].values(f);
+        if (ACT != BSGG_ACT_NONE) {
+          float w[8];
+          v[u].values(w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] *= act_slope<ACT>(w[k]);
+          store8<KIND>(dz, r * ld_dz + j, f);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] += f[k];
+      }
     }
   }
   if (dbias == nullptr) return;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], 8);
-    sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], 16);
-  }
-  if (lane < 8) {
+  for (int o = kDzLanes; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
+  if (lane < kDzLanes) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) part[warp][lane * 8 + k] = sum[k];
   }
   __syncthreads();
-  if (threadIdx.x < kDzCols) {
+  if (threadIdx.x < kCols) {
     float s = 0.0f;
-    for (int w = 0; w < kDzThreads / 32; ++w) s += part[w][threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += part[w][threadIdx.x];
     block_sum[threadIdx.x] = s;
   }
-  cluster_sync();
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * kDzCols + threadIdx.x;
-  if (blockIdx.x == 0 && threadIdx.x < kDzCols && c < n) {
+  if (gridDim.x > 1) cluster_sync(); else __syncthreads();
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + threadIdx.x;
+  if (blockIdx.x == 0 && threadIdx.x < kCols && c < n) {
     float s = 0.0f;
     for (unsigned r = 0; r < gridDim.x; ++r) s += ld_shared_cluster(mapa_shared(smem_u32(&block_sum[threadIdx.x]), r));
     dbias[c] = s;
   }
-  cluster_sync();          // the sums stay until block 0 has read them
+  if (gridDim.x > 1) cluster_sync();          // the sums stay until block 0 has read them
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -294,11 +309,14 @@ bsgg_status launch_product(const Operand& P, const Operand& Q, int in_format, Li
 
 template <int KIND, int ACT>
 cudaError_t launch_dz_one(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias,
-                          cudaStream_t s) {
-  // runs of at least 32 rows, at most the portable cluster's eight
-  const int64_t runs = ceil_div(d->m, 32);
+                          int sms, cudaStream_t s) {
+  // two blocks an SM, runs of at least one step of rows, the portable cluster's eight at most
+  const int64_t groups = ceil_div(d->n, kDzLanes * 8), steps = ceil_div(d->m, kDzThreads / kDzLanes);
+  int64_t runs = 2 * sms / groups;
+  runs = runs < 1 ? 1 : runs > kDzSplit ? kDzSplit : runs;
+  if (runs > steps) runs = steps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(runs < kDzSplit ? runs : kDzSplit), static_cast<unsigned>(ceil_div(d->n, kDzCols)), 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(runs), static_cast<unsigned>(groups), 1);
   cfg.blockDim = dim3(kDzThreads, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -312,18 +330,21 @@ cudaError_t launch_dz_one(const bsgg_linear_bwd_desc* d, const void* dy, const v
 }
 template <int KIND>
 cudaError_t launch_dz_kind(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias,
-                           cudaStream_t s) {
+                           int sms, cudaStream_t s) {
   switch (d->activation) {
-    case BSGG_ACT_RELU: return launch_dz_one<KIND, BSGG_ACT_RELU>(d, dy, z, dz, dbias, s);
-    case BSGG_ACT_SRELU: return launch_dz_one<KIND, BSGG_ACT_SRELU>(d, dy, z, dz, dbias, s);
-    case BSGG_ACT_SILU: return launch_dz_one<KIND, BSGG_ACT_SILU>(d, dy, z, dz, dbias, s);
-    case BSGG_ACT_GELU: return launch_dz_one<KIND, BSGG_ACT_GELU>(d, dy, z, dz, dbias, s);
-    default: return launch_dz_one<KIND, BSGG_ACT_NONE>(d, dy, z, dz, dbias, s);
+    case BSGG_ACT_RELU: return launch_dz_one<KIND, BSGG_ACT_RELU>(d, dy, z, dz, dbias, sms, s);
+    case BSGG_ACT_SRELU: return launch_dz_one<KIND, BSGG_ACT_SRELU>(d, dy, z, dz, dbias, sms, s);
+    case BSGG_ACT_SILU: return launch_dz_one<KIND, BSGG_ACT_SILU>(d, dy, z, dz, dbias, sms, s);
+    case BSGG_ACT_GELU: return launch_dz_one<KIND, BSGG_ACT_GELU>(d, dy, z, dz, dbias, sms, s);
+    default: return launch_dz_one<KIND, BSGG_ACT_NONE>(d, dy, z, dz, dbias, sms, s);
   }
 }
 bsgg_status launch_dz(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias, cudaStream_t s) {
-  const cudaError_t e = d->in_format == BSGG_OUT_BF16 ? launch_dz_kind<OK_BF16>(d, dy, z, dz, dbias, s)
-                                                      : launch_dz_kind<OK_F16>(d, dy, z, dz, dbias, s);
+  const Device* dev = device_state();
+  if (!dev) return BSGG_ERR_CUDA;
+  const int sms = dev->sms;
+  const cudaError_t e = d->in_format == BSGG_OUT_BF16 ? launch_dz_kind<OK_BF16>(d, dy, z, dz, dbias, sms, s)
+                                                      : launch_dz_kind<OK_F16>(d, dy, z, dz, dbias, sms, s);
   return e == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA;
 }
 
