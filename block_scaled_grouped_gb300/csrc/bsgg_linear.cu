@@ -42,6 +42,8 @@ __global__ void __launch_bounds__(kDzThreads, 2) dz_kernel(int64_t m, int64_t n,
   constexpr int kCols = kDzLanes * 8, kWarps = kDzThreads / 32, kStep = kDzThreads / kDzLanes;
   __shared__ float part[kWarps][kCols];
   __shared__ float block_sum[kCols];
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t j = static_cast<int64_t>(blockIdx.y) * kCols + (threadIdx.x % kDzLanes) * 8;
   const int64_t i0 = m * blockIdx.x / gridDim.x, i1 = m * (blockIdx.x + 1) / gridDim.x;
@@ -141,29 +143,6 @@ uint32_t lin_idesc(int in_format, bool p_mn, bool q_mn, int m, int n) {
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// A launch of `ctas` CTAs in clusters of `cluster`; attr holds the attribute.
-cudaLaunchConfig_t lin_config(int64_t ctas, int cluster, int smem, cudaStream_t s, cudaLaunchAttribute* attr) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-  cfg.blockDim = dim3(kLinThreads, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = s;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
-}
-template <typename K>
-cudaError_t launch_lin(K kern, int64_t ctas, int cluster, int smem, const CUtensorMap& tp, const CUtensorMap& tq,
-                       const LinParams& p, int split, cudaStream_t s) {
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = lin_config(ctas, cluster, smem, s, attr);
-  return cudaLaunchKernelEx(&cfg, kern, tp, tq, p, split);
-}
-
 // What a device holds of the products' kernels: SMs, and for each kernel and
 // cluster size the clusters resident at once (a GPC's SMs are shared out in whole
 // clusters, so that 16 clusters of 8 CTAs with an SM each do not fit 152 SMs).
@@ -178,9 +157,19 @@ template <typename K>
 bool prepare_kernel(K kern, int smem, int ctas, int clusters, int* resident) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
   for (int i = 0; i < clusters; ++i) {
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = lin_config(int64_t(ctas) << i, ctas << i, smem, nullptr, attr);
-    if (cudaOccupancyMaxActiveClusters(&resident[i], kern, &cfg) != cudaSuccess || resident[i] < 1) return false;
+    const int cluster = ctas << i;
+    const LaunchConfig c(dim3(static_cast<unsigned>(cluster)), kLinThreads, static_cast<size_t>(smem), nullptr, cluster);
+    if (cluster == 1) {
+      int blocks = 0, sms = 0, dev = 0;
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kern, kLinThreads, static_cast<size_t>(smem)) != cudaSuccess ||
+          cudaGetDevice(&dev) != cudaSuccess ||
+          cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return false;
+      resident[i] = blocks * sms;
+    } else if (cudaOccupancyMaxActiveClusters(&resident[i], kern, &c.cfg) != cudaSuccess) {
+      return false;
+    }
+    if (resident[i] < 1) return false;
   }
   return true;
 }
@@ -210,18 +199,24 @@ const Device* device_state() {
   return &d;
 }
 
-template <int BN>
-cudaError_t launch_tile(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, int sms, cudaStream_t s) {
-  const int64_t ctas = int64_t(p.p_tiles) * p.q_tiles * split;
-  return ctas <= sms ? launch_lin(linear_tile_kernel<BN, true>, ctas, split, LinTile<BN, true>::kSmem, tp, tq, p, split, s)
-                     : launch_lin(linear_tile_kernel<BN, false>, ctas, split, LinTile<BN, false>::kSmem, tp, tq, p, split, s);
+template <int BN, bool ALONE>
+bsgg_status launch_tile_as(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int64_t ctas, int split,
+                           cudaStream_t s) {
+  const LaunchConfig c(dim3(static_cast<unsigned>(ctas)), kLinThreads, LinTile<BN, ALONE>::kSmem, s, split);
+  return launch_kernel(c, linear_tile_kernel<BN, ALONE>, tp, tq, p, split);
 }
 template <int BN>
-cudaError_t launch_pair(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, const Device& dev,
+bsgg_status launch_tile(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, int sms, cudaStream_t s) {
+  const int64_t ctas = int64_t(p.p_tiles) * p.q_tiles * split;
+  return ctas <= sms ? launch_tile_as<BN, true>(tp, tq, p, ctas, split, s) : launch_tile_as<BN, false>(tp, tq, p, ctas, split, s);
+}
+template <int BN>
+bsgg_status launch_pair(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, const Device& dev,
                         cudaStream_t s) {
   const int64_t tiles = int64_t(p.p_tiles) * p.q_tiles, resident = dev.pair_clusters[BN == 256 ? 0 : 1][0];
   const int64_t units = split > 1 || tiles < resident ? tiles : resident;
-  return launch_lin(linear_pair_kernel<BN>, 2 * split * units, 2 * split, LinPair<BN>::kSmem, tp, tq, p, split, s);
+  const LaunchConfig c(dim3(static_cast<unsigned>(2 * split * units)), kLinThreads, LinPair<BN>::kSmem, s, 2 * split);
+  return launch_kernel(c, linear_pair_kernel<BN>, tp, tq, p, split);
 }
 
 // How a product is tiled: 256 x bn on CTA pairs, or 128 x bn on single CTAs, with
@@ -299,37 +294,25 @@ bsgg_status launch_product(const Operand& P, const Operand& Q, int in_format, Li
   p.q_tiles = static_cast<int32_t>(ceil_div(Q.rows, c.bn));
   p.idesc = lin_idesc(in_format, P.mn, Q.mn, side, c.bn);
   if (!encode_operand(&tp, P, 128) || !encode_operand(&tq, Q, c.pair ? c.bn / 2 : c.bn)) return BSGG_ERR_CUDA;
-  cudaError_t e;
-  if (c.pair) e = c.bn == 256 ? launch_pair<256>(tp, tq, p, c.split, *dev, s) : launch_pair<128>(tp, tq, p, c.split, *dev, s);
-  else if (c.bn == 128) e = launch_tile<128>(tp, tq, p, c.split, dev->sms, s);
-  else if (c.bn == 64) e = launch_tile<64>(tp, tq, p, c.split, dev->sms, s);
-  else e = launch_tile<32>(tp, tq, p, c.split, dev->sms, s);
-  return e == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA;
+  if (c.pair) return c.bn == 256 ? launch_pair<256>(tp, tq, p, c.split, *dev, s) : launch_pair<128>(tp, tq, p, c.split, *dev, s);
+  if (c.bn == 128) return launch_tile<128>(tp, tq, p, c.split, dev->sms, s);
+  return c.bn == 64 ? launch_tile<64>(tp, tq, p, c.split, dev->sms, s) : launch_tile<32>(tp, tq, p, c.split, dev->sms, s);
 }
 
 template <int KIND, int ACT>
-cudaError_t launch_dz_one(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias,
+bsgg_status launch_dz_one(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias,
                           int sms, cudaStream_t s) {
   // two blocks an SM, runs of at least one step of rows, the portable cluster's eight at most
   const int64_t groups = ceil_div(d->n, kDzLanes * 8), steps = ceil_div(d->m, kDzThreads / kDzLanes);
   int64_t runs = 2 * sms / groups;
   runs = runs < 1 ? 1 : runs > kDzSplit ? kDzSplit : runs;
   if (runs > steps) runs = steps;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(runs), static_cast<unsigned>(groups), 1);
-  cfg.blockDim = dim3(kDzThreads, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cfg.gridDim.x;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dz_kernel<KIND, ACT>, d->m, d->n, d->ld_dy, d->ldz, d->ld_dz, dy, z, dz, dbias);
+  const LaunchConfig c(dim3(static_cast<unsigned>(runs), static_cast<unsigned>(groups)), kDzThreads, 0, s,
+                       static_cast<int>(runs));
+  return launch_kernel(c, dz_kernel<KIND, ACT>, d->m, d->n, d->ld_dy, d->ldz, d->ld_dz, dy, z, dz, dbias);
 }
 template <int KIND>
-cudaError_t launch_dz_kind(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias,
+bsgg_status launch_dz_kind(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias,
                            int sms, cudaStream_t s) {
   switch (d->activation) {
     case BSGG_ACT_RELU: return launch_dz_one<KIND, BSGG_ACT_RELU>(d, dy, z, dz, dbias, sms, s);
@@ -343,9 +326,8 @@ bsgg_status launch_dz(const bsgg_linear_bwd_desc* d, const void* dy, const void*
   const Device* dev = device_state();
   if (!dev) return BSGG_ERR_CUDA;
   const int sms = dev->sms;
-  const cudaError_t e = d->in_format == BSGG_OUT_BF16 ? launch_dz_kind<OK_BF16>(d, dy, z, dz, dbias, sms, s)
-                                                      : launch_dz_kind<OK_F16>(d, dy, z, dz, dbias, sms, s);
-  return e == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA;
+  return d->in_format == BSGG_OUT_BF16 ? launch_dz_kind<OK_BF16>(d, dy, z, dz, dbias, sms, s)
+                                       : launch_dz_kind<OK_F16>(d, dy, z, dz, dbias, sms, s);
 }
 
 bool is_half_format(int f) { return f == BSGG_OUT_BF16 || f == BSGG_OUT_F16; }

@@ -330,6 +330,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *holder;
+  let_next_kernel_start();
+  wait_for_previous_kernel();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -525,6 +527,8 @@ __global__ void __launch_bounds__(kLinThreads, ALONE ? 1 : 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
+  let_next_kernel_start();
+  wait_for_previous_kernel();
 
   if (warp == 0) {
     if (lane == 0) {

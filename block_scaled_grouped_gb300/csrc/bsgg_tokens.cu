@@ -35,6 +35,8 @@ template <int NI>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(int64_t tokens, int64_t ld, int L, int topk, int kind,
                                                                  int normalize, const void* logits, int32_t* ids,
                                                                  float* weights) {
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (t >= tokens) return;
@@ -85,6 +87,8 @@ template <int NI>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(
     int64_t tokens, int64_t ld, int L, int topk, int kind, int normalize, const void* logits, const int32_t* ids,
     const float* weights, const float* dweights, const int32_t* row_of_slot, int64_t m_pad, void* dlogits) {
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (t >= tokens) return;
@@ -288,6 +292,8 @@ __device__ __forceinline__ void sort_place(const SortParams& p, const SortShared
 __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(SortParams p) {
   extern __shared__ int32_t sm[];
   const SortShared sh(sm, p.L);
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   const int rank = blockIdx.x, blocks = p.blocks;
   sort_count(p, sh, rank);
   if (blocks > 1) cluster_sync(); else __syncthreads();
@@ -311,6 +317,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(SortParams p
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortParams p) {
   extern __shared__ int32_t sm[];
   const SortShared sh(sm, p.L);
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   sort_count(p, sh, blockIdx.x);
   for (int e = threadIdx.x; e < p.L; e += kSortThreads) p.counts[static_cast<int64_t>(blockIdx.x) * p.L + e] = sh.mine[e];
 }
@@ -318,6 +326,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortParams p) 
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) {
   extern __shared__ int32_t sm[];
   const SortShared sh(sm, p.L);
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   for (int e = threadIdx.x; e < p.L; e += kSortThreads) sh.total[e] = sh.before[e] = 0;
   sort_count(p, sh, blockIdx.x);
   // the blocks' counts of an expert: shared out over as many threads as there are
@@ -411,6 +421,8 @@ __global__ void __launch_bounds__(kRowThreads, MODE == ROWS_DISPATCH ? 3 : 2) ro
   constexpr int kBatch = 2;                           // rows of D in flight
   __shared__ float part[MODE == ROWS_DISPATCH ? 1 : kMaxTopk][kRowThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   // columns in whole warps, up to the end of the last scale atom
   const int64_t cols = rf_scaled(FMT) ? p.kq * 4 * rf_vec(FMT) : p.hidden;
   const int64_t end = (cols + 32 * V - 1) / (32 * V) * (32 * V);
@@ -556,6 +568,8 @@ struct CombineParams {
 template <int DK, int KIND, bool STREAM>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
   constexpr int kBatch = 4;
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   const int64_t t = blockIdx.x;
   const int32_t* rows = p.row_of_slot + t * p.topk;
   const float* weights = p.weights != nullptr ? p.weights + t * p.topk : nullptr;
@@ -588,8 +602,6 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
 // ---------------------------------------------------------------- host
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-bsgg_status launch_status() { return cudaGetLastError() == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA; }
-
 bsgg_status check_route(const bsgg_route_desc* d) {
   if (!d || d->tokens < 0 || d->tokens > (int64_t(1) << 30) || d->num_experts < 1 || d->num_experts > 1024)
     return BSGG_ERR_INVALID_ARG;
@@ -601,13 +613,13 @@ bsgg_status check_route(const bsgg_route_desc* d) {
 
 // Registers of logits per lane: the least power of two times 32 that holds L.
 template <typename F>
-void with_route_regs(int L, F&& f) {
-  if (L <= 32) f(std::integral_constant<int, 1>());
-  else if (L <= 64) f(std::integral_constant<int, 2>());
-  else if (L <= 128) f(std::integral_constant<int, 4>());
-  else if (L <= 256) f(std::integral_constant<int, 8>());
-  else if (L <= 512) f(std::integral_constant<int, 16>());
-  else f(std::integral_constant<int, 32>());
+bsgg_status with_route_regs(int L, F&& f) {
+  if (L <= 32) return f(std::integral_constant<int, 1>());
+  if (L <= 64) return f(std::integral_constant<int, 2>());
+  if (L <= 128) return f(std::integral_constant<int, 4>());
+  if (L <= 256) return f(std::integral_constant<int, 8>());
+  if (L <= 512) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>());
 }
 
 // Calls f with the format (f: bf16, f16, f32) as a constant.
@@ -663,8 +675,8 @@ bsgg_status launch_rows(const bsgg_tokens_desc* d, RowsParams p, cudaStream_t s)
       constexpr int K = decltype(kind)::value, F = decltype(fmt)::value;
       p.kq = rf_scaled(F) ? ceil_div(ceil_div(d->hidden, rf_vec(F)), 4) : 0;
       const int64_t grid = d->tokens + ceil_div(d->m_pad, kPadRows);
-      rows_kernel<K, F, MODE><<<static_cast<unsigned>(grid), row_threads(d->hidden, kRowValues), 0, s>>>(p);
-      return launch_status();
+      const LaunchConfig c(dim3(static_cast<unsigned>(grid)), row_threads(d->hidden, kRowValues), 0, s);
+      return launch_kernel(c, rows_kernel<K, F, MODE>, p);
     });
   });
 }
@@ -704,11 +716,11 @@ bsgg_status bsgg_route(const bsgg_route_desc* d, const void* logits, int32_t* id
       !aligned_to(weights, 4))
     return BSGG_ERR_INVALID_ARG;
   const unsigned grid = static_cast<unsigned>(ceil_div(d->tokens, kRouteWarps));
-  with_route_regs(d->num_experts, [&](auto ni) {
-    route_kernel<decltype(ni)::value><<<grid, 32 * kRouteWarps, 0, static_cast<cudaStream_t>(stream)>>>(
-        d->tokens, d->ld, d->num_experts, d->topk, d->logit_format, d->normalize, logits, ids, weights);
+  const LaunchConfig c(dim3(grid), 32 * kRouteWarps, 0, static_cast<cudaStream_t>(stream));
+  return with_route_regs(d->num_experts, [&](auto ni) {
+    return launch_kernel(c, route_kernel<decltype(ni)::value>, d->tokens, d->ld, d->num_experts, d->topk, d->logit_format,
+                         d->normalize, logits, ids, weights);
   });
-  return launch_status();
 }
 
 bsgg_status bsgg_route_backward(const bsgg_route_desc* d, const void* logits, const int32_t* ids, const float* weights,
@@ -723,12 +735,11 @@ bsgg_status bsgg_route_backward(const bsgg_route_desc* d, const void* logits, co
       !aligned_to(ids, 4) || !aligned_to(weights, 4) || !aligned_to(dweights, 4) || !aligned_to(row_of_slot, 4))
     return BSGG_ERR_INVALID_ARG;
   const unsigned grid = static_cast<unsigned>(ceil_div(d->tokens, kRouteWarps));
-  with_route_regs(d->num_experts, [&](auto ni) {
-    route_backward_kernel<decltype(ni)::value><<<grid, 32 * kRouteWarps, 0, static_cast<cudaStream_t>(stream)>>>(
-        d->tokens, d->ld, d->num_experts, d->topk, d->logit_format, d->normalize, logits, ids, weights, dweights,
-        row_of_slot, m_pad, dlogits);
+  const LaunchConfig c(dim3(grid), 32 * kRouteWarps, 0, static_cast<cudaStream_t>(stream));
+  return with_route_regs(d->num_experts, [&](auto ni) {
+    return launch_kernel(c, route_backward_kernel<decltype(ni)::value>, d->tokens, d->ld, d->num_experts, d->topk,
+                         d->logit_format, d->normalize, logits, ids, weights, dweights, row_of_slot, m_pad, dlogits);
   });
-  return launch_status();
 }
 
 int64_t bsgg_sort_rows(int64_t slots, int32_t num_experts) {
@@ -775,25 +786,13 @@ bsgg_status bsgg_sort_tokens(int64_t slots, int32_t num_experts, int64_t m_pad, 
   const size_t smem = sort_shared_bytes(p.L);                // 49 KB at the most: 1024 experts
   if (one_cluster) {
     if (!sort_allowed(sort_cluster_kernel, smem)) return BSGG_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.blocks), 1, 1);
-    cfg.blockDim = dim3(kSortThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cfg.gridDim.x;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sort_cluster_kernel, p) == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA;
+    const LaunchConfig c(dim3(static_cast<unsigned>(p.blocks)), kSortThreads, smem, s, p.blocks);
+    return launch_kernel(c, sort_cluster_kernel, p);
   }
   if (!sort_allowed(sort_count_kernel, smem) || !sort_allowed(sort_place_kernel, smem)) return BSGG_ERR_CUDA;
-  sort_count_kernel<<<p.blocks, kSortThreads, smem, s>>>(p);
-  if (launch_status() != BSGG_OK) return BSGG_ERR_CUDA;
-  sort_place_kernel<<<p.blocks, kSortThreads, smem, s>>>(p);
-  return launch_status();
+  const LaunchConfig c(dim3(static_cast<unsigned>(p.blocks)), kSortThreads, smem, s);
+  const bsgg_status st = launch_kernel(c, sort_count_kernel, p);
+  return st == BSGG_OK ? launch_kernel(c, sort_place_kernel, p) : st;
 }
 
 bsgg_status bsgg_dispatch(const bsgg_tokens_desc* d, const void* x, const int32_t* row_of_slot,
@@ -833,9 +832,8 @@ bsgg_status bsgg_combine(const bsgg_tokens_desc* d, const void* dd, const int32_
       while (threads > 64 && d->tokens * ceil_div(d->hidden, threads * 8) < 608) threads = (threads / 2 + 31) / 32 * 32;
       const dim3 grid(static_cast<unsigned>(d->tokens), static_cast<unsigned>(ceil_div(d->hidden, threads * 8)));
       constexpr int D = decltype(dk)::value, K = decltype(kind)::value;
-      if (large) combine_kernel<D, K, true><<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-      else combine_kernel<D, K, false><<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-      return launch_status();
+      const LaunchConfig c(grid, threads, 0, static_cast<cudaStream_t>(stream));
+      return large ? launch_kernel(c, combine_kernel<D, K, true>, p) : launch_kernel(c, combine_kernel<D, K, false>, p);
     });
   });
 }
@@ -861,9 +859,8 @@ bsgg_status bsgg_combine_backward(const bsgg_tokens_desc* d, const void* dy, con
   p.tokens = d->tokens; p.hidden = d->hidden; p.m_pad = d->m_pad; p.ld_token = d->ld_token; p.topk = d->topk;
   return with_float(d->token_format, [&](auto kind) {
     constexpr int F = BSGG_IN_BF16;
-    rows_kernel<decltype(kind)::value, F, ROWS_DOT>
-        <<<static_cast<unsigned>(d->tokens), row_threads(d->hidden, kRowValues), 0, s>>>(p);
-    return launch_status();
+    const LaunchConfig c(dim3(static_cast<unsigned>(d->tokens)), row_threads(d->hidden, kRowValues), 0, s);
+    return launch_kernel(c, rows_kernel<decltype(kind)::value, F, ROWS_DOT>, p);
   });
 }
 
