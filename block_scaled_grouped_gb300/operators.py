@@ -253,15 +253,17 @@ def sort_tokens(ids, num_experts: int, m_pad: Optional[int] = None, weights=None
     handle = _handle(ids, stream)
     empty, dev = _empty_on(stream), ids.device
     m, e = max(m_pad, 0), max(num_experts, 0)
-    # one allocation for the integers: slots, rows, offsets, rows_used, workspace
-    buf = empty(n + m + e + 1 + nws, dtype=_I32, device=dev)
+    # one allocation for the integers, each part at a multiple of 16 bytes as the
+    # grouped GEMM wants them: rows, slots, offsets, rows_used, workspace
+    i1 = m + (n + 3) // 4 * 4
+    i2 = i1 + (e + 3) // 4 * 4
+    buf = empty(i2 + 4 + nws, dtype=_I32, device=dev)
     prob = empty(m, dtype=_F32, device=dev)
-    row_of_slot, slot_of_row, offsets, used, _ = buf.split_with_sizes((n, m, e, 1, nws))
     at = buf.data_ptr()
-    _check(L.bsgg_sort_tokens(n, num_experts, m_pad, p_ids, p_weights, at + 4 * (n + m), at, at + 4 * n, prob.data_ptr(),
-                              at + 4 * (n + m + e), at + 4 * (n + m + e + 1) if nws else None, _status_of(ids, status),
-                              handle), "bsgg_sort_tokens")
-    return TokenMap(offsets, row_of_slot.view(ids.shape), slot_of_row, prob, used)
+    _check(L.bsgg_sort_tokens(n, num_experts, m_pad, p_ids, p_weights, at + 4 * i1, at + 4 * m, at, prob.data_ptr(),
+                              at + 4 * i2, at + 4 * (i2 + 4) if nws else None, _status_of(ids, status), handle),
+           "bsgg_sort_tokens")
+    return TokenMap(buf[i1:i1 + e], buf[m:m + n].view(ids.shape), buf[:m], prob, buf[i2:i2 + 1])
 
 
 def _row_buffers(m_pad: int, hidden: int, row_format: str, device, empty):

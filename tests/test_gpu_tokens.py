@@ -163,6 +163,13 @@ def test_sort_tokens(T, L, k, masked):
         assert bsgg.operators_status() == 0
 
 
+@pytest.mark.parametrize("T,L,k", [(1, 7, 1), (1, 8, 3), (5, 3, 1), (3001, 5, 3)])
+def test_sort_outputs_are_aligned(T, L, k):
+    """Every output where the grouped GEMM accepts it: 16-byte aligned."""
+    tm = bsgg.sort_tokens(ids_of(T, L, k, 3, False).cuda(), L)
+    assert all(t.data_ptr() % 16 == 0 for t in tm)
+
+
 def test_sort_of_nothing():
     for ids in (torch.full((7, 3), -1, dtype=torch.int32), torch.empty(0, 3, dtype=torch.int32)):
         tm = bsgg.sort_tokens(ids.cuda(), 6)
