@@ -175,54 +175,66 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
   return static_cast<uint32_t>(e < 0 ? 0 : e);   // biased by 127; 2^-127 at the least
 }
 
-// Eight values over the scale of `code`, as packed codes: 2 words (FP8), 1 word
-// (FP4), 4 words (bf16 and f16, no scale).  UE8M0: times 2^-e, exact.  E4M3 scales: the
-// correctly rounded quotient, whose comparison with E2M1's thresholds is that
-// of the exact one (a value off a tie differs from it by more than a rounding).
+// Sixteen values over the scale of `code`, packed as the rows hold them: 4 words of
+// FP8, 2 of FP4, 8 of 16-bit values (no scale).  UE8M0: times 2^-e, exact.  E4M3
+// scales: the correctly rounded quotient, whose comparison with E2M1's thresholds is
+// that of the exact one (a value off a tie differs from it by more than a rounding).
+// A block with the NaN scale has zero codes.
+__host__ __device__ constexpr int rf_words(int f) { return rf_bits(f) / 2; }
 template <int FMT>
-__device__ __forceinline__ void quantize8(const float (&v)[8], uint32_t code, uint32_t (&out)[4]) {
+__device__ __forceinline__ void quantize16(const float (&v)[16], uint32_t code, uint32_t (&out)[rf_words(FMT)]) {
   if constexpr (!rf_scaled(FMT)) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) out[k] = pack2<FMT == BSGG_ROW_F16 ? OK_F16 : OK_BF16>(v[2 * k], v[2 * k + 1]);
+    for (int k = 0; k < 8; ++k) out[k] = pack2<FMT == BSGG_ROW_F16 ? OK_F16 : OK_BF16>(v[2 * k], v[2 * k + 1]);
   } else {
-    float q[8];
-    const bool nan_block = code == (FMT == BSGG_IN_NVFP4 ? 0x7Fu : 0xFFu);
+    float q[16];
     if (FMT == BSGG_IN_NVFP4) {
       const float s = e4m3_to_float(code);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = nan_block ? 0.0f : __fdiv_rn(v[k], s);
+      for (int k = 0; k < 16; ++k) q[k] = __fdiv_rn(v[k], s);
     } else {
       // 2^(127 - code): exponent field 254 - code, at code 254 the subnormal 2^-127
       const float r = code >= 254u ? __uint_as_float(0x400000u) : __uint_as_float((254u - code) << 23);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = nan_block ? 0.0f : v[k] * r;
+      for (int k = 0; k < 16; k += 2) {
+        const float2 f = __fmul2_rn(make_float2(v[k], v[k + 1]), make_float2(r, r));
+        q[k] = f.x;
+        q[k + 1] = f.y;
+      }
     }
-    if (FMT == BSGG_IN_MXFP8_E4M3) {
-      out[0] = cvt_e4m3x2(q[0], q[1]) | (cvt_e4m3x2(q[2], q[3]) << 16);
-      out[1] = cvt_e4m3x2(q[4], q[5]) | (cvt_e4m3x2(q[6], q[7]) << 16);
-    } else if (FMT == BSGG_IN_MXFP8_E5M2) {
-      out[0] = cvt_e5m2x2(q[0], q[1]) | (cvt_e5m2x2(q[2], q[3]) << 16);
-      out[1] = cvt_e5m2x2(q[4], q[5]) | (cvt_e5m2x2(q[6], q[7]) << 16);
-    } else {
-      out[0] = cvt_e2m1x2(q[0], q[1]) | (cvt_e2m1x2(q[2], q[3]) << 8) | (cvt_e2m1x2(q[4], q[5]) << 16) |
-               (cvt_e2m1x2(q[6], q[7]) << 24);
+    const bool nan_block = code == (FMT == BSGG_IN_NVFP4 ? 0x7Fu : 0xFFu);
+#pragma unroll
+    for (int k = 0; k < rf_words(FMT); ++k) {
+      if (FMT == BSGG_IN_MXFP8_E4M3)
+        out[k] = cvt_e4m3x2(q[4 * k], q[4 * k + 1]) | (cvt_e4m3x2(q[4 * k + 2], q[4 * k + 3]) << 16);
+      else if (FMT == BSGG_IN_MXFP8_E5M2)
+        out[k] = cvt_e5m2x2(q[4 * k], q[4 * k + 1]) | (cvt_e5m2x2(q[4 * k + 2], q[4 * k + 3]) << 16);
+      else
+        out[k] = cvt_e2m1x2(q[8 * k], q[8 * k + 1]) | (cvt_e2m1x2(q[8 * k + 2], q[8 * k + 3]) << 8) |
+                 (cvt_e2m1x2(q[8 * k + 4], q[8 * k + 5]) << 16) | (cvt_e2m1x2(q[8 * k + 6], q[8 * k + 7]) << 24);
+      if (nan_block) out[k] = 0u;
     }
   }
 }
 
-// Stores the packed codes of eight values at element i of a row buffer.
+// Stores them; without scales the second eight only if `both`.
 template <int FMT>
-__device__ __forceinline__ void store_codes8(void* base, int64_t i, const uint32_t (&c)[4]) {
-  uint8_t* p = static_cast<uint8_t*>(base) + i * rf_bits(FMT) / 8;
-  if (!rf_scaled(FMT)) *reinterpret_cast<uint4*>(p) = make_uint4(c[0], c[1], c[2], c[3]);
-  else if (rf_fp4(FMT)) *reinterpret_cast<uint32_t*>(p) = c[0];
-  else *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
+__device__ __forceinline__ void store_codes16(uint8_t* p, const uint32_t (&w)[rf_words(FMT)], bool both) {
+  if constexpr (rf_fp4(FMT)) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (!rf_scaled(FMT)) {
+      if (both) *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
 }
 
-__device__ __forceinline__ uint32_t max_abs_bits8(const float (&v)[8]) {
+// The bits of the largest magnitude (a NaN's are above an infinity's).
+__device__ __forceinline__ uint32_t max_abs_bits16(const float (&v)[16]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+  for (int k = 0; k < 16; ++k) m = max(m, __float_as_uint(v[k]) & 0x7FFFFFFFu);
   return m;
 }
 

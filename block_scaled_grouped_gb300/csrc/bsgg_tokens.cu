@@ -353,9 +353,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) 
 
 // ---------------------------------------------------------------- dispatch
 struct RowsParams {
-  int64_t tokens, hidden, m_pad, ld_token;
-  int topk;
-  int64_t kq;                       // scale atoms per 128 rows
+  int64_t tokens, m_pad, ld_token;
+  int hidden, topk;
+  int kq;                           // scale atoms per 128 rows
   const void* x;                    // x or dy
   const int32_t *row_of_slot, *slot_of_row;
   void* a;
@@ -378,30 +378,13 @@ constexpr int kRowThreads = 512, kMaxTopk = 32, kPadRows = 8;
 // in flight.
 constexpr int kRowValues = 16;
 
-template <int FMT>
-__device__ __forceinline__ void store_row_values(void* base, int64_t i, const float (&v)[kRowValues], uint32_t code,
-                                                 bool both) {
-  uint32_t lo[4], hi[4];
-  quantize8<FMT>(reinterpret_cast<const float(&)[8]>(v[0]), code, lo);
-  quantize8<FMT>(reinterpret_cast<const float(&)[8]>(v[8]), code, hi);
-  if constexpr (!rf_scaled(FMT)) {
-    store_codes8<FMT>(base, i, lo);
-    if (both) store_codes8<FMT>(base, i + 8, hi);
-  } else {
-    uint8_t* p = static_cast<uint8_t*>(base) + i * rf_bits(FMT) / 8;
-    if (rf_fp4(FMT)) *reinterpret_cast<uint2*>(p) = make_uint2(lo[0], hi[0]);
-    else *reinterpret_cast<uint4*>(p) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
-  }
-}
-
 // The scale code of this thread's block (shared by rf_vec / 16 lanes), and the
 // word of the four blocks it lies in, complete in every lane: their bytes are
 // neighbours in the scale factors' layout.
 template <int FMT>
 __device__ __forceinline__ uint32_t block_code(const float (&v)[16], bool in, uint32_t& word) {
   constexpr int kLanes = rf_vec(FMT) / 16;
-  uint32_t m = max(max_abs_bits8(reinterpret_cast<const float(&)[8]>(v[0])),
-                   max_abs_bits8(reinterpret_cast<const float(&)[8]>(v[8])));
+  uint32_t m = max_abs_bits16(v);
   if (kLanes == 2) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
   const uint32_t code = scale_code<FMT>(m);
   word = in ? code << (8 * ((threadIdx.x / kLanes) & 3)) : 0u;
@@ -423,32 +406,39 @@ __global__ void __launch_bounds__(kRowThreads, MODE == ROWS_DISPATCH ? 3 : 2) ro
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   let_next_kernel_start();
   wait_for_previous_kernel();
-  // columns in whole warps, up to the end of the last scale atom
-  const int64_t cols = rf_scaled(FMT) ? p.kq * 4 * rf_vec(FMT) : p.hidden;
-  const int64_t end = (cols + 32 * V - 1) / (32 * V) * (32 * V);
+  // columns in whole warps, up to the end of the last scale atom.  A column and a
+  // row's bytes fit 32 bits (hidden is at most 2^24); a row's offset does not
+  const int cols = rf_scaled(FMT) ? p.kq * 4 * rf_vec(FMT) : p.hidden;
+  const int end = (cols + 32 * V - 1) / (32 * V) * (32 * V);
+  const int row_bytes = p.hidden / 8 * rf_bits(FMT), atoms_bytes = p.kq * 512;   // of a row; of 128 rows' scales
+  uint8_t* const a = static_cast<uint8_t*>(p.a);
   if (blockIdx.x >= p.tokens) {
     const int64_t r0 = (static_cast<int64_t>(blockIdx.x) - p.tokens) * kPadRows;
     constexpr uint32_t one = rf_one(FMT) * 0x01010101u;
     for (int64_t r = r0; r < min(r0 + kPadRows, p.m_pad); ++r) {
       const int32_t s = p.slot_of_row[r];
       if (s >= 0 && s < p.tokens * p.topk) continue;
-      const int64_t bytes = p.hidden * rf_bits(FMT) / 8;   // a multiple of 16 (8 for FP4's 16-value tails)
-      uint8_t* row = static_cast<uint8_t*>(p.a) + r * bytes;
-      for (int64_t c = threadIdx.x * 16; c < bytes; c += blockDim.x * 16) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+      uint8_t* row = a + r * row_bytes;                  // row_bytes is a multiple of 16
+      for (int c = threadIdx.x * 16; c < row_bytes; c += blockDim.x * 16) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
       if (rf_scaled(FMT)) {
-        const int64_t kb = (p.hidden + rf_vec(FMT) - 1) / rf_vec(FMT);
-        for (int64_t q = threadIdx.x; q < p.kq; q += blockDim.x) {
-          const int64_t left = kb - 4 * q;               // blocks of this word inside hidden
-          *reinterpret_cast<uint32_t*>(p.sfa + sf_off(r, 4 * q, p.kq)) = left >= 4 ? one : one & ((1u << (8 * left)) - 1u);
+        const int kb = (p.hidden + rf_vec(FMT) - 1) / rf_vec(FMT);
+        uint8_t* sf = p.sfa + sf_off(r, 0, p.kq);
+        for (int q = threadIdx.x; q < p.kq; q += blockDim.x) {
+          const int left = kb - 4 * q;                   // blocks of this word inside hidden
+          *reinterpret_cast<uint32_t*>(sf + static_cast<int64_t>(q) * 512) = left >= 4 ? one : one & ((1u << (8 * left)) - 1u);
         }
       }
     }
     return;
   }
   const int64_t t = blockIdx.x;
-  const int32_t* rows = p.row_of_slot + t * p.topk;
+  // lane j holds choice j's row and weight, fetched beside the token's values
+  int32_t my_row = lane < p.topk ? p.row_of_slot[t * p.topk + lane] : -1;
+  if (my_row >= p.m_pad) my_row = -1;
+  const bool weighted = MODE == ROWS_GRAD && p.weights != nullptr;
+  const float my_weight = weighted && lane < p.topk ? p.weights[t * p.topk + lane] : 1.0f;
   const bool dot = MODE != ROWS_DISPATCH && p.dweights != nullptr;
-  for (int64_t c = threadIdx.x * V; c < end; c += static_cast<int64_t>(blockDim.x) * V) {
+  for (int c = threadIdx.x * V; c < end; c += blockDim.x * V) {
     const bool in = c < p.hidden, both = c + 8 < p.hidden;
     float v[V];
 #pragma unroll
@@ -461,13 +451,12 @@ __global__ void __launch_bounds__(kRowThreads, MODE == ROWS_DISPATCH ? 3 : 2) ro
     if (dot) {
       // D's rows stay packed until they are used: a batch of 16-bit rows in flight
       // costs half the registers of its values
-      const bool first = c == static_cast<int64_t>(threadIdx.x) * V;
+      const bool first = c == static_cast<int>(threadIdx.x) * V;
       for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
         int32_t r[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          r[b] = j0 + b < p.topk ? rows[j0 + b] : -1;
-          if (r[b] >= p.m_pad) r[b] = -1;
+          r[b] = j0 + b < p.topk ? __shfl_sync(0xFFFFFFFFu, my_row, j0 + b) : -1;
         }
         float acc[kBatch];
         if (p.d_kind == OK_F32) {
@@ -477,7 +466,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == ROWS_DISPATCH ? 3 : 2) ro
 #pragma unroll
             for (int h = 0; h < V; h += 8) {
               float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-              if ((h == 0 ? in : both) && r[b] >= 0) load8<OK_F32>(p.d, r[b] * p.hidden + c + h, w);
+              if ((h == 0 ? in : both) && r[b] >= 0) load8<OK_F32>(p.d, static_cast<int64_t>(r[b]) * p.hidden + c + h, w);
 #pragma unroll
               for (int k = 0; k < 8; ++k) acc[b] = fmaf(v[h + k], w[k], acc[b]);
             }
@@ -490,7 +479,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == ROWS_DISPATCH ? 3 : 2) ro
             for (int h = 0; h < V / 8; ++h) {
               u[b][h] = make_uint4(0, 0, 0, 0);
               if ((h == 0 ? in : both) && r[b] >= 0)
-                u[b][h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.d) + r[b] * p.hidden + c + 8 * h);
+                u[b][h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.d) + static_cast<int64_t>(r[b]) * p.hidden + c + 8 * h);
             }
 #pragma unroll
           for (int b = 0; b < kBatch; ++b) {
@@ -517,27 +506,31 @@ __global__ void __launch_bounds__(kRowThreads, MODE == ROWS_DISPATCH ? 3 : 2) ro
       }
     }
     if (MODE == ROWS_DOT) continue;
-    uint32_t code = 0, word = 0;
-    if constexpr (rf_scaled(FMT)) {
-      if (MODE == ROWS_DISPATCH || p.weights == nullptr) code = block_code<FMT>(v, in, word);
+    // quantized once for all rows; with weights, once per row
+    uint32_t word = 0, packed[rf_words(FMT)];
+    if (!weighted) {
+      uint32_t code = 0;
+      if constexpr (rf_scaled(FMT)) code = block_code<FMT>(v, in, word);
+      quantize16<FMT>(v, code, packed);
     }
+    uint8_t* const a_col = a + c / 8 * rf_bits(FMT);
+    uint8_t* const sf_col = rf_scaled(FMT) ? p.sfa + static_cast<int64_t>(c / (4 * rf_vec(FMT))) * 512 : nullptr;
+    const bool writes_word = rf_scaled(FMT) && lane % (4 * kLanes) == 0 && c < cols;
     for (int j = 0; j < p.topk; ++j) {
-      const int32_t r = rows[j];
-      if (r < 0 || r >= p.m_pad) continue;              // the same for the whole block
-      float w[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) w[k] = v[k];
-      if (MODE == ROWS_GRAD && p.weights != nullptr) {
-        const float f = p.weights[t * p.topk + j];
+      const int32_t r = __shfl_sync(0xFFFFFFFFu, my_row, j);
+      if (r < 0) continue;                              // the same for the whole block
+      if (weighted) {
+        const float f = __shfl_sync(0xFFFFFFFFu, my_weight, j);
+        float w[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) w[k] = v[k] * f;
+        uint32_t code = 0;
         if constexpr (rf_scaled(FMT)) code = block_code<FMT>(w, in, word);
+        quantize16<FMT>(w, code, packed);
       }
-      if constexpr (rf_scaled(FMT)) {
-        const int64_t kb = c / rf_vec(FMT);
-        if (lane % (4 * kLanes) == 0 && c < cols) *reinterpret_cast<uint32_t*>(p.sfa + sf_off(r, kb, p.kq)) = word;
-      }
-      if (in) store_row_values<FMT>(p.a, r * p.hidden + c, w, code, both);
+      if (writes_word)
+        *reinterpret_cast<uint32_t*>(sf_col + static_cast<int64_t>(r >> 7) * atoms_bytes + (r & 31) * 16 + ((r >> 5) & 3) * 4) = word;
+      if (in) store_codes16<FMT>(a_col + static_cast<int64_t>(r) * row_bytes, packed, both);
     }
   }
   if (dot) {
@@ -561,7 +554,8 @@ struct CombineParams {
 };
 
 // One token per block of x, a run of columns per block of y; four rows of D are
-// loaded before any is added, so that a thread has 64 bytes of them in flight.
+// loaded before any is added (64 bytes a thread in flight; eight rows are no
+// faster).
 // Rows that L2 cannot hold are marked as read once (8192 tokens, top-8, 7168 wide:
 // 206 us without the mark, 198 with it); smaller ones are where the product that
 // wrote them left them (128 tokens: 3.7 us without, 7.2 with).
@@ -669,11 +663,11 @@ int row_threads(int64_t cols, int values) {
 
 template <int MODE>
 bsgg_status launch_rows(const bsgg_tokens_desc* d, RowsParams p, cudaStream_t s) {
-  p.tokens = d->tokens; p.hidden = d->hidden; p.m_pad = d->m_pad; p.ld_token = d->ld_token; p.topk = d->topk;
+  p.tokens = d->tokens; p.hidden = static_cast<int>(d->hidden); p.m_pad = d->m_pad; p.ld_token = d->ld_token; p.topk = d->topk;
   return with_float(d->token_format, [&](auto kind) {
     return with_rows(d->row_format, [&](auto fmt) {
       constexpr int K = decltype(kind)::value, F = decltype(fmt)::value;
-      p.kq = rf_scaled(F) ? ceil_div(ceil_div(d->hidden, rf_vec(F)), 4) : 0;
+      p.kq = rf_scaled(F) ? static_cast<int>(ceil_div(ceil_div(d->hidden, rf_vec(F)), 4)) : 0;
       const int64_t grid = d->tokens + ceil_div(d->m_pad, kPadRows);
       const LaunchConfig c(dim3(static_cast<unsigned>(grid)), row_threads(d->hidden, kRowValues), 0, s);
       return launch_kernel(c, rows_kernel<K, F, MODE>, p);
@@ -856,7 +850,7 @@ bsgg_status bsgg_combine_backward(const bsgg_tokens_desc* d, const void* dy, con
   p.weights = weights; p.d = rows; p.d_kind = d->d_format; p.dweights = dweights;
   if (dd) return launch_rows<ROWS_GRAD>(d, p, s);
   if (d->tokens == 0) return BSGG_OK;
-  p.tokens = d->tokens; p.hidden = d->hidden; p.m_pad = d->m_pad; p.ld_token = d->ld_token; p.topk = d->topk;
+  p.tokens = d->tokens; p.hidden = static_cast<int>(d->hidden); p.m_pad = d->m_pad; p.ld_token = d->ld_token; p.topk = d->topk;
   return with_float(d->token_format, [&](auto kind) {
     constexpr int F = BSGG_IN_BF16;
     const LaunchConfig c(dim3(static_cast<unsigned>(d->tokens)), row_threads(d->hidden, kRowValues), 0, s);
