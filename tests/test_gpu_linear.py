@@ -137,6 +137,19 @@ def test_linear_of_no_rows():
     assert dw is kept and (kept == 1).all()
 
 
+def test_linear_offsets_past_32_bits():
+    """An output of 2.3e9 elements, its pre-activation and residual: rows at both ends."""
+    M, N, K = 147456, 15616, 72
+    g = gen(61)
+    x, w = torch.randn(M, K, generator=g).bfloat16(), (torch.randn(N, K, generator=g) / 8).bfloat16()
+    res = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    res[-3:] = 2.0
+    y, z = bsgg.linear(x.cuda(), w.cuda(), activation="relu", residual=res, want_z=True)
+    for rows in (slice(0, 5), slice(M // 2, M // 2 + 3), slice(M - 5, M)):
+        check_forward(x[rows], w, None, res[rows].cpu(), "relu", y[rows], z[rows], True)
+    assert bsgg.operators_status() == 0
+
+
 # ------------------------------------------------------------------ gradient
 BWD = [(1, 8, 8), (1, 256, 4096), (3, 40, 24), (17, 136, 264), (64, 64, 512), (100, 1000, 72), (129, 264, 520), (257, 512, 256),
        (300, 60 * 8, 1000), (1000, 128, 200)]

@@ -408,6 +408,43 @@ def test_maps_out_of_range_count_as_no_row():
     assert torch.equal(y, torch.stack([x[0], torch.zeros(H), x[2], x[3] + x[3]]))
 
 
+def test_offsets_past_32_bits():
+    """Rows whose elements lie past 2^31: written, padded and read where they are."""
+    T, H, k, m_pad = 6, 8448, 2, 262144                            # 2.2e9 elements
+    g = gen(51)
+    rs = torch.randint(m_pad - 100000, m_pad, (T, k), generator=g, dtype=torch.int32)
+    rs[0, 0], rs[1, 1], rs[2, 0] = m_pad - 1, -1, 3
+    assert len(set(rs.reshape(-1).tolist())) == T * k
+    sr = torch.full((m_pad,), -1, dtype=torch.int32)
+    for s, r in enumerate(rs.reshape(-1).tolist()):
+        if r >= 0:
+            sr[r] = s
+    x = torch.randn(T, H, generator=g).bfloat16()
+    w = torch.rand(T, k, generator=g)
+    a, sfa = bsgg.dispatch(x.cuda(), rs.cuda(), sr.cuda())
+    codes, sc = R.quantize(x.double(), "mxfp8_e4m3")
+    real = torch.nonzero(sr >= 0)[:, 0]
+    token = sr[real].long() // k
+    assert torch.equal(a[real.cuda()].cpu(), codes[token])
+    assert int((a != 0).any(1).sum()) == real.numel()               # every padding row is zero
+    kq = H // 128
+    full = sfa.view(m_pad // 128, kq, 32, 4, 4)
+    got = full[(real // 128).cuda(), :, (real % 32).cuda(), (real % 128 // 32).cuda()].reshape(real.numel(), -1).cpu()
+    assert torch.equal(got, sc[token])
+    assert int((sfa != 127).sum()) == int((got != 127).sum())        # and its scales one
+    del a, sfa
+    d = torch.zeros(m_pad, H, dtype=torch.bfloat16, device="cuda")
+    d[real.cuda()] = x[token].cuda()
+    y = bsgg.combine(d, rs.cuda(), weights=w.cuda(), out_format="f32").cpu().double()
+    total = torch.where(rs >= 0, w, torch.zeros(())).double().sum(1, keepdim=True)
+    assert ((y - total * x.double()).abs() <= 4 * 2.0 ** -24 * (total * x.double()).abs()).all()
+    dd, _, dw = bsgg.combine_backward(x.cuda(), d, rs.cuda(), sr.cuda(), weights=w.cuda())
+    ws = w.reshape(-1)[sr[real].long()][:, None]
+    assert torch.equal(dd[real.cuda()].cpu(), (x[token].float() * ws).bfloat16())
+    sq = (x.double() ** 2).sum(1, keepdim=True) * (rs >= 0)
+    assert ((dw.cpu().double() - sq).abs() <= sq * (H / 32 + 8) * 2.0 ** -24).all()
+
+
 def test_other_stream_and_graph():
     """The chain on a stream of its own, then captured in a graph and replayed on
     new values."""

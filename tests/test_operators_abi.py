@@ -89,7 +89,7 @@ def tokens_desc(**over):
 
 
 BAD_TOKENS = [dict(tokens=-1), dict(hidden=0), dict(hidden=60, ld_token=64), dict(m_pad=0), dict(m_pad=130), dict(ld_token=56),
-              dict(ld_token=68), dict(topk=0), dict(token_format=3), dict(tokens=2 ** 30, topk=4)]
+              dict(ld_token=68), dict(topk=0), dict(topk=33), dict(token_format=3), dict(tokens=2 ** 30, topk=4)]
 
 
 @pytest.mark.parametrize("over", BAD_TOKENS + [dict(row_format=7), dict(row_format=-1), dict(hidden=72, ld_token=72),
