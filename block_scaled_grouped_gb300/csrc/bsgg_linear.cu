@@ -210,13 +210,42 @@ bsgg_status launch_tile(const CUtensorMap& tp, const CUtensorMap& tq, const LinP
   const int64_t ctas = int64_t(p.p_tiles) * p.q_tiles * split;
   return ctas <= sms ? launch_tile_as<BN, true>(tp, tq, p, ctas, split, s) : launch_tile_as<BN, false>(tp, tq, p, ctas, split, s);
 }
+// Tiles [tile0, tile1), a cluster of `split` pairs each, or the resident pairs
+// walking them.
+template <int BN>
+bsgg_status launch_pairs(const CUtensorMap& tp, const CUtensorMap& tq, LinParams p, int64_t tile0, int64_t tile1, int split,
+                         const Device& dev, cudaStream_t s) {
+  p.tile0 = static_cast<int32_t>(tile0);
+  p.tile1 = static_cast<int32_t>(tile1);
+  const int64_t tiles = tile1 - tile0, resident = dev.pair_clusters[BN == 256 ? 0 : 1][0];
+  const int64_t units = split > 1 || tiles < resident ? tiles : resident;
+  const LaunchConfig c(dim3(static_cast<unsigned>(2 * split * units)), kLinThreads, LinPair<BN>::kSmem, s, 2 * split);
+  return launch_kernel(c, linear_pair_kernel<BN>, tp, tq, p, split);
+}
+
+// All tiles.  Where the last round of the pairs would be less than half full and
+// long, its tiles get a launch of their own, their reduction split over the idle
+// pairs: the gradient dx of 4096 x 14336 x 4096 has 256 tiles for 76 pairs, and takes
+// 273 us in 4 rounds of 224 blocks, 263 in 3 and a split remainder.  (8192 cubed, 36
+// tiles of 128 blocks left after 13 rounds, gains nothing: 12 us have to be in it.)
 template <int BN>
 bsgg_status launch_pair(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, const Device& dev,
                         cudaStream_t s) {
   const int64_t tiles = int64_t(p.p_tiles) * p.q_tiles, resident = dev.pair_clusters[BN == 256 ? 0 : 1][0];
-  const int64_t units = split > 1 || tiles < resident ? tiles : resident;
-  const LaunchConfig c(dim3(static_cast<unsigned>(2 * split * units)), kLinThreads, LinPair<BN>::kSmem, s, 2 * split);
-  return launch_kernel(c, linear_pair_kernel<BN>, tp, tq, p, split);
+  const int64_t rest = tiles % resident;
+  if (split > 1 || tiles < resident || rest == 0) return launch_pairs<BN>(tp, tq, p, 0, tiles, split, dev, s);
+  int best = 1;
+  double most = 12.0;                                  // microseconds saved, by cost_us's figures
+  for (int log2 = 1; log2 <= 2; ++log2) {
+    const int parts = 1 << log2;
+    if (rest > dev.pair_clusters[BN == 256 ? 0 : 1][log2] || p.k_blocks < 2 * parts) continue;
+    const double saved = p.k_blocks * (BN == 256 ? 0.33 : 0.21) * (1.0 - 1.0 / parts) - 8.0 -
+                         double(rest) * parts * 256 * BN * 4.0 / 4e6;
+    if (saved > most) { most = saved; best = parts; }
+  }
+  if (best == 1) return launch_pairs<BN>(tp, tq, p, 0, tiles, 1, dev, s);
+  const bsgg_status st = launch_pairs<BN>(tp, tq, p, 0, tiles - rest, 1, dev, s);
+  return st == BSGG_OK ? launch_pairs<BN>(tp, tq, p, tiles - rest, tiles, best, dev, s) : st;
 }
 
 // How a product is tiled: 256 x bn on CTA pairs, or 128 x bn on single CTAs, with

@@ -30,6 +30,7 @@ struct LinParams {
   int32_t cols, rows;         // i < cols, j < rows
   int32_t k_blocks;           // ceil(depth / 64)
   int32_t p_tiles, q_tiles;
+  int32_t tile0, tile1;       // the tiles of this launch (pairs)
   int32_t p_mn, q_mn;         // MN-major operands
   uint32_t idesc;
   int32_t act, in_kind, out_kind, bias_kind, residual_kind;
@@ -312,7 +313,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int part = static_cast<int>(rank >> 1);
   const bool leader = prank == 0;
   const int unit = blockIdx.x / (2 * split), units = gridDim.x / (2 * split);
-  const int tiles = p.p_tiles * p.q_tiles;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * part / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (part + 1) / split);
 
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       int st = 0;
       uint32_t phase = 0;
       bool ok = true, any = false;
-      for (int t = unit; t < tiles && ok; t += units) {
+      for (int t = p.tile0 + unit; t < p.tile1 && ok; t += units) {
         int tp, tq;
         lin_tile(t, p.p_tiles, p.q_tiles, tp, tq);
         const int p0 = tp * 256 + static_cast<int>(prank) * 128, q0 = tq * BN + static_cast<int>(prank) * (BN / 2);
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const uint64_t qd0 = p.q_mn ? sdesc_mnmajor_sw128(sbase + Ly::kOffQ) : sdesc_kmajor_sw128(sbase + Ly::kOffQ);
       // 16 reduction indices: 32 bytes inside a K-major row, 16 rows of 128 bytes MN-major
       const uint64_t pstep = p.p_mn ? 2048 >> 4 : 32 >> 4, qstep = p.q_mn ? 2048 >> 4 : 32 >> 4;
-      for (int t = unit; t < tiles && ok; t += units) {
+      for (int t = p.tile0 + unit; t < p.tile1 && ok; t += units) {
         if (!__all_sync(0xffffffffu, mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.wait_limit_ns))) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     constexpr int kHalf = BN / 2;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = unit; t < tiles; t += units) {
+    for (int t = p.tile0 + unit; t < p.tile1; t += units) {
       int tp, tq;
       lin_tile(t, p.p_tiles, p.q_tiles, tp, tq);
       const int i = tp * 256 + static_cast<int>(prank) * 128 + q * 32 + lane;
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (warp >= 2) {
       // the pairs' CTAs of this half of p
       int tp, tq;
-      lin_tile(unit, p.p_tiles, p.q_tiles, tp, tq);
+      lin_tile(p.tile0 + unit, p.p_tiles, p.q_tiles, tp, tq);
       lin_join<BN>(p, smem, split, part, 2, prank, tp * 256 + static_cast<int>(prank) * 128, tq * BN);
     }
   }

@@ -194,6 +194,16 @@ def test_linear_backward_sizes(M, N, K, act):
     assert bsgg.operators_status() == 0
 
 
+def test_linear_rounds_with_a_split_remainder():
+    """More tiles than pairs, the last round short and the reduction long, so that
+    the remainder's reduction is split."""
+    M, N, K = 2304, 2304, 8200                                      # 81 tiles of 256 x 256
+    x, w, b, r = problem(M, N, K, "bf16", 79)
+    y, z = bsgg.linear(x.cuda(), w.cuda(), bias=b.cuda(), residual=r.cuda(), activation="silu", want_z=True)
+    check_forward(x, w, b, r, "silu", y, z, True)
+    assert bsgg.operators_status() == 0
+
+
 def test_linear_backward_many_tiles():
     M, N, K = 2310, 2408, 2504
     x, w, _, z = problem(M, N, K, "bf16", 78)
