@@ -19,7 +19,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import BsggError, IN_FORMATS, _check, _stream, lib, sf_bytes
+from . import BsggError, IN_FORMATS, _check, _stream, lib
 
 ROW_FORMATS = {**IN_FORMATS, "f16": 6}
 ACTIVATIONS = {"none": 0, "relu": 1, "srelu": 2, "silu": 3, "gelu": 4}
@@ -253,17 +253,15 @@ def sort_tokens(ids, num_experts: int, m_pad: Optional[int] = None, weights=None
     handle = _handle(ids, stream)
     empty, dev = _empty_on(stream), ids.device
     m, e = max(m_pad, 0), max(num_experts, 0)
-    # one allocation for the integers, each part at a multiple of 16 bytes as the
-    # grouped GEMM wants them: rows, slots, offsets, rows_used, workspace
-    i1 = m + (n + 3) // 4 * 4
-    i2 = i1 + (e + 3) // 4 * 4
-    buf = empty(i2 + 4 + nws, dtype=_I32, device=dev)
+    # a tensor each (a view of a larger one costs the host as much as an allocation)
+    i32 = {"dtype": _I32, "device": dev}
+    offsets, used, row_of_slot, slot_of_row = empty(e, **i32), empty(1, **i32), empty(ids.shape, **i32), empty(m, **i32)
     prob = empty(m, dtype=_F32, device=dev)
-    at = buf.data_ptr()
-    _check(L.bsgg_sort_tokens(n, num_experts, m_pad, p_ids, p_weights, at + 4 * i1, at + 4 * m, at, prob.data_ptr(),
-                              at + 4 * i2, at + 4 * (i2 + 4) if nws else None, _status_of(ids, status), handle),
-           "bsgg_sort_tokens")
-    return TokenMap(buf[i1:i1 + e], buf[m:m + n].view(ids.shape), buf[:m], prob, buf[i2:i2 + 1])
+    ws = empty(nws, **i32) if nws else None
+    _check(L.bsgg_sort_tokens(n, num_experts, m_pad, p_ids, p_weights, offsets.data_ptr(), row_of_slot.data_ptr(),
+                              slot_of_row.data_ptr(), prob.data_ptr(), used.data_ptr(),
+                              ws.data_ptr() if nws else None, _status_of(ids, status), handle), "bsgg_sort_tokens")
+    return TokenMap(offsets, row_of_slot, slot_of_row, prob, used)
 
 
 def _row_buffers(m_pad: int, hidden: int, row_format: str, device, empty):
@@ -272,7 +270,9 @@ def _row_buffers(m_pad: int, hidden: int, row_format: str, device, empty):
         return empty((m_pad, hidden), dtype=_DTYPES[row_format], device=device), None
     v = 16 if row_format in ("nvfp4", "fp4_ue8m0_16") else 32
     a = empty((m_pad, hidden // 2 if row_format in _FP4 else hidden), dtype=_U8, device=device)
-    return a, empty(sf_bytes(m_pad, hidden, v), dtype=_U8, device=device)
+    # bsgg_sf_bytes(m_pad, hidden, v, 1), without the call
+    blocks = (hidden + v - 1) // v
+    return a, empty(((m_pad + 127) // 128) * ((blocks + 3) // 4) * 512, dtype=_U8, device=device)
 
 
 _FP4 = ("nvfp4", "fp4_ue8m0_16", "mxfp4")
