@@ -137,6 +137,26 @@ def test_linear_of_no_rows():
     assert dw is kept and (kept == 1).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 4096, 7168), (40, 2048, 7168), (100, 4096, 4160), (300, 4096, 4160), (600, 4096, 4160)])
+def test_linear_back_to_back(M, N, K):
+    """Launches that follow one another at once, each set up under the one before,
+    on operands that come from memory: every one's result."""
+    n = 6
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    xs = [torch.randn(M, K, generator=g, device="cuda").bfloat16() for _ in range(n)]
+    ws = [(torch.randn(N, K, generator=g, device="cuda") / math.sqrt(K)).bfloat16() for _ in range(n)]
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    flush.fill_(1)                                              # out of L2
+    ys = [bsgg.linear(xs[i % n], ws[i % n], out_format="f32")[0] for i in range(4 * n)]
+    assert bsgg.operators_status() == 0
+    for i in range(n):
+        want = xs[i].double() @ ws[i].double().t()
+        tol = R.product_error(K) * (xs[i].double().abs() @ ws[i].double().abs().t()) + R.rounding(want, torch.float32)
+        for y in ys[i::n]:
+            assert ((y.double() - want).abs() <= tol).all()
+
+
 def test_linear_offsets_past_32_bits():
     """An output of 2.3e9 elements, its pre-activation and residual: rows at both ends."""
     M, N, K = 147456, 15616, 72
