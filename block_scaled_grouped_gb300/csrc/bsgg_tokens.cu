@@ -575,13 +575,17 @@ struct CombineParams {
 
 // One token per block of x, a run of columns per block of y; four rows of D are
 // loaded before any is added (64 bytes a thread in flight; eight rows are no
-// faster).  8192 tokens, top-8, 7168 wide: 1.17 GB in 196 us, 6.0 TB/s, 88 % of the
+// faster).  8192 tokens, top-8, 7168 wide: 1.17 GB in 186 us, 6.3 TB/s, 93 % of the
 // measured copy rate, bound by memory.
 // Rows that L2 cannot hold are marked as read once (8192 tokens, top-8, 7168 wide:
 // 206 us without the mark, 198 with it); smaller ones are where the product that
 // wrote them left them (128 tokens: 3.7 us without, 7.2 with).
+// Small blocks, since a block's first load waits for its token's row numbers: 197 us
+// with 512 threads, 190 with 256, 186 with 128.
+constexpr int kCombineThreads = 128;
+
 template <int DK, int KIND, bool STREAM>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineParams p) {
   constexpr int kBatch = 4;
   let_next_kernel_start();
   wait_for_previous_kernel();
@@ -841,10 +845,11 @@ bsgg_status bsgg_combine(const bsgg_tokens_desc* d, const void* dd, const int32_
                      residual, y};
   return with_float(d->d_format, [&](auto dk) {
     return with_float(d->token_format, [&](auto kind) {
-      // few tokens: their columns over several blocks, down to two warps each, so
-      // that the chip has about four blocks an SM
+      // a token's columns over blocks of four warps; over blocks of two where there
+      // are so few that the chip would have less than four blocks an SM
       int threads = row_threads(d->hidden, 8);
-      while (threads > 64 && d->tokens * ceil_div(d->hidden, threads * 8) < 608) threads = (threads / 2 + 31) / 32 * 32;
+      if (threads > kCombineThreads) threads = kCombineThreads;
+      if (threads > 64 && d->tokens * ceil_div(d->hidden, threads * 8) < 608) threads = 64;
       const dim3 grid(static_cast<unsigned>(d->tokens), static_cast<unsigned>(ceil_div(d->hidden, threads * 8)));
       constexpr int D = decltype(dk)::value, K = decltype(kind)::value;
       const LaunchConfig c(grid, threads, 0, static_cast<cudaStream_t>(stream));
