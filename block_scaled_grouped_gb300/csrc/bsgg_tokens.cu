@@ -416,7 +416,7 @@ __device__ __forceinline__ uint32_t block_code(const float (&v)[16], bool in, ui
 //     thirds of the slots) and the loads' latency;
 //   128 x 7168, top-8 of 64: 59 MB, nearly all of it padding rows, 13 us.
 // The gradient of combine also takes the products <dy, D[row]>, with D's rows in
-// flight while dy is in registers: 4096 x 4096, top-2, 175 MB in 34 us, 5.1 TB/s,
+// flight while dy is in registers: 4096 x 4096, top-2, 175 MB in 30 us, 5.8 TB/s,
 // bound by the loads' latency (as two launches 42 us, reading dy twice).
 template <int KIND, int FMT, int MODE>
 __global__ void __launch_bounds__(kRowThreads, MODE == ROWS_DISPATCH ? 3 : 2) rows_kernel(RowsParams p) {
@@ -686,6 +686,15 @@ int row_threads(int64_t cols, int values) {
   return static_cast<int>(t < kRowThreads ? t : kRowThreads);
 }
 
+// Threads of a token's block of rows_kernel.  With the products <dy, D[row]> four
+// warps, in several passes: loads, reductions and barrier follow one another, and
+// many small blocks overlap them (4096 x 4096, top-2: 256 threads 34.6 us, 128 30.3, 64
+// 29.6).  Without them one pass (128 threads: 3 % slower).
+int rows_threads(int64_t hidden, bool dot) {
+  const int t = row_threads(hidden, kRowValues);
+  return dot && t > 128 ? 128 : t;
+}
+
 template <int MODE>
 bsgg_status launch_rows(const bsgg_tokens_desc* d, RowsParams p, cudaStream_t s) {
   p.tokens = d->tokens; p.hidden = static_cast<int>(d->hidden); p.m_pad = d->m_pad; p.ld_token = d->ld_token; p.topk = d->topk;
@@ -694,7 +703,7 @@ bsgg_status launch_rows(const bsgg_tokens_desc* d, RowsParams p, cudaStream_t s)
       constexpr int K = decltype(kind)::value, F = decltype(fmt)::value;
       p.kq = rf_scaled(F) ? static_cast<int>(ceil_div(ceil_div(d->hidden, rf_vec(F)), 4)) : 0;
       const int64_t grid = d->tokens + ceil_div(d->m_pad, kPadRows);
-      const LaunchConfig c(dim3(static_cast<unsigned>(grid)), row_threads(d->hidden, kRowValues), 0, s);
+      const LaunchConfig c(dim3(static_cast<unsigned>(grid)), rows_threads(d->hidden, p.dweights != nullptr), 0, s);
       return launch_kernel(c, rows_kernel<K, F, MODE>, p);
     });
   });
@@ -879,7 +888,7 @@ bsgg_status bsgg_combine_backward(const bsgg_tokens_desc* d, const void* dy, con
   p.tokens = d->tokens; p.hidden = static_cast<int>(d->hidden); p.m_pad = d->m_pad; p.ld_token = d->ld_token; p.topk = d->topk;
   return with_float(d->token_format, [&](auto kind) {
     constexpr int F = BSGG_IN_BF16;
-    const LaunchConfig c(dim3(static_cast<unsigned>(d->tokens)), row_threads(d->hidden, kRowValues), 0, s);
+    const LaunchConfig c(dim3(static_cast<unsigned>(d->tokens)), rows_threads(d->hidden, true), 0, s);
     return launch_kernel(c, rows_kernel<decltype(kind)::value, F, ROWS_DOT>, p);
   });
 }
