@@ -23,7 +23,7 @@ __device__ __forceinline__ float act_slope(float z) {
     const float e = __expf(fminf(-z, 87.0f)), s = __fdividef(1.0f, 1.0f + e);
     return s * fmaf(z, e * s, 1.0f);
   }
-  if (ACT == BSGG_ACT_GELU) return normcdff(z) + z * 0.398942280401432678f * __expf(-0.5f * z * z);
+  if (ACT == BSGG_ACT_GELU) return normal_cdf(z) + z * 0.398942280401432678f * __expf(-0.5f * z * z);
   return 1.0f;
 }
 

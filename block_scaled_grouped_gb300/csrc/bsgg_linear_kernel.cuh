@@ -43,17 +43,21 @@ struct LinParams {
   uint64_t wait_limit_ns;
 };
 
+// Phi(z) = erfc(-z / sqrt 2) / 2: unlike 1 + erf it keeps its relative accuracy in
+// the lower tail, up to the argument's rounding, z^2 units of 2^-24.  (normcdff, which
+// corrects that rounding too, is more instructions: 333 x 4104 -> 2049 with gelu
+// takes 20.4 us with it and 19.8 with this.)
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.707106781f * z); }
+
 // act(z).  silu = z / (1 + e^-z) with the hardware's exponential and quotient
 // (off by about 2 + 1.2 |z| units of 2^-23, as in the grouped GEMM's epilogues; a quarter of the
-// instructions of expf and an IEEE division); gelu = z Phi(z) with Phi from
-// normcdff, which keeps its relative accuracy in the lower tail where 1 + erf
-// cancels.
+// instructions of expf and an IEEE division); gelu = z Phi(z).
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if (ACT == BSGG_ACT_RELU) return z <= 0.0f ? 0.0f : z;               // a NaN stays
   if (ACT == BSGG_ACT_SRELU) return z <= 0.0f ? 0.0f : z * z;
   if (ACT == BSGG_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
-  if (ACT == BSGG_ACT_GELU) return z * normcdff(z);
+  if (ACT == BSGG_ACT_GELU) return z * normal_cdf(z);
   return z;
 }
 
