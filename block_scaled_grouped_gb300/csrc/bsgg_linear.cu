@@ -33,7 +33,7 @@ __device__ __forceinline__ float act_slope(float z) {
 // cluster's blocks, through distributed shared memory, in a fixed order.  Bound by
 // the loads' latency, so the rows are split no further than fills the chip twice
 // (what a block pays once, its joins above all, cost 4096 x 14336 in eight runs a
-// quarter of its time): 352 MB in 65 us, 5.4 TB/s; in eight runs 83.
+// quarter of its time): 352 MB in 63 us, 5.6 TB/s; in eight runs 83.
 constexpr int kDzThreads = 512, kDzSplit = 8, kDzRows = 3, kDzLanes = 8;
 
 template <int KIND, int ACT>

@@ -267,7 +267,7 @@ __device__ __forceinline__ void lin_load(uint32_t dst, const CUtensorMap* map, u
 // clusters of `split` pairs share a tile's reduction instead, one tile each.
 //   4096 x 14336 x 4096, bf16, bias, silu: 247 us, 1950 TFLOP/s, 103 % of the
 //     measured library product rate of a burst; 8192 cubed 592 us, 1858.  Bound by
-//     the tensor pipe (79 % of the elapsed cycles by counter) and by power: with
+//     the tensor pipe (80 % of the elapsed cycles by counter) and by power: with
 //     operands of zeros, at full clocks, the first takes 209 us.
 //   4096 x 14336 x 64: 45 us, bound by writing (117 MB).
 template <int BN>
