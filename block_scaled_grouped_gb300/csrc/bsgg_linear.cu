@@ -153,9 +153,13 @@ struct Device {
   int tile_clusters[3][2][4];     // [bn 32, 64, 128][shared, alone][split 1, 2, 4, 8]
 };
 
+// The kernel that sums in runs is launched like the other: its own shared-memory
+// limit is raised, and the other's residency holds for both (launch bounds and shared
+// memory are the same, and two blocks' accumulators fit an SM's tensor memory).
 template <typename K>
-bool prepare_kernel(K kern, int smem, int ctas, int clusters, int* resident) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+bool prepare_kernel(K kern, K with_runs, int smem, int ctas, int clusters, int* resident) {
+  for (const K k : {kern, with_runs})
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
   for (int i = 0; i < clusters; ++i) {
     const int cluster = ctas << i;
     const LaunchConfig c(dim3(static_cast<unsigned>(cluster)), kLinThreads, static_cast<size_t>(smem), nullptr, cluster);
@@ -175,8 +179,8 @@ bool prepare_kernel(K kern, int smem, int ctas, int clusters, int* resident) {
 }
 template <int BN>
 bool prepare_tile(int (*resident)[4]) {
-  return prepare_kernel(linear_tile_kernel<BN, false>, LinTile<BN, false>::kSmem, 1, 4, resident[0]) &&
-         prepare_kernel(linear_tile_kernel<BN, true>, LinTile<BN, true>::kSmem, 1, 4, resident[1]);
+  return prepare_kernel(linear_tile_kernel<BN, false, false>, linear_tile_kernel<BN, false, true>, LinTile<BN, false>::kSmem, 1, 4, resident[0]) &&
+         prepare_kernel(linear_tile_kernel<BN, true, false>, linear_tile_kernel<BN, true, true>, LinTile<BN, true>::kSmem, 1, 4, resident[1]);
 }
 
 // The current device's state, set up at its first call.
@@ -189,8 +193,8 @@ const Device* device_state() {
   Device& d = state[dev];
   if (!d.ok) {
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return nullptr;
-    if (!prepare_kernel(linear_pair_kernel<256>, LinPair<256>::kSmem, 2, 3, d.pair_clusters[0]) ||
-        !prepare_kernel(linear_pair_kernel<128>, LinPair<128>::kSmem, 2, 3, d.pair_clusters[1]) ||
+    if (!prepare_kernel(linear_pair_kernel<256, false>, linear_pair_kernel<256, true>, LinPair<256>::kSmem, 2, 3, d.pair_clusters[0]) ||
+        !prepare_kernel(linear_pair_kernel<128, false>, linear_pair_kernel<128, true>, LinPair<128>::kSmem, 2, 3, d.pair_clusters[1]) ||
         !prepare_tile<32>(d.tile_clusters[0]) || !prepare_tile<64>(d.tile_clusters[1]) ||
         !prepare_tile<128>(d.tile_clusters[2]))
       return nullptr;
@@ -199,11 +203,17 @@ const Device* device_state() {
   return &d;
 }
 
+// Whether a part of the reduction is summed in runs (see kLinRun).
+bool in_runs(const LinParams& p, int split) {
+  return ceil_div(p.k_blocks, split) > (p.out_kind == OK_F32 ? kLinRun : kLinWholeHalf);
+}
+
 template <int BN, bool ALONE>
 bsgg_status launch_tile_as(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int64_t ctas, int split,
                            cudaStream_t s) {
   const LaunchConfig c(dim3(static_cast<unsigned>(ctas)), kLinThreads, LinTile<BN, ALONE>::kSmem, s, split);
-  return launch_kernel(c, linear_tile_kernel<BN, ALONE>, tp, tq, p, split);
+  return launch_kernel(c, in_runs(p, split) ? linear_tile_kernel<BN, ALONE, true> : linear_tile_kernel<BN, ALONE, false>, tp,
+                       tq, p, split);
 }
 template <int BN>
 bsgg_status launch_tile(const CUtensorMap& tp, const CUtensorMap& tq, const LinParams& p, int split, int sms, cudaStream_t s) {
@@ -220,7 +230,7 @@ bsgg_status launch_pairs(const CUtensorMap& tp, const CUtensorMap& tq, LinParams
   const int64_t tiles = tile1 - tile0, resident = dev.pair_clusters[BN == 256 ? 0 : 1][0];
   const int64_t units = split > 1 || tiles < resident ? tiles : resident;
   const LaunchConfig c(dim3(static_cast<unsigned>(2 * split * units)), kLinThreads, LinPair<BN>::kSmem, s, 2 * split);
-  return launch_kernel(c, linear_pair_kernel<BN>, tp, tq, p, split);
+  return launch_kernel(c, in_runs(p, split) ? linear_pair_kernel<BN, true> : linear_pair_kernel<BN, false>, tp, tq, p, split);
 }
 
 // All tiles.  Where the last round of the pairs would be less than half full and

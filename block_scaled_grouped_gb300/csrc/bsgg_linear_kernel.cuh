@@ -26,6 +26,17 @@ constexpr int kLinMaxSplit = 8;                // CTAs (or with pairs, twice the
 constexpr int kLinChunk = 16;                 // output rows an epilogue warp finishes at a time
 constexpr int kLinThreads = 32 * (2 + kLinEpiWarps);
 
+// The tensor core cuts what an addition to the accumulator drops instead of rounding
+// it, so a long sum comes out small: by 1.05e-9 of it per element of the reduction,
+// measured from 512 to 28672 (normal operands; 1.7e-5 at 14336, where a rounded sum
+// in float32 is off by 2e-6).  Kernels with RUNS sum runs of kLinRun blocks apiece
+// (512 elements: 6.5e-7) in the two accumulators in turn; the epilogue's warps add
+// each to float32 registers, rounding, while the next is multiplied.  float32
+// outputs take them for every reduction over one run, 16-bit ones, whose own rounding
+// is 2e-4 or more, over kLinWholeHalf blocks (32768: 3.8e-5).
+constexpr int kLinRun = 8;
+constexpr int kLinWholeHalf = 512;
+
 struct LinParams {
   int32_t cols, rows;         // i < cols, j < rows
   int32_t k_blocks;           // ceil(depth / 64)
@@ -92,6 +103,40 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32"
+      " [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      :
+      : "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+
+// sum += the N columns at ta, and the sum back into them.
+template <int N>
+__device__ __forceinline__ void lin_add_run(uint32_t ta, float (&sum)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; c += kLinChunk) {
+    float v[kLinChunk];
+    tmem_ld16(ta + c, reinterpret_cast<uint32_t*>(v));
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < kLinChunk; ++k) sum[c + k] += v[k];
+  }
+}
+template <int N>
+__device__ __forceinline__ void lin_put_sum(uint32_t ta, const float (&sum)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; c += kLinChunk) {
+    uint32_t v[kLinChunk];
+#pragma unroll
+    for (int k = 0; k < kLinChunk; ++k) v[k] = __float_as_uint(sum[c + k]);
+    tmem_st16(ta + c, v);
+  }
+  tmem_wait_st();
 }
 
 // CH values of output column i, rows j0 .. j0 + CH - 1 (FULL: all of them exist).
@@ -301,7 +346,7 @@ __device__ __forceinline__ void lin_tile(int t, int p_tiles, int q_tiles, int& t
   tq = band * kBand + in % w;
 }
 
-template <int BN>
+template <int BN, bool RUNS>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ LinParams p, int split) {
@@ -327,6 +372,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int unit = blockIdx.x / (2 * split), units = gridDim.x / (2 * split);
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * part / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (part + 1) / split);
+  const int run = RUNS ? kLinRun : kb1 - kb0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(full_bar(s), 1); mbar_init(empty_bar(s), 1); }
@@ -393,31 +439,34 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       // 16 reduction indices: 32 bytes inside a K-major row, 16 rows of 128 bytes MN-major
       const uint64_t pstep = p.p_mn ? 2048 >> 4 : 32 >> 4, qstep = p.q_mn ? 2048 >> 4 : 32 >> 4;
       for (int t = p.tile0 + unit; t < p.tile1 && ok; t += units) {
-        if (!__all_sync(0xffffffffu, mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.wait_limit_ns))) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d = tmem + acc * BN;
-        for (int kb = kb0; kb < kb1; kb += Ly::kBlocks) {
-          if (!__all_sync(0xffffffffu, mbar_wait(full_bar(st), phase, abort_flag, p.wait_limit_ns))) { ok = false; break; }
+        for (int kr = kb0; kr < kb1; kr += run) {
+          if (!__all_sync(0xffffffffu, mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.wait_limit_ns))) { ok = false; break; }
           tc_fence_after();
-          const uint64_t pd = pd0 + static_cast<uint64_t>((st * Ly::kPBytes) >> 4);
-          const uint64_t qd = qd0 + static_cast<uint64_t>((st * Ly::kQBytes) >> 4);
-          const bool whole = Ly::kBlocks == 1 || kb + 1 < kb1;
-          if (elect_one()) {
+          const uint32_t d = tmem + acc * BN;
+          const int kend = min(kb1, kr + run);
+          for (int kb = kr; kb < kend; kb += Ly::kBlocks) {
+            if (!__all_sync(0xffffffffu, mbar_wait(full_bar(st), phase, abort_flag, p.wait_limit_ns))) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t pd = pd0 + static_cast<uint64_t>((st * Ly::kPBytes) >> 4);
+            const uint64_t qd = qd0 + static_cast<uint64_t>((st * Ly::kQBytes) >> 4);
+            const bool whole = Ly::kBlocks == 1 || kb + 1 < kb1;
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4 * Ly::kBlocks; ++kk) {
-              if (kk >= 4 && !whole) break;
-              tc_mma_bf16_pair(d, pd + (kk / 4) * (Ly::kPBlock >> 4) + (kk % 4) * pstep,
-                               qd + (kk / 4) * (Ly::kQBlock >> 4) + (kk % 4) * qstep, p.idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < 4 * Ly::kBlocks; ++kk) {
+                if (kk >= 4 && !whole) break;
+                tc_mma_bf16_pair(d, pd + (kk / 4) * (Ly::kPBlock >> 4) + (kk % 4) * pstep,
+                                 qd + (kk / 4) * (Ly::kQBlock >> 4) + (kk % 4) * qstep, p.idesc, (kb > kr || kk > 0) ? 1u : 0u);
+              }
+              tc_commit_pair(empty_bar(st), pair_mask);
             }
-            tc_commit_pair(empty_bar(st), pair_mask);
+            __syncwarp();
+            if (++st == S) { st = 0; phase ^= 1u; }
           }
+          if (!ok) break;
+          if (elect_one()) tc_commit_pair(accf_bar(acc), pair_mask);
           __syncwarp();
-          if (++st == S) { st = 0; phase ^= 1u; }
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
-        if (!ok) break;
-        if (elect_one()) tc_commit_pair(accf_bar(acc), pair_mask);
-        __syncwarp();
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (!ok && elect_one()) {
         if (p.status != nullptr) atomicOr(p.status, kStatusTimeout);
@@ -437,12 +486,32 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       lin_tile(t, p.p_tiles, p.q_tiles, tp, tq);
       const int i = tp * 256 + static_cast<int>(prank) * 128 + q * 32 + lane;
       const float bias = lin_bias(p, i);
-      if (!__all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag, p.wait_limit_ns))) {
+      const uint32_t ta0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kHalf;
+      bool got = __all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag, p.wait_limit_ns));
+      if (RUNS && got) {
+        float sum[kHalf];
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) sum[c] = 0.0f;
+#pragma unroll 1
+        for (int kr = kb0 + run;; kr += run) {
+          tc_fence_after();
+          lin_add_run(ta0 + acc * BN, sum);
+          if (kr >= kb1) break;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(acce_bar(acc), even));
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+          got = __all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag, p.wait_limit_ns));
+          if (!got) break;
+        }
+        if (got) lin_put_sum(ta0 + acc * BN, sum);
+      }
+      if (!got) {
         if (lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusTimeout);
         break;
       }
       tc_fence_after();
-      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + half * kHalf;
+      const uint32_t ta = ta0 + acc * BN;
 #pragma unroll 1
       for (int c = 0; c < kHalf; c += kLinChunk) {
         float v[kLinChunk];
@@ -500,27 +569,29 @@ struct LinTile {
   static constexpr int kStageBytes = kPBytes + kQBytes;
   static constexpr int kStages = (ALONE ? 220 : 110) * 1024 / kStageBytes;
   static constexpr int kHead = 1024;                       // barriers, holder, flag; the ring follows
-  static_assert(8 * (2 * kStages + 1) + 8 <= kHead, "barriers");
+  static_assert(8 * (2 * kStages + 5) + 8 <= kHead, "barriers");
   static_assert(kStages * kStageBytes >= 128 * BN * 4, "the partial tile reuses the stages");
   static constexpr int kSmem = kStages * kStageBytes + kHead + 1024;
 };
 
-template <int BN, bool ALONE>
+template <int BN, bool ALONE, bool RUNS>
 __global__ void __launch_bounds__(kLinThreads, ALONE ? 1 : 2)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ LinParams p, int split) {
   using Ly = LinTile<BN, ALONE>;
   constexpr int S = Ly::kStages;
-  constexpr uint32_t kCols = BN;                     // tensor-memory columns, a power of two >= 32
+  constexpr uint32_t kCols = RUNS ? 2 * BN : BN;     // tensor-memory columns, a power of two >= 32
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t bar0 = smem_u32(smem);
   const uint32_t ring = bar0 + Ly::kHead;                  // stages of P, then of Q
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
-  const uint32_t accf_bar = bar0 + 8u * (2 * S);
-  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + 8 * (2 * S + 1));
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 8 * (2 * S + 1) + 4);
+  auto accf_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
+  auto acce_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * S + 4);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + 8 * (2 * S + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 8 * (2 * S + 5) + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = blockIdx.x / split;
@@ -528,10 +599,12 @@ __global__ void __launch_bounds__(kLinThreads, ALONE ? 1 : 2)
   // this CTA's run of reduction blocks (the host gives every rank at least one)
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / split);
+  const int run = RUNS ? kLinRun : kb1 - kb0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(full_bar(s), 1); mbar_init(empty_bar(s), 1); }
-    mbar_init(accf_bar, 1);
+    for (int a = 0; a < 2; ++a) { mbar_init(accf_bar(a), 1); mbar_init(acce_bar(a), kLinEpiWarps); }
+    mbar_init(drain_bar, 1);
     *abort_flag = 0;
     mbar_fence_init();
     prefetch_tmap(&tmP);
@@ -580,32 +653,41 @@ __global__ void __launch_bounds__(kLinThreads, ALONE ? 1 : 2)
     const uint64_t pd0 = p.p_mn ? sdesc_mnmajor_sw128(ring) : sdesc_kmajor_sw128(ring);
     const uint64_t qd0 = p.q_mn ? sdesc_mnmajor_sw128(ring_q) : sdesc_kmajor_sw128(ring_q);
     const uint64_t pstep = p.p_mn ? 2048 >> 4 : 32 >> 4, qstep = p.q_mn ? 2048 >> 4 : 32 >> 4;
-    for (int kb = kb0; kb < kb1; kb += Ly::kBlocks) {
-      if (!__all_sync(0xffffffffu, mbar_wait(full_bar(st), phase, abort_flag, p.wait_limit_ns))) { ok = false; break; }
-      tc_fence_after();
-      const uint64_t pd = pd0 + static_cast<uint64_t>((st * Ly::kPBytes) >> 4);
-      const uint64_t qd = qd0 + static_cast<uint64_t>((st * Ly::kQBytes) >> 4);
-      const bool whole = Ly::kBlocks == 1 || kb + 1 < kb1;
-      if (elect_one()) {
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int kr = kb0; kr < kb1; kr += run) {
+      if (RUNS && !__all_sync(0xffffffffu, mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.wait_limit_ns))) { ok = false; break; }
+      if (RUNS) tc_fence_after();
+      const uint32_t d = tmem + acc * BN;
+      const int kend = min(kb1, kr + run);
+      for (int kb = kr; kb < kend; kb += Ly::kBlocks) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full_bar(st), phase, abort_flag, p.wait_limit_ns))) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t pd = pd0 + static_cast<uint64_t>((st * Ly::kPBytes) >> 4);
+        const uint64_t qd = qd0 + static_cast<uint64_t>((st * Ly::kQBytes) >> 4);
+        const bool whole = Ly::kBlocks == 1 || kb + 1 < kb1;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4 * Ly::kBlocks; ++kk) {
-          if (kk >= 4 && !whole) break;
-          tc_mma_bf16(tmem, pd + (kk / 4) * (Ly::kPBlock >> 4) + (kk % 4) * pstep,
-                      qd + (kk / 4) * (Ly::kQBlock >> 4) + (kk % 4) * qstep, p.idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 4 * Ly::kBlocks; ++kk) {
+            if (kk >= 4 && !whole) break;
+            tc_mma_bf16(d, pd + (kk / 4) * (Ly::kPBlock >> 4) + (kk % 4) * pstep,
+                        qd + (kk / 4) * (Ly::kQBlock >> 4) + (kk % 4) * qstep, p.idesc, (kb > kr || kk > 0) ? 1u : 0u);
+          }
+          tc_commit(empty_bar(st));
         }
-        tc_commit(empty_bar(st));
+        __syncwarp();
+        if (++st == S) { st = 0; phase ^= 1u; }
       }
+      if (!ok) break;
+      if (elect_one()) tc_commit(accf_bar(acc));
       __syncwarp();
-      if (++st == S) { st = 0; phase ^= 1u; }
+      if (RUNS && ++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
-    if (elect_one()) {
-      // also the drain when a wait ran out: every issued MMA has completed
-      tc_commit(accf_bar);
-      if (!ok) {
-        if (p.status != nullptr) atomicOr(p.status, kStatusTimeout);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(accf_bar, 0) && globaltimer_ns() - t0 < kDrainLimitNs) {}
-      }
+    if (!ok && elect_one()) {
+      if (p.status != nullptr) atomicOr(p.status, kStatusTimeout);
+      tc_commit(drain_bar);                         // every issued MMA has completed
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < kDrainLimitNs) {}
     }
   }
   __syncwarp();
@@ -614,12 +696,33 @@ __global__ void __launch_bounds__(kLinThreads, ALONE ? 1 : 2)
   const int i = tp * 128 + q * 32 + lane;
   if (warp >= 2) {
     const float bias = lin_bias(p, i);
-    const bool got = __all_sync(0xffffffffu, mbar_wait(accf_bar, 0, abort_flag, p.wait_limit_ns));
+    const uint32_t ta0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kHalf;
+    int acc = 0;
+    bool got = __all_sync(0xffffffffu, mbar_wait(accf_bar(0), 0, abort_flag, p.wait_limit_ns));
+    if (RUNS && got) {
+      uint32_t acc_phase = 0;
+      float sum[kHalf];
+#pragma unroll
+      for (int c = 0; c < kHalf; ++c) sum[c] = 0.0f;
+#pragma unroll 1
+      for (int kr = kb0 + run;; kr += run) {
+        tc_fence_after();
+        lin_add_run(ta0 + acc * BN, sum);
+        if (kr >= kb1) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acce_bar(acc));
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        got = __all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag, p.wait_limit_ns));
+        if (!got) break;
+      }
+      if (got) lin_put_sum(ta0 + acc * BN, sum);
+    }
     if (!got) {
       if (lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusTimeout);
     } else {
       tc_fence_after();
-      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kHalf;
+      const uint32_t ta = ta0 + acc * BN;
 #pragma unroll 1
       for (int c = 0; c < kHalf; c += kLinChunk) {
         float v[kLinChunk];
