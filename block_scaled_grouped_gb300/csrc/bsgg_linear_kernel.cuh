@@ -209,6 +209,18 @@ __device__ __forceinline__ float lin_bias(const LinParams& p, int i) {
   return p.bias != nullptr && i < p.cols ? load1(p.bias_kind, p.bias, i) : 0.0f;
 }
 
+// The residual of `rows` output rows from j0 and of the warp's 32 columns from i0, into L2.
+__device__ __forceinline__ void lin_fetch_residual(const LinParams& p, int i0, int j0, int rows) {
+  if (p.residual == nullptr || i0 >= p.cols) return;
+  const int size = p.residual_kind == OK_F32 ? 4 : 2, last = min(i0 + 31, p.cols - 1);
+  const int end = min(j0 + rows, p.rows);
+  for (int j = j0 + (threadIdx.x & 31); j < end; j += 32) {
+    const char* row = static_cast<const char*>(p.residual) + static_cast<int64_t>(j) * p.ld_residual * size;
+    prefetch_l2(row + static_cast<int64_t>(i0) * size);
+    prefetch_l2(row + static_cast<int64_t>(last) * size);       // a row that is off the lines has a second one
+  }
+}
+
 // Partial tiles of a split reduction: CH output rows from row r of the tile, this
 // lane's column, 128 columns per row; the stages' memory takes them, once every
 // load has landed and every MMA completed.
@@ -479,6 +491,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, half = (warp - 2) >> 2;         // lane quadrant, half of the columns
     constexpr int kHalf = BN / 2;
+    // With runs only one of them hides what finishing a tile takes, and the products
+    // wait for the rest: the tile is finished in half the steps, its residual fetched
+    // beforehand.
+    constexpr int kFinish = RUNS ? 2 * kLinChunk : kLinChunk;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = p.tile0 + unit; t < p.tile1; t += units) {
@@ -487,6 +503,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int i = tp * 256 + static_cast<int>(prank) * 128 + q * 32 + lane;
       const float bias = lin_bias(p, i);
       const uint32_t ta0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kHalf;
+      if (RUNS && split == 1) lin_fetch_residual(p, i - lane, tq * BN + half * kHalf, kHalf);
       bool got = __all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag, p.wait_limit_ns));
       if (RUNS && got) {
         float sum[kHalf];
@@ -513,17 +530,18 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tc_fence_after();
       const uint32_t ta = ta0 + acc * BN;
 #pragma unroll 1
-      for (int c = 0; c < kHalf; c += kLinChunk) {
-        float v[kLinChunk];
-        tmem_ld16(ta + c, reinterpret_cast<uint32_t*>(v));
+      for (int c = 0; c < kHalf; c += kFinish) {
+        float v[kFinish];
+#pragma unroll
+        for (int k = 0; k < kFinish; k += 16) tmem_ld16(ta + c + k, reinterpret_cast<uint32_t*>(v) + k);
         tmem_wait_ld();
-        if (c == kHalf - kLinChunk) {
+        if (c == kHalf - kFinish) {
           // every column is in registers or stored: hand the accumulator back
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(acce_bar(acc), even));
         }
-        if (split == 1) lin_finish<kLinChunk>(p, v, i, tq * BN + half * kHalf + c, bias);
+        if (split == 1) lin_finish<kFinish>(p, v, i, tq * BN + half * kHalf + c, bias);
         else lin_put_part(smem, v, half * kHalf + c, q * 32 + lane);
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
