@@ -166,9 +166,10 @@ __device__ __forceinline__ void lin_act(float (&v)[CH]) {
   for (int c = 0; c < CH; ++c) v[c] = act_value<ACT>(v[c]);
 }
 template <int CH, bool FULL>
-__device__ __forceinline__ void lin_finish_rows(const LinParams& p, float (&v)[CH], int i, int j0, int nj, float bias) {
+__device__ __forceinline__ void lin_finish_rows(const LinParams& p, float (&v)[CH], int i, int j0, int nj, float bias,
+                                                bool residual) {
   float r[CH];
-  if (p.residual != nullptr) {
+  if (residual) {
     const int64_t at = static_cast<int64_t>(j0) * p.ld_residual + i;
     if (p.residual_kind == OK_BF16) lin_load_rows<OK_BF16, CH, FULL>(p.residual, at, p.ld_residual, nj, r);
     else if (p.residual_kind == OK_F16) lin_load_rows<OK_F16, CH, FULL>(p.residual, at, p.ld_residual, nj, r);
@@ -189,7 +190,7 @@ __device__ __forceinline__ void lin_finish_rows(const LinParams& p, float (&v)[C
     case BSGG_ACT_SILU: lin_act<BSGG_ACT_SILU>(v); break;
     case BSGG_ACT_GELU: lin_act<BSGG_ACT_GELU>(v); break;
   }
-  if (p.residual != nullptr) {
+  if (residual) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) v[c] += r[c];
   }
@@ -199,11 +200,11 @@ __device__ __forceinline__ void lin_finish_rows(const LinParams& p, float (&v)[C
   else lin_store_rows<OK_F32, CH, FULL>(p.out, at, p.ld_out, nj, v);
 }
 template <int CH>
-__device__ __forceinline__ void lin_finish(const LinParams& p, float (&v)[CH], int i, int j0, float bias) {
+__device__ __forceinline__ void lin_finish(const LinParams& p, float (&v)[CH], int i, int j0, float bias, bool residual) {
   const int nj = p.rows - j0;
   if (i >= p.cols || nj <= 0) return;
-  if (nj >= CH) lin_finish_rows<CH, true>(p, v, i, j0, nj, bias);
-  else lin_finish_rows<CH, false>(p, v, i, j0, nj, bias);
+  if (nj >= CH) lin_finish_rows<CH, true>(p, v, i, j0, nj, bias, residual);
+  else lin_finish_rows<CH, false>(p, v, i, j0, nj, bias, residual);
 }
 __device__ __forceinline__ float lin_bias(const LinParams& p, int i) {
   return p.bias != nullptr && i < p.cols ? load1(p.bias_kind, p.bias, i) : 0.0f;
@@ -272,7 +273,7 @@ __device__ __forceinline__ void lin_finish_part(const LinParams& p, const uint8_
     float v[RUN];
 #pragma unroll
     for (int k = 0; k < RUN; ++k) v[k] = at[k * 128];
-    lin_finish<RUN>(p, v, i, j0 + r, bias);
+    lin_finish<RUN>(p, v, i, j0 + r, bias, p.residual != nullptr);
   }
 }
 // Only the epilogue's warps come here.
@@ -492,9 +493,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int q = warp & 3, half = (warp - 2) >> 2;         // lane quadrant, half of the columns
     constexpr int kHalf = BN / 2;
     // With runs only one of them hides what finishing a tile takes, and the products
-    // wait for the rest: the tile is finished in half the steps, its residual fetched
-    // beforehand.
+    // wait for the rest: the tile is finished in half the steps, its residual is fetched
+    // at its start, and one in float32 that no function of the sum precedes (a gradient
+    // being added to) is summed in while the last run is multiplied.
     constexpr int kFinish = RUNS ? 2 * kLinChunk : kLinChunk;
+    const bool add_early = RUNS && split == 1 && p.residual != nullptr && p.residual_kind == OK_F32 &&
+                           p.act == BSGG_ACT_NONE && p.z == nullptr && kb1 - kb0 > run;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = p.tile0 + unit; t < p.tile1; t += units) {
@@ -503,6 +507,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int i = tp * 256 + static_cast<int>(prank) * 128 + q * 32 + lane;
       const float bias = lin_bias(p, i);
       const uint32_t ta0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kHalf;
+      const bool early = add_early && tq * BN + (half + 1) * kHalf <= p.rows;     // every row exists
       if (RUNS && split == 1) lin_fetch_residual(p, i - lane, tq * BN + half * kHalf, kHalf);
       bool got = __all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag, p.wait_limit_ns));
       if (RUNS && got) {
@@ -518,6 +523,20 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(acce_bar(acc), even));
           if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+          if (early && kr + run >= kb1) {
+            // a lane past the last column reads that one: its sums go nowhere
+            const float* from = static_cast<const float*>(p.residual) +
+                                static_cast<int64_t>(tq * BN + half * kHalf) * p.ld_residual + min(i, p.cols - 1);
+#pragma unroll
+            for (int c = 0; c < kHalf; c += kLinChunk) {
+              float r[kLinChunk];
+#pragma unroll
+              for (int k = 0; k < kLinChunk; ++k) { r[k] = *from; from += p.ld_residual; }
+#pragma unroll
+              for (int k = 0; k < kLinChunk; ++k) sum[c + k] += r[k];
+              asm volatile("" : "+l"(from) :: "memory");   // sixteen addresses at a time, not all of them
+            }
+          }
           got = __all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag, p.wait_limit_ns));
           if (!got) break;
         }
@@ -541,7 +560,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(acce_bar(acc), even));
         }
-        if (split == 1) lin_finish<kFinish>(p, v, i, tq * BN + half * kHalf + c, bias);
+        if (split == 1) lin_finish<kFinish>(p, v, i, tq * BN + half * kHalf + c, bias, p.residual != nullptr && !early);
         else lin_put_part(smem, v, half * kHalf + c, q * 32 + lane);
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
@@ -747,7 +766,7 @@ __global__ void __launch_bounds__(kLinThreads, ALONE ? 1 : 2)
         tmem_ld16(ta + c, reinterpret_cast<uint32_t*>(v));
         tmem_wait_ld();
         if (split == 1) {
-          lin_finish<kLinChunk>(p, v, i, tq * BN + half * kHalf + c, bias);
+          lin_finish<kLinChunk>(p, v, i, tq * BN + half * kHalf + c, bias, p.residual != nullptr);
         } else {
           lin_put_part(smem + Ly::kHead, v, half * kHalf + c, q * 32 + lane);
         }
