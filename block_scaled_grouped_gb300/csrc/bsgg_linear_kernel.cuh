@@ -34,6 +34,8 @@ constexpr int kLinThreads = 32 * (2 + kLinEpiWarps);
 // each to float32 registers, rounding, while the next is multiplied.  float32
 // outputs take them for every reduction over one run, 16-bit ones, whose own rounding
 // is 2e-4 or more, over kLinWholeHalf blocks (32768: 3.8e-5).
+// 2048 x 14336 -> 4096 into float32: 139 us, 136 in one sum; added to a float32 dw,
+// where the finish reads as much as it writes, 4096 x 14336 x 4096 336 us against 280.
 constexpr int kLinRun = 8;
 constexpr int kLinWholeHalf = 512;
 
