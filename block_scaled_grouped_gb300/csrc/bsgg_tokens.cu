@@ -178,7 +178,7 @@ constexpr int64_t kSortClusterSlots = 2 * kSortThreads * kSortMaxCluster;
 
 struct SortParams {
   int64_t slots, m_pad;
-  int L, steps, blocks;          // 32-slot steps per warp (at most 2047: counts are 16 bits wide)
+  int L, steps, blocks;          // steps: of 32 slots, per warp
   const int32_t* ids;
   const float* weights;
   int32_t *offsets, *row_of_slot, *slot_of_row, *rows_used;
@@ -189,15 +189,17 @@ struct SortParams {
 
 // Shared memory of L experts: total and before (this block's first rank) of each,
 // first row of each and one past the last; a scratch word per warp and expert
-// group; the warps' counts, then their ranks inside the block.
+// group; the warps' counts, then their ranks inside the block (a block's slots may
+// all name one expert and are 512 a step: 16 bits would hold the ranks of 128 steps,
+// 9.7 million slots in all).
 struct SortShared {
   int32_t *mine, *total, *before, *first, *scan;
-  uint16_t* warp_count;
+  int32_t* warp_count;
   __device__ SortShared(int32_t* sm, int L)
       : mine(sm), total(sm + L), before(sm + 2 * L), first(sm + 3 * L), scan(sm + 4 * L + 1),
-        warp_count(reinterpret_cast<uint16_t*>(sm + 4 * L + 1 + kSortWarps)) {}
+        warp_count(sm + 4 * L + 1 + kSortWarps) {}
 };
-constexpr size_t sort_shared_bytes(int L) { return 4 * (4 * size_t(L) + 1 + kSortWarps) + 2 * size_t(L) * kSortWarps; }
+constexpr size_t sort_shared_bytes(int L) { return 4 * (4 * size_t(L) + 1 + kSortWarps + size_t(L) * kSortWarps); }
 
 __device__ __forceinline__ int sort_id(const SortParams& p, int64_t s) {
   const int32_t e = s < p.slots ? p.ids[s] : -1;
@@ -213,7 +215,7 @@ __device__ __forceinline__ void sort_count(const SortParams& p, const SortShared
   for (int k = 0; k < p.steps; ++k) {
     const int e = sort_id(p, s0 + 32 * k + lane);
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) sh.warp_count[warp * p.L + e] += static_cast<uint16_t>(__popc(same));
+    if (e >= 0 && lane == __ffs(same) - 1) sh.warp_count[warp * p.L + e] += __popc(same);
     __syncwarp();
   }
   __syncthreads();
@@ -222,7 +224,7 @@ __device__ __forceinline__ void sort_count(const SortParams& p, const SortShared
 #pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
       const int32_t c = sh.warp_count[w * p.L + e];
-      sh.warp_count[w * p.L + e] = static_cast<uint16_t>(run);
+      sh.warp_count[w * p.L + e] = run;
       run += c;
     }
     sh.mine[e] = run;
@@ -267,7 +269,7 @@ __device__ __forceinline__ void sort_place(const SortParams& p, const SortShared
       if (r >= m_pad) r = -1;
     }
     __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) sh.warp_count[warp * p.L + e] += static_cast<uint16_t>(__popc(same));
+    if (e >= 0 && lane == __ffs(same) - 1) sh.warp_count[warp * p.L + e] += __popc(same);
     __syncwarp();
     if (s < p.slots) {
       p.row_of_slot[s] = r;
@@ -801,9 +803,9 @@ bsgg_status bsgg_sort_tokens(int64_t slots, int32_t num_experts, int64_t m_pad, 
     if (!aligned_to(q, 4)) return BSGG_ERR_INVALID_ARG;
   SortParams p = {};
   p.slots = slots; p.m_pad = m_pad; p.L = num_experts;
+  if (slots > (int64_t(1) << 30)) return BSGG_ERR_UNSUPPORTED;   // the padded sizes' sum stays below 2^31
   int64_t blocks, steps;
   sort_shape(slots, &blocks, &steps);
-  if (steps > 2047) return BSGG_ERR_UNSUPPORTED;             // 16-bit counts of a warp's run: 155 million slots
   p.steps = static_cast<int>(steps);
   p.blocks = static_cast<int>(blocks);
   const bool one_cluster = slots <= kSortClusterSlots;
@@ -811,7 +813,7 @@ bsgg_status bsgg_sort_tokens(int64_t slots, int32_t num_experts, int64_t m_pad, 
   p.ids = ids; p.weights = weights; p.offsets = padded_offsets; p.row_of_slot = row_of_slot; p.slot_of_row = slot_of_row;
   p.rows_used = rows_used; p.prob = prob; p.counts = static_cast<int32_t*>(workspace); p.status = status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t smem = sort_shared_bytes(p.L);                // 49 KB at the most: 1024 experts
+  const size_t smem = sort_shared_bytes(p.L);                // 82 KB at the most: 1024 experts
   if (one_cluster) {
     if (!sort_allowed(sort_cluster_kernel, smem)) return BSGG_ERR_CUDA;
     const LaunchConfig c(dim3(static_cast<unsigned>(p.blocks)), kSortThreads, smem, s, p.blocks);

@@ -504,6 +504,7 @@ BSGG_API bsgg_status bsgg_route_backward(const bsgg_route_desc* desc, const void
  *                                 (NULL: not wanted; weights NULL = ones)
  *   rows_used (1)                 the padded sizes' sum, the least m_pad that
  *                                 holds them (NULL: not wanted)
+ * slots: 2^30 at most (BSGG_ERR_UNSUPPORTED beyond).
  * m_pad: a positive multiple of 128; bsgg_sort_rows gives one that always
  * suffices.  Where it is too small the slots that do not fit get no row, offsets
  * are cut at m_pad, and BSGG_ERR_BAD_OFFSETS is reported in `status`.
