@@ -38,15 +38,17 @@ constexpr int kDzThreads = 512, kDzSplit = 8, kDzRows = 3, kDzLanes = 8;
 
 template <int KIND, int ACT>
 __global__ void __launch_bounds__(kDzThreads, 2) dz_kernel(int64_t m, int64_t n, int64_t ld_dy, int64_t ldz, int64_t ld_dz,
-                                                        const void* dy, const void* z, void* dz, float* dbias) {
+                                                        const void* dy, const void* z, void* dz, float* dbias, int runs) {
   constexpr int kCols = kDzLanes * 8, kWarps = kDzThreads / 32, kStep = kDzThreads / kDzLanes;
   __shared__ float part[kWarps][kCols];
   __shared__ float block_sum[kCols];
   let_next_kernel_start();
   wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t j = static_cast<int64_t>(blockIdx.y) * kCols + (threadIdx.x % kDzLanes) * 8;
-  const int64_t i0 = m * blockIdx.x / gridDim.x, i1 = m * (blockIdx.x + 1) / gridDim.x;
+  // the runs of a group of columns are neighbours along x, which alone holds 2^24 / 64 groups
+  const int group = static_cast<int>(blockIdx.x) / runs, run = static_cast<int>(blockIdx.x) - group * runs;
+  const int64_t j = static_cast<int64_t>(group) * kCols + (threadIdx.x % kDzLanes) * 8;
+  const int64_t i0 = m * run / runs, i1 = m * (run + 1) / runs;
   // n need not be a multiple of 8, the pitches are: whole pieces are read, the
   // padding columns' sums are not used and their dz is written as the pitch allows
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -93,14 +95,14 @@ __global__ void __launch_bounds__(kDzThreads, 2) dz_kernel(int64_t m, int64_t n,
     for (int w = 0; w < kWarps; ++w) s += part[w][threadIdx.x];
     block_sum[threadIdx.x] = s;
   }
-  if (gridDim.x > 1) cluster_sync(); else __syncthreads();
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + threadIdx.x;
-  if (blockIdx.x == 0 && threadIdx.x < kCols && c < n) {
+  if (runs > 1) cluster_sync(); else __syncthreads();
+  const int64_t c = static_cast<int64_t>(group) * kCols + threadIdx.x;
+  if (run == 0 && threadIdx.x < kCols && c < n) {
     float s = 0.0f;
-    for (unsigned r = 0; r < gridDim.x; ++r) s += ld_shared_cluster(mapa_shared(smem_u32(&block_sum[threadIdx.x]), r));
+    for (int r = 0; r < runs; ++r) s += ld_shared_cluster(mapa_shared(smem_u32(&block_sum[threadIdx.x]), r));
     dbias[c] = s;
   }
-  if (gridDim.x > 1) cluster_sync();          // the sums stay until block 0 has read them
+  if (runs > 1) cluster_sync();               // the sums stay until block 0 has read them
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -346,9 +348,9 @@ bsgg_status launch_dz_one(const bsgg_linear_bwd_desc* d, const void* dy, const v
   int64_t runs = 2 * sms / groups;
   runs = runs < 1 ? 1 : runs > kDzSplit ? kDzSplit : runs;
   if (runs > steps) runs = steps;
-  const LaunchConfig c(dim3(static_cast<unsigned>(runs), static_cast<unsigned>(groups)), kDzThreads, 0, s,
+  const LaunchConfig c(dim3(static_cast<unsigned>(runs * groups)), kDzThreads, 0, s, static_cast<int>(runs));
+  return launch_kernel(c, dz_kernel<KIND, ACT>, d->m, d->n, d->ld_dy, d->ldz, d->ld_dz, dy, z, dz, dbias,
                        static_cast<int>(runs));
-  return launch_kernel(c, dz_kernel<KIND, ACT>, d->m, d->n, d->ld_dy, d->ldz, d->ld_dz, dy, z, dz, dbias);
 }
 template <int KIND>
 bsgg_status launch_dz_kind(const bsgg_linear_bwd_desc* d, const void* dy, const void* z, void* dz, float* dbias,
