@@ -109,7 +109,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+    if (succeeded(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q)) &&
         q == cudaDriverEntryPointSuccess)
       return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     return nullptr;
@@ -161,18 +161,17 @@ struct Device {
 template <typename K>
 bool prepare_kernel(K kern, K with_runs, int smem, int ctas, int clusters, int* resident) {
   for (const K k : {kern, with_runs})
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+    if (!succeeded(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return false;
   for (int i = 0; i < clusters; ++i) {
     const int cluster = ctas << i;
     const LaunchConfig c(dim3(static_cast<unsigned>(cluster)), kLinThreads, static_cast<size_t>(smem), nullptr, cluster);
     if (cluster == 1) {
       int blocks = 0, sms = 0, dev = 0;
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kern, kLinThreads, static_cast<size_t>(smem)) != cudaSuccess ||
-          cudaGetDevice(&dev) != cudaSuccess ||
-          cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      if (!succeeded(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kern, kLinThreads, static_cast<size_t>(smem))) ||
+          !succeeded(cudaGetDevice(&dev)) || !succeeded(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
         return false;
       resident[i] = blocks * sms;
-    } else if (cudaOccupancyMaxActiveClusters(&resident[i], kern, &c.cfg) != cudaSuccess) {
+    } else if (!succeeded(cudaOccupancyMaxActiveClusters(&resident[i], kern, &c.cfg))) {
       return false;
     }
     if (resident[i] < 1) return false;
@@ -190,11 +189,11 @@ const Device* device_state() {
   static Device state[64];
   static std::mutex mu;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  if (!succeeded(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return nullptr;
   std::lock_guard<std::mutex> lk(mu);
   Device& d = state[dev];
   if (!d.ok) {
-    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return nullptr;
+    if (!succeeded(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev))) return nullptr;
     if (!prepare_kernel(linear_pair_kernel<256, false>, linear_pair_kernel<256, true>, LinPair<256>::kSmem, 2, 3, d.pair_clusters[0]) ||
         !prepare_kernel(linear_pair_kernel<128, false>, linear_pair_kernel<128, true>, LinPair<128>::kSmem, 2, 3, d.pair_clusters[1]) ||
         !prepare_tile<32>(d.tile_clusters[0]) || !prepare_tile<64>(d.tile_clusters[1]) ||
@@ -426,9 +425,9 @@ bsgg_status bsgg_linear_backward(const bsgg_linear_bwd_desc* d, const void* dy, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->m == 0) {
     // empty sums
-    if (dbias && cudaMemsetAsync(dbias, 0, sizeof(float) * d->n, s) != cudaSuccess) return BSGG_ERR_CUDA;
+    if (dbias && !succeeded(cudaMemsetAsync(dbias, 0, sizeof(float) * d->n, s))) return BSGG_ERR_CUDA;
     const size_t es = float_bytes(d->dw_format);
-    if (dw && !d->accumulate_dw && cudaMemset2DAsync(dw, es * d->ld_dw, 0, es * d->k, d->n, s) != cudaSuccess)
+    if (dw && !d->accumulate_dw && !succeeded(cudaMemset2DAsync(dw, es * d->ld_dw, 0, es * d->k, d->n, s)))
       return BSGG_ERR_CUDA;
     return BSGG_OK;
   }
@@ -458,8 +457,8 @@ bsgg_status bsgg_query_status_word(uint32_t* status, void* stream) {
   if (!status) return BSGG_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t w = 0;
-  if (cudaMemcpyAsync(&w, status, sizeof(w), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaMemsetAsync(status, 0, sizeof(w), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+  if (!succeeded(cudaMemcpyAsync(&w, status, sizeof(w), cudaMemcpyDeviceToHost, s)) ||
+      !succeeded(cudaMemsetAsync(status, 0, sizeof(w), s)) || !succeeded(cudaStreamSynchronize(s)))
     return BSGG_ERR_CUDA;
   if (w & kStatusTimeout) return BSGG_ERR_DEVICE_TIMEOUT;
   if (w & kStatusBadOffsets) return BSGG_ERR_BAD_OFFSETS;

@@ -40,9 +40,16 @@ struct LaunchConfig {
   }
   LaunchConfig(const LaunchConfig&) = delete;
 };
+// Whether a call of the runtime succeeded.  The runtime keeps an error until it is
+// read; one left there would be reported by the next launch that asks for it, as the
+// grouped GEMM's do.
+inline bool succeeded(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e == cudaSuccess;
+}
 template <typename... P, typename... A>
 bsgg_status launch_kernel(const LaunchConfig& c, void (*kern)(P...), A... args) {
-  return cudaLaunchKernelEx(&c.cfg, kern, P(args)...) == cudaSuccess ? BSGG_OK : BSGG_ERR_CUDA;
+  return succeeded(cudaLaunchKernelEx(&c.cfg, kern, P(args)...)) ? BSGG_OK : BSGG_ERR_CUDA;
 }
 
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

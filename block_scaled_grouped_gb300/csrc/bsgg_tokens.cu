@@ -731,7 +731,7 @@ void sort_shape(int64_t slots, int64_t* blocks, int64_t* steps) {
 template <typename K>
 bool sort_allowed(K kern, size_t smem) {
   return smem <= 48 * 1024 ||
-         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess;
+         succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
 }
 
 }  // namespace
