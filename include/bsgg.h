@@ -593,7 +593,7 @@ BSGG_API bsgg_status bsgg_linear(const bsgg_linear_desc* desc, const void* x, co
  *   dx = dz W,   dw = dz^T x  (accumulate_dw = 1: dw += dz^T x, read and
  * rounded once).  dz is kept in in_format (its rounding enters dx and dw; dbias
  * sums the unrounded values in 32 bits) in the caller's buffer of m rows of pitch
- * ld_dz, whose columns up to a multiple of 8 are written; without an activation dz is dy itself, z and dz are NULL and nothing is
+ * ld_dz; without an activation dz is dy itself, z and dz are NULL and nothing is
  * rounded.  dx, dw and dbias (float) may each be NULL: not wanted.  dy, z, dz, x
  * and w: 16-byte aligned bases, pitches multiples of 8.  The gradient of the
  * residual is dy. */
