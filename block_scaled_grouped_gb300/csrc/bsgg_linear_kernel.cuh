@@ -62,14 +62,18 @@ struct LinParams {
 // takes 20.4 us with it and 19.8 with this.)
 __device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.707106781f * z); }
 
-// act(z).  silu = z / (1 + e^-z) with the hardware's exponential and quotient
-// (off by about 2 + 1.2 |z| units of 2^-23, as in the grouped GEMM's epilogues; a quarter of the
-// instructions of expf and an IEEE division); gelu = z Phi(z).
+// act(z).  silu = z / (1 + e^-z), below 0 as z e^z / (1 + e^z), so that the divisor
+// stays between 1 and 2 (the hardware's quotient is 0 from a divisor of 2^126, z = -87.3,
+// on), with the hardware's exponential and quotient (off by up to 5 + 1.2 |z| units of
+// 2^-23; a quarter of the instructions of expf and an IEEE division); gelu = z Phi(z).
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if (ACT == BSGG_ACT_RELU) return z <= 0.0f ? 0.0f : z;               // a NaN stays
   if (ACT == BSGG_ACT_SRELU) return z <= 0.0f ? 0.0f : z * z;
-  if (ACT == BSGG_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
+  if (ACT == BSGG_ACT_SILU) {
+    const float e = __expf(-fabsf(z));
+    return __fdividef(z >= 0.0f ? z : z * e, 1.0f + e);
+  }
   if (ACT == BSGG_ACT_GELU) return z * normal_cdf(z);
   return z;
 }
