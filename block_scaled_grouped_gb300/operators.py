@@ -145,9 +145,12 @@ def _empty_on(stream):
     return empty
 
 
-def _handle(t, stream):
-    """The stream's handle; t's device has to be the current one."""
+def _handle(stream, t, *others):
+    """The stream's handle; the tensors (None: absent) have to be on the current device."""
     dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise ValueError(f"tensors on {t.device} and {o.device}: one device expected")
     if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on cuda:{dev}, but cuda:{torch._C._cuda_getDevice()} is the current device")
     if stream is None:
@@ -191,7 +194,7 @@ def route(logits, topk: int, normalize: bool = True, ids=None, weights=None, str
     T, L = logits.shape
     k = int(topk)
     desc = RouteDesc(T, ld, L, k, _format(logits, "logits"), 1 if normalize else 0)
-    handle = _handle(logits, stream)
+    handle = _handle(stream, logits, ids, weights)
     if ids is None or weights is None:
         empty, dev = _empty_on(stream), logits.device
         if ids is None:
@@ -214,7 +217,7 @@ def route_backward(logits, ids, weights, dweights, normalize: bool = True, row_o
     n = ids.numel()
     rows = 0 if row_of_slot is None else dweights.numel()
     desc = RouteDesc(T, ld, L, ids.shape[1], _format(logits, "logits"), 1 if normalize else 0)
-    handle = _handle(logits, stream)
+    handle = _handle(stream, logits, ids, weights, dweights, row_of_slot, dlogits)
     if dlogits is None:
         # the logits' pitch, so that one desc serves both
         dlogits = _empty_on(stream)((T, ld), dtype=logits.dtype, device=logits.device)
@@ -250,7 +253,7 @@ def sort_tokens(ids, num_experts: int, m_pad: Optional[int] = None, weights=None
         m_pad = sort_rows(n, num_experts)
     L = lib()
     nws = L.bsgg_sort_workspace_bytes(n, num_experts) // 4
-    handle = _handle(ids, stream)
+    handle = _handle(stream, ids, weights, status)
     empty, dev = _empty_on(stream), ids.device
     m, e = max(m_pad, 0), max(num_experts, 0)
     # a tensor each (a view of a larger one costs the host as much as an allocation)
@@ -310,7 +313,7 @@ def dispatch(x, row_of_slot, slot_of_row, in_format: str = "mxfp8_e4m3", stream=
     m_pad = slot_of_row.numel()
     p_slots = _flat(slot_of_row, "slot_of_row", m_pad, _I32)
     desc = TokensDesc(T, H, m_pad, ld, 0, k, _format(x, "x"), _row_format(in_format), 0)
-    handle = _handle(x, stream)
+    handle = _handle(stream, x, row_of_slot, slot_of_row)
     a, sfa = _row_buffers(m_pad, H, in_format, x.device, _empty_on(stream))
     _check(lib().bsgg_dispatch(byref(desc), x.data_ptr(), p_rows, p_slots, a.data_ptr(),
                                sfa.data_ptr() if sfa is not None else None, handle), "bsgg_dispatch")
@@ -327,7 +330,7 @@ def combine(d, row_of_slot, weights=None, residual=None, out_format: Optional[st
     k, p_rows = _slots_of(row_of_slot, T)
     dt = _dtype(out_format) if out_format is not None else residual.dtype if residual is not None else d.dtype
     ldr = _matrix(residual, "residual", T, H, dt) if residual is not None else 0
-    handle = _handle(d, stream)
+    handle = _handle(stream, d, row_of_slot, weights, residual, out)
     if out is None:
         y, ldy = _empty_on(stream)((T, H), dtype=dt, device=d.device), H
     else:
@@ -352,7 +355,7 @@ def combine_backward(dy, d, row_of_slot, slot_of_row, weights=None, out_format: 
         _rows_matrix(d, m_pad, H)
         p_d, fd = d.data_ptr(), _format(d, "d")
     desc = TokensDesc(T, H, m_pad, ld, 0, k, _format(dy, "dy"), _row_format(out_format), fd)
-    handle = _handle(dy, stream)
+    handle = _handle(stream, dy, d if want_dweights else None, row_of_slot, slot_of_row, weights)
     empty, dev = _empty_on(stream), dy.device
     dd, sfd = _row_buffers(m_pad, H, out_format, dev, empty)
     dw = empty((T, k), dtype=_F32, device=dev) if want_dweights else None
@@ -395,7 +398,7 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, want_z: boo
     if residual is not None:
         p_res, ldr = residual.data_ptr(), _matrix(residual, "residual", m, n, xt)
     dt = xt if out_format is None else _dtype(out_format)
-    handle = _handle(x, stream)
+    handle = _handle(stream, x, w, bias, residual, out, status)
     empty = _empty_on(stream)
     if out is None:
         y, ldy = empty((m, n), dtype=dt, device=x.device), n
@@ -423,7 +426,7 @@ def linear_backward(dy, x, w, z=None, activation: str = "none", want_dx: bool = 
     k = x.shape[1]
     ldw = _matrix(w, "w", n, k, t)
     act = _activation(activation)
-    handle = _handle(dy, stream)
+    handle = _handle(stream, dy, x, w, z if act else None, dw if want_dw else None, status)
     empty, dev = _empty_on(stream), dy.device
     dz = dx = dbias = p_z = None
     ldz = ld_dz = ld_dx = ld_dw = fx = fw = 0
