@@ -14,6 +14,7 @@ dimension is contiguous; a row pitch is taken from their strides.
 from __future__ import annotations
 
 import ctypes
+import threading
 from ctypes import byref
 from typing import NamedTuple, Optional
 
@@ -159,6 +160,7 @@ def _handle(stream, t, *others):
 
 
 _status_words = {}
+_status_lock = threading.Lock()
 
 
 def _status_of(t, status):
@@ -169,9 +171,13 @@ def _status_of(t, status):
     dev = t.get_device()
     w = _status_words.get(dev)
     if w is None:
-        w = torch.zeros(1, dtype=_I32, device=t.device)
-        torch.cuda.synchronize(t.device)
-        w = _status_words[dev] = (w, w.data_ptr())
+        # one word per device for good: kernels hold its address
+        with _status_lock:
+            w = _status_words.get(dev)
+            if w is None:
+                word = torch.zeros(1, dtype=_I32, device=t.device)
+                torch.cuda.synchronize(t.device)
+                w = _status_words[dev] = (word, word.data_ptr())
     return w[1]
 
 
