@@ -183,11 +183,13 @@ def _status_of(t, status):
 
 def operators_status(stream=None, status=None) -> int:
     """Synchronize and read/clear the status word of sort_tokens, linear and
-    linear_backward on the current device (0 = ok)."""
+    linear_backward on the current device (0 = ok).  The word that calls without one
+    share is read after all the device's work; a given `status` after `stream`'s."""
     if status is None:
         w = _status_words.get(torch.cuda.current_device())
         if w is None:                        # nothing has run here
             return 0
+        torch.cuda.synchronize()             # any stream's kernels may report to it
         status = w[0]
     return int(lib().bsgg_query_status_word(status.data_ptr(), _stream(stream)))
 
