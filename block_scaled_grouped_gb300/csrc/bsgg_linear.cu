@@ -121,6 +121,12 @@ __global__ void __launch_bounds__(kDzThreads, 2) dz_kernel(int64_t m, int64_t n,
   if (runs > 1) cluster_sync();               // the sums stay until block 0 has read them
 }
 
+__global__ void clear_bits_kernel(uint32_t* word, uint32_t bits) {
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  atomicAnd(word, ~bits);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* p = nullptr;
@@ -473,9 +479,13 @@ bsgg_status bsgg_query_status_word(uint32_t* status, void* stream) {
   if (!status) return BSGG_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t w = 0;
-  if (!succeeded(cudaMemcpyAsync(&w, status, sizeof(w), cudaMemcpyDeviceToHost, s)) ||
-      !succeeded(cudaMemsetAsync(status, 0, sizeof(w), s)) || !succeeded(cudaStreamSynchronize(s)))
+  if (!succeeded(cudaMemcpyAsync(&w, status, sizeof(w), cudaMemcpyDeviceToHost, s)) || !succeeded(cudaStreamSynchronize(s)))
     return BSGG_ERR_CUDA;
+  if (w != 0) {
+    // the bits that were read, no others: another stream's kernel may have set one since
+    const LaunchConfig c(dim3(1), 1, 0, s);
+    if (launch_kernel(c, clear_bits_kernel, status, w) != BSGG_OK || !succeeded(cudaStreamSynchronize(s))) return BSGG_ERR_CUDA;
+  }
   if (w & kStatusTimeout) return BSGG_ERR_DEVICE_TIMEOUT;
   if (w & kStatusBadOffsets) return BSGG_ERR_BAD_OFFSETS;
   return w == 0 ? BSGG_OK : BSGG_ERR_CUDA;

@@ -611,10 +611,11 @@ BSGG_API bsgg_status bsgg_linear_backward(const bsgg_linear_bwd_desc* desc, cons
                                           const void* w, const void* z, void* dz, void* dx, void* dw,
                                           float* dbias, uint32_t* status, void* stream);
 
-/* Synchronize `stream`, then read and clear a status word that the operators
- * above were given: BSGG_OK, BSGG_ERR_BAD_OFFSETS (m_pad too small for the
- * sort), BSGG_ERR_DEVICE_TIMEOUT (a wait of bsgg_linear ran out; its outputs are
- * incomplete), or BSGG_ERR_CUDA. */
+/* Synchronize `stream`, then read a status word that the operators above were
+ * given and clear what was read (a report that a kernel on another stream makes
+ * meanwhile stays for the next call): BSGG_OK, BSGG_ERR_BAD_OFFSETS (m_pad too
+ * small for the sort), BSGG_ERR_DEVICE_TIMEOUT (a wait of bsgg_linear ran out; its
+ * outputs are incomplete), or BSGG_ERR_CUDA. */
 BSGG_API bsgg_status bsgg_query_status_word(uint32_t* status, void* stream);
 
 #ifdef __cplusplus
