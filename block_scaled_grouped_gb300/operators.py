@@ -350,9 +350,10 @@ def combine(d, row_of_slot, weights=None, residual=None, out_format: Optional[st
 
 
 def combine_backward(dy, d, row_of_slot, slot_of_row, weights=None, out_format: str = "bf16", want_dweights: bool = True,
-                     stream=None):
+                     stream=None, want_dd: bool = True):
     """Gradient of combine: (dd, sfd, dweights); dd (m_pad, hidden) in the row
-    format out_format with its scale factors sfd (None for bf16 and f16)."""
+    format out_format with its scale factors sfd (None for bf16 and f16).  dd and
+    dweights are None where not wanted."""
     ld = _matrix(dy, "dy")
     T, H = dy.shape
     k, p_rows = _slots_of(row_of_slot, T)
@@ -365,11 +366,10 @@ def combine_backward(dy, d, row_of_slot, slot_of_row, weights=None, out_format: 
     desc = TokensDesc(T, H, m_pad, ld, 0, k, _format(dy, "dy"), _row_format(out_format), fd)
     handle = _handle(stream, dy, d if want_dweights else None, row_of_slot, slot_of_row, weights)
     empty, dev = _empty_on(stream), dy.device
-    dd, sfd = _row_buffers(m_pad, H, out_format, dev, empty)
+    dd, sfd = _row_buffers(m_pad, H, out_format, dev, empty) if want_dd else (None, None)
     dw = empty((T, k), dtype=_F32, device=dev) if want_dweights else None
-    _check(lib().bsgg_combine_backward(byref(desc), dy.data_ptr(), p_d, p_rows, p_slots, p_weights, dd.data_ptr(),
-                                       sfd.data_ptr() if sfd is not None else None,
-                                       dw.data_ptr() if dw is not None else None, handle), "bsgg_combine_backward")
+    _check(lib().bsgg_combine_backward(byref(desc), dy.data_ptr(), p_d, p_rows, p_slots, p_weights,
+                                       *(v.data_ptr() if v is not None else None for v in (dd, sfd, dw)), handle), "bsgg_combine_backward")
     return dd, sfd, dw
 
 
