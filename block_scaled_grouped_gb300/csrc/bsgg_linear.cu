@@ -430,7 +430,8 @@ bsgg_status bsgg_linear_backward(const bsgg_linear_bwd_desc* d, const void* dy, 
   if (!d || d->m < 0 || d->m > (int64_t(1) << 24) || !good_extent(d->n) || !good_extent(d->k)) return BSGG_ERR_INVALID_ARG;
   if (!is_half_format(d->in_format) || !good_act(d->activation) || (d->accumulate_dw != 0 && d->accumulate_dw != 1))
     return BSGG_ERR_INVALID_ARG;
-  if ((dx && !is_float_format(d->dx_format)) || (dw && !is_float_format(d->dw_format)) || (!dx && !dw && !dbias))
+  if ((dx && !is_float_format(d->dx_format)) || (dw && !is_float_format(d->dw_format)) ||
+      (!dx && !dw && !dbias && d->m > 0))                    // no rows: an empty dx may be NULL
     return BSGG_ERR_INVALID_ARG;
   const bool has_act = d->activation != BSGG_ACT_NONE;
   if (has_act ? (d->m > 0 && (!z || !dz)) : (z || dz)) return BSGG_ERR_INVALID_ARG;

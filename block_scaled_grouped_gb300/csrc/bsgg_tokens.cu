@@ -874,7 +874,7 @@ bsgg_status bsgg_combine_backward(const bsgg_tokens_desc* d, const void* dy, con
                                   void* sfd, float* dweights, void* stream) {
   const bsgg_status st = check_tokens(d, dd != nullptr, dweights != nullptr);
   if (st != BSGG_OK) return st;
-  if (!dd && !dweights) return BSGG_ERR_INVALID_ARG;
+  if (!dd && !dweights) return d->tokens == 0 ? BSGG_OK : BSGG_ERR_INVALID_ARG;   // no tokens: an empty dweights may be NULL
   if (d->tokens > 0 && (!dy || !row_of_slot || (dweights && !rows))) return BSGG_ERR_INVALID_ARG;
   if (dd ? (!slot_of_row || (rf_scaled(d->row_format) ? !sfd : sfd != nullptr)) : sfd != nullptr)
     return BSGG_ERR_INVALID_ARG;
