@@ -14,7 +14,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // act'(z).  silu: s (1 + z (1 - s)) with e = e^-z, s = 1 / (1 + e), 1 - s = e s: no
 // cancellation, one exponential and one reciprocal (the argument is held below 87,
-// where s is 1e-38, so that e s stays a number); gelu: Phi(z) + z phi(z).
+// where s is 1e-38, so that e s stays a number: below z = -87 the slope, which falls
+// under 1e-36 there, stays near -2e-36; with e^-|z| it would follow it to 0, and this
+// pass take 64 us for 62); gelu: Phi(z) + z phi(z).
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == BSGG_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
@@ -27,13 +29,16 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.0f;
 }
 
-// dz = dy act'(z) and dbias.  A block owns 64 columns (a lane eight of them, so
+// dz = dy act'(z) and dbias.  dz is rounded to the operands' 16 bits, which is what the
+// products take (dx and dw come out 2.3e-3 off in norm where a dz in 32 bits would leave
+// their own rounding's 1.7e-3; into float32 about 1e-3 of it remains); dbias sums the
+// values before that.  A block owns 64 columns (a lane eight of them, so
 // that a warp reads four 128-byte pieces of rows at a time) and one of the
 // cluster's runs of rows; its sums join through shared memory and, between the
 // cluster's blocks, through distributed shared memory, in a fixed order.  Bound by
 // the loads' latency, so the rows are split no further than fills the chip twice
 // (what a block pays once, its joins above all, cost 4096 x 14336 in eight runs a
-// quarter of its time): 352 MB in 63 us, 5.6 TB/s; in eight runs 83.
+// quarter of its time): 352 MB in 62 us, 5.7 TB/s; in eight runs 83.
 constexpr int kDzThreads = 512, kDzSplit = 8, kDzRows = 3, kDzLanes = 8;
 
 template <int KIND, int ACT>

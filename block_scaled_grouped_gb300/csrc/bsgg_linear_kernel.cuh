@@ -329,11 +329,12 @@ __device__ __forceinline__ void lin_load(uint32_t dst, const CUtensorMap* map, u
 // is what shared memory and L2 can feed; single CTAs of 128 x 128 need twice that
 // (2048 x 4096 x 4096: 60 us against 45).  Where there are too few tiles for the SMs,
 // clusters of `split` pairs share a tile's reduction instead, one tile each.
-//   4096 x 14336 x 4096, bf16, bias, silu: 247 us, 1950 TFLOP/s, 103 % of the
-//     measured library product rate of a burst; 8192 cubed 592 us, 1858.  Bound by
-//     the tensor pipe (80 % of the elapsed cycles by counter) and by power: with
-//     operands of zeros, at full clocks, the first takes 209 us.
-//   4096 x 14336 x 64: 45 us, bound by writing (117 MB).
+//   4096 x 14336 x 4096, bf16, bias, silu, z kept: 249 us, 1930 TFLOP/s (the library's
+//     product of the shape alone: 229); 8192 cubed 592 us, 1858.  Bound by the tensor
+//     pipe (80 % of the elapsed cycles by counter) and by power: with operands of
+//     zeros, at full clocks, the first takes 209 us.
+//   4096 x 14336 x 64: 44 us for 117 MB written, 2.7 TB/s: bound by the epilogue, whose
+//     lanes store 2 bytes at a time (a plain fill of as much takes 30 us).
 template <int BN>
 struct LinPair {
   // 64-blocks of the reduction per stage.  Handing a stage over costs its threads

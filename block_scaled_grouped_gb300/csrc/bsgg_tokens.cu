@@ -33,8 +33,9 @@ constexpr int kRouteWarps = 4;
 // keys): the largest key, then the lowest index that has it.  The weights need no
 // second pass: the first choice is the maximum, and every lane sees each chosen
 // logit.  NI: registers of logits per lane, ceil(L / 32) rounded up.
-// Bound by issue (56 % of the slots) and the first load's latency, not by bytes:
-// 16384 x 128 float32, top-4 (8.4 MB, 1.2 us of them) takes 6 us, 128 x 64 top-8 2 us.
+// What takes the time is this loop's issue (56 % of the slots) and the first load's
+// latency, not the bytes: 16384 x 128 float32, top-4 (8.4 MB, 1.2 us of them) takes
+// 6 us, 128 x 64 top-8 2 us.
 template <int NI>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(int64_t tokens, int64_t ld, int L, int topk, int kind,
                                                                  int normalize, const void* logits, int32_t* ids,
@@ -169,9 +170,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(
 // totals meeting in distributed shared memory; more slots take a launch that
 // counts and one that places, since scattered 4-byte stores want many SMs.
 // Either way the bytes (16 a slot) are nothing and what is left is a chain of
-// latencies: load, match, prefix, exchange, scatter.  1024 slots over 64 experts
-// 5.5 us (one block of 256 threads: 11), 8192 over 8 experts 7, 65536 over 64
-// experts 4.6 and 9 us (in one cluster the scatter alone would take 8).
+// latencies: load, match, prefix, exchange, scatter.  One after the other in a graph,
+// 1024 slots over 64 experts and 8192 over 8 take 5.0 us (1024 in one block of 256
+// threads: 11), 65536 over 64 10.2 (in one cluster the scatter alone would take 8) and
+// over 1024 29.7.
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxCluster = 8;
 constexpr int64_t kSortClusterSlots = 2 * kSortThreads * kSortMaxCluster;
@@ -413,7 +415,7 @@ __device__ __forceinline__ uint32_t block_code(const float (&v)[16], bool in, ui
 // each.  A lane holds 16 values: half a block of 32, whose other half is one
 // exchange away, and a whole 16-byte store of FP8 codes.
 //   8192 x 7168 float16, top-8 of 64 into E5M2: 117 MB read, 546 written, 126 us,
-//     4.8 TB/s, bound by writing (a plain fill of 554 MB takes 139 us);
+//     5.3 TB/s, bound by writing (a plain fill of 554 MB takes 139 us);
 //   4096 x 4096 bfloat16, top-2 of 8 into E4M3: 72 MB, 15 us, bound by issue (two
 //     thirds of the slots) and the loads' latency;
 //   128 x 7168, top-8 of 64: 59 MB, nearly all of it padding rows, 13 us.
@@ -719,7 +721,7 @@ void sort_shape(int64_t slots, int64_t* blocks, int64_t* steps) {
     while (*blocks < kSortMaxCluster && *blocks * kSortThreads < slots) *blocks *= 2;
     *steps = slots > *blocks * kSortThreads ? 2 : 1;
   } else {
-    // two steps, as many blocks as an SM each, then more steps
+    // two steps while the blocks are at most about one an SM (152 here), then more steps
     constexpr int64_t kBlocks = 148;
     *steps = ceil_div(slots, kBlocks * kSortThreads);
     if (*steps < 2) *steps = 2;
