@@ -31,7 +31,9 @@ SYMBOLS = ("bsgg_create", "bsgg_run", "bsgg_run_host", "bsgg_run_host_async", "b
            "bsgg_debug_bounds_violation",
            "bsgg_route", "bsgg_route_backward", "bsgg_sort_rows", "bsgg_sort_workspace_bytes", "bsgg_sort_tokens",
            "bsgg_dispatch", "bsgg_combine", "bsgg_combine_backward", "bsgg_linear", "bsgg_linear_backward",
-           "bsgg_query_status_word")
+           "bsgg_query_status_word",
+           "bsgg_route_groups", "bsgg_route_groups_backward", "bsgg_rms_norm", "bsgg_rms_norm_workspace_bytes",
+           "bsgg_rms_norm_backward", "bsgg_adapters", "bsgg_adapters_backward")
 
 
 class BsggError(RuntimeError):
@@ -363,5 +365,6 @@ def run_noalloc(*, stream=None, wait_status: bool = True, **kw) -> int:
 
 
 from . import operators  # noqa: E402  (needs the names above)
-from .operators import (TokenMap, combine, combine_backward, dispatch, linear, linear_backward,  # noqa: E402,F401
-                        operators_status, route, route_backward, sort_rows, sort_tokens)
+from .operators import (Norm, TokenMap, adapters, adapters_backward, combine, combine_backward,  # noqa: E402,F401
+                        dispatch, linear, linear_backward, operators_status, rms_norm, rms_norm_backward, route,
+                        route_backward, route_groups, route_groups_backward, sort_rows, sort_tokens)

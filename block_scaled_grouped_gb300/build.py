@@ -25,7 +25,8 @@ _SHAPES = ["mxf8_128", "mxf8_256", "mxf8_pair", "nvf4_128", "nvf4_256", "nvf4_pa
            "f4e8_pair"]
 # forward and backward instances of each input family and tile shape in units
 # of their own, so that they compile in parallel
-UNITS = (["bsgg_host.cu", "bsgg_peak.cu", "bsgg_tokens.cu", "bsgg_linear.cu"] + [f"bsgg_launch_{s}.cu" for s in _SHAPES] +
+UNITS = (["bsgg_host.cu", "bsgg_peak.cu", "bsgg_tokens.cu", "bsgg_linear.cu", "bsgg_router.cu",
+          "bsgg_norm.cu", "bsgg_adapters.cu"] + [f"bsgg_launch_{s}.cu" for s in _SHAPES] +
          [f"bsgg_launch_{s}_bwd.cu" for s in _SHAPES] + ["bsgg_launch_bf16_bwd.cu"])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # hidden visibility (only the C ABI is exported) and no process-unique symbols:

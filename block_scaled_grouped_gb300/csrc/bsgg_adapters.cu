@@ -1,0 +1,841 @@
+// bsgg_adapters.cu -- low-rank adapters of many requests at once beside a dense layer,
+// and their gradient.
+//
+// Three products cover both directions, since A (rank, k) and B (rank, n) both have
+// their rows along the wide dimension.  W is either, i the adapter of a token:
+//   shrink  u[t]  = f_i X[t] W_i^T        forward u = x A^T; backward du = s dy B^T
+//   expand  Y[t]  = base[t] + f_i u[t] W_i  forward y (B); backward dx (A)
+//   outer   dW_i  = f_i sum_t g[t]^T X[t]   dA from du and x, dB from u and dy
+// Each reads its wide operand once, 2 rank products per value of two bytes: at a rank of 64
+// and the memory's rate that is 435 TFLOP/s, which mma.sync delivers, so memory bounds
+// them and the tensor cores' large tiles (128 rows of one adapter, whatever the batch
+// holds) would only be padding.
+#include "bsgg_ops.cuh"
+
+namespace {
+
+using namespace bsgg;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+// Sums of more than this many products are added up in registers in runs of this length
+// (the matrix instruction cuts what an addition drops, 1e-9 of the sum per element).
+constexpr int kRun = 512;
+constexpr int kMaxCluster = 8;
+
+struct AdapterMap {
+  int64_t tokens, m_pad;
+  int adapters;
+  const int32_t *offsets, *row_of_slot, *slot_of_row;
+};
+
+// ---------------------------------------------------------------- pieces
+// 16 bytes from global to shared memory, zeros where !present.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool present) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(present ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void load_matrices_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// c (16 x 8) += a (16 x 16) b (16 x 8)
+template <int KIND>
+__device__ __forceinline__ void multiply(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (KIND == OK_BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The place of 16-byte piece `piece` of a 128-byte row: eight rows' pieces of one
+// column lie in different banks.
+__device__ __forceinline__ uint32_t swizzled(int row, int piece) {
+  return static_cast<uint32_t>(row * 128 + ((piece ^ (row & 7)) << 4));
+}
+
+// A pair of 32-bit values as a sum of TERMS pairs of 16-bit ones: the products take them one
+// after the other, so that u and du enter unrounded (two terms: to 2^-17 of the value in
+// bfloat16, to 2^-22 in float16; three of bfloat16: 2^-24).
+template <int KIND, int TERMS>
+__device__ __forceinline__ void split_terms(float x, float y, uint32_t (&t)[TERMS]) {
+#pragma unroll
+  for (int i = 0; i < TERMS; ++i) {
+    t[i] = pack2<KIND>(x, y);
+    const float2 f = unpack2<KIND>(t[i]);
+    // nothing is left of an infinity
+    x = fabsf(f.x) < INFINITY ? x - f.x : 0.0f;
+    y = fabsf(f.y) < INFINITY ? y - f.y : 0.0f;
+  }
+}
+// 2^-e for a value whose largest magnitude is 2^e to 2^(e+1): float16 has to be kept
+// inside its range, bfloat16 has float's.
+__device__ __forceinline__ float unit_of(float largest) {
+  const uint32_t e = __float_as_uint(largest) >> 23;
+  return e >= 1u && e <= 253u ? __uint_as_float((254u - e) << 23) : 1.0f;
+}
+
+// The adapter whose rows hold `row`.  All threads call it.
+__device__ __forceinline__ int adapter_of(const AdapterMap& m, int64_t row) {
+  int n = 0;
+  for (int i = 0; i < m.adapters; i += kThreads) {
+    const int at = i + threadIdx.x;
+    n += __syncthreads_count(at < m.adapters && m.offsets[at] <= row);
+  }
+  return min(n, m.adapters - 1);
+}
+__device__ __forceinline__ int32_t token_at(const AdapterMap& m, int64_t row) {
+  const int32_t t = row < m.m_pad ? m.slot_of_row[row] : -1;
+  return t >= 0 && t < m.tokens ? t : -1;
+}
+// Tokens of ROWS rows from row0 into shared memory; one past the last row that has one.
+template <int ROWS>
+__device__ __forceinline__ int tokens_of(const AdapterMap& m, int64_t row0, int32_t* token) {
+  bool has = false;
+  if (threadIdx.x < ROWS) {
+    const int32_t t = token_at(m, row0 + threadIdx.x);
+    token[threadIdx.x] = t;
+    has = t >= 0;
+  }
+  __shared__ uint32_t mask[ROWS / 32];
+  const uint32_t b = __ballot_sync(0xFFFFFFFFu, has);
+  if ((threadIdx.x & 31) == 0 && threadIdx.x < ROWS) mask[threadIdx.x >> 5] = b;
+  __syncthreads();
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < ROWS / 32; ++i)
+    if (mask[i] != 0) n = 32 * i + 32 - __clz(mask[i]);
+  return n;
+}
+// Groups of 16 rows, as a power of two, that hold n rows.
+__device__ __forceinline__ int row_groups(int n) { return n <= 16 ? 1 : n <= 32 ? 2 : n <= 64 ? 4 : 8; }
+
+// ---------------------------------------------------------------- shrink
+// A block takes 64 rows of one adapter and one of `split` parts of the reduction; the
+// cluster's blocks join through distributed shared memory, in order.  Its warps are as
+// many groups of 16 rows as there are tokens, and share the reduction's steps of 16 beyond
+// that: a decoding batch has a token or two per adapter, and is then a stream of A.
+template <int R>
+struct Shrink {
+  static constexpr int kRows = 64, kStages = 4;
+  // rows of 128 bytes in a stage: 64 of X and R of W, or with few tokens several blocks of
+  // 64 of the reduction
+  static constexpr int kStageRows = R == 16 ? 128 : R == 32 ? 96 : R == 64 ? 160 : 192;
+  static constexpr int kStageBytes = kStageRows * 128;
+  static constexpr int kSmem = kStages * kStageBytes + 128;
+};
+
+struct ShrinkParams {
+  AdapterMap map;
+  const void* x;
+  const void* w;
+  const float* scales;
+  float* u;
+  int64_t ldx, depth;
+  int rank, split;
+};
+
+template <int KIND, int R>
+__global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant__ ShrinkParams p) {
+  using S = Shrink<R>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int32_t token[S::kRows];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const uint32_t base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t tile = blockIdx.x / p.split;
+  const int part = static_cast<int>(blockIdx.x - tile * p.split);
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const int64_t row0 = tile * S::kRows;
+  const int n = tokens_of<S::kRows>(p.map, row0, token);
+  if (n == 0) return;                                  // for the whole cluster
+  const int adapter = adapter_of(p.map, row0);
+  const int groups = row_groups(n), rows = 16 * groups, shares = kWarps / groups;
+  const int mw = warp % groups, kw = warp / groups;
+  const int blocks = max(1, min(4, S::kStageRows / (rows + p.rank)));   // of 64, a stage
+  const int64_t nb = (p.depth + 63) / 64;
+  const int b0 = static_cast<int>(nb * part / p.split), b1 = static_cast<int>(nb * (part + 1) / p.split);
+  const int steps = (b1 - b0 + blocks - 1) / blocks;
+  const uint16_t* x = static_cast<const uint16_t*>(p.x);
+  const uint16_t* w = static_cast<const uint16_t*>(p.w) + static_cast<int64_t>(adapter) * p.rank * p.depth;
+  const uint32_t block_bytes = static_cast<uint32_t>(rows + p.rank) * 128;
+
+  auto load = [&](int step) {
+    if (step < steps) {
+      for (int j = 0; j < blocks; ++j) {
+        const int b = b0 + step * blocks + j;
+        if (b >= b1) break;
+        const uint32_t to = base + (step % S::kStages) * S::kStageBytes + j * block_bytes;
+        for (int c = threadIdx.x; c < (rows + p.rank) * 8; c += kThreads) {
+          const int r = c >> 3, piece = c & 7;
+          const int64_t k = static_cast<int64_t>(b) * 64 + piece * 8;
+          if (r < rows) {
+            const int32_t t = r < n ? token[r] : -1;
+            const bool in = t >= 0 && k < p.depth;
+            copy16(to + swizzled(r, piece), in ? x + t * p.ldx + k : x, in);
+          } else {
+            const bool in = k < p.depth;
+            copy16(to + swizzled(r, piece), in ? w + (r - rows) * p.depth + k : w, in);
+          }
+        }
+      }
+    }
+    copies_commit();
+  };
+
+  float acc[R / 8][4], sum[R / 8][4];
+#pragma unroll
+  for (int i = 0; i < R / 8; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[i][k] = sum[i][k] = 0.0f;
+  int run = 0;
+  auto flush = [&]() {
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) { sum[i][k] += acc[i][k]; acc[i][k] = 0.0f; }
+    run = 0;
+  };
+  for (int s = 0; s < S::kStages - 1; ++s) load(s);
+  for (int s = 0; s < steps; ++s) {
+    copies_wait<S::kStages - 2>();
+    __syncthreads();                                   // stage s is there, and s - 1 is read
+    load(s + S::kStages - 1);
+    const uint32_t stage = base + (s % S::kStages) * S::kStageBytes;
+    for (int q = kw; q < 4 * blocks; q += shares) {    // steps of 16
+      const int j = q >> 2, kk = q & 3;
+      if (b0 + s * blocks + j >= b1) break;
+      const uint32_t xs = stage + j * block_bytes, ws = xs + rows * 128;
+      uint32_t a[4];
+      load_matrices(a, xs + swizzled(mw * 16 + (lane & 15), kk * 2 + (lane >> 4)));
+#pragma unroll
+      for (int i = 0; i < R / 8; i += 2) {
+        if (i * 8 >= p.rank) break;
+        uint32_t b[4];
+        // of an odd number of eights the last pair's second half is what lies behind: inside the stage, and unused
+        load_matrices(b, ws + swizzled(i * 8 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+        multiply<KIND>(acc[i], a, b[0], b[1]);
+        if ((i + 1) * 8 < p.rank) multiply<KIND>(acc[i + 1], a, b[2], b[3]);
+      }
+      run += 16;
+    }
+    if (run >= kRun) flush();
+  }
+  flush();
+  copies_wait<0>();
+  __syncthreads();
+  // the warps' shares, then the cluster's parts, in order
+  float* sums = reinterpret_cast<float*>(smem);
+  {
+    const int row = mw * 16 + (lane >> 2);
+    float* at = sums + (static_cast<int64_t>(kw) * rows + row) * p.rank + 2 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i) {
+      if (i * 8 >= p.rank) break;
+      *reinterpret_cast<float2*>(at + i * 8) = make_float2(sum[i][0], sum[i][1]);
+      *reinterpret_cast<float2*>(at + 8 * p.rank + i * 8) = make_float2(sum[i][2], sum[i][3]);
+    }
+  }
+  __syncthreads();
+  const int quads = rows * p.rank / 4;
+  for (int e = threadIdx.x; e < quads; e += kThreads) {
+    float4* at = reinterpret_cast<float4*>(sums) + e;
+    float4 v = *at;
+    for (int k = 1; k < shares; ++k) {
+      const float4 o = at[k * quads];
+      v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+    }
+    *at = v;
+  }
+  if (p.split > 1) cluster_sync(); else __syncthreads();
+  const float f = p.scales != nullptr ? p.scales[adapter] : 1.0f;
+  const int e0 = quads * part / p.split, e1 = quads * (part + 1) / p.split;
+  for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
+    const uint32_t at = smem_u32(sums) + e * 16;
+    float4 v = make_float4(0, 0, 0, 0);
+    for (int k = 0; k < p.split; ++k) {
+      const float4 o = ld_shared_cluster4(mapa_shared(at, k));
+      v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+    }
+    const int row = e * 4 / p.rank, col = e * 4 - row * p.rank;
+    const int32_t t = row < n ? token[row] : -1;
+    if (t >= 0) *reinterpret_cast<float4*>(p.u + static_cast<int64_t>(t) * p.rank + col) = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
+  }
+  if (p.split > 1) cluster_sync();                     // the sums stay until every block has read them
+}
+
+// ---------------------------------------------------------------- expand
+// A block takes 128 rows of one adapter and 512 columns, in passes: base and W come in by
+// asynchronous copies, a warp multiplies 16 rows by 64 columns, adds the base where it
+// lies in shared memory, and stores rows of 128 bytes.  Eight groups of 16 rows are eight
+// warps on the same 64 columns; with fewer tokens the warps lie along the columns.  The
+// blocks behind the tiles see to the tokens without an adapter.
+template <int R>
+struct Expand {
+  static constexpr int kRows = 128, kCols = 512, kPasses = 3;
+  static constexpr int kMaxAcross = R == 128 ? 4 : 8;     // warps along the columns
+  static constexpr int kSmem = (R == 16 ? 54 : R == 32 ? 60 : R == 64 ? 80 : 96) * 1024 + 128;
+};
+
+struct ExpandParams {
+  AdapterMap map;
+  const float* u;
+  const void* w;
+  const float* scales;
+  const void* base;
+  void* y;
+  float* zero_u;              // u's rows of tokens without an adapter, where wanted
+  int64_t ld_base, ldy, width, tiles;
+  int rank;
+};
+
+// Tokens without an adapter: y = base, u = 0.
+__device__ __noinline__ void expand_rest(const ExpandParams& p, int64_t block, int cols) {
+  __shared__ int32_t list[kThreads];
+  __shared__ int count[kWarps];
+  const int64_t t = block * kThreads + threadIdx.x;
+  bool none = false;
+  if (t < p.map.tokens) {
+    const int32_t r = p.map.row_of_slot[t];
+    none = r < 0 || r >= p.map.m_pad;
+  }
+  const uint32_t b = __ballot_sync(0xFFFFFFFFu, none);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) count[warp] = __popc(b);
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    before += w < warp ? count[w] : 0;
+    all += count[w];
+  }
+  if (none) list[before + __popc(b & ((1u << lane) - 1u))] = static_cast<int32_t>(t);
+  __syncthreads();
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * cols;
+  if (p.base != p.y) {
+    const int pieces = cols / 8;
+    for (int e = threadIdx.x; e < all * pieces; e += kThreads) {
+      const int64_t tok = list[e / pieces], c = c0 + (e % pieces) * 8;
+      if (c >= p.width) continue;
+      const uint4 v = p.base != nullptr ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + tok * p.ld_base + c)
+                                        : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + tok * p.ldy + c) = v;
+    }
+  }
+  if (p.zero_u != nullptr && blockIdx.y == 0) {
+    const int pieces = p.rank / 4;
+    for (int e = threadIdx.x; e < all * pieces; e += kThreads)
+      *reinterpret_cast<float4*>(p.zero_u + static_cast<int64_t>(list[e / pieces]) * p.rank + (e % pieces) * 4) = make_float4(0, 0, 0, 0);
+  }
+}
+
+template <int KIND, int R>
+__global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ ExpandParams p) {
+  using E = Expand<R>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int32_t token[E::kRows];
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  if (blockIdx.x >= p.tiles) {
+    expand_rest(p, blockIdx.x - p.tiles, E::kCols);
+    return;
+  }
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const uint32_t base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * E::kRows, col0 = static_cast<int64_t>(blockIdx.y) * E::kCols;
+  const int n = tokens_of<E::kRows>(p.map, row0, token);
+  if (n == 0) return;
+  const int adapter = adapter_of(p.map, row0);
+  const int groups = row_groups(n), rows = 16 * groups, across = min(kWarps / groups, E::kMaxAcross);
+  const int mw = warp % groups, cw = warp / groups;
+  const int ranks = (p.rank + 15) & ~15;               // whole steps of 16, zeros behind the rank
+  const int cols = static_cast<int>(min(int64_t(E::kCols), p.width - col0));
+  const int passes = (cols + 64 * across - 1) / (64 * across);
+  const uint32_t group_bytes = rows * 128, w_bytes = ranks * 128;
+  const uint32_t pass_bytes = across * (group_bytes + w_bytes);
+  const int buffers = max(1, min(E::kPasses, static_cast<int>((E::kSmem - 128) / pass_bytes)));
+  const uint16_t* w = static_cast<const uint16_t*>(p.w) + static_cast<int64_t>(adapter) * p.rank * p.width;
+  const uint16_t* from = static_cast<const uint16_t*>(p.base);
+
+  // of 64 columns each: the rows of the base, then those of W
+  auto load = [&](int pass) {
+    if (pass < passes) {
+      const uint32_t to = base + (pass % buffers) * pass_bytes;
+      for (int g = 0; g < across; ++g) {
+        const int64_t c0 = col0 + (pass * across + g) * 64;
+        for (int e = threadIdx.x; e < (rows + ranks) * 8; e += kThreads) {
+          const int r = e >> 3, piece = e & 7;
+          const int64_t c = c0 + piece * 8;
+          if (r < rows) {
+            if (from == nullptr) continue;
+            const int32_t t = r < n ? token[r] : -1;
+            const bool in = t >= 0 && c < p.width;
+            copy16(to + g * group_bytes + swizzled(r, piece), in ? from + t * p.ld_base + c : from, in);
+          } else {
+            const int k = r - rows;
+            const bool in = k < p.rank && c < p.width;
+            copy16(to + across * group_bytes + g * w_bytes + swizzled(k, piece), in ? w + k * p.width + c : w, in);
+          }
+        }
+      }
+    }
+    copies_commit();
+  };
+  for (int i = 0; i < E::kPasses; ++i) {
+    if (i < buffers) load(i); else copies_commit();
+  }
+
+  // this warp's rows of u, as the products take them
+  constexpr int kTerms = 2;
+  uint32_t a[kTerms][R / 16][4];
+  float factor[2];
+  const float f = p.scales != nullptr ? p.scales[adapter] : 1.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = mw * 16 + (lane >> 2) + 8 * h;
+    const int32_t t = r < n ? token[r] : -1;
+    const float* u = p.u + static_cast<int64_t>(t < 0 ? 0 : t) * p.rank + 2 * (lane & 3);
+    float2 v[R / 8];
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i) {
+      v[i] = t >= 0 && i * 8 < p.rank ? *reinterpret_cast<const float2*>(u + i * 8) : make_float2(0.0f, 0.0f);
+      most = fmaxf(most, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+    }
+    float unit = 1.0f;
+    if (KIND == OK_F16) {
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+      unit = unit_of(most);
+    }
+    factor[h] = f / unit;
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i) {
+      uint32_t term[kTerms];
+      split_terms<KIND, kTerms>(v[i].x * unit, v[i].y * unit, term);
+#pragma unroll
+      for (int k = 0; k < kTerms; ++k) a[k][i / 2][2 * (i & 1) + h] = term[k];
+    }
+  }
+
+  for (int pass = 0; pass < passes; ++pass) {
+    if (buffers == 1) copies_wait<0>();
+    else if (buffers == 2) copies_wait<1>();
+    else copies_wait<2>();
+    __syncthreads();
+    const uint32_t at = base + (pass % buffers) * pass_bytes;
+    const int64_t c0 = col0 + (pass * across + cw) * 64;
+    if (cw < across && c0 < p.width) {
+      const uint32_t ys = at + cw * group_bytes, ws = at + across * group_bytes + cw * w_bytes;
+      float acc[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+#pragma unroll
+      for (int s = 0; s < R / 16; ++s) {
+        if (s * 16 >= p.rank) break;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          uint32_t b[4];
+          load_matrices_t(b, ws + swizzled(s * 16 + (lane & 15), i + (lane >> 4)));
+#pragma unroll
+          for (int k = 0; k < kTerms; ++k) {
+            multiply<KIND>(acc[i], a[k][s], b[0], b[1]);
+            multiply<KIND>(acc[i + 1], a[k][s], b[2], b[3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = mw * 16 + (lane >> 2) + 8 * h;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t* to = reinterpret_cast<uint32_t*>(smem + (ys - base) + swizzled(r, i) + 4 * (lane & 3));
+          const float2 old = from != nullptr ? unpack2<KIND>(*to) : make_float2(0.0f, 0.0f);
+          *to = pack2<KIND>(fmaf(factor[h], acc[i][2 * h], old.x), fmaf(factor[h], acc[i][2 * h + 1], old.y));
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = mw * 16 + e * 4 + (lane >> 3), piece = lane & 7;
+        const int32_t t = r < n ? token[r] : -1;
+        const int64_t c = c0 + piece * 8;
+        if (t >= 0 && c < p.width)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + t * p.ldy + c) =
+              *reinterpret_cast<const uint4*>(smem + (ys - base) + swizzled(r, piece));
+      }
+    }
+    __syncthreads();                                   // the buffer is read
+    load(pass + buffers);
+  }
+  copies_wait<0>();
+}
+
+// ---------------------------------------------------------------- outer
+// A block takes one adapter and COLS columns, and of the adapter's rows every split-th
+// chunk of 64; the cluster's blocks join through distributed shared memory, in order.  The
+// products are (rank x 64 tokens) (64 tokens x columns), both read across their rows.
+template <int R>
+struct Outer {
+  static constexpr int kCols = R == 128 ? 128 : 256, kTokens = 64, kStages = 3;
+  static constexpr int kXBytes = kTokens * kCols * 2, kGBytes = kTokens * R * 4;
+  static constexpr int kStageBytes = kXBytes + kGBytes;
+  static constexpr int kTermPitch = 2 * R + 16;         // bytes of a token's ranks: eight rows in different banks
+  static constexpr int kTermBytes = kTokens * kTermPitch;
+  static constexpr int smem(int terms) { return kStages * kStageBytes + terms * kTermBytes + 128; }
+  static_assert(R * kCols * 4 <= kStages * kStageBytes, "the partial sums reuse the stages");
+};
+
+struct OuterParams {
+  AdapterMap map;
+  const float* g;
+  const void* x;
+  const float* scales;
+  void* out;
+  int64_t ldx, width, blocks;     // blocks of columns
+  int rank, split, out_kind;
+};
+
+template <int KIND, int R, int TERMS>
+__global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__ OuterParams p) {
+  using O = Outer<R>;
+  constexpr int kTiles = O::kCols / 8 / kWarps;         // of 8 columns, a warp
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int32_t token[O::kStages + 1][O::kTokens];
+  __shared__ float most_of[kWarps];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const uint32_t base = smem_u32(smem);
+  const uint32_t terms = base + O::kStages * O::kStageBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t unit_index = blockIdx.x / p.split;
+  const int part = static_cast<int>(blockIdx.x - unit_index * p.split);
+  const int adapter = static_cast<int>(unit_index / p.blocks);
+  const int64_t col0 = (unit_index - adapter * p.blocks) * O::kCols;
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const int64_t row0 = adapter > 0 ? max(0, p.map.offsets[adapter - 1]) : 0;
+  const int64_t row1 = min(p.map.m_pad, static_cast<int64_t>(p.map.offsets[adapter]));
+  // chunks of this block; rows past the adapter's last token are padding, at the end
+  const int64_t all = row1 > row0 ? (row1 - row0 + O::kTokens - 1) / O::kTokens : 0;
+  const int chunks = static_cast<int>(all > part ? (all - part + p.split - 1) / p.split : 0);
+  auto chunk_row = [&](int c) { return row0 + (static_cast<int64_t>(c) * p.split + part) * O::kTokens; };
+  auto token_of = [&](int c, int i) {
+    const int64_t r = chunk_row(c) + i;
+    return c < chunks && r < row1 ? token_at(p.map, r) : -1;
+  };
+  const uint16_t* x = static_cast<const uint16_t*>(p.x);
+
+  float unit = 1.0f;
+  if (KIND == OK_F16) {
+    // this block's own power of two: its sums are scaled back before they are joined
+    float most = 0.0f;
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(chunks) * O::kTokens; i += kThreads) {
+      const int32_t t = token_of(static_cast<int>(i / O::kTokens), static_cast<int>(i % O::kTokens));
+      if (t < 0) continue;
+      for (int k = 0; k < p.rank; k += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p.g + static_cast<int64_t>(t) * p.rank + k);
+        most = fmaxf(fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    if (lane == 0) most_of[warp] = most;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) most = fmaxf(most, most_of[w]);
+    unit = unit_of(most);
+  }
+
+  auto load = [&](int c) {
+    if (c < chunks) {
+      const int32_t* tok = token[c % (O::kStages + 1)];
+      const uint32_t to = base + (c % O::kStages) * O::kStageBytes;
+      for (int e = threadIdx.x; e < O::kTokens * O::kCols / 8; e += kThreads) {
+        const int r = e / (O::kCols / 8), q = e % (O::kCols / 8);
+        const int32_t t = tok[r];
+        const int64_t col = col0 + q * 8;
+        const bool in = t >= 0 && col < p.width;
+        copy16(to + (q >> 3) * (O::kTokens * 128) + swizzled(r, q & 7), in ? x + t * p.ldx + col : x, in);
+      }
+      for (int e = threadIdx.x; e < O::kTokens * p.rank / 4; e += kThreads) {
+        const int r = e / (p.rank / 4), q = e % (p.rank / 4);
+        const int32_t t = tok[r];
+        copy16(to + O::kXBytes + (r * R + q * 4) * 4, t >= 0 ? p.g + static_cast<int64_t>(t) * p.rank + q * 4 : p.g, t >= 0);
+      }
+    }
+    copies_commit();
+  };
+
+  float acc[R / 16][kTiles][4], sum[R / 16][kTiles][4];
+#pragma unroll
+  for (int m = 0; m < R / 16; ++m)
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[m][i][k] = sum[m][i][k] = 0.0f;
+  for (int c = 0; c < O::kStages - 1; ++c)
+    if (threadIdx.x < O::kTokens) token[c][threadIdx.x] = token_of(c, threadIdx.x);
+  __syncthreads();
+  for (int c = 0; c < O::kStages - 1; ++c) load(c);
+  for (int c = 0; c < chunks; ++c) {
+    int32_t next = -1;
+    const int ahead = c + O::kStages - 1;
+    if (threadIdx.x < O::kTokens) next = token_of(ahead, threadIdx.x);
+    copies_wait<O::kStages - 2>();
+    if (threadIdx.x < O::kTokens) token[ahead % (O::kStages + 1)][threadIdx.x] = next;
+    __syncthreads();                                   // chunk c is there, c - 1 is read, the next one's tokens are known
+    load(ahead);
+    const uint32_t stage = base + (c % O::kStages) * O::kStageBytes;
+    // g as terms of 16 bits, ranks up to a multiple of 16
+    const int ranks = (p.rank + 15) & ~15;
+    const float* g = reinterpret_cast<const float*>(smem + (stage - base) + O::kXBytes);
+    for (int e = threadIdx.x; e < O::kTokens * ranks / 4; e += kThreads) {
+      const int r = e / (ranks / 4), q = e % (ranks / 4);
+      float4 v = make_float4(0, 0, 0, 0);
+      if (q * 4 < p.rank) v = *reinterpret_cast<const float4*>(g + r * R + q * 4);
+      uint32_t lo[TERMS], hi[TERMS];
+      split_terms<KIND, TERMS>(v.x * unit, v.y * unit, lo);
+      split_terms<KIND, TERMS>(v.z * unit, v.w * unit, hi);
+#pragma unroll
+      for (int k = 0; k < TERMS; ++k)
+        *reinterpret_cast<uint2*>(smem + (terms - base) + k * O::kTermBytes + r * O::kTermPitch + q * 8) = make_uint2(lo[k], hi[k]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < O::kTokens / 16; ++s) {
+      uint32_t b[kTiles / 2][4];
+#pragma unroll
+      for (int i = 0; i < kTiles; i += 2) {
+        const int tile = warp * kTiles + i;              // of 8 columns; 8 of them share 128 bytes
+        load_matrices_t(b[i / 2], stage + (tile >> 3) * (O::kTokens * 128) + swizzled(s * 16 + (lane & 15), (tile & 7) + (lane >> 4)));
+      }
+#pragma unroll
+      for (int m = 0; m < R / 16; ++m) {
+        if (m * 16 >= p.rank) break;
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) {
+          uint32_t a[4];
+          load_matrices_t(a, terms + k * O::kTermBytes + (s * 16 + (lane & 7) + ((lane >> 4) << 3)) * O::kTermPitch +
+                                 (m * 2 + ((lane >> 3) & 1)) * 16);
+#pragma unroll
+          for (int i = 0; i < kTiles; i += 2) {
+            multiply<KIND>(acc[m][i], a, b[i / 2][0], b[i / 2][1]);
+            multiply<KIND>(acc[m][i + 1], a, b[i / 2][2], b[i / 2][3]);
+          }
+        }
+      }
+    }
+    if ((c + 1) % (kRun / O::kTokens) == 0 || c + 1 == chunks) {
+#pragma unroll
+      for (int m = 0; m < R / 16; ++m)
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) { sum[m][i][k] += acc[m][i][k]; acc[m][i][k] = 0.0f; }
+    }
+  }
+  copies_wait<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem);
+  const float back = 1.0f / unit;
+#pragma unroll
+  for (int m = 0; m < R / 16; ++m) {
+    if (m * 16 >= p.rank) break;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      float* at = sums + (m * 16 + (lane >> 2)) * O::kCols + (warp * kTiles + i) * 8 + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(at) = make_float2(sum[m][i][0] * back, sum[m][i][1] * back);
+      *reinterpret_cast<float2*>(at + 8 * O::kCols) = make_float2(sum[m][i][2] * back, sum[m][i][3] * back);
+    }
+  }
+  if (p.split > 1) cluster_sync(); else __syncthreads();
+  const float f = p.scales != nullptr ? p.scales[adapter] : 1.0f;
+  const int pieces = p.rank * (O::kCols / 8);            // of 8 columns
+  const int e0 = pieces * part / p.split, e1 = pieces * (part + 1) / p.split;
+  for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
+    const int r = e / (O::kCols / 8), q = e % (O::kCols / 8);
+    const int64_t col = col0 + q * 8;
+    if (col >= p.width) continue;
+    const uint32_t at = smem_u32(sums) + (r * O::kCols + q * 8) * 4;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int k = 0; k < p.split; ++k) {
+      const uint32_t from = mapa_shared(at, k);
+      const float4 lo = ld_shared_cluster4(from), hi = ld_shared_cluster4(from + 16);
+      v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+      v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= f;
+    const int64_t to = (static_cast<int64_t>(adapter) * p.rank + r) * p.width + col;
+    if (p.out_kind == OK_F32) store8<OK_F32>(p.out, to, v);
+    else if (p.out_kind == OK_F16) store8<OK_F16>(p.out, to, v);
+    else store8<OK_BF16>(p.out, to, v);
+  }
+  if (p.split > 1) cluster_sync();                     // the sums stay until every block has read them
+}
+
+// ---------------------------------------------------------------- host
+// Calls f with the least of 16, 32, 64, 128 that holds the rank.
+template <typename F>
+bsgg_status with_rank(int rank, F&& f) {
+  if (rank <= 16) return f(std::integral_constant<int, 16>());
+  if (rank <= 32) return f(std::integral_constant<int, 32>());
+  if (rank <= 64) return f(std::integral_constant<int, 64>());
+  return f(std::integral_constant<int, 128>());
+}
+template <typename F>
+bsgg_status with_half(int format, F&& f) {
+  return format == BSGG_OUT_BF16 ? f(std::integral_constant<int, OK_BF16>()) : f(std::integral_constant<int, OK_F16>());
+}
+// Shared memory beyond the default 48 KB has to be asked for.
+template <typename K>
+bool allowed(K kern, int smem) {
+  return succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+}
+
+// Tiles of `rows` rows that can hold tokens, at the most.
+int64_t busy_tiles(const AdapterMap& m, int rows) {
+  const int64_t most = (m.tokens < m.adapters ? m.tokens : m.adapters) + m.tokens / rows;
+  const int64_t all = m.m_pad / rows;
+  return most < all ? most : all;
+}
+
+bsgg_status launch_shrink(int format, ShrinkParams p, cudaStream_t s) {
+  const int64_t tiles = p.map.m_pad / 64, busy = busy_tiles(p.map, 64), nb = ceil_div(p.depth, 64);
+  p.split = 1;
+  while (p.split < kMaxCluster && busy * p.split < 304 && nb >= 4 * p.split) p.split *= 2;
+  return with_half(format, [&](auto kind) {
+    return with_rank(p.rank, [&](auto r) {
+      constexpr int K = decltype(kind)::value, R = decltype(r)::value;
+      if (!allowed(shrink_kernel<K, R>, Shrink<R>::kSmem)) return BSGG_ERR_CUDA;
+      const LaunchConfig c(dim3(static_cast<unsigned>(tiles * p.split)), kThreads, Shrink<R>::kSmem, s, p.split);
+      return launch_kernel(c, shrink_kernel<K, R>, p);
+    });
+  });
+}
+
+bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
+  p.tiles = p.map.m_pad / 128;
+  const int64_t blocks = p.tiles + ceil_div(p.map.tokens, kThreads);
+  return with_half(format, [&](auto kind) {
+    return with_rank(p.rank, [&](auto r) {
+      constexpr int K = decltype(kind)::value, R = decltype(r)::value;
+      if (!allowed(expand_kernel<K, R>, Expand<R>::kSmem)) return BSGG_ERR_CUDA;
+      const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ceil_div(p.width, Expand<R>::kCols)));
+      const LaunchConfig c(grid, kThreads, Expand<R>::kSmem, s);
+      return launch_kernel(c, expand_kernel<K, R>, p);
+    });
+  });
+}
+
+bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
+  // parts of an adapter's tokens: of twice the chunks that it has on average
+  const int64_t chunks = ceil_div(p.map.tokens, int64_t(64) * p.map.adapters);
+  p.split = 1;
+  while (p.split < kMaxCluster && p.split < 2 * chunks) p.split *= 2;
+  return with_half(format, [&](auto kind) {
+    return with_rank(p.rank, [&](auto r) {
+      constexpr int K = decltype(kind)::value, R = decltype(r)::value;
+      p.blocks = ceil_div(p.width, Outer<R>::kCols);
+      const int64_t grid = p.map.adapters * p.blocks * p.split;
+      auto launch = [&](auto terms) {
+        constexpr int N = decltype(terms)::value;
+        if (!allowed(outer_kernel<K, R, N>, Outer<R>::smem(N))) return BSGG_ERR_CUDA;
+        const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, Outer<R>::smem(N), s, p.split);
+        return launch_kernel(c, outer_kernel<K, R, N>, p);
+      };
+      if constexpr (K == OK_BF16) {
+        if (p.out_kind == OK_F32) return launch(std::integral_constant<int, 3>());
+      }
+      return launch(std::integral_constant<int, 2>());
+    });
+  });
+}
+
+bool good_width(int64_t v) { return v >= 8 && v <= (int64_t(1) << 24) && v % 8 == 0; }
+bool good_pitch(int64_t ld, int64_t cols) { return ld >= cols && ld <= (int64_t(1) << 30) && ld % 8 == 0; }
+
+bsgg_status check_adapters(int64_t tokens, int64_t k, int64_t n, int64_t m_pad, int adapters, int rank, int format) {
+  if (tokens < 0 || tokens > (int64_t(1) << 30) || !good_width(k) || !good_width(n) || m_pad <= 0 || m_pad % 128 != 0 ||
+      m_pad > (int64_t(1) << 30) || adapters < 1 || adapters > 1024 || rank < 8 || rank > 128 || rank % 8 != 0 ||
+      (format != BSGG_OUT_BF16 && format != BSGG_OUT_F16))
+    return BSGG_ERR_INVALID_ARG;
+  return BSGG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+bsgg_status bsgg_adapters(const bsgg_adapters_desc* d, const void* x, const void* a, const void* b, const float* scales,
+                          const int32_t* padded_offsets, const int32_t* row_of_slot, const int32_t* slot_of_row,
+                          const void* base, float* u, void* y, void* stream) {
+  if (!d || d->reserved != 0) return BSGG_ERR_INVALID_ARG;
+  const bsgg_status st = check_adapters(d->tokens, d->k, d->n, d->m_pad, d->adapters, d->rank, d->format);
+  if (st != BSGG_OK) return st;
+  if (!good_pitch(d->ldx, d->k) || !good_pitch(d->ldy, d->n) || (base && !good_pitch(d->ld_base, d->n)) ||
+      (base && base == y && d->ld_base != d->ldy))
+    return BSGG_ERR_INVALID_ARG;
+  if (d->tokens == 0) return BSGG_OK;
+  if (!x || !a || !b || !padded_offsets || !row_of_slot || !slot_of_row || !u || !y) return BSGG_ERR_INVALID_ARG;
+  for (const void* q : {x, a, b, base, static_cast<const void*>(u), static_cast<const void*>(y)})
+    if (!aligned_to(q, 16)) return BSGG_ERR_INVALID_ARG;
+  if (!aligned_to(scales, 4) || !aligned_to(padded_offsets, 4) || !aligned_to(row_of_slot, 4) || !aligned_to(slot_of_row, 4))
+    return BSGG_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const AdapterMap map = {d->tokens, d->m_pad, d->adapters, padded_offsets, row_of_slot, slot_of_row};
+  const bsgg_status ran = launch_shrink(d->format, {map, x, a, nullptr, u, d->ldx, d->k, d->rank, 1}, s);
+  if (ran != BSGG_OK) return ran;
+  return launch_expand(d->format, {map, u, b, scales, base, y, u, d->ld_base, d->ldy, d->n, 0, d->rank}, s);
+}
+
+bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* dy, const void* x, const float* u,
+                                   const void* a, const void* b, const float* scales, const int32_t* padded_offsets,
+                                   const int32_t* row_of_slot, const int32_t* slot_of_row, const void* base, float* du,
+                                   void* dx, void* da, void* db, void* stream) {
+  if (!d) return BSGG_ERR_INVALID_ARG;
+  const bsgg_status st = check_adapters(d->tokens, d->k, d->n, d->m_pad, d->adapters, d->rank, d->format);
+  if (st != BSGG_OK) return st;
+  if (!good_pitch(d->ld_dy, d->n) || (da && !good_pitch(d->ldx, d->k)) || (dx && !good_pitch(d->ld_dx, d->k)) ||
+      (dx && base && !good_pitch(d->ld_base, d->k)) || (dx && base && base == dx && d->ld_base != d->ld_dx))
+    return BSGG_ERR_INVALID_ARG;
+  if ((da || db) && !is_float_format(d->grad_format)) return BSGG_ERR_INVALID_ARG;
+  for (const void* q : {dy, x, a, b, base, static_cast<const void*>(u), static_cast<const void*>(du),
+                        static_cast<const void*>(dx), static_cast<const void*>(da), static_cast<const void*>(db)})
+    if (!aligned_to(q, 16)) return BSGG_ERR_INVALID_ARG;
+  if (!aligned_to(scales, 4) || !aligned_to(padded_offsets, 4) || !aligned_to(row_of_slot, 4) || !aligned_to(slot_of_row, 4))
+    return BSGG_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d->tokens == 0) {
+    // empty sums
+    const size_t es = static_cast<size_t>(float_bytes(d->grad_format)) * d->adapters * d->rank;
+    if ((da && !succeeded(cudaMemsetAsync(da, 0, es * d->k, s))) || (db && !succeeded(cudaMemsetAsync(db, 0, es * d->n, s))))
+      return BSGG_ERR_CUDA;
+    return BSGG_OK;
+  }
+  if (!dx && !da && !db) return BSGG_ERR_INVALID_ARG;
+  const bool wants_du = dx || da;
+  if (!dy || !padded_offsets || !slot_of_row || (wants_du && (!b || !du)) || (dx && (!a || !row_of_slot)) || (da && !x) ||
+      (db && !u))
+    return BSGG_ERR_INVALID_ARG;
+  const AdapterMap map = {d->tokens, d->m_pad, d->adapters, padded_offsets, row_of_slot, slot_of_row};
+  bsgg_status ran = BSGG_OK;
+  if (wants_du) ran = launch_shrink(d->format, {map, dy, b, scales, du, d->ld_dy, d->n, d->rank, 1}, s);
+  if (ran == BSGG_OK && db) ran = launch_outer(d->format, {map, u, dy, scales, db, d->ld_dy, d->n, 0, d->rank, 1, d->grad_format}, s);
+  if (ran == BSGG_OK && da) ran = launch_outer(d->format, {map, du, x, nullptr, da, d->ldx, d->k, 0, d->rank, 1, d->grad_format}, s);
+  if (ran == BSGG_OK && dx)
+    ran = launch_expand(d->format, {map, du, a, nullptr, base, dx, nullptr, d->ld_base, d->ld_dx, d->k, 0, d->rank}, s);
+  return ran;
+}
+
+}  // extern "C"

@@ -10,8 +10,6 @@ namespace {
 
 using namespace bsgg;
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // act'(z).  silu: s (1 + z (1 - s)) with e = e^-z, s = 1 / (1 + e), 1 - s = e s: no
 // cancellation, one exponential and one reciprocal (the argument is held below 87,
 // where s is 1e-38, so that e s stays a number: below z = -87 the slope, which falls

@@ -1,0 +1,456 @@
+// bsgg_norm.cu -- root-mean-square norm with the residual's addition, out in 16 or 32
+// bits and as quantized rows of the grouped GEMM's A; and its gradient.
+#include <cmath>
+
+#include "bsgg_ops.cuh"
+
+namespace {
+
+using namespace bsgg;
+
+// Values of a row that a thread holds at a time, in two runs of eight, as the block
+// quantizer takes them.
+constexpr int kNormValues = 16;
+constexpr int kNormMaxThreads = 512, kNormWarpRows = 4, kNormPadRows = 8;
+
+struct NormParams {
+  int64_t tokens, m_pad;
+  int64_t ld_x, ld_residual, ld_h, ld_y;
+  int hidden, kq;             // kq: scale words of a row
+  int weight_kind, y_kind;
+  float eps, inv_hidden;
+  const void *x, *residual, *weight;
+  void *h, *y;
+  float* rstd;
+  uint8_t *a, *sfa;
+};
+
+// The sum over the threads of a row: a warp's, or (WARP = false) the block's, every
+// thread's in the same order.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+  v = warp_sum(v);
+  if (WARP) return v;
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0f;
+  const int warps = blockDim.x >> 5;
+  for (int w = 0; w < warps; ++w) v += part[w];
+  return v;
+}
+
+template <int KIND>
+__device__ __forceinline__ float round_to(float v) {
+  if (KIND == OK_F32) return v;
+  if (KIND == OK_F16) return __half2float(__float2half_rn(v));
+  return __bfloat162float(__float2bfloat16_rn(v));
+}
+
+// Eight values of a tensor whose type is known at run time only.
+__device__ __forceinline__ void load8_as(int kind, const void* base, int64_t i, float* v) {
+  float(&r)[8] = *reinterpret_cast<float(*)[8]>(v);
+  if (kind == OK_F32) load8<OK_F32>(base, i, r);
+  else if (kind == OK_F16) load8<OK_F16>(base, i, r);
+  else load8<OK_BF16>(base, i, r);
+}
+__device__ __forceinline__ void store8_as(int kind, void* base, int64_t i, const float* v) {
+  const float(&r)[8] = *reinterpret_cast<const float(*)[8]>(v);
+  if (kind == OK_F32) store8<OK_F32>(base, i, r);
+  else if (kind == OK_F16) store8<OK_F16>(base, i, r);
+  else store8<OK_BF16>(base, i, r);
+}
+
+// One row per warp (WARP) or per block; a thread holds NV runs of 16 values from the
+// first load to the last store, so that every tensor is passed over once.  FMT: the
+// quantized rows' format, BSGG_IN_BF16 for none.  The blocks past the tokens write A's
+// padding rows.
+template <int KIND, int FMT, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : kNormMaxThreads)
+    rms_norm_kernel(const __grid_constant__ NormParams p) {
+  constexpr int V = kNormValues;
+  constexpr bool kRows = rf_scaled(FMT);
+  constexpr int kLanes = kRows ? rf_vec(FMT) / 16 : 1;
+  __shared__ float part[kNormMaxThreads / 32];
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const int row_bytes = p.hidden / 8 * rf_bits(FMT);
+  const int64_t blocks = WARP ? (p.tokens + kNormWarpRows - 1) / kNormWarpRows : p.tokens;
+  if (kRows && blockIdx.x >= blocks) {
+    const int64_t r0 = p.tokens + (static_cast<int64_t>(blockIdx.x) - blocks) * kNormPadRows;
+    constexpr uint32_t one = rf_one(FMT) * 0x01010101u;
+    for (int64_t r = r0; r < min(r0 + kNormPadRows, p.m_pad); ++r) {
+      uint8_t* row = p.a + r * row_bytes;                // row_bytes is a multiple of 16
+      for (int c = threadIdx.x * 16; c < row_bytes; c += blockDim.x * 16) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+      const int kb = (p.hidden + rf_vec(FMT) - 1) / rf_vec(FMT);
+      uint8_t* sf = p.sfa + sf_off(r, 0, p.kq);
+      for (int q = threadIdx.x; q < p.kq; q += blockDim.x) {
+        const int left = kb - 4 * q;                     // blocks of this word inside hidden
+        *reinterpret_cast<uint32_t*>(sf + static_cast<int64_t>(q) * 512) = left >= 4 ? one : one & ((1u << (8 * left)) - 1u);
+      }
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 31, first = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
+  const int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * kNormWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && t >= p.tokens) return;
+  const bool added = p.residual != nullptr;
+  float v[NV][V];
+  // all loads before the first use
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (first + i * step) * V;
+#pragma unroll
+    for (int h = 0; h < V; h += 8) {
+      float(&r)[8] = reinterpret_cast<float(&)[8]>(v[i][h]);
+      if (c + h < p.hidden) {
+        load8<KIND>(p.x, t * p.ld_x + c + h, r);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r[k] = 0.0f;
+      }
+    }
+  }
+  if (added) {
+    Raw8<KIND, false> raw[NV][V / 8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int h = 0; h < V / 8; ++h) {
+        const int c = (first + i * step) * V + 8 * h;
+        raw[i][h].load(p.residual, t * p.ld_residual + c, c < p.hidden);
+      }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int h = 0; h < V / 8; ++h) {
+        float r[8];
+        raw[i][h].values(r);
+        // what is normed is what is kept: the backward sees the same h
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][8 * h + k] = round_to<KIND>(v[i][8 * h + k] + r[k]);
+      }
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) s = fmaf(v[i][k], v[i][k], s);
+    sum += s;
+  }
+  if (p.h != nullptr) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int h = 0; h < V; h += 8) {
+        const int c = (first + i * step) * V + h;
+        if (c < p.hidden) store8<KIND>(p.h, t * p.ld_h + c, reinterpret_cast<float(&)[8]>(v[i][h]));
+      }
+  }
+  sum = row_sum<WARP>(sum, part);
+  const float rstd = 1.0f / sqrtf(fmaf(sum, p.inv_hidden, p.eps));
+  if (p.rstd != nullptr && first == 0) p.rstd[t] = rstd;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (first + i * step) * V;
+#pragma unroll
+    for (int h = 0; h < V; h += 8) {
+      if (c + h >= p.hidden) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][h + k] *= rstd;
+      if (p.weight != nullptr) {
+        float w[8];
+        load8_as(p.weight_kind, p.weight, c + h, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][h + k] *= w[k];
+      }
+      if (p.y != nullptr) store8_as(p.y_kind, p.y, t * p.ld_y + c + h, &v[i][h]);
+    }
+    if constexpr (kRows) {
+      const bool in = c < p.hidden;
+      uint32_t word = 0, packed[rf_words(FMT)];
+      const uint32_t code = block_code<FMT>(v[i], in, word);
+      quantize16<FMT>(v[i], code, packed);
+      if (lane % (4 * kLanes) == 0 && c < p.kq * 4 * rf_vec(FMT))
+        *reinterpret_cast<uint32_t*>(p.sfa + sf_off(t, 0, p.kq) + static_cast<int64_t>(c / (4 * rf_vec(FMT))) * 512) = word;
+      if (in) store_codes16<FMT>(p.a + t * row_bytes + c / 8 * rf_bits(FMT), packed, true);
+    }
+  }
+}
+
+struct NormBwdParams {
+  int64_t tokens;
+  int64_t ld_dy, ld_h, ld_dh, ld_dx;
+  int hidden, weight_kind;
+  float inv_hidden;
+  const void *dy, *h, *weight, *dh;
+  const float* rstd;
+  void* dx;
+  float* part;                // (blocks, hidden) sums of dy * n, with a dweight
+};
+
+// With n = h rstd and g = dy w:  dx = rstd (g - n mean(g n)) + dh,  dweight = sum dy n.
+// A block (or each of its warps) walks rows, gridDim apart, its threads holding the
+// same columns of each, so that the weight's gradient stays in registers until the
+// block's rows are done; the blocks' sums meet in a second launch, in order.
+template <int KIND, int YKIND, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : kNormMaxThreads)
+    rms_norm_backward_kernel(const __grid_constant__ NormBwdParams p) {
+  constexpr int V = kNormValues;
+  __shared__ float part[2][kNormMaxThreads / 32];
+  __shared__ float warp_sums[WARP ? kNormWarpRows : 1][WARP ? 32 * V * NV : 1];
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const int lane = threadIdx.x & 31, first = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
+  const int64_t rows = WARP ? kNormWarpRows : 1, row0 = blockIdx.x * rows + (WARP ? threadIdx.x >> 5 : 0);
+  float acc[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[i][k] = 0.0f;
+  int turn = 0;
+  for (int64_t t = row0; t < p.tokens; t += gridDim.x * rows, turn ^= 1) {
+    Raw8<YKIND, false> dy[NV][V / 8];
+    Raw8<KIND, false> h[NV][V / 8], dh[NV][V / 8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < V / 8; ++j) {
+        const int c = (first + i * step) * V + 8 * j;
+        dy[i][j].load(p.dy, t * p.ld_dy + c, c < p.hidden);
+        h[i][j].load(p.h, t * p.ld_h + c, c < p.hidden);
+        dh[i][j].load(p.dh, t * p.ld_dh + c, p.dh != nullptr && c < p.hidden);
+      }
+    const float rstd = p.rstd[t];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < V / 8; ++j) {
+        const int c = (first + i * step) * V + 8 * j;
+        float g[8], n[8], w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
+        dy[i][j].values(g);
+        h[i][j].values(n);
+        if (p.weight != nullptr && c < p.hidden) load8_as(p.weight_kind, p.weight, c, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float q = g[k] * (n[k] * rstd);
+          acc[i][8 * j + k] += q;
+          sum = fmaf(q, w[k], sum);
+        }
+      }
+    // two buffers: the next row's sums are written while this row's may still be read
+    const float mean = row_sum<WARP>(sum, part[turn]) * p.inv_hidden;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < V / 8; ++j) {
+        const int c = (first + i * step) * V + 8 * j;
+        if (c >= p.hidden) continue;
+        float g[8], n[8], d[8], w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
+        dy[i][j].values(g);
+        h[i][j].values(n);
+        dh[i][j].values(d);
+        if (p.weight != nullptr) load8_as(p.weight_kind, p.weight, c, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] += rstd * (g[k] * w[k] - n[k] * rstd * mean);
+        store8<KIND>(p.dx, t * p.ld_dx + c, d);
+      }
+  }
+  if (p.part == nullptr) return;
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.hidden;
+  if constexpr (WARP) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) warp_sums[threadIdx.x >> 5][(lane + 32 * i) * V + k] = acc[i][k];
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kNormWarpRows; ++w) s += warp_sums[w][c];
+      out[c] = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < V; j += 8) {
+        const int c = (first + i * step) * V + j;
+        if (c < p.hidden) store8<OK_F32>(out, c, reinterpret_cast<float(&)[8]>(acc[i][j]));
+      }
+  }
+}
+
+// dweight[c] = the sum of the blocks' parts: 32 columns a block, eight warps that take
+// every eighth part, joined in order.
+constexpr int kNormJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kNormJoinWarps) norm_join_kernel(const float* part, int64_t parts, int hidden, float* dweight) {
+  __shared__ float sums[kNormJoinWarps][32];
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (c < hidden) {
+#pragma unroll 8
+    for (int64_t b = warp; b < parts; b += kNormJoinWarps) s += part[b * hidden + c];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < hidden) {
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kNormJoinWarps; ++w) s += sums[w][lane];
+    dweight[c] = s;
+  }
+}
+
+// ---------------------------------------------------------------- host
+constexpr int64_t kNormMaxHidden = 32768;
+constexpr int64_t kNormBwdBlocks = 304;       // two on each of the 152 SMs
+
+// How rows of `cols` columns lie: a warp each with one or two runs of 16 a lane, or a
+// block each with the fewest runs that 256 threads (512 at the most) hold.
+struct RowShape {
+  bool warp;
+  int values, threads;
+};
+RowShape row_shape(int64_t cols) {
+  const int64_t runs = ceil_div(cols, kNormValues);
+  if (runs <= 64) return {true, runs <= 32 ? 1 : 2, 32 * kNormWarpRows};
+  const int nv = runs <= 256 ? 1 : runs <= 512 ? 2 : 4;
+  return {false, nv, static_cast<int>(ceil_div(ceil_div(runs, nv), 32) * 32)};
+}
+template <typename F>
+bsgg_status with_shape(const RowShape& s, F&& f) {
+  using std::integral_constant;
+  if (s.warp) return s.values == 1 ? f(integral_constant<int, 1>(), std::true_type()) : f(integral_constant<int, 2>(), std::true_type());
+  if (s.values == 1) return f(integral_constant<int, 1>(), std::false_type());
+  if (s.values == 2) return f(integral_constant<int, 2>(), std::false_type());
+  return f(integral_constant<int, 4>(), std::false_type());
+}
+
+bool good_rows(int64_t ld, int64_t hidden, int format) {
+  return ld >= hidden && ld <= (int64_t(1) << 30) && ld * float_bytes(format) % 16 == 0;
+}
+
+bsgg_status check_norm(int64_t tokens, int64_t hidden, int token_format, int weight_format, int y_format) {
+  if (tokens < 0 || tokens > (int64_t(1) << 30) || hidden < 8 || hidden % 8 != 0) return BSGG_ERR_INVALID_ARG;
+  if (!is_float_format(token_format) || !is_float_format(weight_format) || !is_float_format(y_format))
+    return BSGG_ERR_INVALID_ARG;
+  return hidden > kNormMaxHidden ? BSGG_ERR_UNSUPPORTED : BSGG_OK;
+}
+
+// Calls f with the row format as a constant, BSGG_IN_BF16 standing for none.
+template <typename F>
+bsgg_status with_quantized(int fmt, F&& f) {
+  switch (fmt) {
+    case BSGG_IN_MXFP8_E4M3: return f(std::integral_constant<int, BSGG_IN_MXFP8_E4M3>());
+    case BSGG_IN_MXFP8_E5M2: return f(std::integral_constant<int, BSGG_IN_MXFP8_E5M2>());
+    case BSGG_IN_NVFP4: return f(std::integral_constant<int, BSGG_IN_NVFP4>());
+    case BSGG_IN_FP4_UE8M0_16: return f(std::integral_constant<int, BSGG_IN_FP4_UE8M0_16>());
+    case BSGG_IN_MXFP4: return f(std::integral_constant<int, BSGG_IN_MXFP4>());
+    default: return f(std::integral_constant<int, BSGG_IN_BF16>());
+  }
+}
+
+int64_t norm_bwd_blocks(int64_t tokens, int64_t hidden) {
+  const int64_t rows = row_shape(hidden).warp ? ceil_div(tokens, kNormWarpRows) : tokens;
+  return rows < kNormBwdBlocks ? rows : kNormBwdBlocks;
+}
+
+}  // namespace
+
+extern "C" {
+
+bsgg_status bsgg_rms_norm(const bsgg_norm_desc* d, const void* x, const void* residual, const void* weight, void* h,
+                          void* y, float* rstd, void* a, void* sfa, void* stream) {
+  if (!d) return BSGG_ERR_INVALID_ARG;
+  const bsgg_status st = check_norm(d->tokens, d->hidden, d->token_format, d->weight_format, d->y_format);
+  if (st == BSGG_ERR_INVALID_ARG || !std::isfinite(d->eps) || !(d->eps >= 0.0f)) return BSGG_ERR_INVALID_ARG;
+  const int tf = d->token_format;
+  if (!good_rows(d->ld_x, d->hidden, tf) || (residual && !good_rows(d->ld_residual, d->hidden, tf)) ||
+      (h && (!residual || !good_rows(d->ld_h, d->hidden, tf))) || (y && !good_rows(d->ld_y, d->hidden, d->y_format)))
+    return BSGG_ERR_INVALID_ARG;
+  if (a ? !sfa : sfa != nullptr) return BSGG_ERR_INVALID_ARG;
+  if (a) {
+    if (d->row_format < BSGG_IN_MXFP8_E4M3 || d->row_format > BSGG_IN_MXFP4 ||
+        d->hidden % (rf_fp4(d->row_format) ? 32 : 16) != 0 || d->m_pad <= 0 || d->m_pad % 128 != 0 || d->m_pad < d->tokens ||
+        d->m_pad > (int64_t(1) << 30))
+      return BSGG_ERR_INVALID_ARG;
+  }
+  if (d->tokens > 0 && (!x || (!y && !a))) return BSGG_ERR_INVALID_ARG;
+  if (!aligned_to(x, 16) || !aligned_to(residual, 16) || !aligned_to(weight, 16) || !aligned_to(h, 16) || !aligned_to(y, 16) ||
+      !aligned_to(rstd, 4) || !aligned_to(a, 16) || !aligned_to(sfa, 16))
+    return BSGG_ERR_INVALID_ARG;
+  if (st != BSGG_OK) return st;
+  const RowShape shape = row_shape(d->hidden);
+  const int64_t blocks = shape.warp ? ceil_div(d->tokens, kNormWarpRows) : d->tokens;
+  const int64_t pads = a ? ceil_div(d->m_pad - d->tokens, kNormPadRows) : 0;
+  if (blocks + pads == 0) return BSGG_OK;
+  NormParams p = {};
+  p.tokens = d->tokens; p.m_pad = d->m_pad; p.ld_x = d->ld_x; p.ld_residual = d->ld_residual; p.ld_h = d->ld_h; p.ld_y = d->ld_y;
+  p.hidden = static_cast<int>(d->hidden); p.weight_kind = d->weight_format; p.y_kind = d->y_format;
+  p.eps = d->eps; p.inv_hidden = 1.0f / static_cast<float>(d->hidden);
+  p.x = x; p.residual = residual; p.weight = weight; p.h = h; p.y = y; p.rstd = rstd;
+  p.a = static_cast<uint8_t*>(a); p.sfa = static_cast<uint8_t*>(sfa);
+  const LaunchConfig c(dim3(static_cast<unsigned>(blocks + pads)), shape.threads, 0, static_cast<cudaStream_t>(stream));
+  return with_float(tf, [&](auto kind) {
+    return with_quantized(a ? d->row_format : BSGG_IN_BF16, [&](auto fmt) {
+      return with_shape(shape, [&](auto nv, auto warp) {
+        constexpr int K = decltype(kind)::value, F = decltype(fmt)::value, N = decltype(nv)::value;
+        p.kq = rf_scaled(F) ? static_cast<int>(ceil_div(ceil_div(d->hidden, rf_vec(F)), 4)) : 0;
+        return launch_kernel(c, rms_norm_kernel<K, F, N, decltype(warp)::value>, p);
+      });
+    });
+  });
+}
+
+uint64_t bsgg_rms_norm_workspace_bytes(int64_t tokens, int64_t hidden) {
+  if (check_norm(tokens, hidden, 0, 0, 0) != BSGG_OK) return 0;
+  return uint64_t(4) * norm_bwd_blocks(tokens, hidden) * hidden;
+}
+
+bsgg_status bsgg_rms_norm_backward(const bsgg_norm_bwd_desc* d, const void* dy, const void* h, const void* weight,
+                                   const float* rstd, const void* dh, void* dx, float* dweight, void* workspace,
+                                   void* stream) {
+  if (!d || d->reserved != 0) return BSGG_ERR_INVALID_ARG;
+  const bsgg_status st = check_norm(d->tokens, d->hidden, d->token_format, d->weight_format, d->y_format);
+  if (st == BSGG_ERR_INVALID_ARG) return st;
+  const int tf = d->token_format;
+  if (!good_rows(d->ld_dy, d->hidden, d->y_format) || !good_rows(d->ld_h, d->hidden, tf) ||
+      (dh && !good_rows(d->ld_dh, d->hidden, tf)) || !good_rows(d->ld_dx, d->hidden, tf))
+    return BSGG_ERR_INVALID_ARG;
+  if (d->tokens > 0 && (!dy || !h || !rstd || !dx || (dweight && !workspace))) return BSGG_ERR_INVALID_ARG;
+  if (!aligned_to(dy, 16) || !aligned_to(h, 16) || !aligned_to(weight, 16) || !aligned_to(rstd, 4) || !aligned_to(dh, 16) ||
+      !aligned_to(dx, 16) || !aligned_to(dweight, 4) || !aligned_to(workspace, 16))
+    return BSGG_ERR_INVALID_ARG;
+  if (st != BSGG_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int hidden = static_cast<int>(d->hidden);
+  if (d->tokens == 0) {
+    // an empty sum
+    return !dweight || succeeded(cudaMemsetAsync(dweight, 0, sizeof(float) * hidden, s)) ? BSGG_OK : BSGG_ERR_CUDA;
+  }
+  NormBwdParams p = {};
+  p.tokens = d->tokens; p.ld_dy = d->ld_dy; p.ld_h = d->ld_h; p.ld_dh = d->ld_dh; p.ld_dx = d->ld_dx;
+  p.hidden = hidden; p.weight_kind = d->weight_format; p.inv_hidden = 1.0f / static_cast<float>(hidden);
+  p.dy = dy; p.h = h; p.weight = weight; p.dh = dh; p.rstd = rstd; p.dx = dx;
+  p.part = dweight ? static_cast<float*>(workspace) : nullptr;
+  const RowShape shape = row_shape(d->hidden);
+  const int64_t blocks = norm_bwd_blocks(d->tokens, d->hidden);
+  const LaunchConfig c(dim3(static_cast<unsigned>(blocks)), shape.threads, 0, s);
+  const bsgg_status ran = with_float(tf, [&](auto kind) {
+    return with_float(d->y_format, [&](auto ykind) {
+      return with_shape(shape, [&](auto nv, auto warp) {
+        constexpr int K = decltype(kind)::value, Y = decltype(ykind)::value, N = decltype(nv)::value;
+        return launch_kernel(c, rms_norm_backward_kernel<K, Y, N, decltype(warp)::value>, p);
+      });
+    });
+  });
+  if (ran != BSGG_OK || !dweight) return ran;
+  const LaunchConfig j(dim3(static_cast<unsigned>(ceil_div(hidden, 32))), 32 * kNormJoinWarps, 0, s);
+  return launch_kernel(j, norm_join_kernel, static_cast<const float*>(workspace), blocks, hidden, dweight);
+}
+
+}  // extern "C"

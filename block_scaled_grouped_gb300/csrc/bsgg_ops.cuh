@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/bsgg.h"
 #include "bsgg_kernel.cuh"
@@ -55,6 +56,38 @@ bsgg_status launch_kernel(const LaunchConfig& c, void (*kern)(P...), A... args) 
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool is_float_format(int f) { return f == BSGG_OUT_BF16 || f == BSGG_OUT_F16 || f == BSGG_OUT_F32; }
 inline int float_bytes(int f) { return f == BSGG_OUT_F32 ? 4 : 2; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Shared memory of a block of the cluster.
+__device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Order-preserving key of a logit: larger float, larger key; NaN above all;
+// -0 = +0.  -inf and below it is kMaskedKey.
+constexpr uint32_t kMaskedKey = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t logit_key(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
 
 // One element of a bf16, f16 or f32 tensor (KIND: OK_BF16, OK_F16, OK_F32).
 template <int KIND>
@@ -243,6 +276,44 @@ __device__ __forceinline__ uint32_t max_abs_bits16(const float (&v)[16]) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) m = max(m, __float_as_uint(v[k]) & 0x7FFFFFFFu);
   return m;
+}
+
+// The scale code of this thread's block (shared by rf_vec / 16 lanes), and the
+// word of the four blocks it lies in, complete in every lane: their bytes are
+// neighbours in the scale factors' layout.
+template <int FMT>
+__device__ __forceinline__ uint32_t block_code(const float (&v)[16], bool in, uint32_t& word) {
+  constexpr int kLanes = rf_vec(FMT) / 16;
+  uint32_t m = max_abs_bits16(v);
+  if (kLanes == 2) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  const uint32_t code = scale_code<FMT>(m);
+  word = in ? code << (8 * ((threadIdx.x / kLanes) & 3)) : 0u;
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, kLanes);
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * kLanes);
+  return code;
+}
+
+// ---------------------------------------------------------------- host
+// Calls f with the format (f: bf16, f16, f32) as a constant.
+template <typename F>
+inline bsgg_status with_float(int fmt, F&& f) {
+  switch (fmt) {
+    case BSGG_OUT_BF16: return f(std::integral_constant<int, OK_BF16>());
+    case BSGG_OUT_F16: return f(std::integral_constant<int, OK_F16>());
+    default: return f(std::integral_constant<int, OK_F32>());
+  }
+}
+template <typename F>
+inline bsgg_status with_rows(int fmt, F&& f) {
+  switch (fmt) {
+    case BSGG_IN_MXFP8_E4M3: return f(std::integral_constant<int, BSGG_IN_MXFP8_E4M3>());
+    case BSGG_IN_MXFP8_E5M2: return f(std::integral_constant<int, BSGG_IN_MXFP8_E5M2>());
+    case BSGG_IN_NVFP4: return f(std::integral_constant<int, BSGG_IN_NVFP4>());
+    case BSGG_IN_FP4_UE8M0_16: return f(std::integral_constant<int, BSGG_IN_FP4_UE8M0_16>());
+    case BSGG_IN_MXFP4: return f(std::integral_constant<int, BSGG_IN_MXFP4>());
+    case BSGG_ROW_F16: return f(std::integral_constant<int, BSGG_ROW_F16>());
+    default: return f(std::integral_constant<int, BSGG_IN_BF16>());
+  }
 }
 
 }  // namespace bsgg

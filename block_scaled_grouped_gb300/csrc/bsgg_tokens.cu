@@ -8,24 +8,6 @@ namespace {
 using namespace bsgg;
 
 // ---------------------------------------------------------------- routing
-// Order-preserving key of a logit: larger float, larger key; NaN above all;
-// -0 = +0.  -inf and below it is kMaskedKey.
-constexpr uint32_t kMaskedKey = 0x007FFFFFu;
-__device__ __forceinline__ uint32_t logit_key(float x) {
-  if (x != x) return 0xFFFFFFFFu;
-  const uint32_t u = __float_as_uint(x + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_logit(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
 constexpr int kRouteWarps = 4;
 
 // One warp per token; lane i holds logits i, i + 32, ... in registers.  Each of
@@ -393,21 +375,6 @@ constexpr int kRowThreads = 512, kMaxTopk = 32, kPadRows = 8;
 // in flight.
 constexpr int kRowValues = 16;
 
-// The scale code of this thread's block (shared by rf_vec / 16 lanes), and the
-// word of the four blocks it lies in, complete in every lane: their bytes are
-// neighbours in the scale factors' layout.
-template <int FMT>
-__device__ __forceinline__ uint32_t block_code(const float (&v)[16], bool in, uint32_t& word) {
-  constexpr int kLanes = rf_vec(FMT) / 16;
-  uint32_t m = max_abs_bits16(v);
-  if (kLanes == 2) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  const uint32_t code = scale_code<FMT>(m);
-  word = in ? code << (8 * ((threadIdx.x / kLanes) & 3)) : 0u;
-  word |= __shfl_xor_sync(0xFFFFFFFFu, word, kLanes);
-  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * kLanes);
-  return code;
-}
-
 // Blocks [0, tokens): one token each.  Its values are read once, and (without
 // weights) quantized once, for all of its rows: x is T H elements where the rows
 // are topk times that, and reading and quantizing per row took 276 us for 8192
@@ -623,8 +590,6 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineParams 
 }
 
 // ---------------------------------------------------------------- host
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 bsgg_status check_route(const bsgg_route_desc* d) {
   if (!d || d->tokens < 0 || d->tokens > (int64_t(1) << 30) || d->num_experts < 1 || d->num_experts > 1024)
     return BSGG_ERR_INVALID_ARG;
@@ -643,28 +608,6 @@ bsgg_status with_route_regs(int L, F&& f) {
   if (L <= 256) return f(std::integral_constant<int, 8>());
   if (L <= 512) return f(std::integral_constant<int, 16>());
   return f(std::integral_constant<int, 32>());
-}
-
-// Calls f with the format (f: bf16, f16, f32) as a constant.
-template <typename F>
-bsgg_status with_float(int fmt, F&& f) {
-  switch (fmt) {
-    case BSGG_OUT_BF16: return f(std::integral_constant<int, OK_BF16>());
-    case BSGG_OUT_F16: return f(std::integral_constant<int, OK_F16>());
-    default: return f(std::integral_constant<int, OK_F32>());
-  }
-}
-template <typename F>
-bsgg_status with_rows(int fmt, F&& f) {
-  switch (fmt) {
-    case BSGG_IN_MXFP8_E4M3: return f(std::integral_constant<int, BSGG_IN_MXFP8_E4M3>());
-    case BSGG_IN_MXFP8_E5M2: return f(std::integral_constant<int, BSGG_IN_MXFP8_E5M2>());
-    case BSGG_IN_NVFP4: return f(std::integral_constant<int, BSGG_IN_NVFP4>());
-    case BSGG_IN_FP4_UE8M0_16: return f(std::integral_constant<int, BSGG_IN_FP4_UE8M0_16>());
-    case BSGG_IN_MXFP4: return f(std::integral_constant<int, BSGG_IN_MXFP4>());
-    case BSGG_ROW_F16: return f(std::integral_constant<int, BSGG_ROW_F16>());
-    default: return f(std::integral_constant<int, BSGG_IN_BF16>());
-  }
 }
 
 // What dispatch, combine and combine_backward share.

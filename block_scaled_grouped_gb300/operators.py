@@ -3,7 +3,10 @@
 ``route`` (softmax top-k) -> ``sort_tokens`` (tokens by expert, rows padded to
 128) -> ``dispatch`` (rows quantized into A and SFA) -> the grouped GEMMs ->
 ``combine`` (rows back to tokens), the dense layers beside the experts
-(``linear``), and their gradients.  As in the rest of the binding nothing is
+(``linear``), and their gradients; in front of them ``rms_norm`` (residual added,
+out in 16 bits and as quantized rows) and ``route_groups`` (softmax or sigmoid scores,
+a bias, groups of experts); beside the dense layers ``adapters`` (low-rank adapters of
+many requests at once).  As in the rest of the binding nothing is
 computed here: shapes and types are checked, outputs allocated (on the stream the
 call runs on), and the C ABI's entry points called.  ``include/bsgg.h`` states
 each operator's formula, layouts and errors.
@@ -47,6 +50,42 @@ class LinearBwdDesc(ctypes.Structure):
                [(n, ctypes.c_int32) for n in ("in_format", "dx_format", "dw_format", "activation", "accumulate_dw")]
 
 
+class RouteGroupsDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("ld", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("num_experts", "topk", "groups", "topk_groups", "group_top", "score", "logit_format",
+                                              "normalize")] + [("scale", ctypes.c_float)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "hidden", "m_pad", "ld_x", "ld_residual", "ld_h", "ld_y")] + \
+               [(n, ctypes.c_int32) for n in ("token_format", "weight_format", "y_format", "row_format")] + [("eps", ctypes.c_float)]
+
+
+class NormBwdDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "hidden", "ld_dy", "ld_h", "ld_dh", "ld_dx")] + \
+               [(n, ctypes.c_int32) for n in ("token_format", "weight_format", "y_format", "reserved")]
+
+
+class AdaptersDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "k", "n", "m_pad", "ldx", "ld_base", "ldy")] + \
+               [(n, ctypes.c_int32) for n in ("adapters", "rank", "format", "reserved")]
+
+
+class AdaptersBwdDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "k", "n", "m_pad", "ld_dy", "ldx", "ld_base", "ld_dx")] + \
+               [(n, ctypes.c_int32) for n in ("adapters", "rank", "format", "grad_format")]
+
+
+class Norm(NamedTuple):
+    """rms_norm's outputs, None where not wanted: y (tokens, hidden), h (the sum with the
+    residual), rstd (tokens), and the quantized rows a with their scale factors sfa."""
+    y: "object"
+    h: "object"
+    rstd: "object"
+    a: "object"
+    sfa: "object"
+
+
 class TokenMap(NamedTuple):
     """bsgg_sort_tokens' outputs: padded_offsets (num_experts), row_of_slot
     (tokens, topk), slot_of_row (m_pad), prob (m_pad) and rows_used (1)."""
@@ -71,7 +110,16 @@ def bind(L) -> None:
     L.bsgg_linear.argtypes = [ctypes.POINTER(LinearDesc)] + [vp] * 8
     L.bsgg_linear_backward.argtypes = [ctypes.POINTER(LinearBwdDesc)] + [vp] * 10
     L.bsgg_query_status_word.argtypes = [vp, vp]
-    for name in ("bsgg_route", "bsgg_route_backward", "bsgg_sort_tokens", "bsgg_dispatch", "bsgg_combine",
+    L.bsgg_route_groups.argtypes = [ctypes.POINTER(RouteGroupsDesc)] + [vp] * 5
+    L.bsgg_route_groups_backward.argtypes = [ctypes.POINTER(RouteGroupsDesc)] + [vp] * 5 + [i64, vp, vp]
+    L.bsgg_rms_norm.argtypes = [ctypes.POINTER(NormDesc)] + [vp] * 9
+    L.bsgg_rms_norm_workspace_bytes.restype, L.bsgg_rms_norm_workspace_bytes.argtypes = ctypes.c_uint64, [i64, i64]
+    L.bsgg_rms_norm_backward.argtypes = [ctypes.POINTER(NormBwdDesc)] + [vp] * 9
+    L.bsgg_adapters.argtypes = [ctypes.POINTER(AdaptersDesc)] + [vp] * 11
+    L.bsgg_adapters_backward.argtypes = [ctypes.POINTER(AdaptersBwdDesc)] + [vp] * 15
+    for name in ("bsgg_route_groups", "bsgg_route_groups_backward", "bsgg_rms_norm", "bsgg_rms_norm_backward", "bsgg_adapters",
+                 "bsgg_adapters_backward",
+                 "bsgg_route", "bsgg_route_backward", "bsgg_sort_tokens", "bsgg_dispatch", "bsgg_combine",
                  "bsgg_combine_backward", "bsgg_linear", "bsgg_linear_backward", "bsgg_query_status_word"):
         getattr(L, name).restype = ctypes.c_int
 
@@ -462,3 +510,224 @@ def linear_backward(dy, x, w, z=None, activation: str = "none", want_dx: bool = 
                                       *(v.data_ptr() if v is not None else None for v in (dz, dx, dw, dbias)),
                                       _status_of(dy, status), handle), "bsgg_linear_backward")
     return dx, dw, dbias
+
+
+# ---------------------------------------------------------------- routing with scores and groups
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(name: str) -> int:
+    s = SCORES.get(name)
+    if s is None:
+        raise ValueError(f"score: one of {sorted(SCORES)} expected, got {name!r}")
+    return s
+
+
+def route_groups(logits, topk: int, score: str = "sigmoid", bias=None, groups: int = 1, topk_groups: int = 1, group_top: int = 2,
+                 normalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """Top-k of (tokens, experts) logits by their softmax or sigmoid scores plus a bias
+    (float32, experts), among the topk_groups of `groups` runs of experts whose group_top
+    best add up to most: (ids int32, weights float32), each (tokens, topk).  The weights are
+    the scores without the bias, over their sum if normalize, times scale."""
+    ld = _matrix(logits, "logits")
+    T, L = logits.shape
+    k = int(topk)
+    desc = RouteGroupsDesc(T, ld, L, k, int(groups), int(topk_groups), int(group_top), _score(score), _format(logits, "logits"),
+                           1 if normalize else 0, scale)
+    handle = _handle(stream, logits, bias, ids, weights)
+    if ids is None or weights is None:
+        empty, dev = _empty_on(stream), logits.device
+        if ids is None:
+            ids = empty((T, max(k, 0)), dtype=_I32, device=dev)
+        if weights is None:
+            weights = empty((T, max(k, 0)), dtype=_F32, device=dev)
+    _check(lib().bsgg_route_groups(byref(desc), logits.data_ptr(), _flat(bias, "bias", L, _F32), _flat(ids, "ids", T * k, _I32),
+                                   _flat(weights, "weights", T * k, _F32), handle), "bsgg_route_groups")
+    return ids, weights
+
+
+def route_groups_backward(logits, ids, weights, dweights, score: str = "sigmoid", normalize: bool = True, scale: float = 1.0,
+                          row_of_slot=None, dlogits=None, stream=None):
+    """Gradient of route_groups with respect to the logits, in their type; score,
+    normalize and scale as they were.  dweights is (tokens, topk), or with row_of_slot a
+    per-row gradient (the backward GEMM's dprob)."""
+    ld = _matrix(logits, "logits")
+    T, L = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids: ({T}, topk) expected, got {tuple(ids.shape)}")
+    n = ids.numel()
+    rows = 0 if row_of_slot is None else dweights.numel()
+    desc = RouteGroupsDesc(T, ld, L, ids.shape[1], 1, 1, 1, _score(score), _format(logits, "logits"), 1 if normalize else 0, scale)
+    handle = _handle(stream, logits, ids, weights, dweights, row_of_slot, dlogits)
+    if dlogits is None:
+        # the logits' pitch, so that one desc serves both
+        dlogits = _empty_on(stream)((T, ld), dtype=logits.dtype, device=logits.device)
+        if ld != L:
+            dlogits = dlogits[:, :L]
+    elif _matrix(dlogits, "dlogits", T, L, logits.dtype) != ld:
+        raise ValueError("dlogits: the logits' row pitch expected")
+    _check(lib().bsgg_route_groups_backward(byref(desc), logits.data_ptr(), _flat(ids, "ids", n, _I32),
+                                            _flat(weights, "weights", n, _F32), _flat(dweights, "dweights", rows or n, _F32),
+                                            _flat(row_of_slot, "row_of_slot", n, _I32), rows, dlogits.data_ptr(), handle),
+           "bsgg_route_groups_backward")
+    return dlogits
+
+
+# ---------------------------------------------------------------- norm
+def _vector(t, what: str, numel: int):
+    """The address and format of a contiguous vector on the GPU (None passes)."""
+    if t is None:
+        return None, 0
+    if t.numel() != numel or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: {numel} contiguous values on the GPU expected, got {tuple(t.shape)} on {t.device}")
+    return t.data_ptr(), _format(t, what)
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out_format: Optional[str] = None, want_y: bool = True,
+             row_format: Optional[str] = None, m_pad: Optional[int] = None, want_rstd: bool = True, h=None, stream=None) -> Norm:
+    """Root-mean-square norm of h = x + residual (tokens, hidden): y = h rstd weight in
+    out_format (by default x's type), and with a row_format the same values quantized into
+    rows of a grouped GEMM's A, m_pad of them (by default the tokens rounded up to 128), and
+    their scale factors.  The sum goes into a given h (x and residual will do) or a new one."""
+    ldx = _matrix(x, "x")
+    T, H = x.shape
+    xt = x.dtype
+    ldr = _matrix(residual, "residual", T, H, xt) if residual is not None else 0
+    p_w, fw = _vector(weight, "weight", H)
+    dt = xt if out_format is None else _dtype(out_format)
+    handle = _handle(stream, x, weight, residual, h)
+    empty, dev = _empty_on(stream), x.device
+    ldh = 0
+    if residual is not None:
+        if h is None:
+            h, ldh = empty((T, H), dtype=xt, device=dev), H
+        else:
+            ldh = _matrix(h, "h", T, H, xt)
+    elif h is not None:
+        raise ValueError("h: without a residual it would be x")
+    y = empty((T, H), dtype=dt, device=dev) if want_y else None
+    rstd = empty(T, dtype=_F32, device=dev) if want_rstd else None
+    a = sfa = None
+    rows = 0
+    rf = 0
+    if row_format is not None:
+        rf = _row_format(row_format)
+        if row_format in ("bf16", "f16"):
+            raise ValueError(f"row format: one with scale factors expected, got {row_format!r} (y has 16 bits)")
+        rows = max(128, (T + 127) // 128 * 128) if m_pad is None else int(m_pad)
+        a, sfa = _row_buffers(max(rows, 0), H, row_format, dev, empty)
+    desc = NormDesc(T, H, rows, ldx, ldr, ldh, H, _format(x, "x"), fw, _FORMATS[dt], rf, eps)
+    _check(lib().bsgg_rms_norm(byref(desc), x.data_ptr(), residual.data_ptr() if residual is not None else None, p_w,
+                               *(v.data_ptr() if v is not None else None for v in (h, y, rstd, a, sfa)), handle), "bsgg_rms_norm")
+    return Norm(y, h, rstd, a, sfa)
+
+
+def rms_norm_backward(dy, h, weight, rstd, dh=None, want_dweight: bool = True, dx=None, stream=None):
+    """Gradient of rms_norm: (dx, dweight); dx, in h's type, is that of x and of the residual
+    alike, dh (what reaches h past the norm) added.  dweight is float32, None where not
+    wanted.  dx goes into a given tensor (dh will do) or a new one."""
+    ld_dy = _matrix(dy, "dy")
+    T, H = dy.shape
+    ldh = _matrix(h, "h", T, H)
+    ht = h.dtype
+    ld_dh = _matrix(dh, "dh", T, H, ht) if dh is not None else 0
+    p_w, fw = _vector(weight, "weight", H)
+    handle = _handle(stream, dy, h, weight, rstd, dh, dx)
+    empty, dev = _empty_on(stream), dy.device
+    if dx is None:
+        dx, ld_dx = empty((T, H), dtype=ht, device=dev), H
+    else:
+        ld_dx = _matrix(dx, "dx", T, H, ht)
+    L = lib()
+    dw = ws = None
+    if want_dweight:
+        dw = empty(H, dtype=_F32, device=dev)
+        ws = empty(L.bsgg_rms_norm_workspace_bytes(T, H) // 4, dtype=_F32, device=dev)
+    desc = NormBwdDesc(T, H, ld_dy, ldh, ld_dh, ld_dx, _format(h, "h"), fw, _format(dy, "dy"), 0)
+    _check(L.bsgg_rms_norm_backward(byref(desc), dy.data_ptr(), h.data_ptr(), p_w, _flat(rstd, "rstd", T, _F32),
+                                    *(v.data_ptr() if v is not None else None for v in (dh, dx, dw, ws)), handle),
+           "bsgg_rms_norm_backward")
+    return dx, dw
+
+
+# ---------------------------------------------------------------- adapters
+def _adapter_weights(a, b, dtype):
+    """(adapters, rank, k, n) of dense A (adapters, rank, k) and B (adapters, rank, n)."""
+    if a.dim() != 3 or b.dim() != 3 or a.shape[:2] != b.shape[:2]:
+        raise ValueError(f"a, b: (adapters, rank, k) and (adapters, rank, n) expected, got {tuple(a.shape)} and {tuple(b.shape)}")
+    for t, what in ((a, "a"), (b, "b")):
+        if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what}: contiguous {dtype} on the GPU expected, got {t.dtype} on {t.device}")
+    return a.shape[0], a.shape[1], a.shape[2], b.shape[2]
+
+
+def _adapter_map(tokens: TokenMap, T: int, adapters: int):
+    """m_pad and the addresses of a TokenMap of one adapter per token."""
+    k, p_rows = _slots_of(tokens.row_of_slot, T)
+    if k != 1:
+        raise ValueError(f"tokens: one adapter per token expected, got {k}")
+    m_pad = tokens.slot_of_row.numel()
+    return m_pad, _flat(tokens.padded_offsets, "padded_offsets", adapters, _I32), p_rows, \
+        _flat(tokens.slot_of_row, "slot_of_row", m_pad, _I32)
+
+
+def adapters(x, a, b, tokens: TokenMap, scales=None, base=None, out=None, stream=None):
+    """Low-rank adapters beside a dense layer: y = base + scales_i (x A_i^T) B_i, i each token's
+    adapter: x (tokens, k), a (adapters, rank, k), b (adapters, rank, n), base (tokens, n; None:
+    zeros), all bfloat16 or float16, scales float32 (adapters) -> (y, u), u = x A_i^T float32
+    (tokens, rank) for the backward.  `tokens` is sort_tokens of the tokens' adapters
+    (tokens, 1), -1 for none.  y goes into a given out (base will do) or a new tensor."""
+    xt = x.dtype
+    ldx = _matrix(x, "x")
+    T = x.shape[0]
+    S, r, K, N = _adapter_weights(a, b, xt)
+    _matrix(x, "x", T, K)
+    ldb = _matrix(base, "base", T, N, xt) if base is not None else 0
+    m_pad, p_off, p_row, p_slot = _adapter_map(tokens, T, S)
+    handle = _handle(stream, x, a, b, tokens.padded_offsets, tokens.row_of_slot, tokens.slot_of_row, scales, base, out)
+    empty, dev = _empty_on(stream), x.device
+    if out is None:
+        y, ldy = empty((T, N), dtype=xt, device=dev), N
+    else:
+        y, ldy = out, _matrix(out, "out", T, N, xt)
+    u = empty((T, r), dtype=_F32, device=dev)
+    desc = AdaptersDesc(T, K, N, m_pad, ldx, ldb, ldy, S, r, _format(x, "x"), 0)
+    _check(lib().bsgg_adapters(byref(desc), x.data_ptr(), a.data_ptr(), b.data_ptr(), _flat(scales, "scales", S, _F32), p_off,
+                               p_row, p_slot, base.data_ptr() if base is not None else None, u.data_ptr(), y.data_ptr(), handle),
+           "bsgg_adapters")
+    return y, u
+
+
+def adapters_backward(dy, x, u, a, b, tokens: TokenMap, scales=None, base=None, want_dx: bool = True, want_da: bool = True,
+                      want_db: bool = True, grad_format: Optional[str] = None, dx=None, stream=None):
+    """Gradient of adapters: (dx, da, db), each None where not wanted.  dx (tokens, k) is
+    base (the dense layer's own dx; None: zeros) plus the adapters' share, and goes into a
+    given tensor (base will do) or a new one; da and db, dense like a and b, are in
+    grad_format (by default x's type), zeros for an adapter without tokens."""
+    t = dy.dtype
+    ld_dy = _matrix(dy, "dy")
+    T = dy.shape[0]
+    S, r, K, N = _adapter_weights(a, b, t)
+    _matrix(dy, "dy", T, N)
+    ldx = _matrix(x, "x", T, K, t)
+    ldb = _matrix(base, "base", T, K, t) if base is not None else 0
+    m_pad, p_off, p_row, p_slot = _adapter_map(tokens, T, S)
+    handle = _handle(stream, dy, x, u, a, b, tokens.padded_offsets, tokens.row_of_slot, tokens.slot_of_row, scales, base, dx)
+    empty, dev = _empty_on(stream), dy.device
+    ld_dx = 0
+    if not want_dx:
+        dx = None
+    elif dx is None:
+        dx, ld_dx = empty((T, K), dtype=t, device=dev), K
+    else:
+        ld_dx = _matrix(dx, "dx", T, K, t)
+    gt = t if grad_format is None else _dtype(grad_format)
+    da = empty((S, r, K), dtype=gt, device=dev) if want_da else None
+    db = empty((S, r, N), dtype=gt, device=dev) if want_db else None
+    du = empty((T, r), dtype=_F32, device=dev) if want_dx or want_da else None
+    desc = AdaptersBwdDesc(T, K, N, m_pad, ld_dy, ldx, ldb, ld_dx, S, r, _format(dy, "dy"), _FORMATS[gt])
+    _check(lib().bsgg_adapters_backward(byref(desc), dy.data_ptr(), x.data_ptr(), _flat(u, "u", T * r, _F32), a.data_ptr(),
+                                        b.data_ptr(), _flat(scales, "scales", S, _F32), p_off, p_row, p_slot,
+                                        *(v.data_ptr() if v is not None else None for v in (base, du, dx, da, db)), handle),
+           "bsgg_adapters_backward")
+    return dx, da, db

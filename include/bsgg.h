@@ -611,6 +611,150 @@ BSGG_API bsgg_status bsgg_linear_backward(const bsgg_linear_bwd_desc* desc, cons
                                           const void* w, const void* z, void* dz, void* dx, void* dw,
                                           float* dbias, uint32_t* status, void* stream);
 
+/* Routing of layers with many experts: scores that may be sigmoids, a bias that
+ * only steers the choice, experts in groups.  For a row l of logits:
+ *   s   = softmax(l) (BSGG_SCORE_SOFTMAX) or 1 / (1 + e^-l) (BSGG_SCORE_SIGMOID)
+ *   c   = s + bias  (bias NULL: s)
+ *   the experts are `groups` runs of num_experts / groups; a group's score is the
+ *   sum of its group_top (1 or 2) largest c, and the topk_groups best groups stay
+ *   ids = the topk largest c of those groups, largest first
+ *   weights = scale * s_id (normalize = 0) or scale * s_id / sum of s over the chosen
+ * Equal ones go by lowest index, groups as well as experts; c and the groups' scores
+ * are compared as if they had been computed in 64 bits (where 32 do not decide, the
+ * kernel computes them so).  An expert whose logit or bias is -inf is never chosen:
+ * where fewer than topk are left the id is -1 and its weight 0.  Without a bias experts
+ * are ordered by their logits, a NaN as the largest; with one a NaN score or bias counts
+ * as the largest.  A NaN among the chosen scores makes the row's weights NaN. */
+typedef enum { BSGG_SCORE_SOFTMAX = 0, BSGG_SCORE_SIGMOID = 1 } bsgg_score;
+
+typedef struct {
+  int64_t tokens;         /* 0..2^30; 0 launches nothing */
+  int64_t ld;             /* row pitch of logits and dlogits in elements, >= num_experts */
+  int32_t num_experts;    /* 1..1024 */
+  int32_t topk;           /* 1..32, at most the experts of topk_groups groups */
+  int32_t groups;         /* 1..32, divides num_experts */
+  int32_t topk_groups;    /* 1..groups */
+  int32_t group_top;      /* 1 or 2 */
+  int32_t score;          /* bsgg_score */
+  int32_t logit_format;   /* f: logits, and dlogits of the backward */
+  int32_t normalize;      /* 0 or 1 */
+  float scale;            /* finite, > 0 */
+} bsgg_route_groups_desc;
+
+BSGG_API bsgg_status bsgg_route_groups(const bsgg_route_groups_desc* desc, const void* logits, const float* bias,
+                                       int32_t* ids, float* weights, void* stream);
+
+/* Gradient of bsgg_route_groups with respect to the logits, given the ids and weights
+ * it returned (a row's ids differ from one another) and g = dweights, with
+ * inner = sum_j g_j w_j / scale:
+ *   softmax, normalize = 1   dlogits_i = w_i (g_i - inner) for the chosen i, 0 elsewhere
+ *   softmax, normalize = 0   dlogits_i = scale s_i (g_i [i chosen] - inner)
+ *   sigmoid, normalize = 1   dlogits_i = w_i (1 - s_i) (g_i - inner) for the chosen i, 0 elsewhere
+ *   sigmoid, normalize = 0   dlogits_i = w_i (1 - s_i) g_i for the chosen i, 0 elsewhere
+ * The choice itself (and so the bias) has no gradient.  row_of_slot and m_pad as in
+ * bsgg_route_backward; groups, topk_groups and group_top are not read. */
+BSGG_API bsgg_status bsgg_route_groups_backward(const bsgg_route_groups_desc* desc, const void* logits,
+                                                const int32_t* ids, const float* weights, const float* dweights,
+                                                const int32_t* row_of_slot, int64_t m_pad, void* dlogits, void* stream);
+
+/* Root-mean-square norm in front of the router and the experts:
+ *   h = x + residual, rounded to token_format (without a residual h is x)
+ *   rstd = 1 / sqrt(mean of h^2 over the row + eps)
+ *   y = h * rstd * weight   (weight NULL: ones), rounded to y_format
+ *   a, sfa = the same unrounded values quantized as bsgg_dispatch does, token t in row t of
+ *            the grouped GEMM's A: the rows from `tokens` to m_pad are 0 with scale 1
+ * What is normed is the rounded h, which is what the backward is given.  Each of h, y, rstd
+ * and a (with sfa) may be NULL: not wanted (one of y and a is); h is NULL without a residual.
+ * h may be x or the residual itself, y may be x where their formats and pitches are the same. */
+typedef struct {
+  int64_t tokens;         /* 0..2^30 */
+  int64_t hidden;         /* 8..32768 (BSGG_ERR_UNSUPPORTED beyond), a multiple of 8, for rows of 16 (FP8) or 32 (FP4) */
+  int64_t m_pad;          /* rows of a: a multiple of 128, >= tokens; not read without a */
+  int64_t ld_x, ld_residual, ld_h, ld_y;   /* row pitches in elements, >= hidden (not read for an absent tensor) */
+  int32_t token_format;   /* f: x, residual, h */
+  int32_t weight_format;  /* f */
+  int32_t y_format;       /* f */
+  int32_t row_format;     /* a bsgg_in_format with scale factors (0..4); not read without a */
+  float eps;              /* finite, >= 0 */
+} bsgg_norm_desc;
+
+BSGG_API bsgg_status bsgg_rms_norm(const bsgg_norm_desc* desc, const void* x, const void* residual, const void* weight,
+                                   void* h, void* y, float* rstd, void* a, void* sfa, void* stream);
+
+/* Gradient of bsgg_rms_norm, given h (x where there was no residual), rstd, dy and
+ * optionally dh, the gradient that reaches h on the residual stream.  With n = h * rstd:
+ *   dx = rstd * (dy * weight - n * mean of (dy * weight * n) over the row) + dh
+ *   dweight = sum over the tokens of dy * n      (float, hidden values)
+ * dx is the gradient of x and of the residual alike.  dh and dweight may be NULL (dweight:
+ * not wanted; without tokens it is zeros).  dx may be dy or dh itself where the formats and
+ * pitches are the same.  workspace: bsgg_rms_norm_workspace_bytes(tokens, hidden) bytes with
+ * a dweight, 16-byte aligned; it is free once the call's work on the stream is done. */
+typedef struct {
+  int64_t tokens;
+  int64_t hidden;         /* as in bsgg_norm_desc */
+  int64_t ld_dy, ld_h, ld_dh, ld_dx;
+  int32_t token_format;   /* f: h, dh, dx */
+  int32_t weight_format;  /* f */
+  int32_t y_format;       /* f: dy */
+  int32_t reserved;       /* 0 */
+} bsgg_norm_bwd_desc;
+
+BSGG_API uint64_t bsgg_rms_norm_workspace_bytes(int64_t tokens, int64_t hidden);
+BSGG_API bsgg_status bsgg_rms_norm_backward(const bsgg_norm_bwd_desc* desc, const void* dy, const void* h,
+                                            const void* weight, const float* rstd, const void* dh, void* dx,
+                                            float* dweight, void* workspace, void* stream);
+
+/* Low-rank adapters of many requests at once, beside a dense layer.  Token t has adapter
+ * i = i(t), or none:
+ *   u[t] = x[t] A_i^T                        (rank values, float, kept for the backward)
+ *   y[t] = base[t] + scales[i] * u[t] B_i    (scales NULL: ones; base NULL: zeros)
+ * and without an adapter u[t] = 0, y[t] = base[t].  A is (adapters, rank, k) and B is
+ * (adapters, rank, n), both dense: B's rows lie along n, the transpose of an (n, rank)
+ * weight, so that both products and all gradients read rows.  x, A, B, base and y are in
+ * `format` (bfloat16 or float16); u is rounded nowhere, y once.  base may be y.
+ * The tokens' adapters come as bsgg_sort_tokens writes them for ids (tokens, 1), -1 for
+ * none: padded_offsets (adapters), row_of_slot (tokens), slot_of_row (m_pad); one sort
+ * serves all layers of a step.  k, n multiples of 8, rank a multiple of 8 up to 128; all
+ * of x, A, B, base, y and u 16-byte aligned with pitches that are multiples of 8. */
+typedef struct {
+  int64_t tokens;         /* 0..2^30 */
+  int64_t k, n;           /* 8..2^24 */
+  int64_t m_pad;          /* rows of slot_of_row: a positive multiple of 128 */
+  int64_t ldx, ld_base, ldy;   /* row pitches in elements (ld_base is not read without a base) */
+  int32_t adapters;       /* 1..1024 */
+  int32_t rank;
+  int32_t format;         /* BSGG_OUT_BF16 or BSGG_OUT_F16 */
+  int32_t reserved;       /* 0 */
+} bsgg_adapters_desc;
+
+BSGG_API bsgg_status bsgg_adapters(const bsgg_adapters_desc* desc, const void* x, const void* a, const void* b,
+                                   const float* scales, const int32_t* padded_offsets, const int32_t* row_of_slot,
+                                   const int32_t* slot_of_row, const void* base, float* u, void* y, void* stream);
+
+/* Gradient of bsgg_adapters, given dy (tokens, n) and the forward's u:
+ *   du[t] = scales[i] * dy[t] B_i^T     (tokens, rank) float, the caller's buffer
+ *   dx[t] = base[t] + du[t] A_i         base: the dense layer's own dx (NULL: zeros); may be dx
+ *   da_i  = sum over its tokens of du[t]^T x[t],   db_i = sum of (scales[i] u[t])^T dy[t]
+ * da and db are dense like A and B, in grad_format, zeros for an adapter without tokens.
+ * dx, da and db may each be NULL: not wanted (x, u, a are then not read where only they need them).
+ * The scales are constants: they get no gradient. */
+typedef struct {
+  int64_t tokens;
+  int64_t k, n;
+  int64_t m_pad;
+  int64_t ld_dy, ldx, ld_base, ld_dx;
+  int32_t adapters;
+  int32_t rank;
+  int32_t format;
+  int32_t grad_format;    /* f: da, db */
+} bsgg_adapters_bwd_desc;
+
+BSGG_API bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* desc, const void* dy, const void* x,
+                                            const float* u, const void* a, const void* b, const float* scales,
+                                            const int32_t* padded_offsets, const int32_t* row_of_slot,
+                                            const int32_t* slot_of_row, const void* base, float* du, void* dx, void* da,
+                                            void* db, void* stream);
+
 /* Synchronize `stream`, then read a status word that the operators above were
  * given and clear what was read (a report that a kernel on another stream makes
  * meanwhile stays for the next call): BSGG_OK, BSGG_ERR_BAD_OFFSETS (m_pad too

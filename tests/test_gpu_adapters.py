@@ -1,0 +1,272 @@
+"""Low-rank adapters on the GPU against 64-bit references: ranks, widths and adapters'
+shares of the tokens from one up, tokens without an adapter, adapters without a token,
+both types, pitches, in place, and gradients."""
+import math
+
+import pytest
+import torch
+
+import block_scaled_grouped_gb300 as bsgg
+import layer_operator_refs as R
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+ROUND = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -149}
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def pitched(t, extra):
+    """t on the GPU as a view of a wider buffer (extra columns, poisoned)."""
+    buf = torch.full((t.shape[0], t.shape[1] + extra), math.nan, dtype=t.dtype, device="cuda")
+    buf[:, :t.shape[1]] = t.cuda()
+    return buf[:, :t.shape[1]]
+
+
+def rounding(ref, dtype):
+    return ref.abs() * ROUND[dtype] + TINY[dtype]
+
+
+def product_error(depth):
+    """Bound on |error| / sum |a b| of a product accumulated in 32 bits: steps of 16 products,
+    each added with one rounding or truncation of 2^-23, and as much again for the joins."""
+    return (depth / 16 + 32) * 2.0 ** -23
+
+
+# u's and du's terms: two of bfloat16 hold them to 2^-17 (2^-16 where both are rounded up), two
+# of float16 to 2^-21 of the row's largest, three of bfloat16 to 2^-24
+TERMS = {torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -20}
+
+
+def problem(T, S, r, K, N, dtype, kind, seed):
+    g = gen(seed)
+    dt = DT[dtype]
+    if kind == "one":
+        ids = torch.full((T,), S - 1)
+    elif kind == "none":
+        ids = torch.full((T,), -1)
+    else:
+        ids = torch.randint(-1, S, (T,), generator=g)
+        if kind == "runs":
+            ids = ids[torch.cummax(torch.where(torch.rand(T, generator=g) < 0.02, torch.arange(T), torch.zeros(T, dtype=torch.long)), 0).values]
+    return dict(ids=ids.to(torch.int32), x=torch.randn(T, K, generator=g).to(dt), a=(torch.randn(S, r, K, generator=g) / K ** 0.5).to(dt),
+                b=(torch.randn(S, r, N, generator=g) / r ** 0.5).to(dt), scales=torch.rand(S, generator=g) + 0.5,
+                base=torch.randn(T, N, generator=g).to(dt), dy=torch.randn(T, N, generator=g).to(dt), basex=torch.randn(T, K, generator=g).to(dt))
+
+
+def map_of(p, S, m_pad=None):
+    return bsgg.sort_tokens(p["ids"].cuda().view(-1, 1), S, m_pad=m_pad)
+
+
+# tokens, adapters, rank, k, n, type, tokens' adapters
+CASES = [(1, 1, 8, 8, 8, "bf16", "one"), (1, 4, 16, 2048, 512, "f16", "any"), (3, 2, 16, 64, 72, "bf16", "any"), (17, 1, 24, 136, 520, "f16", "one"),
+         (16, 3, 32, 256, 1024, "bf16", "any"), (40, 1, 8, 4096, 64, "bf16", "one"), (33, 1, 40, 72, 200, "bf16", "one"),
+         (64, 5, 64, 320, 1032, "f16", "any"), (65, 1, 128, 128, 136, "bf16", "one"), (130, 1, 128, 200, 600, "f16", "one"),
+         (70, 1, 56, 1000, 264, "bf16", "one"), (100, 2, 72, 88, 520, "bf16", "any"), (128, 64, 16, 512, 640, "bf16", "any"),
+         (300, 3, 16, 256, 512, "f16", "runs"), (600, 2, 32, 128, 2056, "bf16", "runs"), (20, 1, 120, 64, 64, "f16", "one"),
+         (9, 3, 16, 64, 64, "bf16", "none"), (50, 1000, 8, 64, 64, "f16", "any"), (120, 1, 112, 640, 1096, "bf16", "one")]
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_adapters(case):
+    T, S, r, K, N, dtype, kind = case
+    p = problem(*case, seed=T + r)
+    t = map_of(p, S)
+    want, want_u = R.adapters(p["x"], p["a"], p["b"], p["ids"], p["scales"], p["base"])
+    dev = dict(scales=p["scales"].cuda(), base=pitched(p["base"], 8))
+    y, u = bsgg.adapters(pitched(p["x"], 24), p["a"].cuda(), p["b"].cuda(), t, **dev)
+    at = p["ids"].clamp(min=0).long()
+    sizes = torch.einsum("tk,trk->tr", p["x"].double().abs(), p["a"].double().abs()[at])
+    utol = sizes * product_error(K)
+    assert ((u.cpu().double() - want_u).abs() <= utol + 1e-38).all()
+    dt = DT[dtype]
+    # of the row's largest |u| for the terms; b's products in up to 8 steps of 16
+    largest = want_u.abs().amax(1, keepdim=True)
+    f = p["scales"].double()[at][:, None]
+    bs = p["b"].double().abs()[at]
+    tol = f * (torch.einsum("tr,trn->tn", utol + largest * TERMS[dt], bs) +
+               torch.einsum("tr,trn->tn", want_u.abs(), bs) * product_error(2 * r))
+    tol = torch.where((p["ids"] >= 0)[:, None], tol, torch.zeros_like(tol))
+    assert ((y.cpu().double() - want).abs() <= tol + want.abs() * 2.0 ** -23 + rounding(want, dt)).all()
+    none = p["ids"] < 0
+    assert torch.equal(y.cpu()[none], p["base"][none]) and (u.cpu()[none] == 0).all()
+    # in place, and into a wider buffer
+    into = pitched(p["base"], 8)
+    same, _ = bsgg.adapters(p["x"].cuda(), p["a"].cuda(), p["b"].cuda(), t, scales=dev["scales"], base=into, out=into)
+    assert same is into and torch.equal(into, y)
+    out = pitched(torch.zeros_like(p["base"]), 16)
+    bsgg.adapters(p["x"].cuda(), p["a"].cuda(), p["b"].cuda(), t, out=out, **dev)
+    assert torch.equal(out, y) and torch.isnan(out._base[:, N:].float()).all()
+    # neither base nor scales
+    want, _ = R.adapters(p["x"], p["a"], p["b"], p["ids"], None, None)
+    z, _ = bsgg.adapters(p["x"].cuda(), p["a"].cuda(), p["b"].cuda(), t)
+    assert ((z.cpu().double() - want).abs() <= tol / f + want.abs() * 2.0 ** -23 + rounding(want, dt)).all()
+    # a map with more rows than it needs
+    wide = map_of(p, S, m_pad=bsgg.sort_rows(T, S) + 384)
+    assert torch.equal(bsgg.adapters(p["x"].cuda(), p["a"].cuda(), p["b"].cuda(), wide, **dev)[0], y)
+
+
+@pytest.mark.parametrize("grads", [None, "f32"])
+@pytest.mark.parametrize("case", CASES)
+def test_adapters_backward(case, grads):
+    T, S, r, K, N, dtype, kind = case
+    p = problem(*case, seed=T + r + 1)
+    t = map_of(p, S)
+    dt = DT[dtype]
+    gt = DT[dtype] if grads is None else torch.float32
+    u = R.adapters(p["x"], p["a"], p["b"], p["ids"], None, None)[1].float()
+    want_dx, want_da, want_db, want_du = R.adapters_backward(p["dy"], p["x"], u, p["a"], p["b"], p["ids"], p["scales"], p["basex"])
+    args = (pitched(p["dy"], 8), pitched(p["x"], 16), u.cuda(), p["a"].cuda(), p["b"].cuda(), t)
+    how = dict(scales=p["scales"].cuda(), base=p["basex"].cuda(), grad_format=grads)
+    dx, da, db = bsgg.adapters_backward(*args, **how)
+    assert da.dtype == gt and db.dtype == gt
+    on = (p["ids"] >= 0)[:, None]
+    at = p["ids"].clamp(min=0).long()
+    f = p["scales"].double()[at][:, None]
+    zero = torch.zeros((), dtype=torch.float64)
+    dutol = torch.where(on, f * torch.einsum("tn,trn->tr", p["dy"].double().abs(), p["b"].double().abs()[at]) * product_error(N), zero)
+    one = torch.nn.functional.one_hot(at, S).double() * on
+    terms = 2.0 ** -23 if gt == torch.float32 and dt == torch.bfloat16 else TERMS[dt]
+    largest = want_du.abs().amax(1, keepdim=True)
+    as_ = p["a"].double().abs()[at]
+    tol = torch.einsum("tr,trk->tk", dutol + largest * TERMS[dt], as_) + torch.einsum("tr,trk->tk", want_du.abs(), as_) * product_error(2 * r)
+    assert ((dx.cpu().double() - want_dx).abs() <= tol + want_dx.abs() * 2.0 ** -23 + rounding(want_dx, dt)).all()
+    # float16's terms are of the block's largest
+    most = want_du.abs().max() if dt == torch.float16 else zero
+    x = p["x"].double().abs()
+    tol = torch.einsum("ts,tr,tk->srk", one, dutol + want_du.abs() * (terms + product_error(3 * T)) + most * TERMS[dt], x)
+    assert ((da.cpu().double() - want_da).abs() <= tol + rounding(want_da, gt)).all()
+    most = u.double().abs().max() if dt == torch.float16 else zero
+    tol = torch.einsum("ts,tr,tn->srn", one * p["scales"].double(), u.double().abs() * (terms + product_error(3 * T)) + most * TERMS[dt],
+                       p["dy"].double().abs())
+    assert ((db.cpu().double() - want_db).abs() <= tol + want_db.abs() * 2.0 ** -23 + rounding(want_db, gt)).all()
+    # an adapter without tokens has zeros, a token without an adapter its base
+    unused = [i for i in range(S) if not (p["ids"] == i).any()]
+    assert (da[unused] == 0).all() and (db[unused] == 0).all()
+    none = p["ids"] < 0
+    assert torch.equal(dx.cpu()[none], p["basex"][none])
+    # each alone
+    for i, name in enumerate(("want_dx", "want_da", "want_db")):
+        only = bsgg.adapters_backward(*args, **{**dict(want_dx=False, want_da=False, want_db=False), name: True}, **how)
+        assert [v is not None for v in only] == [j == i for j in range(3)] and torch.equal(only[i], (dx, da, db)[i])
+    # the dense layer's own dx updated where it is
+    into = p["basex"].cuda()
+    assert bsgg.adapters_backward(*args, **{**how, "base": into}, dx=into, want_da=False, want_db=False)[0] is into and torch.equal(into, dx)
+
+
+def test_gradients_are_those_of_the_forward_by_differences():
+    """Adapters are linear in A, in B and in x, so differences are exact up to rounding."""
+    T, S, r, K, N = 24, 2, 16, 64, 48
+    p = problem(T, S, r, K, N, "f16", "any", 3)
+    t = map_of(p, S)
+    x, a, b, s, dy = (p[n].cuda() for n in ("x", "a", "b", "scales", "dy"))
+    f = lambda x, a, b: (bsgg.adapters(x, a, b, t, scales=s)[0].double() * dy.double()).sum()  # noqa: E731
+    u = bsgg.adapters(x, a, b, t, scales=s)[1]
+    grads = bsgg.adapters_backward(dy, x, u, a, b, t, scales=s, grad_format="f32")
+    y_size = bsgg.adapters(x.abs(), a.abs(), b.abs(), t, scales=s)[0].double()
+    for i, v in enumerate((x, a, b)):
+        d = torch.randn(v.shape, generator=gen(i)).to(v.dtype).cuda() * 0.25
+        args = [[x, a, b], [x, a, b]]
+        args[0][i], args[1][i] = v + d, v - d
+        moved = (args[0][i].double() - args[1][i].double())
+        want = float((grads[i].double() * moved).sum())
+        # the two y are rounded to float16 (and dx is): |dy| 2^-11 of their sizes
+        tol = 4 * float((dy.double().abs() * (y_size * 2 + 1)).sum()) * 2.0 ** -11 / (T * N) ** 0.5 * 6
+        assert abs(float(f(*args[0]) - f(*args[1])) - want) <= tol
+
+
+def test_many_tokens_of_few_adapters():
+    """Several tiles of an adapter, long sums, against the same in 64 bits by products."""
+    T, S, r, K, N = 3000, 3, 32, 1024, 1536
+    p = problem(T, S, r, K, N, "bf16", "runs", 7)
+    t = map_of(p, S)
+    x, a, b, base, dy = (p[n].cuda() for n in ("x", "a", "b", "base", "dy"))
+    y, u = bsgg.adapters(x, a, b, t, base=base)
+    dx, da, db = bsgg.adapters_backward(dy, x, u, a, b, t, grad_format="f32")
+    far = lambda g, w: float((g.double() - w).norm() / w.norm())  # noqa: E731
+    ids = p["ids"].cuda()
+    want_y, want_dx, want_da, want_db = base.double(), torch.zeros(T, K, dtype=torch.float64, device="cuda"), [], []
+    for i in range(S):
+        m = (ids == i).double()[:, None]
+        ui, dui = m * (x.double() @ a[i].double().t()), m * (dy.double() @ b[i].double().t())
+        want_y = want_y + ui @ b[i].double()
+        want_dx += dui @ a[i].double()
+        want_da.append(dui.t() @ x.double())
+        want_db.append(ui.t() @ dy.double())
+    # 16-bit results carry their own rounding, 2^-9.2 in norm; those in 32 bits the sums' 2^-19
+    assert far(y, want_y) < 2.0 ** -8.5 and far(dx, want_dx) < 2.0 ** -8.5
+    assert far(da, torch.stack(want_da)) < 2.0 ** -19 and far(db, torch.stack(want_db)) < 2.0 ** -19
+    for _ in range(2):                                # no order depends on timing
+        again = bsgg.adapters_backward(dy, x, u, a, b, t, grad_format="f32")
+        assert torch.equal(again[0], dx) and torch.equal(again[1], da) and torch.equal(again[2], db)
+
+
+def test_float16_keeps_small_and_large_values():
+    """du far below float16's smallest number and u far above its largest."""
+    T, S, r, K, N = 20, 1, 16, 64, 64
+    p = problem(T, S, r, K, N, "f16", "one", 9)
+    t = map_of(p, S)
+    a, b = (p["a"] * 2.0 ** -4).half(), (p["b"] * 2.0 ** -4).half()
+    dy = (p["dy"].double() * 2.0 ** -13).half()
+    u = torch.randn(T, r, generator=gen(1))
+    dx, da, db = bsgg.adapters_backward(dy.cuda(), p["x"].cuda(), (u * 1e9).cuda(), a.cuda(), b.cuda(), t, grad_format="f32",
+                                        scales=torch.full((1,), 2.0 ** -13).cuda())
+    want = R.adapters_backward(dy, p["x"], u.double() * 1e9, a, b, p["ids"], torch.tensor([2.0 ** -13]), None)
+    for g, w in ((da, want[1]), (db, want[2])):
+        assert float((g.cpu().double() - w).norm() / w.norm()) < 2.0 ** -18
+    x = (p["x"].double() * 2.0 ** 15).clamp(-60000, 60000).half()
+    big = torch.full((1, r, K), 60000.0).half()
+    tiny = torch.full((1, r, N), 2.0 ** -24).half()
+    y, uu = bsgg.adapters(x.cuda(), big.cuda(), tiny.cuda(), t, scales=torch.full((1,), 2.0 ** -14).cuda())
+    want, _ = R.adapters(x, big, tiny, p["ids"], torch.tensor([2.0 ** -14]), None)
+    assert float(uu.abs().max()) > 1e6
+    assert float((y.cpu().double() - want).norm() / want.norm()) < 2.0 ** -10
+
+
+def test_streams_and_graph():
+    """A captured step, replayed on new inputs; two streams at once."""
+    T, S, r, K, N = 130, 4, 16, 256, 512
+    p, q = problem(T, S, r, K, N, "bf16", "any", 5), problem(T, S, r, K, N, "bf16", "runs", 6)
+    dev = {n: v.cuda() for n, v in p.items()}
+    ids = dev["ids"].view(-1, 1)
+
+    def step(ids, d):
+        t = bsgg.sort_tokens(ids, S)
+        y, u = bsgg.adapters(d["x"], d["a"], d["b"], t, scales=d["scales"], base=d["base"])
+        return (y, u) + bsgg.adapters_backward(d["dy"], d["x"], u, d["a"], d["b"], t, scales=d["scales"], base=d["basex"])
+
+    want_p = [v.clone() for v in step(ids, dev)]
+    other = {n: v.cuda() for n, v in q.items()}
+    want_q = [v.clone() for v in step(other["ids"].view(-1, 1), other)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(ids, dev)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(out, want_p))
+    for n in dev:
+        dev[n].copy_(other[n])
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(out, want_q))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append(step(ids, dev))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want_q))
+
+
+def test_no_tokens():
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    a, b = (torch.zeros(2, 8, n, dtype=torch.bfloat16, device="cuda") for n in (64, 32))
+    t = bsgg.sort_tokens(torch.empty(0, 1, dtype=torch.int32, device="cuda"), 2)
+    y, u = bsgg.adapters(x, a, b, t)
+    assert y.shape == (0, 32) and u.shape == (0, 8)
+    dx, da, db = bsgg.adapters_backward(y, x, u, a, b, t)
+    assert dx.shape == (0, 64) and (da == 0).all() and (db == 0).all()
