@@ -139,8 +139,8 @@ struct ShrinkParams {
   const void* w;
   const float* scales;
   float* u;
-  int64_t ldx, depth;
-  int rank, split;
+  int64_t ldx;
+  int depth, rank, split;
 };
 
 template <int KIND, int R>
@@ -165,32 +165,40 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
   const int64_t nb = (p.depth + 63) / 64;
   const int b0 = static_cast<int>(nb * part / p.split), b1 = static_cast<int>(nb * (part + 1) / p.split);
   const int steps = (b1 - b0 + blocks - 1) / blocks;
-  const uint16_t* x = static_cast<const uint16_t*>(p.x);
-  const uint16_t* w = static_cast<const uint16_t*>(p.w) + static_cast<int64_t>(adapter) * p.rank * p.depth;
   const uint32_t block_bytes = static_cast<uint32_t>(rows + p.rank) * 128;
+  // a thread copies one 16-byte piece of every 32nd row: what changes from block to block
+  // is an offset
+  const int piece = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const uint16_t* xp[S::kRows / 32];
+#pragma unroll
+  for (int i = 0; i < S::kRows / 32; ++i) {
+    const int32_t t = r0 + 32 * i < n ? token[r0 + 32 * i] : -1;
+    xp[i] = t >= 0 ? static_cast<const uint16_t*>(p.x) + t * p.ldx + piece * 8 : nullptr;
+  }
+  const uint16_t* wp = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * p.rank + r0) * p.depth + piece * 8;
+  const uint32_t to0 = base + swizzled(r0, piece);
 
   auto load = [&](int step) {
     if (step < steps) {
-      for (int j = 0; j < blocks; ++j) {
+      uint32_t to = to0 + (step % S::kStages) * S::kStageBytes;
+      for (int j = 0; j < blocks; ++j, to += block_bytes) {
         const int b = b0 + step * blocks + j;
         if (b >= b1) break;
-        const uint32_t to = base + (step % S::kStages) * S::kStageBytes + j * block_bytes;
-        for (int c = threadIdx.x; c < (rows + p.rank) * 8; c += kThreads) {
-          const int r = c >> 3, piece = c & 7;
-          const int64_t k = static_cast<int64_t>(b) * 64 + piece * 8;
-          if (r < rows) {
-            const int32_t t = r < n ? token[r] : -1;
-            const bool in = t >= 0 && k < p.depth;
-            copy16(to + swizzled(r, piece), in ? x + t * p.ldx + k : x, in);
-          } else {
-            const bool in = k < p.depth;
-            copy16(to + swizzled(r, piece), in ? w + (r - rows) * p.depth + k : w, in);
+        const bool in = b * 64 + piece * 8 < p.depth;
+#pragma unroll
+        for (int i = 0; i < S::kRows / 32; ++i)
+          if (r0 + 32 * i < rows) {
+            const bool has = in && xp[i] != nullptr;
+            copy16(to + 4096 * i, has ? xp[i] + b * 64 : p.x, has);
           }
-        }
+#pragma unroll
+        for (int i = 0; i < (R + 31) / 32; ++i)
+          if (r0 + 32 * i < p.rank) copy16(to + rows * 128 + 4096 * i, in ? wp + 32 * i * p.depth + b * 64 : p.w, in);
       }
     }
     copies_commit();
   };
+  const int ar = mw * 16 + (lane & 15), br = (lane & 7) + ((lane >> 4) << 3);
 
   float acc[R / 8][4], sum[R / 8][4];
 #pragma unroll
@@ -216,13 +224,14 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
       if (b0 + s * blocks + j >= b1) break;
       const uint32_t xs = stage + j * block_bytes, ws = xs + rows * 128;
       uint32_t a[4];
-      load_matrices(a, xs + swizzled(mw * 16 + (lane & 15), kk * 2 + (lane >> 4)));
+      load_matrices(a, xs + swizzled(ar, kk * 2 + (lane >> 4)));
+      const uint32_t bs = ws + swizzled(br, kk * 2 + ((lane >> 3) & 1));
 #pragma unroll
       for (int i = 0; i < R / 8; i += 2) {
         if (i * 8 >= p.rank) break;
         uint32_t b[4];
         // of an odd number of eights the last pair's second half is what lies behind: inside the stage, and unused
-        load_matrices(b, ws + swizzled(i * 8 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+        load_matrices(b, bs + i * 1024);
         multiply<KIND>(acc[i], a, b[0], b[1]);
         if ((i + 1) * 8 < p.rank) multiply<KIND>(acc[i + 1], a, b[2], b[3]);
       }
@@ -294,8 +303,8 @@ struct ExpandParams {
   const void* base;
   void* y;
   float* zero_u;              // u's rows of tokens without an adapter, where wanted
-  int64_t ld_base, ldy, width, tiles;
-  int rank;
+  int64_t ld_base, ldy, tiles;
+  int width, rank;
 };
 
 // Tokens without an adapter: y = base, u = 0.
@@ -338,7 +347,7 @@ __device__ __noinline__ void expand_rest(const ExpandParams& p, int64_t block, i
 }
 
 template <int KIND, int R>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ ExpandParams p) {
+__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_constant__ ExpandParams p) {
   using E = Expand<R>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int32_t token[E::kRows];
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
   const int n = tokens_of<E::kRows>(p.map, row0, token);
   if (n == 0) return;
   const int adapter = adapter_of(p.map, row0);
-  const int groups = row_groups(n), rows = 16 * groups, across = min(kWarps / groups, E::kMaxAcross);
+  const int groups = row_groups(n), rows = 16 * groups, log_rows = 31 - __clz(rows), across = min(kWarps / groups, E::kMaxAcross);
   const int mw = warp % groups, cw = warp / groups;
   const int ranks = (p.rank + 15) & ~15;               // whole steps of 16, zeros behind the rank
   const int cols = static_cast<int>(min(int64_t(E::kCols), p.width - col0));
@@ -363,28 +372,41 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
   const uint32_t group_bytes = rows * 128, w_bytes = ranks * 128;
   const uint32_t pass_bytes = across * (group_bytes + w_bytes);
   const int buffers = max(1, min(E::kPasses, static_cast<int>((E::kSmem - 128) / pass_bytes)));
-  const uint16_t* w = static_cast<const uint16_t*>(p.w) + static_cast<int64_t>(adapter) * p.rank * p.width;
   const uint16_t* from = static_cast<const uint16_t*>(p.base);
+  // a thread copies one 16-byte piece of every 32nd row, of the base's rows * across and of
+  // W's: what changes from pass to pass is an offset
+  const int piece = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const uint16_t* fp[E::kRows / 32];
+#pragma unroll
+  for (int i = 0; i < E::kRows / 32; ++i) {
+    const int q = r0 + 32 * i, r = q & (rows - 1);
+    const int32_t t = q < rows * across && r < n ? token[r] : -1;
+    fp[i] = from != nullptr && t >= 0 ? from + t * p.ld_base + col0 + (q >> log_rows) * 64 + piece * 8 : nullptr;
+  }
+  const uint16_t* wp = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * p.rank + r0) * p.width + col0 + piece * 8;
+  const uint32_t to0 = base + swizzled(r0, piece);
 
   // of 64 columns each: the rows of the base, then those of W
   auto load = [&](int pass) {
     if (pass < passes) {
-      const uint32_t to = base + (pass % buffers) * pass_bytes;
-      for (int g = 0; g < across; ++g) {
-        const int64_t c0 = col0 + (pass * across + g) * 64;
-        for (int e = threadIdx.x; e < (rows + ranks) * 8; e += kThreads) {
-          const int r = e >> 3, piece = e & 7;
-          const int64_t c = c0 + piece * 8;
-          if (r < rows) {
-            if (from == nullptr) continue;
-            const int32_t t = r < n ? token[r] : -1;
-            const bool in = t >= 0 && c < p.width;
-            copy16(to + g * group_bytes + swizzled(r, piece), in ? from + t * p.ld_base + c : from, in);
-          } else {
-            const int k = r - rows;
-            const bool in = k < p.rank && c < p.width;
-            copy16(to + across * group_bytes + g * w_bytes + swizzled(k, piece), in ? w + k * p.width + c : w, in);
-          }
+      uint32_t to = to0 + (pass % buffers) * pass_bytes;
+      const int c0 = pass * across * 64;
+#pragma unroll
+      for (int i = 0; i < E::kRows / 32; ++i) {
+        const int q = r0 + 32 * i;
+        if (from != nullptr && q < rows * across) {
+          const bool in = fp[i] != nullptr && c0 + (q >> log_rows) * 64 + piece * 8 < cols;
+          copy16(to + 4096 * i, in ? fp[i] + c0 : from, in);
+        }
+      }
+      to += across * group_bytes;
+      const uint16_t* wg = wp + c0;
+      for (int g = 0; g < across; ++g, to += w_bytes, wg += 64) {
+        const bool in = c0 + g * 64 + piece * 8 < cols;
+#pragma unroll
+        for (int i = 0; i < (R + 31) / 32; ++i) {
+          const int k = r0 + 32 * i;
+          if (k < ranks) copy16(to + 4096 * i, in && k < p.rank ? wg + 32 * i * p.width : p.w, in && k < p.rank);
         }
       }
     }
@@ -427,14 +449,21 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
     }
   }
 
+  uint16_t* yp[4];             // this lane's pieces of the rows that the warp stores
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r = mw * 16 + e * 4 + (lane >> 3);
+    const int32_t t = r < n ? token[r] : -1;
+    yp[e] = t >= 0 ? static_cast<uint16_t*>(p.y) + t * p.ldy + col0 + (lane & 7) * 8 : nullptr;
+  }
   for (int pass = 0; pass < passes; ++pass) {
     if (buffers == 1) copies_wait<0>();
     else if (buffers == 2) copies_wait<1>();
     else copies_wait<2>();
     __syncthreads();
     const uint32_t at = base + (pass % buffers) * pass_bytes;
-    const int64_t c0 = col0 + (pass * across + cw) * 64;
-    if (cw < across && c0 < p.width) {
+    const int c0 = (pass * across + cw) * 64;
+    if (cw < across && c0 < cols) {
       const uint32_t ys = at + cw * group_bytes, ws = at + across * group_bytes + cw * w_bytes;
       float acc[8][4];
 #pragma unroll
@@ -447,7 +476,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           uint32_t b[4];
-          load_matrices_t(b, ws + swizzled(s * 16 + (lane & 15), i + (lane >> 4)));
+          load_matrices_t(b, ws + s * 2048 + swizzled(lane & 15, i + (lane >> 4)));
 #pragma unroll
           for (int k = 0; k < kTerms; ++k) {
             multiply<KIND>(acc[i], a[k][s], b[0], b[1]);
@@ -468,12 +497,9 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
       __syncwarp();
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = mw * 16 + e * 4 + (lane >> 3), piece = lane & 7;
-        const int32_t t = r < n ? token[r] : -1;
-        const int64_t c = c0 + piece * 8;
-        if (t >= 0 && c < p.width)
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + t * p.ldy + c) =
-              *reinterpret_cast<const uint4*>(smem + (ys - base) + swizzled(r, piece));
+        if (yp[e] != nullptr && c0 + (lane & 7) * 8 < cols)
+          *reinterpret_cast<uint4*>(yp[e] + c0) =
+              *reinterpret_cast<const uint4*>(smem + (ys - base) + swizzled(mw * 16 + e * 4 + (lane >> 3), lane & 7));
       }
     }
     __syncthreads();                                   // the buffer is read
@@ -488,7 +514,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
 // products are (rank x 64 tokens) (64 tokens x columns), both read across their rows.
 template <int R>
 struct Outer {
-  static constexpr int kCols = R == 128 ? 128 : 256, kTokens = 64, kStages = 3;
+  static constexpr int kCols = R == 128 ? 128 : 256, kTokens = 64, kStages = R <= 32 ? 2 : 3;
   static constexpr int kXBytes = kTokens * kCols * 2, kGBytes = kTokens * R * 4;
   static constexpr int kStageBytes = kXBytes + kGBytes;
   static constexpr int kTermPitch = 2 * R + 16;         // bytes of a token's ranks: eight rows in different banks
@@ -503,8 +529,8 @@ struct OuterParams {
   const void* x;
   const float* scales;
   void* out;
-  int64_t ldx, width, blocks;     // blocks of columns
-  int rank, split, out_kind;
+  int64_t ldx, blocks;            // blocks of columns
+  int width, rank, split, out_kind;
 };
 
 template <int KIND, int R, int TERMS>
@@ -513,6 +539,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
   constexpr int kTiles = O::kCols / 8 / kWarps;         // of 8 columns, a warp
   extern __shared__ uint8_t smem_raw[];
   __shared__ int32_t token[O::kStages + 1][O::kTokens];
+  __shared__ uint32_t has[O::kStages + 1][O::kTokens / 32];
   __shared__ float most_of[kWarps];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const uint32_t base = smem_u32(smem);
@@ -534,8 +561,6 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     const int64_t r = chunk_row(c) + i;
     return c < chunks && r < row1 ? token_at(p.map, r) : -1;
   };
-  const uint16_t* x = static_cast<const uint16_t*>(p.x);
-
   float unit = 1.0f;
   if (KIND == OK_F16) {
     // this block's own power of two: its sums are scaled back before they are joined
@@ -556,21 +581,32 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     unit = unit_of(most);
   }
 
+  // a thread copies one piece of every kStep-th token's columns, and one of every G-step-th
+  // token's ranks
+  constexpr int kPieces = O::kCols / 8, kStep = kThreads / kPieces, kQuads = R / 4, kGStep = kThreads / kQuads;
+  const int piece = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
+  const int quad = threadIdx.x % kQuads, g0 = threadIdx.x / kQuads;
+  const bool in_cols = col0 + piece * 8 < p.width;
+  const uint16_t* xp = static_cast<const uint16_t*>(p.x) + col0 + piece * 8;
+  const uint32_t x_to = base + (piece >> 3) * (O::kTokens * 128) + swizzled(r0, piece & 7);
+  static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
   auto load = [&](int c) {
     if (c < chunks) {
       const int32_t* tok = token[c % (O::kStages + 1)];
-      const uint32_t to = base + (c % O::kStages) * O::kStageBytes;
-      for (int e = threadIdx.x; e < O::kTokens * O::kCols / 8; e += kThreads) {
-        const int r = e / (O::kCols / 8), q = e % (O::kCols / 8);
-        const int32_t t = tok[r];
-        const int64_t col = col0 + q * 8;
-        const bool in = t >= 0 && col < p.width;
-        copy16(to + (q >> 3) * (O::kTokens * 128) + swizzled(r, q & 7), in ? x + t * p.ldx + col : x, in);
+      const uint32_t stage = (c % O::kStages) * O::kStageBytes;
+#pragma unroll
+      for (int i = 0; i < O::kTokens / kStep; ++i) {
+        const int32_t t = tok[r0 + i * kStep];
+        const bool in = t >= 0 && in_cols;
+        copy16(x_to + stage + i * kStep * 128, in ? xp + t * p.ldx : p.x, in);
       }
-      for (int e = threadIdx.x; e < O::kTokens * p.rank / 4; e += kThreads) {
-        const int r = e / (p.rank / 4), q = e % (p.rank / 4);
-        const int32_t t = tok[r];
-        copy16(to + O::kXBytes + (r * R + q * 4) * 4, t >= 0 ? p.g + static_cast<int64_t>(t) * p.rank + q * 4 : p.g, t >= 0);
+      if (quad * 4 < p.rank) {
+#pragma unroll
+        for (int i = 0; i < O::kTokens / kGStep; ++i) {
+          const int r = g0 + i * kGStep;
+          const int32_t t = tok[r];
+          copy16(base + stage + O::kXBytes + (r * R + quad * 4) * 4, t >= 0 ? p.g + static_cast<int64_t>(t) * p.rank + quad * 4 : p.g, t >= 0);
+        }
       }
     }
     copies_commit();
@@ -583,8 +619,20 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[m][i][k] = sum[m][i][k] = 0.0f;
-  for (int c = 0; c < O::kStages - 1; ++c)
-    if (threadIdx.x < O::kTokens) token[c][threadIdx.x] = token_of(c, threadIdx.x);
+  auto flush = [&]() {
+#pragma unroll
+    for (int m = 0; m < R / 16; ++m)
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) { sum[m][i][k] += acc[m][i][k]; acc[m][i][k] = 0.0f; }
+  };
+  auto put_tokens = [&](int c, int32_t t) {
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, t >= 0);
+    if (threadIdx.x < O::kTokens) token[c % (O::kStages + 1)][threadIdx.x] = t;
+    if (threadIdx.x < O::kTokens && lane == 0) has[c % (O::kStages + 1)][warp] = b;
+  };
+  for (int c = 0; c < O::kStages - 1; ++c) put_tokens(c, threadIdx.x < O::kTokens ? token_of(c, threadIdx.x) : -1);
   __syncthreads();
   for (int c = 0; c < O::kStages - 1; ++c) load(c);
   for (int c = 0; c < chunks; ++c) {
@@ -592,23 +640,25 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     const int ahead = c + O::kStages - 1;
     if (threadIdx.x < O::kTokens) next = token_of(ahead, threadIdx.x);
     copies_wait<O::kStages - 2>();
-    if (threadIdx.x < O::kTokens) token[ahead % (O::kStages + 1)][threadIdx.x] = next;
+    put_tokens(ahead, next);
     __syncthreads();                                   // chunk c is there, c - 1 is read, the next one's tokens are known
+    // an adapter's tokens come first: behind them there are only padding rows
+    if ((has[c % (O::kStages + 1)][0] | has[c % (O::kStages + 1)][1]) == 0) break;
     load(ahead);
     const uint32_t stage = base + (c % O::kStages) * O::kStageBytes;
     // g as terms of 16 bits, ranks up to a multiple of 16
-    const int ranks = (p.rank + 15) & ~15;
     const float* g = reinterpret_cast<const float*>(smem + (stage - base) + O::kXBytes);
-    for (int e = threadIdx.x; e < O::kTokens * ranks / 4; e += kThreads) {
-      const int r = e / (ranks / 4), q = e % (ranks / 4);
+#pragma unroll
+    for (int i = 0; i < O::kTokens / kGStep; ++i) {
+      const int r = g0 + i * kGStep;
       float4 v = make_float4(0, 0, 0, 0);
-      if (q * 4 < p.rank) v = *reinterpret_cast<const float4*>(g + r * R + q * 4);
+      if (quad * 4 < p.rank) v = *reinterpret_cast<const float4*>(g + r * R + quad * 4);
       uint32_t lo[TERMS], hi[TERMS];
       split_terms<KIND, TERMS>(v.x * unit, v.y * unit, lo);
       split_terms<KIND, TERMS>(v.z * unit, v.w * unit, hi);
 #pragma unroll
       for (int k = 0; k < TERMS; ++k)
-        *reinterpret_cast<uint2*>(smem + (terms - base) + k * O::kTermBytes + r * O::kTermPitch + q * 8) = make_uint2(lo[k], hi[k]);
+        *reinterpret_cast<uint2*>(smem + (terms - base) + k * O::kTermBytes + r * O::kTermPitch + quad * 8) = make_uint2(lo[k], hi[k]);
     }
     __syncthreads();
 #pragma unroll
@@ -635,15 +685,9 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
         }
       }
     }
-    if ((c + 1) % (kRun / O::kTokens) == 0 || c + 1 == chunks) {
-#pragma unroll
-      for (int m = 0; m < R / 16; ++m)
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) { sum[m][i][k] += acc[m][i][k]; acc[m][i][k] = 0.0f; }
-    }
+    if ((c + 1) % (kRun / O::kTokens) == 0) flush();
   }
+  flush();
   copies_wait<0>();
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
@@ -713,7 +757,7 @@ int64_t busy_tiles(const AdapterMap& m, int rows) {
 bsgg_status launch_shrink(int format, ShrinkParams p, cudaStream_t s) {
   const int64_t tiles = p.map.m_pad / 64, busy = busy_tiles(p.map, 64), nb = ceil_div(p.depth, 64);
   p.split = 1;
-  while (p.split < kMaxCluster && busy * p.split < 304 && nb >= 4 * p.split) p.split *= 2;
+  while (p.split < kMaxCluster && busy * p.split < 228 && nb >= 4 * p.split) p.split *= 2;
   return with_half(format, [&](auto kind) {
     return with_rank(p.rank, [&](auto r) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
@@ -739,14 +783,15 @@ bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
 }
 
 bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
-  // parts of an adapter's tokens: of twice the chunks that it has on average
-  const int64_t chunks = ceil_div(p.map.tokens, int64_t(64) * p.map.adapters);
-  p.split = 1;
-  while (p.split < kMaxCluster && p.split < 2 * chunks) p.split *= 2;
   return with_half(format, [&](auto kind) {
     return with_rank(p.rank, [&](auto r) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
       p.blocks = ceil_div(p.width, Outer<R>::kCols);
+      // parts of an adapter's tokens: until two blocks an SM have work, of two chunks at least
+      const int64_t used = p.map.tokens < p.map.adapters ? p.map.tokens : p.map.adapters;
+      const int64_t chunks = ceil_div(p.map.tokens, 64 * used);
+      p.split = 1;
+      while (p.split < kMaxCluster && used * p.blocks * p.split < 304 && 4 * p.split <= chunks) p.split *= 2;
       const int64_t grid = p.map.adapters * p.blocks * p.split;
       auto launch = [&](auto terms) {
         constexpr int N = decltype(terms)::value;
@@ -794,9 +839,9 @@ bsgg_status bsgg_adapters(const bsgg_adapters_desc* d, const void* x, const void
     return BSGG_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const AdapterMap map = {d->tokens, d->m_pad, d->adapters, padded_offsets, row_of_slot, slot_of_row};
-  const bsgg_status ran = launch_shrink(d->format, {map, x, a, nullptr, u, d->ldx, d->k, d->rank, 1}, s);
+  const bsgg_status ran = launch_shrink(d->format, {map, x, a, nullptr, u, d->ldx, static_cast<int>(d->k), d->rank, 1}, s);
   if (ran != BSGG_OK) return ran;
-  return launch_expand(d->format, {map, u, b, scales, base, y, u, d->ld_base, d->ldy, d->n, 0, d->rank}, s);
+  return launch_expand(d->format, {map, u, b, scales, base, y, u, d->ld_base, d->ldy, 0, static_cast<int>(d->n), d->rank}, s);
 }
 
 bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* dy, const void* x, const float* u,
@@ -830,11 +875,11 @@ bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* 
     return BSGG_ERR_INVALID_ARG;
   const AdapterMap map = {d->tokens, d->m_pad, d->adapters, padded_offsets, row_of_slot, slot_of_row};
   bsgg_status ran = BSGG_OK;
-  if (wants_du) ran = launch_shrink(d->format, {map, dy, b, scales, du, d->ld_dy, d->n, d->rank, 1}, s);
-  if (ran == BSGG_OK && db) ran = launch_outer(d->format, {map, u, dy, scales, db, d->ld_dy, d->n, 0, d->rank, 1, d->grad_format}, s);
-  if (ran == BSGG_OK && da) ran = launch_outer(d->format, {map, du, x, nullptr, da, d->ldx, d->k, 0, d->rank, 1, d->grad_format}, s);
+  if (wants_du) ran = launch_shrink(d->format, {map, dy, b, scales, du, d->ld_dy, static_cast<int>(d->n), d->rank, 1}, s);
+  if (ran == BSGG_OK && db) ran = launch_outer(d->format, {map, u, dy, scales, db, d->ld_dy, 0, static_cast<int>(d->n), d->rank, 1, d->grad_format}, s);
+  if (ran == BSGG_OK && da) ran = launch_outer(d->format, {map, du, x, nullptr, da, d->ldx, 0, static_cast<int>(d->k), d->rank, 1, d->grad_format}, s);
   if (ran == BSGG_OK && dx)
-    ran = launch_expand(d->format, {map, du, a, nullptr, base, dx, nullptr, d->ld_base, d->ld_dx, d->k, 0, d->rank}, s);
+    ran = launch_expand(d->format, {map, du, a, nullptr, base, dx, nullptr, d->ld_base, d->ld_dx, 0, static_cast<int>(d->k), d->rank}, s);
   return ran;
 }
 
