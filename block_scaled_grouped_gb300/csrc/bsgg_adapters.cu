@@ -29,9 +29,28 @@ struct AdapterMap {
 };
 
 // ---------------------------------------------------------------- pieces
-// 16 bytes from global to shared memory, zeros where !present.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool present) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(present ? 16 : 0) : "memory");
+// `bytes` (16 or 0) from global to shared memory, zeros behind them; with 0 the source is
+// not read.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t get_shared(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 get_shared4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void put_shared(uint32_t at, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
+__device__ __forceinline__ void put_shared2(uint32_t at, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ float4 get_shared4f(uint32_t at) {
+  const uint4 v = get_shared4(at);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -143,8 +162,8 @@ struct ShrinkParams {
   int depth, rank, split;
 };
 
-template <int KIND, int R>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant__ ShrinkParams p) {
+template <int KIND, int R, bool FULL>
+__global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) shrink_kernel(const __grid_constant__ ShrinkParams p) {
   using S = Shrink<R>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int32_t token[S::kRows];
@@ -165,36 +184,35 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
   const int64_t nb = (p.depth + 63) / 64;
   const int b0 = static_cast<int>(nb * part / p.split), b1 = static_cast<int>(nb * (part + 1) / p.split);
   const int steps = (b1 - b0 + blocks - 1) / blocks;
-  const uint32_t block_bytes = static_cast<uint32_t>(rows + p.rank) * 128;
-  // a thread copies one 16-byte piece of every 32nd row: what changes from block to block
-  // is an offset
+  const int rank = FULL ? R : p.rank;
+  const uint32_t block_bytes = static_cast<uint32_t>(rows + rank) * 128;
+  // a thread copies one 16-byte piece of every 32nd row; its sources move on by a block of 64
+  // with each block loaded
   const int piece = threadIdx.x & 7, r0 = threadIdx.x >> 3;
   const uint16_t* xp[S::kRows / 32];
+  int xb[S::kRows / 32];
 #pragma unroll
   for (int i = 0; i < S::kRows / 32; ++i) {
     const int32_t t = r0 + 32 * i < n ? token[r0 + 32 * i] : -1;
-    xp[i] = t >= 0 ? static_cast<const uint16_t*>(p.x) + t * p.ldx + piece * 8 : nullptr;
+    xb[i] = t >= 0 ? 16 : 0;
+    xp[i] = static_cast<const uint16_t*>(p.x) + (t >= 0 ? t * p.ldx + b0 * 64 + piece * 8 : 0);
   }
-  const uint16_t* wp = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * p.rank + r0) * p.depth + piece * 8;
+  const uint16_t* wp = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * rank + r0) * p.depth + b0 * 64 + piece * 8;
   const uint32_t to0 = base + swizzled(r0, piece);
+  int left = p.depth - b0 * 64 - piece * 8;            // of the reduction from this thread's piece on
+  int next = b0;                                       // the next block to load
 
   auto load = [&](int step) {
-    if (step < steps) {
-      uint32_t to = to0 + (step % S::kStages) * S::kStageBytes;
-      for (int j = 0; j < blocks; ++j, to += block_bytes) {
-        const int b = b0 + step * blocks + j;
-        if (b >= b1) break;
-        const bool in = b * 64 + piece * 8 < p.depth;
+    uint32_t to = to0 + (step % S::kStages) * S::kStageBytes;
+    for (int j = 0; j < blocks && next < b1; ++j, ++next, to += block_bytes, left -= 64, wp += 64) {
 #pragma unroll
-        for (int i = 0; i < S::kRows / 32; ++i)
-          if (r0 + 32 * i < rows) {
-            const bool has = in && xp[i] != nullptr;
-            copy16(to + 4096 * i, has ? xp[i] + b * 64 : p.x, has);
-          }
-#pragma unroll
-        for (int i = 0; i < (R + 31) / 32; ++i)
-          if (r0 + 32 * i < p.rank) copy16(to + rows * 128 + 4096 * i, in ? wp + 32 * i * p.depth + b * 64 : p.w, in);
+      for (int i = 0; i < S::kRows / 32; ++i) {
+        if (r0 + 32 * i < rows) copy16(to + 4096 * i, xp[i], left > 0 ? xb[i] : 0);
+        xp[i] += 64;
       }
+#pragma unroll
+      for (int i = 0; i < (R + 31) / 32; ++i)
+        if (r0 + 32 * i < rank) copy16(to + rows * 128 + 4096 * i, wp + 32 * i * static_cast<int64_t>(p.depth), left > 0 ? 16 : 0);
     }
     copies_commit();
   };
@@ -204,58 +222,59 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
 #pragma unroll
   for (int i = 0; i < R / 8; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[i][k] = sum[i][k] = 0.0f;
-  int run = 0;
-  auto flush = [&]() {
+    for (int k = 0; k < 4; ++k) sum[i][k] = 0.0f;
+  for (int s = 0; s < S::kStages - 1; ++s) load(s);
+  const int run = kRun / 64 * shares / blocks;          // stages until a warp has summed kRun products
+  for (int s0 = 0; s0 < steps; s0 += run) {
 #pragma unroll
     for (int i = 0; i < R / 8; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) { sum[i][k] += acc[i][k]; acc[i][k] = 0.0f; }
-    run = 0;
-  };
-  for (int s = 0; s < S::kStages - 1; ++s) load(s);
-  for (int s = 0; s < steps; ++s) {
-    copies_wait<S::kStages - 2>();
-    __syncthreads();                                   // stage s is there, and s - 1 is read
-    load(s + S::kStages - 1);
-    const uint32_t stage = base + (s % S::kStages) * S::kStageBytes;
-    for (int q = kw; q < 4 * blocks; q += shares) {    // steps of 16
-      const int j = q >> 2, kk = q & 3;
-      if (b0 + s * blocks + j >= b1) break;
-      const uint32_t xs = stage + j * block_bytes, ws = xs + rows * 128;
-      uint32_t a[4];
-      load_matrices(a, xs + swizzled(ar, kk * 2 + (lane >> 4)));
-      const uint32_t bs = ws + swizzled(br, kk * 2 + ((lane >> 3) & 1));
+      for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+    const int s1 = min(s0 + run, steps);
+    for (int s = s0; s < s1; ++s) {
+      copies_wait<S::kStages - 2>();
+      __syncthreads();                                 // stage s is there, and s - 1 is read
+      load(s + S::kStages - 1);
+      const uint32_t stage = base + (s % S::kStages) * S::kStageBytes;
+      const int end = 4 * min(blocks, b1 - b0 - s * blocks);
+      for (int q = kw; q < end; q += shares) {         // steps of 16
+        const uint32_t xs = stage + (q >> 2) * block_bytes;
+        const int kk = (q & 3) * 2;
+        uint32_t a[4];
+        load_matrices(a, xs + swizzled(ar, kk + (lane >> 4)));
+        const uint32_t bs = xs + rows * 128 + swizzled(br, kk + ((lane >> 3) & 1));
 #pragma unroll
-      for (int i = 0; i < R / 8; i += 2) {
-        if (i * 8 >= p.rank) break;
-        uint32_t b[4];
-        // of an odd number of eights the last pair's second half is what lies behind: inside the stage, and unused
-        load_matrices(b, bs + i * 1024);
-        multiply<KIND>(acc[i], a, b[0], b[1]);
-        if ((i + 1) * 8 < p.rank) multiply<KIND>(acc[i + 1], a, b[2], b[3]);
+        for (int i = 0; i < R / 8; i += 2) {
+          if (!FULL && i * 8 >= rank) break;
+          uint32_t b[4];
+          // of an odd number of eights the last pair's second half is what lies behind: inside the stage, and unused
+          load_matrices(b, bs + i * 1024);
+          multiply<KIND>(acc[i], a, b[0], b[1]);
+          if (FULL || (i + 1) * 8 < rank) multiply<KIND>(acc[i + 1], a, b[2], b[3]);
+        }
       }
-      run += 16;
     }
-    if (run >= kRun) flush();
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[i][k] += acc[i][k];
   }
-  flush();
   copies_wait<0>();
   __syncthreads();
   // the warps' shares, then the cluster's parts, in order
   float* sums = reinterpret_cast<float*>(smem);
   {
     const int row = mw * 16 + (lane >> 2);
-    float* at = sums + (static_cast<int64_t>(kw) * rows + row) * p.rank + 2 * (lane & 3);
+    float* at = sums + (static_cast<int64_t>(kw) * rows + row) * rank + 2 * (lane & 3);
 #pragma unroll
     for (int i = 0; i < R / 8; ++i) {
-      if (i * 8 >= p.rank) break;
+      if (i * 8 >= rank) break;
       *reinterpret_cast<float2*>(at + i * 8) = make_float2(sum[i][0], sum[i][1]);
-      *reinterpret_cast<float2*>(at + 8 * p.rank + i * 8) = make_float2(sum[i][2], sum[i][3]);
+      *reinterpret_cast<float2*>(at + 8 * rank + i * 8) = make_float2(sum[i][2], sum[i][3]);
     }
   }
   __syncthreads();
-  const int quads = rows * p.rank / 4;
+  const int quads = rows * rank / 4;
   for (int e = threadIdx.x; e < quads; e += kThreads) {
     float4* at = reinterpret_cast<float4*>(sums) + e;
     float4 v = *at;
@@ -275,9 +294,9 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
       const float4 o = ld_shared_cluster4(mapa_shared(at, k));
       v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
     }
-    const int row = e * 4 / p.rank, col = e * 4 - row * p.rank;
+    const int row = e * 4 / rank, col = e * 4 - row * rank;
     const int32_t t = row < n ? token[row] : -1;
-    if (t >= 0) *reinterpret_cast<float4*>(p.u + static_cast<int64_t>(t) * p.rank + col) = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
+    if (t >= 0) *reinterpret_cast<float4*>(p.u + static_cast<int64_t>(t) * rank + col) = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
   }
   if (p.split > 1) cluster_sync();                     // the sums stay until every block has read them
 }
@@ -346,7 +365,7 @@ __device__ __noinline__ void expand_rest(const ExpandParams& p, int64_t block, i
   }
 }
 
-template <int KIND, int R>
+template <int KIND, int R, bool FULL>
 __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_constant__ ExpandParams p) {
   using E = Expand<R>;
   extern __shared__ uint8_t smem_raw[];
@@ -366,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
   const int adapter = adapter_of(p.map, row0);
   const int groups = row_groups(n), rows = 16 * groups, log_rows = 31 - __clz(rows), across = min(kWarps / groups, E::kMaxAcross);
   const int mw = warp % groups, cw = warp / groups;
-  const int ranks = (p.rank + 15) & ~15;               // whole steps of 16, zeros behind the rank
+  const int rank = FULL ? R : p.rank, ranks = FULL ? R : (rank + 15) & ~15;   // whole steps of 16, zeros behind the rank
   const int cols = static_cast<int>(min(int64_t(E::kCols), p.width - col0));
   const int passes = (cols + 64 * across - 1) / (64 * across);
   const uint32_t group_bytes = rows * 128, w_bytes = ranks * 128;
@@ -377,13 +396,15 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
   // W's: what changes from pass to pass is an offset
   const int piece = threadIdx.x & 7, r0 = threadIdx.x >> 3;
   const uint16_t* fp[E::kRows / 32];
+  int left[E::kRows / 32];                             // columns of the block from this piece on, 0 without a token
 #pragma unroll
   for (int i = 0; i < E::kRows / 32; ++i) {
-    const int q = r0 + 32 * i, r = q & (rows - 1);
+    const int q = r0 + 32 * i, r = q & (rows - 1), c = (q >> log_rows) * 64 + piece * 8;
     const int32_t t = q < rows * across && r < n ? token[r] : -1;
-    fp[i] = from != nullptr && t >= 0 ? from + t * p.ld_base + col0 + (q >> log_rows) * 64 + piece * 8 : nullptr;
+    left[i] = t >= 0 ? cols - c : 0;
+    fp[i] = from + (t >= 0 ? t * p.ld_base + col0 + c : 0);
   }
-  const uint16_t* wp = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * p.rank + r0) * p.width + col0 + piece * 8;
+  const uint16_t* wp = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * rank + r0) * p.width + col0 + piece * 8;
   const uint32_t to0 = base + swizzled(r0, piece);
 
   // of 64 columns each: the rows of the base, then those of W
@@ -391,22 +412,19 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
     if (pass < passes) {
       uint32_t to = to0 + (pass % buffers) * pass_bytes;
       const int c0 = pass * across * 64;
+      if (from != nullptr) {
 #pragma unroll
-      for (int i = 0; i < E::kRows / 32; ++i) {
-        const int q = r0 + 32 * i;
-        if (from != nullptr && q < rows * across) {
-          const bool in = fp[i] != nullptr && c0 + (q >> log_rows) * 64 + piece * 8 < cols;
-          copy16(to + 4096 * i, in ? fp[i] + c0 : from, in);
-        }
+        for (int i = 0; i < E::kRows / 32; ++i)
+          if (r0 + 32 * i < rows * across) copy16(to + 4096 * i, fp[i] + c0, left[i] > c0 ? 16 : 0);
       }
       to += across * group_bytes;
       const uint16_t* wg = wp + c0;
-      for (int g = 0; g < across; ++g, to += w_bytes, wg += 64) {
-        const bool in = c0 + g * 64 + piece * 8 < cols;
+      int more = cols - c0 - piece * 8;
+      for (int g = 0; g < across; ++g, to += w_bytes, wg += 64, more -= 64) {
 #pragma unroll
         for (int i = 0; i < (R + 31) / 32; ++i) {
           const int k = r0 + 32 * i;
-          if (k < ranks) copy16(to + 4096 * i, in && k < p.rank ? wg + 32 * i * p.width : p.w, in && k < p.rank);
+          if (k < ranks) copy16(to + 4096 * i, wg + 32 * i * static_cast<int64_t>(p.width), more > 0 && (FULL || k < rank) ? 16 : 0);
         }
       }
     }
@@ -419,31 +437,31 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
   // this warp's rows of u, as the products take them
   constexpr int kTerms = 2;
   uint32_t a[kTerms][R / 16][4];
-  float factor[2];
+  float unit[2] = {1.0f, 1.0f}, back[2] = {1.0f, 1.0f};
   const float f = p.scales != nullptr ? p.scales[adapter] : 1.0f;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = mw * 16 + (lane >> 2) + 8 * h;
     const int32_t t = r < n ? token[r] : -1;
-    const float* u = p.u + static_cast<int64_t>(t < 0 ? 0 : t) * p.rank + 2 * (lane & 3);
+    const float* u = p.u + static_cast<int64_t>(t < 0 ? 0 : t) * rank + 2 * (lane & 3);
     float2 v[R / 8];
     float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < R / 8; ++i) {
-      v[i] = t >= 0 && i * 8 < p.rank ? *reinterpret_cast<const float2*>(u + i * 8) : make_float2(0.0f, 0.0f);
+      v[i] = t >= 0 && i * 8 < rank ? *reinterpret_cast<const float2*>(u + i * 8) : make_float2(0.0f, 0.0f);
       most = fmaxf(most, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
     }
-    float unit = 1.0f;
     if (KIND == OK_F16) {
       most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-      unit = unit_of(most);
+      // bounded, so that the base times it stays a number of full precision
+      unit[h] = fminf(fmaxf(unit_of(most * fabsf(f)), 0x1p-90f), 0x1p40f);
+      back[h] = 1.0f / unit[h];
     }
-    factor[h] = f / unit;
 #pragma unroll
     for (int i = 0; i < R / 8; ++i) {
       uint32_t term[kTerms];
-      split_terms<KIND, kTerms>(v[i].x * unit, v[i].y * unit, term);
+      split_terms<KIND, kTerms>(v[i].x * f * unit[h], v[i].y * f * unit[h], term);
 #pragma unroll
       for (int k = 0; k < kTerms; ++k) a[k][i / 2][2 * (i & 1) + h] = term[k];
     }
@@ -465,14 +483,22 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
     const int c0 = (pass * across + cw) * 64;
     if (cw < across && c0 < cols) {
       const uint32_t ys = at + cw * group_bytes, ws = at + across * group_bytes + cw * w_bytes;
+      // the sums start from the base
+      const uint32_t mine = ys + (mw * 16 + (lane >> 2)) * 128 + 4 * (lane & 3);
+      const uint32_t turn = (lane >> 2) << 4;
       float acc[8][4];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+        for (int h = 0; h < 2; ++h) {
+          float2 v = make_float2(0.0f, 0.0f);
+          if (from != nullptr) v = unpack2<KIND>(get_shared(mine + ((i << 4) ^ turn) + 1024 * h));
+          acc[i][2 * h] = KIND == OK_F16 ? v.x * unit[h] : v.x;
+          acc[i][2 * h + 1] = KIND == OK_F16 ? v.y * unit[h] : v.y;
+        }
 #pragma unroll
       for (int s = 0; s < R / 16; ++s) {
-        if (s * 16 >= p.rank) break;
+        if (!FULL && s * 16 >= rank) break;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           uint32_t b[4];
@@ -485,21 +511,16 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
         }
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = mw * 16 + (lane >> 2) + 8 * h;
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t* to = reinterpret_cast<uint32_t*>(smem + (ys - base) + swizzled(r, i) + 4 * (lane & 3));
-          const float2 old = from != nullptr ? unpack2<KIND>(*to) : make_float2(0.0f, 0.0f);
-          *to = pack2<KIND>(fmaf(factor[h], acc[i][2 * h], old.x), fmaf(factor[h], acc[i][2 * h + 1], old.y));
-        }
-      }
+        for (int h = 0; h < 2; ++h)
+          put_shared(mine + ((i << 4) ^ turn) + 1024 * h,
+                     KIND == OK_F16 ? pack2<KIND>(acc[i][2 * h] * back[h], acc[i][2 * h + 1] * back[h]) : pack2<KIND>(acc[i][2 * h], acc[i][2 * h + 1]));
       __syncwarp();
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (yp[e] != nullptr && c0 + (lane & 7) * 8 < cols)
-          *reinterpret_cast<uint4*>(yp[e] + c0) =
-              *reinterpret_cast<const uint4*>(smem + (ys - base) + swizzled(mw * 16 + e * 4 + (lane >> 3), lane & 7));
+          *reinterpret_cast<uint4*>(yp[e] + c0) = get_shared4(ys + swizzled(mw * 16 + e * 4 + (lane >> 3), lane & 7));
       }
     }
     __syncthreads();                                   // the buffer is read
@@ -533,10 +554,11 @@ struct OuterParams {
   int width, rank, split, out_kind;
 };
 
-template <int KIND, int R, int TERMS>
-__global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__ OuterParams p) {
+template <int KIND, int R, int TERMS, bool FULL>
+__global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const __grid_constant__ OuterParams p) {
   using O = Outer<R>;
   constexpr int kTiles = O::kCols / 8 / kWarps;         // of 8 columns, a warp
+  const int rank = FULL ? R : p.rank;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int32_t token[O::kStages + 1][O::kTokens];
   __shared__ uint32_t has[O::kStages + 1][O::kTokens / 32];
@@ -568,8 +590,8 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     for (int64_t i = threadIdx.x; i < static_cast<int64_t>(chunks) * O::kTokens; i += kThreads) {
       const int32_t t = token_of(static_cast<int>(i / O::kTokens), static_cast<int>(i % O::kTokens));
       if (t < 0) continue;
-      for (int k = 0; k < p.rank; k += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p.g + static_cast<int64_t>(t) * p.rank + k);
+      for (int k = 0; k < rank; k += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p.g + static_cast<int64_t>(t) * rank + k);
         most = fmaxf(fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
       }
     }
@@ -587,7 +609,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
   const int piece = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
   const int quad = threadIdx.x % kQuads, g0 = threadIdx.x / kQuads;
   const bool in_cols = col0 + piece * 8 < p.width;
-  const uint16_t* xp = static_cast<const uint16_t*>(p.x) + col0 + piece * 8;
+  const uint16_t* xp = static_cast<const uint16_t*>(p.x) + (in_cols ? col0 + piece * 8 : 0);
   const uint32_t x_to = base + (piece >> 3) * (O::kTokens * 128) + swizzled(r0, piece & 7);
   static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
   auto load = [&](int c) {
@@ -597,15 +619,14 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
 #pragma unroll
       for (int i = 0; i < O::kTokens / kStep; ++i) {
         const int32_t t = tok[r0 + i * kStep];
-        const bool in = t >= 0 && in_cols;
-        copy16(x_to + stage + i * kStep * 128, in ? xp + t * p.ldx : p.x, in);
+        copy16(x_to + stage + i * kStep * 128, xp + (t >= 0 ? t * p.ldx : 0), t >= 0 && in_cols ? 16 : 0);
       }
-      if (quad * 4 < p.rank) {
+      if (FULL || quad * 4 < rank) {
 #pragma unroll
         for (int i = 0; i < O::kTokens / kGStep; ++i) {
           const int r = g0 + i * kGStep;
           const int32_t t = tok[r];
-          copy16(base + stage + O::kXBytes + (r * R + quad * 4) * 4, t >= 0 ? p.g + static_cast<int64_t>(t) * p.rank + quad * 4 : p.g, t >= 0);
+          copy16(base + stage + O::kXBytes + (r * R + quad * 4) * 4, p.g + (t >= 0 ? static_cast<int64_t>(t) * rank + quad * 4 : 0), t >= 0 ? 16 : 0);
         }
       }
     }
@@ -618,15 +639,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[m][i][k] = sum[m][i][k] = 0.0f;
-  auto flush = [&]() {
-#pragma unroll
-    for (int m = 0; m < R / 16; ++m)
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) { sum[m][i][k] += acc[m][i][k]; acc[m][i][k] = 0.0f; }
-  };
+      for (int k = 0; k < 4; ++k) sum[m][i][k] = 0.0f;
   auto put_tokens = [&](int c, int32_t t) {
     const uint32_t b = __ballot_sync(0xFFFFFFFFu, t >= 0);
     if (threadIdx.x < O::kTokens) token[c % (O::kStages + 1)][threadIdx.x] = t;
@@ -635,66 +648,82 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
   for (int c = 0; c < O::kStages - 1; ++c) put_tokens(c, threadIdx.x < O::kTokens ? token_of(c, threadIdx.x) : -1);
   __syncthreads();
   for (int c = 0; c < O::kStages - 1; ++c) load(c);
-  for (int c = 0; c < chunks; ++c) {
-    int32_t next = -1;
-    const int ahead = c + O::kStages - 1;
-    if (threadIdx.x < O::kTokens) next = token_of(ahead, threadIdx.x);
-    copies_wait<O::kStages - 2>();
-    put_tokens(ahead, next);
-    __syncthreads();                                   // chunk c is there, c - 1 is read, the next one's tokens are known
-    // an adapter's tokens come first: behind them there are only padding rows
-    if ((has[c % (O::kStages + 1)][0] | has[c % (O::kStages + 1)][1]) == 0) break;
-    load(ahead);
-    const uint32_t stage = base + (c % O::kStages) * O::kStageBytes;
-    // g as terms of 16 bits, ranks up to a multiple of 16
-    const float* g = reinterpret_cast<const float*>(smem + (stage - base) + O::kXBytes);
+  bool done = false;
+  for (int c0 = 0; c0 < chunks && !done; c0 += kRun / O::kTokens) {
 #pragma unroll
-    for (int i = 0; i < O::kTokens / kGStep; ++i) {
-      const int r = g0 + i * kGStep;
-      float4 v = make_float4(0, 0, 0, 0);
-      if (quad * 4 < p.rank) v = *reinterpret_cast<const float4*>(g + r * R + quad * 4);
-      uint32_t lo[TERMS], hi[TERMS];
-      split_terms<KIND, TERMS>(v.x * unit, v.y * unit, lo);
-      split_terms<KIND, TERMS>(v.z * unit, v.w * unit, hi);
+    for (int m = 0; m < R / 16; ++m)
 #pragma unroll
-      for (int k = 0; k < TERMS; ++k)
-        *reinterpret_cast<uint2*>(smem + (terms - base) + k * O::kTermBytes + r * O::kTermPitch + quad * 8) = make_uint2(lo[k], hi[k]);
-    }
-    __syncthreads();
+      for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-    for (int s = 0; s < O::kTokens / 16; ++s) {
-      uint32_t b[kTiles / 2][4];
-#pragma unroll
-      for (int i = 0; i < kTiles; i += 2) {
-        const int tile = warp * kTiles + i;              // of 8 columns; 8 of them share 128 bytes
-        load_matrices_t(b[i / 2], stage + (tile >> 3) * (O::kTokens * 128) + swizzled(s * 16 + (lane & 15), (tile & 7) + (lane >> 4)));
+        for (int k = 0; k < 4; ++k) acc[m][i][k] = 0.0f;
+    const int c1 = min(c0 + kRun / O::kTokens, chunks);
+    for (int c = c0; c < c1; ++c) {
+      int32_t next = -1;
+      const int ahead = c + O::kStages - 1;
+      if (threadIdx.x < O::kTokens) next = token_of(ahead, threadIdx.x);
+      copies_wait<O::kStages - 2>();
+      put_tokens(ahead, next);
+      __syncthreads();                                   // chunk c is there, c - 1 is read, the next one's tokens are known
+      // an adapter's tokens come first: behind them there are only padding rows
+      if ((has[c % (O::kStages + 1)][0] | has[c % (O::kStages + 1)][1]) == 0) {
+        done = true;
+        break;
       }
+      load(ahead);
+      const uint32_t stage = base + (c % O::kStages) * O::kStageBytes;
+      // g as terms of 16 bits, ranks up to a multiple of 16
 #pragma unroll
-      for (int m = 0; m < R / 16; ++m) {
-        if (m * 16 >= p.rank) break;
+      for (int i = 0; i < O::kTokens / kGStep; ++i) {
+        const int r = g0 + i * kGStep;
+        float4 v = make_float4(0, 0, 0, 0);
+        if (FULL || quad * 4 < rank) v = get_shared4f(stage + O::kXBytes + (r * R + quad * 4) * 4);
+        uint32_t lo[TERMS], hi[TERMS];
+        split_terms<KIND, TERMS>(v.x * unit, v.y * unit, lo);
+        split_terms<KIND, TERMS>(v.z * unit, v.w * unit, hi);
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k) {
-          uint32_t a[4];
-          load_matrices_t(a, terms + k * O::kTermBytes + (s * 16 + (lane & 7) + ((lane >> 4) << 3)) * O::kTermPitch +
-                                 (m * 2 + ((lane >> 3) & 1)) * 16);
+        for (int k = 0; k < TERMS; ++k)
+          put_shared2(terms + k * O::kTermBytes + r * O::kTermPitch + quad * 8, lo[k], hi[k]);
+      }
+      __syncthreads();
 #pragma unroll
-          for (int i = 0; i < kTiles; i += 2) {
-            multiply<KIND>(acc[m][i], a, b[i / 2][0], b[i / 2][1]);
-            multiply<KIND>(acc[m][i + 1], a, b[i / 2][2], b[i / 2][3]);
+      for (int s = 0; s < O::kTokens / 16; ++s) {
+        uint32_t b[kTiles / 2][4];
+#pragma unroll
+        for (int i = 0; i < kTiles; i += 2) {
+          const int tile = warp * kTiles + i;              // of 8 columns; 8 of them share 128 bytes
+          load_matrices_t(b[i / 2], stage + (tile >> 3) * (O::kTokens * 128) + swizzled(s * 16 + (lane & 15), (tile & 7) + (lane >> 4)));
+        }
+#pragma unroll
+        for (int m = 0; m < R / 16; ++m) {
+          if (!FULL && m * 16 >= rank) break;
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) {
+            uint32_t a[4];
+            load_matrices_t(a, terms + k * O::kTermBytes + (s * 16 + (lane & 7) + ((lane >> 4) << 3)) * O::kTermPitch +
+                                   (m * 2 + ((lane >> 3) & 1)) * 16);
+#pragma unroll
+            for (int i = 0; i < kTiles; i += 2) {
+              multiply<KIND>(acc[m][i], a, b[i / 2][0], b[i / 2][1]);
+              multiply<KIND>(acc[m][i + 1], a, b[i / 2][2], b[i / 2][3]);
+            }
           }
         }
       }
     }
-    if ((c + 1) % (kRun / O::kTokens) == 0) flush();
+#pragma unroll
+    for (int m = 0; m < R / 16; ++m)
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[m][i][k] += acc[m][i][k];
   }
-  flush();
   copies_wait<0>();
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
   const float back = 1.0f / unit;
 #pragma unroll
   for (int m = 0; m < R / 16; ++m) {
-    if (m * 16 >= p.rank) break;
+    if (!FULL && m * 16 >= rank) break;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       float* at = sums + (m * 16 + (lane >> 2)) * O::kCols + (warp * kTiles + i) * 8 + 2 * (lane & 3);
@@ -704,7 +733,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
   }
   if (p.split > 1) cluster_sync(); else __syncthreads();
   const float f = p.scales != nullptr ? p.scales[adapter] : 1.0f;
-  const int pieces = p.rank * (O::kCols / 8);            // of 8 columns
+  const int pieces = rank * (O::kCols / 8);            // of 8 columns
   const int e0 = pieces * part / p.split, e1 = pieces * (part + 1) / p.split;
   for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
     const int r = e / (O::kCols / 8), q = e % (O::kCols / 8);
@@ -720,7 +749,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] *= f;
-    const int64_t to = (static_cast<int64_t>(adapter) * p.rank + r) * p.width + col;
+    const int64_t to = (static_cast<int64_t>(adapter) * rank + r) * p.width + col;
     if (p.out_kind == OK_F32) store8<OK_F32>(p.out, to, v);
     else if (p.out_kind == OK_F16) store8<OK_F16>(p.out, to, v);
     else store8<OK_BF16>(p.out, to, v);
@@ -729,13 +758,16 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- host
-// Calls f with the least of 16, 32, 64, 128 that holds the rank.
+// Calls f with the least of 16, 32, 64, 128 that holds the rank, and whether it is the rank.
 template <typename F>
 bsgg_status with_rank(int rank, F&& f) {
-  if (rank <= 16) return f(std::integral_constant<int, 16>());
-  if (rank <= 32) return f(std::integral_constant<int, 32>());
-  if (rank <= 64) return f(std::integral_constant<int, 64>());
-  return f(std::integral_constant<int, 128>());
+  auto at = [&](auto r) {
+    return rank == decltype(r)::value ? f(r, std::true_type()) : f(r, std::false_type());
+  };
+  if (rank <= 16) return at(std::integral_constant<int, 16>());
+  if (rank <= 32) return at(std::integral_constant<int, 32>());
+  if (rank <= 64) return at(std::integral_constant<int, 64>());
+  return at(std::integral_constant<int, 128>());
 }
 template <typename F>
 bsgg_status with_half(int format, F&& f) {
@@ -759,11 +791,12 @@ bsgg_status launch_shrink(int format, ShrinkParams p, cudaStream_t s) {
   p.split = 1;
   while (p.split < kMaxCluster && busy * p.split < 228 && nb >= 4 * p.split) p.split *= 2;
   return with_half(format, [&](auto kind) {
-    return with_rank(p.rank, [&](auto r) {
+    return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
-      if (!allowed(shrink_kernel<K, R>, Shrink<R>::kSmem)) return BSGG_ERR_CUDA;
+      constexpr bool E = decltype(full)::value;
+      if (!allowed(shrink_kernel<K, R, E>, Shrink<R>::kSmem)) return BSGG_ERR_CUDA;
       const LaunchConfig c(dim3(static_cast<unsigned>(tiles * p.split)), kThreads, Shrink<R>::kSmem, s, p.split);
-      return launch_kernel(c, shrink_kernel<K, R>, p);
+      return launch_kernel(c, shrink_kernel<K, R, E>, p);
     });
   });
 }
@@ -772,20 +805,22 @@ bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
   p.tiles = p.map.m_pad / 128;
   const int64_t blocks = p.tiles + ceil_div(p.map.tokens, kThreads);
   return with_half(format, [&](auto kind) {
-    return with_rank(p.rank, [&](auto r) {
+    return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
-      if (!allowed(expand_kernel<K, R>, Expand<R>::kSmem)) return BSGG_ERR_CUDA;
+      constexpr bool E = decltype(full)::value;
+      if (!allowed(expand_kernel<K, R, E>, Expand<R>::kSmem)) return BSGG_ERR_CUDA;
       const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ceil_div(p.width, Expand<R>::kCols)));
       const LaunchConfig c(grid, kThreads, Expand<R>::kSmem, s);
-      return launch_kernel(c, expand_kernel<K, R>, p);
+      return launch_kernel(c, expand_kernel<K, R, E>, p);
     });
   });
 }
 
 bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
   return with_half(format, [&](auto kind) {
-    return with_rank(p.rank, [&](auto r) {
+    return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
+      constexpr bool E = decltype(full)::value;
       p.blocks = ceil_div(p.width, Outer<R>::kCols);
       // parts of an adapter's tokens: until two blocks an SM have work, of two chunks at least
       const int64_t used = p.map.tokens < p.map.adapters ? p.map.tokens : p.map.adapters;
@@ -795,9 +830,9 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
       const int64_t grid = p.map.adapters * p.blocks * p.split;
       auto launch = [&](auto terms) {
         constexpr int N = decltype(terms)::value;
-        if (!allowed(outer_kernel<K, R, N>, Outer<R>::smem(N))) return BSGG_ERR_CUDA;
+        if (!allowed(outer_kernel<K, R, N, E>, Outer<R>::smem(N))) return BSGG_ERR_CUDA;
         const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, Outer<R>::smem(N), s, p.split);
-        return launch_kernel(c, outer_kernel<K, R, N>, p);
+        return launch_kernel(c, outer_kernel<K, R, N, E>, p);
       };
       if constexpr (K == OK_BF16) {
         if (p.out_kind == OK_F32) return launch(std::integral_constant<int, 3>());
