@@ -302,16 +302,18 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) shrink_kernel(const
 }
 
 // ---------------------------------------------------------------- expand
-// A block takes 128 rows of one adapter and 512 columns, in passes: base and W come in by
-// asynchronous copies, a warp multiplies 16 rows by 64 columns, adds the base where it
-// lies in shared memory, and stores rows of 128 bytes.  Eight groups of 16 rows are eight
-// warps on the same 64 columns; with fewer tokens the warps lie along the columns.  The
-// blocks behind the tiles see to the tokens without an adapter.
+// A block takes 128 rows of one adapter and kCols columns.  W's columns come in at once;
+// behind that one barrier the warps go their own ways: each fetches the base of its 16 rows
+// and 64 columns by asynchronous copies, kBuffers passes ahead, starts its sums from it,
+// multiplies, and stores rows of 128 bytes.  Eight groups of 16 rows are eight warps that
+// walk the same columns; with fewer tokens the warps lie along the columns too.  The blocks
+// behind the tiles see to the tokens without an adapter.
 template <int R>
 struct Expand {
-  static constexpr int kRows = 128, kCols = 512, kPasses = 3;
-  static constexpr int kMaxAcross = R == 128 ? 4 : 8;     // warps along the columns
-  static constexpr int kSmem = (R == 16 ? 54 : R == 32 ? 60 : R == 64 ? 80 : 96) * 1024 + 128;
+  static constexpr int kRows = 128, kCols = R == 16 ? 1024 : R == 128 ? 256 : 512, kBuffers = R == 16 ? 2 : 3;
+  static constexpr int kTileBytes = 16 * 128;             // a warp's rows of 64 columns
+  static constexpr int kWBytes = kCols * R * 2;
+  static constexpr int kSmem = kWBytes + kWarps * kBuffers * kTileBytes + 128;
 };
 
 struct ExpandParams {
@@ -322,14 +324,14 @@ struct ExpandParams {
   const void* base;
   void* y;
   float* zero_u;              // u's rows of tokens without an adapter, where wanted
-  int64_t ld_base, ldy, tiles;
-  int width, rank;
+  int64_t tiles;
+  int ld_base, ldy, width, rank;
 };
 
 // Tokens without an adapter: y = base, u = 0.
-__device__ __noinline__ void expand_rest(const ExpandParams& p, int64_t block, int cols) {
-  __shared__ int32_t list[kThreads];
-  __shared__ int count[kWarps];
+__device__ __noinline__ void expand_rest(const ExpandParams& p, int64_t block, int cols, uint8_t* smem) {
+  int32_t* list = reinterpret_cast<int32_t*>(smem);
+  int* count = list + kThreads;
   const int64_t t = block * kThreads + threadIdx.x;
   bool none = false;
   if (t < p.map.tokens) {
@@ -353,9 +355,9 @@ __device__ __noinline__ void expand_rest(const ExpandParams& p, int64_t block, i
     for (int e = threadIdx.x; e < all * pieces; e += kThreads) {
       const int64_t tok = list[e / pieces], c = c0 + (e % pieces) * 8;
       if (c >= p.width) continue;
-      const uint4 v = p.base != nullptr ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + tok * p.ld_base + c)
+      const uint4 v = p.base != nullptr ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + tok * static_cast<int64_t>(p.ld_base) + c)
                                         : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + tok * p.ldy + c) = v;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + tok * static_cast<int64_t>(p.ldy) + c) = v;
     }
   }
   if (p.zero_u != nullptr && blockIdx.y == 0) {
@@ -366,14 +368,14 @@ __device__ __noinline__ void expand_rest(const ExpandParams& p, int64_t block, i
 }
 
 template <int KIND, int R, bool FULL>
-__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_constant__ ExpandParams p) {
+__global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const __grid_constant__ ExpandParams p) {
   using E = Expand<R>;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ int32_t token[E::kRows];
   let_next_kernel_start();
   wait_for_previous_kernel();
   if (blockIdx.x >= p.tiles) {
-    expand_rest(p, blockIdx.x - p.tiles, E::kCols);
+    expand_rest(p, blockIdx.x - p.tiles, E::kCols, smem_raw);
     return;
   }
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -383,56 +385,61 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
   const int n = tokens_of<E::kRows>(p.map, row0, token);
   if (n == 0) return;
   const int adapter = adapter_of(p.map, row0);
-  const int groups = row_groups(n), rows = 16 * groups, log_rows = 31 - __clz(rows), across = min(kWarps / groups, E::kMaxAcross);
+  const int groups = row_groups(n), across = min(kWarps / groups, E::kCols / 64 < kWarps ? E::kCols / 64 : kWarps);
   const int mw = warp % groups, cw = warp / groups;
   const int rank = FULL ? R : p.rank, ranks = FULL ? R : (rank + 15) & ~15;   // whole steps of 16, zeros behind the rank
   const int cols = static_cast<int>(min(int64_t(E::kCols), p.width - col0));
   const int passes = (cols + 64 * across - 1) / (64 * across);
-  const uint32_t group_bytes = rows * 128, w_bytes = ranks * 128;
-  const uint32_t pass_bytes = across * (group_bytes + w_bytes);
-  const int buffers = max(1, min(E::kPasses, static_cast<int>((E::kSmem - 128) / pass_bytes)));
-  const uint16_t* from = static_cast<const uint16_t*>(p.base);
-  // a thread copies one 16-byte piece of every 32nd row, of the base's rows * across and of
-  // W's: what changes from pass to pass is an offset
-  const int piece = threadIdx.x & 7, r0 = threadIdx.x >> 3;
-  const uint16_t* fp[E::kRows / 32];
-  int left[E::kRows / 32];                             // columns of the block from this piece on, 0 without a token
-#pragma unroll
-  for (int i = 0; i < E::kRows / 32; ++i) {
-    const int q = r0 + 32 * i, r = q & (rows - 1), c = (q >> log_rows) * 64 + piece * 8;
-    const int32_t t = q < rows * across && r < n ? token[r] : -1;
-    left[i] = t >= 0 ? cols - c : 0;
-    fp[i] = from + (t >= 0 ? t * p.ld_base + col0 + c : 0);
-  }
-  const uint16_t* wp = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * rank + r0) * p.width + col0 + piece * 8;
-  const uint32_t to0 = base + swizzled(r0, piece);
+  const uint32_t w_bytes = ranks * 128;                 // of 64 columns
 
-  // of 64 columns each: the rows of the base, then those of W
-  auto load = [&](int pass) {
-    if (pass < passes) {
-      uint32_t to = to0 + (pass % buffers) * pass_bytes;
-      const int c0 = pass * across * 64;
-      if (from != nullptr) {
+  // W: a thread copies one 16-byte piece of every 32nd row of each 64 columns
+  {
+    const int piece = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+    const uint16_t* w = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * rank + r0) * p.width + col0 + piece * 8;
+    uint32_t to = base + swizzled(r0, piece);
+    for (int c = piece * 8; c - piece * 8 < cols; c += 64, to += w_bytes, w += 64) {
 #pragma unroll
-        for (int i = 0; i < E::kRows / 32; ++i)
-          if (r0 + 32 * i < rows * across) copy16(to + 4096 * i, fp[i] + c0, left[i] > c0 ? 16 : 0);
-      }
-      to += across * group_bytes;
-      const uint16_t* wg = wp + c0;
-      int more = cols - c0 - piece * 8;
-      for (int g = 0; g < across; ++g, to += w_bytes, wg += 64, more -= 64) {
-#pragma unroll
-        for (int i = 0; i < (R + 31) / 32; ++i) {
-          const int k = r0 + 32 * i;
-          if (k < ranks) copy16(to + 4096 * i, wg + 32 * i * static_cast<int64_t>(p.width), more > 0 && (FULL || k < rank) ? 16 : 0);
-        }
+      for (int i = 0; i < (R + 31) / 32; ++i) {
+        const int k = r0 + 32 * i;
+        if (k < ranks) copy16(to + 4096 * i, w + 32 * i * static_cast<int64_t>(p.width), c < cols && (FULL || k < rank) ? 16 : 0);
       }
     }
+  }
+  copies_commit();
+
+  // this lane's pieces of the warp's rows, of base and y alike
+  const uint16_t* from = static_cast<const uint16_t*>(p.base);
+  const uint32_t tile = base + E::kWBytes + warp * E::kBuffers * E::kTileBytes;
+  const int at_row = lane >> 3, at_col = static_cast<int>(cw * 64 + (lane & 7) * 8);
+  int32_t at_token[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r = mw * 16 + e * 4 + at_row;
+    at_token[e] = r < n ? token[r] : -1;
+  }
+  // rows e * 4 + at_row of the tile: the swizzle of row 4 + r is that of r with its piece moved by 4
+  const uint32_t at0 = swizzled(at_row, lane & 7), at1 = swizzled(4 + at_row, lane & 7);
+  const int stride = across * 64;
+  int load_col = at_col;
+  const uint16_t* load_from = from + col0 + at_col;
+  auto load = [&](int pass) {
+    if (from != nullptr && cw < across && load_col < cols) {
+      const uint32_t to = tile + (pass % E::kBuffers) * E::kTileBytes;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        copy16(to + ((e & 1) ? at1 : at0) + (e >> 1) * 1024, load_from + static_cast<int64_t>(max(at_token[e], 0)) * p.ld_base,
+               at_token[e] >= 0 ? 16 : 0);
+    }
+    load_col += stride;
+    load_from += stride;
     copies_commit();
   };
-  for (int i = 0; i < E::kPasses; ++i) {
-    if (i < buffers) load(i); else copies_commit();
-  }
+  uint16_t* store_to = static_cast<uint16_t*>(p.y) + col0 + at_col;
+  uint32_t w_at[4];                                    // pieces 2 i of the products' rows of W
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w_at[i] = base + swizzled(lane & 15, 2 * i + (lane >> 4));
+#pragma unroll
+  for (int i = 0; i < E::kBuffers; ++i) load(i);
 
   // this warp's rows of u, as the products take them
   constexpr int kTerms = 2;
@@ -448,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
     float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < R / 8; ++i) {
-      v[i] = t >= 0 && i * 8 < rank ? *reinterpret_cast<const float2*>(u + i * 8) : make_float2(0.0f, 0.0f);
+      v[i] = t >= 0 && (FULL || i * 8 < rank) ? *reinterpret_cast<const float2*>(u + i * 8) : make_float2(0.0f, 0.0f);
       most = fmaxf(most, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
     }
     if (KIND == OK_F16) {
@@ -466,25 +473,17 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
       for (int k = 0; k < kTerms; ++k) a[k][i / 2][2 * (i & 1) + h] = term[k];
     }
   }
+  copies_wait<E::kBuffers>();
+  __syncthreads();                                     // W is there
 
-  uint16_t* yp[4];             // this lane's pieces of the rows that the warp stores
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int r = mw * 16 + e * 4 + (lane >> 3);
-    const int32_t t = r < n ? token[r] : -1;
-    yp[e] = t >= 0 ? static_cast<uint16_t*>(p.y) + t * p.ldy + col0 + (lane & 7) * 8 : nullptr;
-  }
   for (int pass = 0; pass < passes; ++pass) {
-    if (buffers == 1) copies_wait<0>();
-    else if (buffers == 2) copies_wait<1>();
-    else copies_wait<2>();
-    __syncthreads();
-    const uint32_t at = base + (pass % buffers) * pass_bytes;
+    copies_wait<E::kBuffers - 1>();
+    __syncwarp();                                      // and this pass's base
     const int c0 = (pass * across + cw) * 64;
     if (cw < across && c0 < cols) {
-      const uint32_t ys = at + cw * group_bytes, ws = at + across * group_bytes + cw * w_bytes;
+      const uint32_t ys = tile + (pass % E::kBuffers) * E::kTileBytes, ws = (c0 >> 6) * w_bytes;
       // the sums start from the base
-      const uint32_t mine = ys + (mw * 16 + (lane >> 2)) * 128 + 4 * (lane & 3);
+      const uint32_t mine = ys + (lane >> 2) * 128 + 4 * (lane & 3);
       const uint32_t turn = (lane >> 2) << 4;
       float acc[8][4];
 #pragma unroll
@@ -502,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           uint32_t b[4];
-          load_matrices_t(b, ws + s * 2048 + swizzled(lane & 15, i + (lane >> 4)));
+          load_matrices_t(b, w_at[i / 2] + ws + s * 2048);
 #pragma unroll
           for (int k = 0; k < kTerms; ++k) {
             multiply<KIND>(acc[i], a[k][s], b[0], b[1]);
@@ -517,14 +516,16 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
           put_shared(mine + ((i << 4) ^ turn) + 1024 * h,
                      KIND == OK_F16 ? pack2<KIND>(acc[i][2 * h] * back[h], acc[i][2 * h + 1] * back[h]) : pack2<KIND>(acc[i][2 * h], acc[i][2 * h + 1]));
       __syncwarp();
+      const int c = pass * across * 64 + at_col;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (yp[e] != nullptr && c0 + (lane & 7) * 8 < cols)
-          *reinterpret_cast<uint4*>(yp[e] + c0) = get_shared4(ys + swizzled(mw * 16 + e * 4 + (lane >> 3), lane & 7));
+        const uint4 v = get_shared4(ys + ((e & 1) ? at1 : at0) + (e >> 1) * 1024);
+        if (at_token[e] >= 0 && c < cols) *reinterpret_cast<uint4*>(store_to + static_cast<int64_t>(at_token[e]) * p.ldy) = v;
       }
+      __syncwarp();                                    // the buffer is read
     }
-    __syncthreads();                                   // the buffer is read
-    load(pass + buffers);
+    store_to += stride;
+    load(pass + E::kBuffers);
   }
   copies_wait<0>();
 }
@@ -876,7 +877,8 @@ bsgg_status bsgg_adapters(const bsgg_adapters_desc* d, const void* x, const void
   const AdapterMap map = {d->tokens, d->m_pad, d->adapters, padded_offsets, row_of_slot, slot_of_row};
   const bsgg_status ran = launch_shrink(d->format, {map, x, a, nullptr, u, d->ldx, static_cast<int>(d->k), d->rank, 1}, s);
   if (ran != BSGG_OK) return ran;
-  return launch_expand(d->format, {map, u, b, scales, base, y, u, d->ld_base, d->ldy, 0, static_cast<int>(d->n), d->rank}, s);
+  return launch_expand(d->format, {map, u, b, scales, base, y, u, 0, base ? static_cast<int>(d->ld_base) : 0, static_cast<int>(d->ldy),
+                                   static_cast<int>(d->n), d->rank}, s);
 }
 
 bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* dy, const void* x, const float* u,
@@ -914,7 +916,8 @@ bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* 
   if (ran == BSGG_OK && db) ran = launch_outer(d->format, {map, u, dy, scales, db, d->ld_dy, 0, static_cast<int>(d->n), d->rank, 1, d->grad_format}, s);
   if (ran == BSGG_OK && da) ran = launch_outer(d->format, {map, du, x, nullptr, da, d->ldx, 0, static_cast<int>(d->k), d->rank, 1, d->grad_format}, s);
   if (ran == BSGG_OK && dx)
-    ran = launch_expand(d->format, {map, du, a, nullptr, base, dx, nullptr, d->ld_base, d->ld_dx, 0, static_cast<int>(d->k), d->rank}, s);
+    ran = launch_expand(d->format, {map, du, a, nullptr, base, dx, nullptr, 0, base ? static_cast<int>(d->ld_base) : 0,
+                                   static_cast<int>(d->ld_dx), static_cast<int>(d->k), d->rank}, s);
   return ran;
 }
 
