@@ -33,7 +33,7 @@ SYMBOLS = ("bsgg_create", "bsgg_run", "bsgg_run_host", "bsgg_run_host_async", "b
            "bsgg_dispatch", "bsgg_combine", "bsgg_combine_backward", "bsgg_linear", "bsgg_linear_backward",
            "bsgg_query_status_word",
            "bsgg_route_groups", "bsgg_route_groups_backward", "bsgg_rms_norm", "bsgg_rms_norm_workspace_bytes",
-           "bsgg_rms_norm_backward", "bsgg_adapters", "bsgg_adapters_backward")
+           "bsgg_rms_norm_backward", "bsgg_adapters", "bsgg_adapters_workspace_bytes", "bsgg_adapters_backward")
 
 
 class BsggError(RuntimeError):

@@ -68,10 +68,10 @@ __device__ __forceinline__ void load_matrices_t(uint32_t (&r)[4], uint32_t addr)
 template <int KIND>
 __device__ __forceinline__ void multiply(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (KIND == OK_BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
@@ -163,7 +163,7 @@ struct ShrinkParams {
 };
 
 template <int KIND, int R, bool FULL>
-__global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) shrink_kernel(const __grid_constant__ ShrinkParams p) {
+__global__ void __launch_bounds__(kThreads, R <= 32 ? 3 : R == 64 ? 2 : 1) shrink_kernel(const __grid_constant__ ShrinkParams p) {
   using S = Shrink<R>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int32_t token[S::kRows];
@@ -243,14 +243,15 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) shrink_kernel(const
         uint32_t a[4];
         load_matrices(a, xs + swizzled(ar, kk + (lane >> 4)));
         const uint32_t bs = xs + rows * 128 + swizzled(br, kk + ((lane >> 3) & 1));
+        uint32_t b[R / 16][4];
 #pragma unroll
-        for (int i = 0; i < R / 8; i += 2) {
-          if (!FULL && i * 8 >= rank) break;
-          uint32_t b[4];
+        for (int i = 0; i < R / 16; ++i)
           // of an odd number of eights the last pair's second half is what lies behind: inside the stage, and unused
-          load_matrices(b, bs + i * 1024);
-          multiply<KIND>(acc[i], a, b[0], b[1]);
-          if (FULL || (i + 1) * 8 < rank) multiply<KIND>(acc[i + 1], a, b[2], b[3]);
+          if (FULL || i * 16 < rank) load_matrices(b[i], bs + i * 2048);
+#pragma unroll
+        for (int i = 0; i < R / 16; ++i) {
+          if (FULL || i * 16 < rank) multiply<KIND>(acc[2 * i], a, b[i][0], b[i][1]);
+          if (FULL || i * 16 + 8 < rank) multiply<KIND>(acc[2 * i + 1], a, b[i][2], b[i][3]);
         }
       }
     }
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) shrink_kernel(const
 // behind the tiles see to the tokens without an adapter.
 template <int R>
 struct Expand {
-  static constexpr int kRows = 128, kCols = R == 16 ? 1024 : R == 128 ? 256 : 512, kBuffers = R == 16 ? 2 : 3;
+  static constexpr int kRows = 128, kCols = R == 16 ? 1024 : R == 128 ? 256 : 512, kBuffers = 2;
   static constexpr int kTileBytes = 16 * 128;             // a warp's rows of 64 columns
   static constexpr int kWBytes = kCols * R * 2;
   static constexpr int kSmem = kWBytes + kWarps * kBuffers * kTileBytes + 128;
@@ -498,16 +499,16 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
 #pragma unroll
       for (int s = 0; s < R / 16; ++s) {
         if (!FULL && s * 16 >= rank) break;
+        uint32_t b[4][4];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          uint32_t b[4];
-          load_matrices_t(b, w_at[i / 2] + ws + s * 2048);
+        for (int i = 0; i < 4; ++i) load_matrices_t(b[i], w_at[i] + ws + s * 2048);
 #pragma unroll
-          for (int k = 0; k < kTerms; ++k) {
-            multiply<KIND>(acc[i], a[k][s], b[0], b[1]);
-            multiply<KIND>(acc[i + 1], a[k][s], b[2], b[3]);
+        for (int k = 0; k < kTerms; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            multiply<KIND>(acc[2 * i], a[k][s], b[i][0], b[i][1]);
+            multiply<KIND>(acc[2 * i + 1], a[k][s], b[i][2], b[i][3]);
           }
-        }
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -531,9 +532,11 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
 }
 
 // ---------------------------------------------------------------- outer
-// A block takes one adapter and COLS columns, and of the adapter's rows every split-th
-// chunk of 64; the cluster's blocks join through distributed shared memory, in order.  The
-// products are (rank x 64 tokens) (64 tokens x columns), both read across their rows.
+// dA and dB together: a block takes one segment of an adapter's rows (`segment` of them, so
+// that blocks are alike however the tokens are shared out) and COLS columns of x or dy.
+// An adapter of one segment is finished there; the segments' sums of the others meet in a
+// second launch, in order.  The products are (rank x 64 tokens) (64 tokens x columns),
+// both read across their rows.
 template <int R>
 struct Outer {
   static constexpr int kCols = R == 128 ? 128 : 256, kTokens = 64, kStages = R <= 32 ? 2 : 3;
@@ -542,57 +545,122 @@ struct Outer {
   static constexpr int kTermPitch = 2 * R + 16;         // bytes of a token's ranks: eight rows in different banks
   static constexpr int kTermBytes = kTokens * kTermPitch;
   static constexpr int smem(int terms) { return kStages * kStageBytes + terms * kTermBytes + 128; }
-  static_assert(R * kCols * 4 <= kStages * kStageBytes, "the partial sums reuse the stages");
+  static_assert(R * kCols * 4 <= kStages * kStageBytes, "the sums reuse the stages");
 };
 
-struct OuterParams {
-  AdapterMap map;
+// One of the two gradients: sum over an adapter's tokens of g[t]^T X[t], times f_i.
+struct OuterSide {
   const float* g;
   const void* x;
   const float* scales;
   void* out;
-  int64_t ldx, blocks;            // blocks of columns
-  int width, rank, split, out_kind;
+  float* part;                    // (slots, rank, width) sums of segments
+  int64_t ldx;
+  int width, blocks;              // blocks of columns; 0: not wanted
 };
+struct OuterParams {
+  AdapterMap map;
+  const int32_t* rows_used;       // where the last adapter's rows end
+  OuterSide side[2];
+  int rank, segment, slots, out_kind;
+};
+
+// Where an adapter's segments are.
+struct Segment {
+  int adapter;                    // -1: there is no such segment
+  int index, count;               // of the adapter's segments
+  int slot;                       // of the first one's sums, if there are several
+};
+__device__ __forceinline__ int64_t adapter_end(const OuterParams& p, int i) {
+  int64_t end = p.map.offsets[i];
+  if (i + 1 == p.map.adapters) end = min(end, static_cast<int64_t>(*p.rows_used));
+  return max(int64_t(0), min(end, p.map.m_pad));
+}
+__device__ __forceinline__ int64_t adapter_begin(const OuterParams& p, int i) {
+  return i > 0 ? max(int64_t(0), min(static_cast<int64_t>(p.map.offsets[i - 1]), p.map.m_pad)) : 0;
+}
+// The segment with this number (wanted >= 0), or those of an adapter (index 0).  All
+// threads call it: four adapters each, their counts summed over the block.
+__device__ __forceinline__ Segment find_segment(const OuterParams& p, int64_t wanted, int of_adapter) {
+  __shared__ int sums[2][kWarps];
+  __shared__ Segment found;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int count[4], all = 0, slots = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = 4 * threadIdx.x + k;
+    count[k] = 0;
+    if (i < p.map.adapters) {
+      const int64_t rows = adapter_end(p, i) - adapter_begin(p, i);
+      count[k] = rows > 0 ? static_cast<int>((rows + p.segment - 1) / p.segment) : 0;
+    }
+    all += count[k];
+    slots += count[k] > 1 ? count[k] : 0;
+  }
+  int before = all, slot = slots;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xFFFFFFFFu, before, o), y = __shfl_up_sync(0xFFFFFFFFu, slot, o);
+    if (lane >= o) { before += x; slot += y; }
+  }
+  if (lane == 31) { sums[0][warp] = before; sums[1][warp] = slot; }
+  if (threadIdx.x == 0) found.adapter = -1;
+  __syncthreads();
+  before -= all;
+  slot -= slots;
+  for (int w = 0; w < warp; ++w) { before += sums[0][w]; slot += sums[1][w]; }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = 4 * threadIdx.x + k;
+    if (i < p.map.adapters && (wanted >= 0 ? wanted >= before && wanted < before + count[k] : i == of_adapter))
+      found = {i, wanted >= 0 ? static_cast<int>(wanted - before) : 0, count[k], slot};
+    before += count[k];
+    slot += count[k] > 1 ? count[k] : 0;
+  }
+  __syncthreads();
+  return found;
+}
 
 template <int KIND, int R, int TERMS, bool FULL>
 __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const __grid_constant__ OuterParams p) {
   using O = Outer<R>;
   constexpr int kTiles = O::kCols / 8 / kWarps;         // of 8 columns, a warp
-  const int rank = FULL ? R : p.rank;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int32_t token[O::kStages + 1][O::kTokens];
-  __shared__ uint32_t has[O::kStages + 1][O::kTokens / 32];
   __shared__ float most_of[kWarps];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const int rank = FULL ? R : p.rank;
   const uint32_t base = smem_u32(smem);
   const uint32_t terms = base + O::kStages * O::kStageBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t unit_index = blockIdx.x / p.split;
-  const int part = static_cast<int>(blockIdx.x - unit_index * p.split);
-  const int adapter = static_cast<int>(unit_index / p.blocks);
-  const int64_t col0 = (unit_index - adapter * p.blocks) * O::kCols;
+  const int per_segment = p.side[0].blocks + p.side[1].blocks;
+  const int64_t number = blockIdx.x / per_segment;
+  int block = static_cast<int>(blockIdx.x - number * per_segment);
+  const bool second = block >= p.side[0].blocks;
+  const OuterSide& side = p.side[second ? 1 : 0];
+  if (second) block -= p.side[0].blocks;
+  const int64_t col0 = static_cast<int64_t>(block) * O::kCols;
   let_next_kernel_start();
   wait_for_previous_kernel();
-  const int64_t row0 = adapter > 0 ? max(0, p.map.offsets[adapter - 1]) : 0;
-  const int64_t row1 = min(p.map.m_pad, static_cast<int64_t>(p.map.offsets[adapter]));
-  // chunks of this block; rows past the adapter's last token are padding, at the end
-  const int64_t all = row1 > row0 ? (row1 - row0 + O::kTokens - 1) / O::kTokens : 0;
-  const int chunks = static_cast<int>(all > part ? (all - part + p.split - 1) / p.split : 0);
-  auto chunk_row = [&](int c) { return row0 + (static_cast<int64_t>(c) * p.split + part) * O::kTokens; };
+  const Segment seg = find_segment(p, number, 0);
+  // more sums than there is room for come of no map that the sort writes
+  if (seg.adapter < 0 || (seg.count > 1 && seg.slot + seg.index >= p.slots)) return;
+  const int64_t row0 = adapter_begin(p, seg.adapter) + static_cast<int64_t>(seg.index) * p.segment;
+  const int64_t row1 = min(row0 + p.segment, adapter_end(p, seg.adapter));
+  const int chunks = static_cast<int>((row1 - row0 + O::kTokens - 1) / O::kTokens);
   auto token_of = [&](int c, int i) {
-    const int64_t r = chunk_row(c) + i;
-    return c < chunks && r < row1 ? token_at(p.map, r) : -1;
+    const int64_t r = row0 + static_cast<int64_t>(c) * O::kTokens + i;
+    return r < row1 ? token_at(p.map, r) : -1;
   };
+
   float unit = 1.0f;
   if (KIND == OK_F16) {
     // this block's own power of two: its sums are scaled back before they are joined
     float most = 0.0f;
-    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(chunks) * O::kTokens; i += kThreads) {
-      const int32_t t = token_of(static_cast<int>(i / O::kTokens), static_cast<int>(i % O::kTokens));
+    for (int64_t r = row0 + threadIdx.x; r < row1; r += kThreads) {
+      const int32_t t = token_at(p.map, r);
       if (t < 0) continue;
       for (int k = 0; k < rank; k += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p.g + static_cast<int64_t>(t) * rank + k);
+        const float4 v = *reinterpret_cast<const float4*>(side.g + static_cast<int64_t>(t) * rank + k);
         most = fmaxf(fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
       }
     }
@@ -604,15 +672,18 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
     unit = unit_of(most);
   }
 
-  // a thread copies one piece of every kStep-th token's columns, and one of every G-step-th
+  // a thread copies one piece of every kStep-th token's columns, and one of every kGStep-th
   // token's ranks
   constexpr int kPieces = O::kCols / 8, kStep = kThreads / kPieces, kQuads = R / 4, kGStep = kThreads / kQuads;
+  static_assert(kStep % 8 == 0 && kGStep <= O::kTokens, "a thread's rows have one swizzle");
   const int piece = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
   const int quad = threadIdx.x % kQuads, g0 = threadIdx.x / kQuads;
-  const bool in_cols = col0 + piece * 8 < p.width;
-  const uint16_t* xp = static_cast<const uint16_t*>(p.x) + (in_cols ? col0 + piece * 8 : 0);
+  const bool in_cols = col0 + piece * 8 < side.width;
+  const int64_t ldx = side.ldx;
+  const uint16_t* xp = static_cast<const uint16_t*>(side.x) + (in_cols ? col0 + piece * 8 : 0);
+  const float* gp = side.g + quad * 4;
   const uint32_t x_to = base + (piece >> 3) * (O::kTokens * 128) + swizzled(r0, piece & 7);
-  static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
+  const uint32_t g_to = base + O::kXBytes + (g0 * R + quad * 4) * 4;
   auto load = [&](int c) {
     if (c < chunks) {
       const int32_t* tok = token[c % (O::kStages + 1)];
@@ -620,14 +691,13 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
 #pragma unroll
       for (int i = 0; i < O::kTokens / kStep; ++i) {
         const int32_t t = tok[r0 + i * kStep];
-        copy16(x_to + stage + i * kStep * 128, xp + (t >= 0 ? t * p.ldx : 0), t >= 0 && in_cols ? 16 : 0);
+        copy16(x_to + stage + i * kStep * 128, xp + (t >= 0 ? t * ldx : 0), t >= 0 && in_cols ? 16 : 0);
       }
       if (FULL || quad * 4 < rank) {
 #pragma unroll
         for (int i = 0; i < O::kTokens / kGStep; ++i) {
-          const int r = g0 + i * kGStep;
-          const int32_t t = tok[r];
-          copy16(base + stage + O::kXBytes + (r * R + quad * 4) * 4, p.g + (t >= 0 ? static_cast<int64_t>(t) * rank + quad * 4 : 0), t >= 0 ? 16 : 0);
+          const int32_t t = tok[g0 + i * kGStep];
+          copy16(g_to + stage + i * kGStep * R * 4, gp + (t >= 0 ? static_cast<int64_t>(t) * rank : 0), t >= 0 ? 16 : 0);
         }
       }
     }
@@ -641,16 +711,13 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) sum[m][i][k] = 0.0f;
-  auto put_tokens = [&](int c, int32_t t) {
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, t >= 0);
-    if (threadIdx.x < O::kTokens) token[c % (O::kStages + 1)][threadIdx.x] = t;
-    if (threadIdx.x < O::kTokens && lane == 0) has[c % (O::kStages + 1)][warp] = b;
-  };
-  for (int c = 0; c < O::kStages - 1; ++c) put_tokens(c, threadIdx.x < O::kTokens ? token_of(c, threadIdx.x) : -1);
+  for (int c = 0; c < O::kStages - 1; ++c)
+    if (threadIdx.x < O::kTokens) token[c][threadIdx.x] = token_of(c, threadIdx.x);
   __syncthreads();
   for (int c = 0; c < O::kStages - 1; ++c) load(c);
-  bool done = false;
-  for (int c0 = 0; c0 < chunks && !done; c0 += kRun / O::kTokens) {
+  // a chunk's tokens are fetched two rounds before their rows are
+  int32_t next = threadIdx.x < O::kTokens ? token_of(O::kStages - 1, threadIdx.x) : -1;
+  for (int c0 = 0; c0 < chunks; c0 += kRun / O::kTokens) {
 #pragma unroll
     for (int m = 0; m < R / 16; ++m)
 #pragma unroll
@@ -659,31 +726,24 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
         for (int k = 0; k < 4; ++k) acc[m][i][k] = 0.0f;
     const int c1 = min(c0 + kRun / O::kTokens, chunks);
     for (int c = c0; c < c1; ++c) {
-      int32_t next = -1;
       const int ahead = c + O::kStages - 1;
-      if (threadIdx.x < O::kTokens) next = token_of(ahead, threadIdx.x);
       copies_wait<O::kStages - 2>();
-      put_tokens(ahead, next);
-      __syncthreads();                                   // chunk c is there, c - 1 is read, the next one's tokens are known
-      // an adapter's tokens come first: behind them there are only padding rows
-      if ((has[c % (O::kStages + 1)][0] | has[c % (O::kStages + 1)][1]) == 0) {
-        done = true;
-        break;
-      }
+      if (threadIdx.x < O::kTokens) token[ahead % (O::kStages + 1)][threadIdx.x] = next;
+      __syncthreads();                                 // chunk c is there, c - 1 is read, the next one's tokens are known
       load(ahead);
+      if (threadIdx.x < O::kTokens) next = token_of(ahead + 1, threadIdx.x);
       const uint32_t stage = base + (c % O::kStages) * O::kStageBytes;
-      // g as terms of 16 bits, ranks up to a multiple of 16
+      // g as terms of 16 bits, zeros behind the rank
 #pragma unroll
       for (int i = 0; i < O::kTokens / kGStep; ++i) {
-        const int r = g0 + i * kGStep;
         float4 v = make_float4(0, 0, 0, 0);
-        if (FULL || quad * 4 < rank) v = get_shared4f(stage + O::kXBytes + (r * R + quad * 4) * 4);
+        if (FULL || quad * 4 < rank) v = get_shared4f(g_to - base + stage + i * kGStep * R * 4);
         uint32_t lo[TERMS], hi[TERMS];
         split_terms<KIND, TERMS>(v.x * unit, v.y * unit, lo);
         split_terms<KIND, TERMS>(v.z * unit, v.w * unit, hi);
 #pragma unroll
         for (int k = 0; k < TERMS; ++k)
-          put_shared2(terms + k * O::kTermBytes + r * O::kTermPitch + quad * 8, lo[k], hi[k]);
+          put_shared2(terms + k * O::kTermBytes + (g0 + i * kGStep) * O::kTermPitch + quad * 8, lo[k], hi[k]);
       }
       __syncthreads();
 #pragma unroll
@@ -691,21 +751,23 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
         uint32_t b[kTiles / 2][4];
 #pragma unroll
         for (int i = 0; i < kTiles; i += 2) {
-          const int tile = warp * kTiles + i;              // of 8 columns; 8 of them share 128 bytes
+          const int tile = warp * kTiles + i;          // of 8 columns; 8 of them share 128 bytes
           load_matrices_t(b[i / 2], stage + (tile >> 3) * (O::kTokens * 128) + swizzled(s * 16 + (lane & 15), (tile & 7) + (lane >> 4)));
         }
+        const uint32_t as = terms + (s * 16 + (lane & 7) + ((lane >> 4) << 3)) * O::kTermPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
-        for (int m = 0; m < R / 16; ++m) {
-          if (!FULL && m * 16 >= rank) break;
+        for (int k = 0; k < TERMS; ++k) {
+          uint32_t a[R / 16][4];
 #pragma unroll
-          for (int k = 0; k < TERMS; ++k) {
-            uint32_t a[4];
-            load_matrices_t(a, terms + k * O::kTermBytes + (s * 16 + (lane & 7) + ((lane >> 4) << 3)) * O::kTermPitch +
-                                   (m * 2 + ((lane >> 3) & 1)) * 16);
+          for (int m = 0; m < R / 16; ++m)
+            if (FULL || m * 16 < rank) load_matrices_t(a[m], as + k * O::kTermBytes + m * 32);
+#pragma unroll
+          for (int m = 0; m < R / 16; ++m) {
+            if (!FULL && m * 16 >= rank) break;
 #pragma unroll
             for (int i = 0; i < kTiles; i += 2) {
-              multiply<KIND>(acc[m][i], a, b[i / 2][0], b[i / 2][1]);
-              multiply<KIND>(acc[m][i + 1], a, b[i / 2][2], b[i / 2][3]);
+              multiply<KIND>(acc[m][i], a[m], b[i / 2][0], b[i / 2][1]);
+              multiply<KIND>(acc[m][i + 1], a[m], b[i / 2][2], b[i / 2][3]);
             }
           }
         }
@@ -721,41 +783,65 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
   copies_wait<0>();
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
-  const float back = 1.0f / unit;
+  const bool alone = seg.count == 1;
+  const float f = (alone && side.scales != nullptr ? side.scales[seg.adapter] : 1.0f), back = 1.0f / unit;
 #pragma unroll
   for (int m = 0; m < R / 16; ++m) {
     if (!FULL && m * 16 >= rank) break;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       float* at = sums + (m * 16 + (lane >> 2)) * O::kCols + (warp * kTiles + i) * 8 + 2 * (lane & 3);
-      *reinterpret_cast<float2*>(at) = make_float2(sum[m][i][0] * back, sum[m][i][1] * back);
-      *reinterpret_cast<float2*>(at + 8 * O::kCols) = make_float2(sum[m][i][2] * back, sum[m][i][3] * back);
+      *reinterpret_cast<float2*>(at) = make_float2(sum[m][i][0] * back * f, sum[m][i][1] * back * f);
+      *reinterpret_cast<float2*>(at + 8 * O::kCols) = make_float2(sum[m][i][2] * back * f, sum[m][i][3] * back * f);
     }
   }
-  if (p.split > 1) cluster_sync(); else __syncthreads();
-  const float f = p.scales != nullptr ? p.scales[adapter] : 1.0f;
-  const int pieces = rank * (O::kCols / 8);            // of 8 columns
-  const int e0 = pieces * part / p.split, e1 = pieces * (part + 1) / p.split;
-  for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
-    const int r = e / (O::kCols / 8), q = e % (O::kCols / 8);
-    const int64_t col = col0 + q * 8;
-    if (col >= p.width) continue;
-    const uint32_t at = smem_u32(sums) + (r * O::kCols + q * 8) * 4;
+  __syncthreads();
+  const int64_t to = (alone ? static_cast<int64_t>(seg.adapter) : seg.slot + seg.index) * rank * side.width + col0 + piece * 8;
+  for (int r = r0; r < rank; r += kStep) {
+    if (!in_cols) break;
+    const uint32_t at = base + (r * O::kCols + piece * 8) * 4;
+    const float4 lo = get_shared4f(at), hi = get_shared4f(at + 16);
+    const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const int64_t e = to + static_cast<int64_t>(r) * side.width;
+    if (!alone) store8<OK_F32>(side.part, e, v);
+    else if (p.out_kind == OK_F32) store8<OK_F32>(side.out, e, v);
+    else if (p.out_kind == OK_F16) store8<OK_F16>(side.out, e, v);
+    else store8<OK_BF16>(side.out, e, v);
+  }
+}
+
+// The adapters of several segments (their sums in order, times f_i) and those of none
+// (zeros): blockIdx.y is the adapter, a thread has eight values of either gradient.
+__global__ void __launch_bounds__(kThreads) outer_join_kernel(const __grid_constant__ OuterParams p) {
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const Segment seg = find_segment(p, -1, blockIdx.y);
+  if (seg.count == 1) return;
+  const int64_t size0 = p.side[0].blocks > 0 ? static_cast<int64_t>(p.rank) * p.side[0].width : 0;
+  const int64_t size1 = p.side[1].blocks > 0 ? static_cast<int64_t>(p.rank) * p.side[1].width : 0;
+  for (int64_t e = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 8; e < size0 + size1;
+       e += static_cast<int64_t>(gridDim.x) * kThreads * 8) {
+    const bool second = e >= size0;
+    const OuterSide& side = p.side[second ? 1 : 0];
+    const int64_t at = second ? e - size0 : e, size = second ? size1 : size0;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int k = 0; k < p.split; ++k) {
-      const uint32_t from = mapa_shared(at, k);
-      const float4 lo = ld_shared_cluster4(from), hi = ld_shared_cluster4(from + 16);
-      v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-      v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
-    }
+#pragma unroll 4
+    for (int k = 0; k < min(seg.count, p.slots - seg.slot); ++k) {
+      float w[8];
+      load8<OK_F32>(side.part, (seg.slot + k) * size + at, w);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= f;
-    const int64_t to = (static_cast<int64_t>(adapter) * rank + r) * p.width + col;
-    if (p.out_kind == OK_F32) store8<OK_F32>(p.out, to, v);
-    else if (p.out_kind == OK_F16) store8<OK_F16>(p.out, to, v);
-    else store8<OK_BF16>(p.out, to, v);
+      for (int i = 0; i < 8; ++i) v[i] += w[i];
+    }
+    if (side.scales != nullptr && seg.count > 0) {
+      const float f = side.scales[seg.adapter];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= f;
+    }
+    const int64_t to = seg.adapter * size + at;
+    if (p.out_kind == OK_F32) store8<OK_F32>(side.out, to, v);
+    else if (p.out_kind == OK_F16) store8<OK_F16>(side.out, to, v);
+    else store8<OK_BF16>(side.out, to, v);
   }
-  if (p.split > 1) cluster_sync();                     // the sums stay until every block has read them
 }
 
 // ---------------------------------------------------------------- host
@@ -817,23 +903,45 @@ bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
   });
 }
 
+// Rows of a segment: 64 to 512 (or more, where the blocks would be more than a few rounds),
+// until two blocks an SM have work.
+int64_t outer_segment(int64_t tokens, int64_t k, int64_t n) {
+  const int64_t blocks = ceil_div(k, 256) + ceil_div(n, 256);
+  int64_t rows = 128;
+  while (ceil_div(tokens, rows) * blocks > 608) rows *= 2;
+  return rows;
+}
+// Sums of segments that can be needed at once: only adapters of several segments have any.
+int64_t outer_slots(int64_t tokens, int64_t k, int64_t n) {
+  const int64_t rows = outer_segment(tokens, k, n);
+  return tokens > rows ? 2 * ceil_div(tokens, rows) : 0;
+}
+
 bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
   return with_half(format, [&](auto kind) {
     return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
       constexpr bool E = decltype(full)::value;
-      p.blocks = ceil_div(p.width, Outer<R>::kCols);
-      // parts of an adapter's tokens: until two blocks an SM have work, of two chunks at least
+      int64_t most = 0;
+      for (OuterSide& side : p.side) {
+        side.blocks = side.out != nullptr ? static_cast<int>(ceil_div(side.width, Outer<R>::kCols)) : 0;
+        most += side.out != nullptr ? ceil_div(int64_t(p.rank) * side.width, 8 * kThreads) : 0;
+      }
+      // an adapter's rows are its tokens rounded up to 128
       const int64_t used = p.map.tokens < p.map.adapters ? p.map.tokens : p.map.adapters;
-      const int64_t chunks = ceil_div(p.map.tokens, 64 * used);
-      p.split = 1;
-      while (p.split < kMaxCluster && used * p.blocks * p.split < 304 && 4 * p.split <= chunks) p.split *= 2;
-      const int64_t grid = p.map.adapters * p.blocks * p.split;
+      const int64_t all = p.map.tokens + 128 * used < p.map.m_pad ? p.map.tokens + 128 * used : p.map.m_pad;
+      const int64_t grid = (used + all / p.segment) * (p.side[0].blocks + p.side[1].blocks);
+      if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
       auto launch = [&](auto terms) {
         constexpr int N = decltype(terms)::value;
         if (!allowed(outer_kernel<K, R, N, E>, Outer<R>::smem(N))) return BSGG_ERR_CUDA;
-        const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, Outer<R>::smem(N), s, p.split);
-        return launch_kernel(c, outer_kernel<K, R, N, E>, p);
+        const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, Outer<R>::smem(N), s);
+        const bsgg_status st = launch_kernel(c, outer_kernel<K, R, N, E>, p);
+        if (st != BSGG_OK) return st;
+        // two rounds of blocks over all adapters
+        const int64_t each = 2432 / p.map.adapters < 1 ? 1 : 2432 / p.map.adapters;
+        const LaunchConfig j(dim3(static_cast<unsigned>(most < each ? most : each), static_cast<unsigned>(p.map.adapters)), kThreads, 0, s);
+        return launch_kernel(j, outer_join_kernel, p);
       };
       if constexpr (K == OK_BF16) {
         if (p.out_kind == OK_F32) return launch(std::integral_constant<int, 3>());
@@ -881,10 +989,15 @@ bsgg_status bsgg_adapters(const bsgg_adapters_desc* d, const void* x, const void
                                    static_cast<int>(d->n), d->rank}, s);
 }
 
+uint64_t bsgg_adapters_workspace_bytes(int64_t tokens, int64_t k, int64_t n, int32_t rank) {
+  if (check_adapters(tokens, k, n, 128, 1, rank, BSGG_OUT_BF16) != BSGG_OK) return 0;
+  return uint64_t(4) * outer_slots(tokens, k, n) * rank * (k + n);
+}
+
 bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* dy, const void* x, const float* u,
                                    const void* a, const void* b, const float* scales, const int32_t* padded_offsets,
-                                   const int32_t* row_of_slot, const int32_t* slot_of_row, const void* base, float* du,
-                                   void* dx, void* da, void* db, void* stream) {
+                                   const int32_t* row_of_slot, const int32_t* slot_of_row, const int32_t* rows_used,
+                                   const void* base, float* du, void* dx, void* da, void* db, void* workspace, void* stream) {
   if (!d) return BSGG_ERR_INVALID_ARG;
   const bsgg_status st = check_adapters(d->tokens, d->k, d->n, d->m_pad, d->adapters, d->rank, d->format);
   if (st != BSGG_OK) return st;
@@ -893,9 +1006,11 @@ bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* 
     return BSGG_ERR_INVALID_ARG;
   if ((da || db) && !is_float_format(d->grad_format)) return BSGG_ERR_INVALID_ARG;
   for (const void* q : {dy, x, a, b, base, static_cast<const void*>(u), static_cast<const void*>(du),
-                        static_cast<const void*>(dx), static_cast<const void*>(da), static_cast<const void*>(db)})
+                        static_cast<const void*>(dx), static_cast<const void*>(da), static_cast<const void*>(db),
+                        static_cast<const void*>(workspace)})
     if (!aligned_to(q, 16)) return BSGG_ERR_INVALID_ARG;
-  if (!aligned_to(scales, 4) || !aligned_to(padded_offsets, 4) || !aligned_to(row_of_slot, 4) || !aligned_to(slot_of_row, 4))
+  if (!aligned_to(scales, 4) || !aligned_to(padded_offsets, 4) || !aligned_to(row_of_slot, 4) || !aligned_to(slot_of_row, 4) ||
+      !aligned_to(rows_used, 4))
     return BSGG_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->tokens == 0) {
@@ -908,13 +1023,21 @@ bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* 
   if (!dx && !da && !db) return BSGG_ERR_INVALID_ARG;
   const bool wants_du = dx || da;
   if (!dy || !padded_offsets || !slot_of_row || (wants_du && (!b || !du)) || (dx && (!a || !row_of_slot)) || (da && !x) ||
-      (db && !u))
+      (db && !u) || ((da || db) && !rows_used) || ((da || db) && !workspace && outer_slots(d->tokens, d->k, d->n) > 0))
     return BSGG_ERR_INVALID_ARG;
   const AdapterMap map = {d->tokens, d->m_pad, d->adapters, padded_offsets, row_of_slot, slot_of_row};
   bsgg_status ran = BSGG_OK;
   if (wants_du) ran = launch_shrink(d->format, {map, dy, b, scales, du, d->ld_dy, static_cast<int>(d->n), d->rank, 1}, s);
-  if (ran == BSGG_OK && db) ran = launch_outer(d->format, {map, u, dy, scales, db, d->ld_dy, 0, static_cast<int>(d->n), d->rank, 1, d->grad_format}, s);
-  if (ran == BSGG_OK && da) ran = launch_outer(d->format, {map, du, x, nullptr, da, d->ldx, 0, static_cast<int>(d->k), d->rank, 1, d->grad_format}, s);
+  if (ran == BSGG_OK && (da || db)) {
+    OuterParams p = {};
+    p.map = map; p.rows_used = rows_used; p.rank = d->rank; p.out_kind = d->grad_format;
+    p.segment = static_cast<int>(outer_segment(d->tokens, d->k, d->n));
+    p.slots = static_cast<int>(outer_slots(d->tokens, d->k, d->n));
+    float* part = static_cast<float*>(workspace);
+    p.side[0] = {u, dy, scales, db, part, d->ld_dy, static_cast<int>(d->n), 0};
+    p.side[1] = {du, x, nullptr, da, part + outer_slots(d->tokens, d->k, d->n) * d->rank * d->n, d->ldx, static_cast<int>(d->k), 0};
+    ran = launch_outer(d->format, p, s);
+  }
   if (ran == BSGG_OK && dx)
     ran = launch_expand(d->format, {map, du, a, nullptr, base, dx, nullptr, 0, base ? static_cast<int>(d->ld_base) : 0,
                                    static_cast<int>(d->ld_dx), static_cast<int>(d->k), d->rank}, s);

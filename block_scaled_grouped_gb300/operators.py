@@ -116,7 +116,8 @@ def bind(L) -> None:
     L.bsgg_rms_norm_workspace_bytes.restype, L.bsgg_rms_norm_workspace_bytes.argtypes = ctypes.c_uint64, [i64, i64]
     L.bsgg_rms_norm_backward.argtypes = [ctypes.POINTER(NormBwdDesc)] + [vp] * 9
     L.bsgg_adapters.argtypes = [ctypes.POINTER(AdaptersDesc)] + [vp] * 11
-    L.bsgg_adapters_backward.argtypes = [ctypes.POINTER(AdaptersBwdDesc)] + [vp] * 15
+    L.bsgg_adapters_workspace_bytes.restype, L.bsgg_adapters_workspace_bytes.argtypes = ctypes.c_uint64, [i64, i64, i64, i32]
+    L.bsgg_adapters_backward.argtypes = [ctypes.POINTER(AdaptersBwdDesc)] + [vp] * 17
     for name in ("bsgg_route_groups", "bsgg_route_groups_backward", "bsgg_rms_norm", "bsgg_rms_norm_backward", "bsgg_adapters",
                  "bsgg_adapters_backward",
                  "bsgg_route", "bsgg_route_backward", "bsgg_sort_tokens", "bsgg_dispatch", "bsgg_combine",
@@ -712,7 +713,8 @@ def adapters_backward(dy, x, u, a, b, tokens: TokenMap, scales=None, base=None, 
     ldx = _matrix(x, "x", T, K, t)
     ldb = _matrix(base, "base", T, K, t) if base is not None else 0
     m_pad, p_off, p_row, p_slot = _adapter_map(tokens, T, S)
-    handle = _handle(stream, dy, x, u, a, b, tokens.padded_offsets, tokens.row_of_slot, tokens.slot_of_row, scales, base, dx)
+    handle = _handle(stream, dy, x, u, a, b, tokens.padded_offsets, tokens.row_of_slot, tokens.slot_of_row, tokens.rows_used,
+                     scales, base, dx)
     empty, dev = _empty_on(stream), dy.device
     ld_dx = 0
     if not want_dx:
@@ -725,9 +727,13 @@ def adapters_backward(dy, x, u, a, b, tokens: TokenMap, scales=None, base=None, 
     da = empty((S, r, K), dtype=gt, device=dev) if want_da else None
     db = empty((S, r, N), dtype=gt, device=dev) if want_db else None
     du = empty((T, r), dtype=_F32, device=dev) if want_dx or want_da else None
+    L = lib()
+    nws = L.bsgg_adapters_workspace_bytes(T, K, N, r) // 4 if want_da or want_db else 0
+    ws = empty(nws, dtype=_F32, device=dev) if nws else None
     desc = AdaptersBwdDesc(T, K, N, m_pad, ld_dy, ldx, ldb, ld_dx, S, r, _format(dy, "dy"), _FORMATS[gt])
-    _check(lib().bsgg_adapters_backward(byref(desc), dy.data_ptr(), x.data_ptr(), _flat(u, "u", T * r, _F32), a.data_ptr(),
-                                        b.data_ptr(), _flat(scales, "scales", S, _F32), p_off, p_row, p_slot,
-                                        *(v.data_ptr() if v is not None else None for v in (base, du, dx, da, db)), handle),
+    _check(L.bsgg_adapters_backward(byref(desc), dy.data_ptr(), x.data_ptr(), _flat(u, "u", T * r, _F32), a.data_ptr(),
+                                    b.data_ptr(), _flat(scales, "scales", S, _F32), p_off, p_row, p_slot,
+                                    _flat(tokens.rows_used, "rows_used", 1, _I32),
+                                    *(v.data_ptr() if v is not None else None for v in (base, du, dx, da, db, ws)), handle),
            "bsgg_adapters_backward")
     return dx, da, db

@@ -162,7 +162,7 @@ ADAPT_BWD = dict(tokens=4, k=64, n=32, m_pad=128, ld_dy=32, ldx=64, ld_base=64, 
 
 
 def adapt_bwd(lib, ptrs=None, **over):
-    ok = dict(dy=P, x=P, u=P, a=P, b=P, scales=P, off=P, row=P, slot=P, base=Q, du=P, dx=P, da=P, db=P)
+    ok = dict(dy=P, x=P, u=P, a=P, b=P, scales=P, off=P, row=P, slot=P, used=P, base=Q, du=P, dx=P, da=P, db=P, ws=P)
     return lib.bsgg_adapters_backward(desc(ops.AdaptersBwdDesc, ADAPT_BWD, over), *{**ok, **(ptrs or {})}.values(), None)
 
 
@@ -173,11 +173,14 @@ def test_adapters_backward_refuses(lib, over):
 
 
 def test_adapters_backward_refuses_pointers(lib):
-    for name in ("dy", "x", "u", "a", "b", "off", "row", "slot", "du"):
+    for name in ("dy", "x", "u", "a", "b", "off", "row", "slot", "used", "du"):
         assert adapt_bwd(lib, {name: None}) == 1, name
-    for name in ("dy", "x", "u", "a", "b", "scales", "off", "row", "slot", "base", "du", "dx", "da", "db"):
+    for name in ("dy", "x", "u", "a", "b", "scales", "off", "row", "slot", "used", "base", "du", "dx", "da", "db", "ws"):
         assert adapt_bwd(lib, {name: ODD}) == 1, name
     assert adapt_bwd(lib, dict(dx=None, da=None, db=None)) == 1        # nothing wanted
+    big = dict(tokens=100000, k=4096, n=14336, ld_dy=14336, ldx=4096, ld_base=4096, ld_dx=4096)
+    assert lib.bsgg_adapters_workspace_bytes(100000, 4096, 14336, 16) > 0 and adapt_bwd(lib, dict(ws=None), **big) == 1
+    assert lib.bsgg_adapters_workspace_bytes(100, 4096, 14336, 16) == 0 and lib.bsgg_adapters_workspace_bytes(-1, 8, 8, 8) == 0
     assert adapt_bwd(lib, dict(base=P), ld_base=72) == 1               # in place under another pitch
     assert adapt_bwd(lib, dict(dy=None, da=None, db=None), tokens=0) == 0
 
@@ -226,7 +229,7 @@ class OnGpu:
 T, H, L, K, M, N, S, r = 4, 64, 8, 2, 128, 16, 3, 8
 BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 MAP = dict(off=(I32, S), row=(I32, T, 1), slot=(I32, M))
-map_of = lambda t: bsgg.TokenMap(t["off"], t["row"], t["slot"], None, None)  # noqa: E731
+map_of = lambda t: bsgg.TokenMap(t["off"], t["row"], t["slot"], None, t.get("used"))  # noqa: E731
 CALLS = {
     "route_groups": (lambda t: bsgg.route_groups(t["logits"], K, bias=t["bias"], ids=t["ids"], weights=t["weights"]),
                      dict(logits=(F32, T, L), bias=(F32, L), ids=(I32, T, K), weights=(F32, T, K))),
@@ -243,7 +246,7 @@ CALLS = {
     "adapters_backward": (lambda t: bsgg.adapters_backward(t["dy"], t["x"], t["u"], t["a"], t["b"], map_of(t), scales=t["s"],
                                                            base=t["base"], dx=t["dx"]),
                           dict(dy=(BF, T, N), x=(BF, T, H), u=(F32, T, r), a=(BF, S, r, H), b=(BF, S, r, N), s=(F32, S),
-                               base=(BF, T, H), dx=(BF, T, H), **MAP)),
+                               base=(BF, T, H), dx=(BF, T, H), used=(I32, 1), **MAP)),
 }
 
 
