@@ -189,73 +189,126 @@ struct NormBwdParams {
   float* part;                // (blocks, hidden) sums of dy * n, with a dweight
 };
 
+// A row's dy, h and dh in the registers of their stored form.
+template <int KIND, int YKIND, int NV>
+struct NormRow {
+  Raw8<YKIND, false> dy[NV][2];
+  Raw8<KIND, false> h[NV][2], dh[NV][2];
+  float rstd;
+  __device__ __forceinline__ void load(const NormBwdParams& p, int64_t t, int first, int step) {
+    const bool on = t < p.tokens;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = (first + i * step) * kNormValues + 8 * j;
+        const bool in = on && c < p.hidden;
+        dy[i][j].load(p.dy, t * p.ld_dy + c, in);
+        h[i][j].load(p.h, t * p.ld_h + c, in);
+        dh[i][j].load(p.dh, t * p.ld_dh + c, in && p.dh != nullptr);
+      }
+    rstd = on ? p.rstd[t] : 0.0f;
+  }
+};
+
 // With n = h rstd and g = dy w:  dx = rstd (g - n mean(g n)) + dh,  dweight = sum dy n.
 // A block (or each of its warps) walks rows, gridDim apart, its threads holding the
 // same columns of each, so that the weight's gradient stays in registers until the
-// block's rows are done; the blocks' sums meet in a second launch, in order.
+// block's rows are done; the blocks' sums meet in a second launch, in order.  The next
+// row is on its way while this one is reduced and written (AHEAD: where registers hold two).
 template <int KIND, int YKIND, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : kNormMaxThreads)
+__global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : NV <= 2 ? 256 : kNormMaxThreads, WARP ? 1 : NV <= 2 ? 2 : 1)
     rms_norm_backward_kernel(const __grid_constant__ NormBwdParams p) {
   constexpr int V = kNormValues;
+  constexpr bool kAhead = NV == 1, kKeepWeight = NV == 1;
+  // rows too wide for that keep the weight's gradient in shared memory, a thread its own values
+  constexpr bool kShared = NV == 4;
+  extern __shared__ float4 wide[];
   __shared__ float part[2][kNormMaxThreads / 32];
   __shared__ float warp_sums[WARP ? kNormWarpRows : 1][WARP ? 32 * V * NV : 1];
   let_next_kernel_start();
   wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, first = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
   const int64_t rows = WARP ? kNormWarpRows : 1, row0 = blockIdx.x * rows + (WARP ? threadIdx.x >> 5 : 0);
-  float acc[NV][V];
+  auto weight = [&](int i, int j, float (&w)[8]) {
+    const int c = (first + i * step) * V + 8 * j;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int k = 0; k < 8; ++k) w[k] = 1.0f;
+    if (p.weight != nullptr && c < p.hidden) load8_as(p.weight_kind, p.weight, c, w);
+  };
+  float acc[kShared ? 1 : NV][V], keep[kKeepWeight ? NV : 1][V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[i][k] = 0.0f;
+  for (int i = 0; i < NV; ++i) {
+    if (kShared) {
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) wide[(i * 4 + q) * blockDim.x + threadIdx.x] = make_float4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[kShared ? 0 : i][k] = 0.0f;
+    }
+    if (kKeepWeight) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) weight(i, j, reinterpret_cast<float(&)[8]>(keep[i][8 * j]));
+    }
+  }
   int turn = 0;
+  NormRow<KIND, YKIND, NV> row, next;
+  if (kAhead) row.load(p, row0, first, step);
   for (int64_t t = row0; t < p.tokens; t += gridDim.x * rows, turn ^= 1) {
-    Raw8<YKIND, false> dy[NV][V / 8];
-    Raw8<KIND, false> h[NV][V / 8], dh[NV][V / 8];
+    if (!kAhead) row.load(p, t, first, step);
+    const float2 rstd = make_float2(row.rstd, row.rstd);
+    float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < V / 8; ++j) {
-        const int c = (first + i * step) * V + 8 * j;
-        dy[i][j].load(p.dy, t * p.ld_dy + c, c < p.hidden);
-        h[i][j].load(p.h, t * p.ld_h + c, c < p.hidden);
-        dh[i][j].load(p.dh, t * p.ld_dh + c, p.dh != nullptr && c < p.hidden);
-      }
-    const float rstd = p.rstd[t];
-    float sum = 0.0f;
+      for (int j = 0; j < 2; ++j) {
+        float g[8], n[8], w[8];
+        row.dy[i][j].values(g);
+        row.h[i][j].values(n);
+        if (!kKeepWeight) weight(i, j, w);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < V / 8; ++j) {
-        const int c = (first + i * step) * V + 8 * j;
-        float g[8], n[8], w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-        dy[i][j].values(g);
-        h[i][j].values(n);
-        if (p.weight != nullptr && c < p.hidden) load8_as(p.weight_kind, p.weight, c, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float q = g[k] * (n[k] * rstd);
-          acc[i][8 * j + k] += q;
-          sum = fmaf(q, w[k], sum);
+        for (int k = 0; k < 8; k += 2) {
+          const float* ww = kKeepWeight ? &keep[kKeepWeight ? i : 0][8 * j + k] : &w[k];
+          const float2 q = __fmul2_rn(make_float2(g[k], g[k + 1]), __fmul2_rn(make_float2(n[k], n[k + 1]), rstd));
+          if (kShared) {
+            float2* at = reinterpret_cast<float2*>(&wide[(i * 4 + 2 * j + k / 4) * blockDim.x + threadIdx.x]) + (k & 2) / 2;
+            *at = __fadd2_rn(*at, q);
+          } else {
+            float* at = &acc[kShared ? 0 : i][8 * j + k];
+            const float2 a = __fadd2_rn(make_float2(at[0], at[1]), q);
+            at[0] = a.x;
+            at[1] = a.y;
+          }
+          sum = __ffma2_rn(q, make_float2(ww[0], ww[1]), sum);
         }
       }
+    if (kAhead) next.load(p, t + gridDim.x * rows, first, step);
     // two buffers: the next row's sums are written while this row's may still be read
-    const float mean = row_sum<WARP>(sum, part[turn]) * p.inv_hidden;
+    const float mean = row_sum<WARP>(sum.x + sum.y, part[turn]) * p.inv_hidden;
+    const float2 minus = make_float2(-mean, -mean);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < V / 8; ++j) {
+      for (int j = 0; j < 2; ++j) {
         const int c = (first + i * step) * V + 8 * j;
         if (c >= p.hidden) continue;
-        float g[8], n[8], d[8], w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-        dy[i][j].values(g);
-        h[i][j].values(n);
-        dh[i][j].values(d);
-        if (p.weight != nullptr) load8_as(p.weight_kind, p.weight, c, w);
+        float g[8], n[8], d[8], w[8];
+        row.dy[i][j].values(g);
+        row.h[i][j].values(n);
+        row.dh[i][j].values(d);
+        if (!kKeepWeight) weight(i, j, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] += rstd * (g[k] * w[k] - n[k] * rstd * mean);
+        for (int k = 0; k < 8; k += 2) {
+          const float* ww = kKeepWeight ? &keep[kKeepWeight ? i : 0][8 * j + k] : &w[k];
+          const float2 m = __fmul2_rn(make_float2(n[k], n[k + 1]), rstd);
+          const float2 u = __ffma2_rn(m, minus, __fmul2_rn(make_float2(g[k], g[k + 1]), make_float2(ww[0], ww[1])));
+          const float2 v = __ffma2_rn(u, rstd, make_float2(d[k], d[k + 1]));
+          d[k] = v.x;
+          d[k + 1] = v.y;
+        }
         store8<KIND>(p.dx, t * p.ld_dx + c, d);
       }
+    if (kAhead) row = next;
   }
   if (p.part == nullptr) return;
   float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.hidden;
@@ -263,7 +316,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : kNormMaxThreads)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k) warp_sums[threadIdx.x >> 5][(lane + 32 * i) * V + k] = acc[i][k];
+      for (int k = 0; k < V; ++k) warp_sums[threadIdx.x >> 5][(lane + 32 * i) * V + k] = acc[kShared ? 0 : i][k];
     __syncthreads();
     for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) {
       float s = 0.0f;
@@ -277,14 +330,20 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : kNormMaxThreads)
 #pragma unroll
       for (int j = 0; j < V; j += 8) {
         const int c = (first + i * step) * V + j;
-        if (c < p.hidden) store8<OK_F32>(out, c, reinterpret_cast<float(&)[8]>(acc[i][j]));
+        if (c >= p.hidden) continue;
+        if (kShared) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) reinterpret_cast<float4*>(out + c)[q] = wide[(i * 4 + j / 4 + q) * blockDim.x + threadIdx.x];
+        } else {
+          store8<OK_F32>(out, c, reinterpret_cast<float(&)[8]>(acc[kShared ? 0 : i][j]));
+        }
       }
   }
 }
 
-// dweight[c] = the sum of the blocks' parts: 32 columns a block, eight warps that take
-// every eighth part, joined in order.
-constexpr int kNormJoinWarps = 8;
+// dweight[c] = the sum of the blocks' parts: 32 columns a block, 32 warps that take
+// every 32nd part, joined in order.
+constexpr int kNormJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kNormJoinWarps) norm_join_kernel(const float* part, int64_t parts, int hidden, float* dweight) {
   __shared__ float sums[kNormJoinWarps][32];
   let_next_kernel_start();
@@ -307,7 +366,8 @@ __global__ void __launch_bounds__(32 * kNormJoinWarps) norm_join_kernel(const fl
 
 // ---------------------------------------------------------------- host
 constexpr int64_t kNormMaxHidden = 32768;
-constexpr int64_t kNormBwdBlocks = 304;       // two on each of the 152 SMs
+// Blocks of the gradient: two on each of the 152 SMs, of rows that are a warp's eight.
+constexpr int64_t kNormBwdBlocks = 304, kNormBwdWarpBlocks = 1216;
 
 // How rows of `cols` columns lie: a warp each with one or two runs of 16 a lane, or a
 // block each with the fewest runs that 256 threads (512 at the most) hold.
@@ -355,8 +415,9 @@ bsgg_status with_quantized(int fmt, F&& f) {
 }
 
 int64_t norm_bwd_blocks(int64_t tokens, int64_t hidden) {
-  const int64_t rows = row_shape(hidden).warp ? ceil_div(tokens, kNormWarpRows) : tokens;
-  return rows < kNormBwdBlocks ? rows : kNormBwdBlocks;
+  const bool warp = row_shape(hidden).warp;
+  const int64_t rows = warp ? ceil_div(tokens, kNormWarpRows) : tokens, most = warp ? kNormBwdWarpBlocks : kNormBwdBlocks;
+  return rows < most ? rows : most;
 }
 
 }  // namespace
@@ -439,12 +500,17 @@ bsgg_status bsgg_rms_norm_backward(const bsgg_norm_bwd_desc* d, const void* dy, 
   p.part = dweight ? static_cast<float*>(workspace) : nullptr;
   const RowShape shape = row_shape(d->hidden);
   const int64_t blocks = norm_bwd_blocks(d->tokens, d->hidden);
-  const LaunchConfig c(dim3(static_cast<unsigned>(blocks)), shape.threads, 0, s);
   const bsgg_status ran = with_float(tf, [&](auto kind) {
     return with_float(d->y_format, [&](auto ykind) {
       return with_shape(shape, [&](auto nv, auto warp) {
         constexpr int K = decltype(kind)::value, Y = decltype(ykind)::value, N = decltype(nv)::value;
-        return launch_kernel(c, rms_norm_backward_kernel<K, Y, N, decltype(warp)::value>, p);
+        constexpr auto kernel = rms_norm_backward_kernel<K, Y, N, decltype(warp)::value>;
+        const size_t smem = N == 4 ? sizeof(float) * kNormValues * N * shape.threads : 0;       // 128 KB at the most
+        if (smem > 0 &&
+            !succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))))
+          return BSGG_ERR_CUDA;
+        const LaunchConfig c(dim3(static_cast<unsigned>(blocks)), shape.threads, smem, s);
+        return launch_kernel(c, kernel, p);
       });
     });
   });
