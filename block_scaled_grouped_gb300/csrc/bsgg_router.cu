@@ -28,6 +28,10 @@ __device__ __forceinline__ float sigmoid32(float l) {
   const float e = expf(-fabsf(l));
   return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
 }
+// The same for the choice, with the hardware's exponential and quotient: off by 2^-21 at most
+// (e^-l by (2 + 1.2 |l|) 2^-23 of itself, which moves the score by its slope, the quotient by
+// 2^-22), and by 2^-15 of itself down to l = -88, below which it is 0.
+__device__ __forceinline__ float sigmoid_choice(float l) { return __fdividef(1.0f, 1.0f + __expf(-l)); }
 __device__ __forceinline__ double sigmoid64(double l) {
   const double e = exp(-fabs(l));
   return (l >= 0.0 ? 1.0 : e) / (1.0 + e);
@@ -92,13 +96,19 @@ __device__ __forceinline__ void top_two(T& a, T& b, T x, T y) {
   b = b < low ? low : b;
 }
 
-// A group's score in 64 bits, as a key, the same in all of its lanes; called by all
-// lanes of the warp.
-__device__ __noinline__ uint64_t group64(const RouterParams& p, Row r) {
+// A group's score in 64 bits, as a key, the same in all of its lanes, from those of this
+// lane's experts that are in `open` (bits: the ones that may be among its best two); called
+// by all lanes of the warp.
+__device__ __noinline__ uint64_t group64(const RouterParams& p, Row r, uint64_t open) {
   const double sum = row_sum64(p, r);
   uint64_t a = 0, b = 0;
 #pragma unroll 1
-  for (int i = 0; i < r.own; ++i) top_two(a, b, row_choice64(p, r, sum, i), uint64_t(0));
+  while (open != 0) {
+    const int i = __ffsll(static_cast<long long>(open)) - 1;
+    open &= open - 1;
+    top_two(a, b, row_choice64(p, r, sum, i), uint64_t(0));
+  }
+  __syncwarp();
   for (int o = 1; o < p.per; o <<= 1) {
     const uint64_t x = __shfl_xor_sync(kAll, a, o), y = __shfl_xor_sync(kAll, b, o);
     top_two(a, b, x, y);
@@ -130,12 +140,42 @@ __device__ __forceinline__ void load_logits(const RouterParams& p, const Row& r,
   for (int i = 0; i < NI; ++i) l[i] = i < r.own ? load1<KIND>(p.logits, r.at + r.first + p.per * i) : -INFINITY;
 }
 
-// One warp per token.  The order of the experts is that of 32-bit keys (logits
-// themselves without a bias, where it is exact); with a bias, and for sums of two,
-// the best of a round is certain only where it leads by more than what the 32-bit
-// scores may be off, and the others that near are compared in 64 bits, which
-// happens in one round of some thousands.  Each round is a warp's maximum and, where it
-// was certain, the lowest index that has it.
+// The experts left with a key of at least `least`, as bits of this lane's.
+template <int NI>
+__device__ __forceinline__ uint64_t keys_from(const uint32_t (&key)[NI], uint32_t least) {
+  uint64_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+    if (key[i] >= least && key[i] > kMaskedKey) bits |= 1ull << i;
+  return bits;
+}
+// The best expert left: its key, and its index (the lowest of equals).
+template <int NI>
+__device__ __forceinline__ uint32_t best_left(const uint32_t (&key)[NI], const Row& row, int per, uint32_t& e) {
+  uint32_t m = key[0];
+  int at = 0;
+#pragma unroll
+  for (int i = 1; i < NI; ++i)
+    if (key[i] > m) { m = key[i]; at = i; }
+  const uint32_t best = __reduce_max_sync(kAll, m);
+  e = __reduce_min_sync(kAll, m == best ? static_cast<uint32_t>(row.first + per * at) : kAll);
+  return best;
+}
+template <int NI>
+__device__ __forceinline__ void set_key(uint32_t (&key)[NI], const Row& row, int per, uint32_t e, uint32_t to) {
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+    if (e == static_cast<uint32_t>(row.first + per * i) && i < row.own) key[i] = to;
+}
+
+// One warp per token.  Its experts go by 32-bit keys (logits themselves without a bias,
+// where they are exact): each round takes a warp's maximum and the lowest index that has
+// it.  With a bias a choice is certain only where it leads the next one by more than
+// what 32-bit scores may be off; that is looked at once for all rounds, a lane per choice,
+// one round more than there are choices.  Where it fails, in some hundredths of a per
+// cent of the rows, the rounds are gone through again, and those of each round that are
+// that near are compared in 64 bits.  Equal logits under equal biases are equal, and
+// need none of it.  Groups likewise, but there only the last one kept has to lead.
 template <int NI>
 __global__ void __launch_bounds__(32 * kRouterWarps) route_groups_kernel(const __grid_constant__ RouterParams p) {
   let_next_kernel_start();
@@ -166,15 +206,13 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_groups_kernel(const _
     }
   }
   if (biased) {
-    // a sigmoid is off by 2^-22 at most (the exponential's two units and two roundings; twice
-    // that is taken), a softmax's score, 1 / total at most, by 2^-17 of that (64 + 5 roundings
-    // of the sum)
+    // a softmax's score, 1 / total at most, is off by 2^-17 of that (64 + 5 roundings of the sum)
     const float inv = p.sigmoid ? 0.0f : 1.0f / total;
     off = p.sigmoid ? 0x1p-21f : 0x1p-17f * fminf(inv, 1.0f);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       float c = -INFINITY;
-      if (!(l[i] == -INFINITY)) c = (p.sigmoid ? sigmoid32(l[i]) : expf(l[i] - row.m) * inv) + p.bias[row.first + p.per * i];
+      if (!(l[i] == -INFINITY)) c = (p.sigmoid ? sigmoid_choice(l[i]) : expf(l[i] - row.m) * inv) + p.bias[row.first + p.per * i];
       key[i] = logit_key(c);
     }
   } else {
@@ -198,7 +236,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_groups_kernel(const _
     } else {
       auto value = [&](uint32_t k) {
         const float v = key_logit(k);
-        return biased ? v : p.sigmoid ? sigmoid32(v) : expf(v - row.m);
+        return biased ? v : p.sigmoid ? sigmoid_choice(v) : expf(v - row.m);
       };
       size = fabsf(key_logit(a));
       if (p.group_top == 2) {
@@ -207,32 +245,44 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_groups_kernel(const _
         size = fabsf(x) + fabsf(y);
       }
     }
-    // logits are exact; everything else is not
-    const bool exact = !biased && p.group_top == 1;
+    const uint32_t g0 = g;
     bool kept = false;
+    uint32_t last = 0;                             // the last group kept
+    int who = 0;
     for (int j = 0; j < p.topk_groups; ++j) {
       const uint32_t best = __reduce_max_sync(kAll, g);
-      if (best == 0) break;
-      bool take = g == best;
-      if (!exact) {
-        const int who = __ffs(__ballot_sync(kAll, take)) - 1;
-        const float v = key_logit(best), sizes = size + __shfl_sync(kAll, size, who);
-        // with a bias two scores of `off` each and roundings; without one each is positive
-        // and off by 2^-17 of itself at most (l - m, down to -100, is rounded)
-        const float slack = biased ? 4.0f * off + 0x1p-22f * sizes : 0x1p-16f * sizes + 0x1p-120f;
-        const bool near = g != 0 && (g == best || key_logit(g) >= v - slack);
-        // groups with the same two logits are equal: common where logits have few bits
-        const uint32_t best_a = __shfl_sync(kAll, a, who), best_b = __shfl_sync(kAll, b, who);
-        const bool same = !biased && a == best_a && b == best_b;
-        const bool open = biased ? __popc(__ballot_sync(kAll, near)) > p.per : __any_sync(kAll, near && !same);
-        if (open) {
-          uint64_t k = group64(p, row);
-          if (!near) k = 0;
-          take = k == warp_max64(k);
+      if (best == 0) { last = 0; break; }
+      last = best;
+      who = __ffs(__ballot_sync(kAll, g == best)) - 1;             // the lowest of equals
+      if (group == who / p.per) { kept = true; g = 0; }
+    }
+    const uint32_t rest = __reduce_max_sync(kAll, g);
+    if ((biased || p.group_top == 2) && last != 0 && rest != 0) {
+      // with a bias two scores of `off` each and roundings; without one each is positive and
+      // off by 2^-15 of itself at most
+      const float most = warp_max(size);
+      const float slack = biased ? 4.0f * off + 0x1p-20f * most : 0x1p-13f * most + 0x1p-120f;
+      const uint32_t last_a = __shfl_sync(kAll, a, who), last_b = __shfl_sync(kAll, b, who);
+      const bool near = g0 != 0 && (g0 == last || fabsf(key_logit(g0) - key_logit(last)) <= slack);
+      // groups with the same two logits are equal, and in order of index: common where logits
+      // have few bits
+      const bool same = !biased && a == last_a && b == last_b;
+      const bool left_out = __any_sync(kAll, near && g != 0), unlike = __any_sync(kAll, near && !same);
+      if (left_out && unlike) {
+        // all of the groups in 64 bits, from the experts that may be their best two
+        const float least = b > kMaskedKey ? key_logit(b) : -INFINITY;
+        const float under = least - (2.0f * off + 0x1p-21f * fabsf(least));
+        const uint64_t open = keys_from(key, biased && b != kAll ? logit_key(under) : biased ? 0u : p.group_top == 2 ? b : a);
+        uint64_t k = group64(p, row, g0 != 0 ? open : 0);
+        if (g0 == 0) k = 0;
+        kept = false;
+        for (int j = 0; j < p.topk_groups; ++j) {
+          const uint64_t best = warp_max64(k);
+          if (best == 0) break;
+          const int winner = (__ffs(__ballot_sync(kAll, k == best)) - 1) / p.per;
+          if (group == winner) { kept = true; k = 0; }
         }
       }
-      const int winner = (__ffs(__ballot_sync(kAll, take)) - 1) / p.per;     // the lowest of equals
-      if (group == winner) { kept = true; g = 0; }
     }
     if (!kept) {
 #pragma unroll
@@ -240,36 +290,58 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_groups_kernel(const _
     }
   }
 
-  // ---- experts
+  // ---- experts: lane j has choice j, its key and (with a bias) its logit and bias
   int32_t my_id = -1;
+  uint32_t my_key = 0;
   for (int j = 0; j < p.topk; ++j) {
-    uint32_t m = key[0];
-    int at = 0;
-#pragma unroll
-    for (int i = 1; i < NI; ++i)
-      if (key[i] > m) { m = key[i]; at = i; }
-    const uint32_t best = __reduce_max_sync(kAll, m);
+    uint32_t e;
+    const uint32_t best = best_left(key, row, p.per, e);
     if (best <= kMaskedKey) break;                 // only masked experts are left
-    uint32_t mine = m == best ? static_cast<uint32_t>(row.first + p.per * at) : kAll;
-    if (biased) {
-      const float v = key_logit(best);
-      const uint32_t least = best == kAll ? kAll : logit_key(v - (2.0f * off + 0x1p-22f * fabsf(v)));
-      uint64_t near = 0;
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (key[i] >= least && key[i] > kMaskedKey) near |= 1ull << i;
-      const uint32_t some = __ballot_sync(kAll, near != 0);
-      if (__popc(some) > 1 || __any_sync(kAll, (near & (near - 1)) != 0)) mine = expert64(p, row, near);
+    set_key(key, row, p.per, e, 0u);
+    if (lane == j) { my_id = static_cast<int32_t>(e); my_key = best; }
+  }
+  float mine = my_id >= 0 ? load1(p.kind, p.logits, row.at + my_id) : -INFINITY;
+  if (biased) {
+    uint32_t rest_id;
+    const uint32_t rest = best_left(key, row, p.per, rest_id);
+    const float my_bias = my_id >= 0 ? p.bias[my_id] : 0.0f;
+    uint32_t next = __shfl_down_sync(kAll, my_key, 1);
+    float next_logit = __shfl_down_sync(kAll, mine, 1), next_bias = __shfl_down_sync(kAll, my_bias, 1);
+    if (lane == p.topk - 1) {
+      next = rest;
+      if (rest > kMaskedKey) {
+        next_logit = load1(p.kind, p.logits, row.at + rest_id);
+        next_bias = p.bias[rest_id];
+      }
     }
-    const uint32_t e = __reduce_min_sync(kAll, mine);
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if (e == static_cast<uint32_t>(row.first + p.per * i) && i < row.own) key[i] = 0u;
-    if (lane == j) my_id = static_cast<int32_t>(e);
+    const float v = key_logit(my_key);
+    const bool tie = my_key == next && mine == next_logit && my_bias == next_bias;     // in order of index already
+    const bool open = lane < p.topk && my_id >= 0 && next > kMaskedKey && !tie &&
+                      !(key_logit(next) < v - (2.0f * off + 0x1p-22f * fabsf(v))) && v < INFINITY;
+    // equal infinities, and NaN, are in order of index
+    if (__any_sync(kAll, open && v == v)) {
+      for (int j = 0; j < p.topk; ++j) {
+        const uint32_t e = static_cast<uint32_t>(__shfl_sync(kAll, my_id, j)), k = __shfl_sync(kAll, my_key, j);
+        set_key(key, row, p.per, e, k);
+      }
+      my_id = -1;
+      for (int j = 0; j < p.topk; ++j) {
+        uint32_t e;
+        const uint32_t best = best_left(key, row, p.per, e);
+        if (best <= kMaskedKey) break;
+        const float lead = key_logit(best);
+        const uint64_t near = keys_from(key, best == kAll ? kAll : logit_key(lead - (2.0f * off + 0x1p-22f * fabsf(lead))));
+        const uint32_t some = __ballot_sync(kAll, near != 0);
+        const bool several = __any_sync(kAll, (near & (near - 1)) != 0);
+        if (__popc(some) > 1 || several) e = __reduce_min_sync(kAll, expert64(p, row, near));
+        set_key(key, row, p.per, e, 0u);
+        if (lane == j) my_id = static_cast<int32_t>(e);
+      }
+      mine = my_id >= 0 ? load1(p.kind, p.logits, row.at + my_id) : -INFINITY;
+    }
   }
 
   // ---- weights, lane j's for choice j
-  const float mine = my_id >= 0 ? load1(p.kind, p.logits, row.at + my_id) : -INFINITY;
   float w = 0.0f;
   if (!p.normalize) {
     if (my_id >= 0) w = p.scale * (p.sigmoid ? sigmoid32(mine) : expf(mine - row.m) / total);
