@@ -10,6 +10,8 @@
 // and the memory's rate that is 435 TFLOP/s, which mma.sync delivers, so memory bounds
 // them and the tensor cores' large tiles (128 rows of one adapter, whatever the batch
 // holds) would only be padding.
+#include <atomic>
+
 #include "bsgg_ops.cuh"
 
 namespace {
@@ -34,17 +36,11 @@ struct AdapterMap {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ uint32_t get_shared(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint4 get_shared4(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ void put_shared(uint32_t at, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
 __device__ __forceinline__ void put_shared2(uint32_t at, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
 }
@@ -63,6 +59,9 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void load_matrices_t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 // c (16 x 8) += a (16 x 16) b (16 x 8)
 template <int KIND>
@@ -439,6 +438,9 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
   uint32_t w_at[4];                                    // pieces 2 i of the products' rows of W
 #pragma unroll
   for (int i = 0; i < 4; ++i) w_at[i] = base + swizzled(lane & 15, 2 * i + (lane >> 4));
+  uint32_t y_at[4];                                    // pieces 2 i of the tile's rows: the same places
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y_at[i] = w_at[i] - base;
 #pragma unroll
   for (int i = 0; i < E::kBuffers; ++i) load(i);
 
@@ -483,19 +485,19 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
     const int c0 = (pass * across + cw) * 64;
     if (cw < across && c0 < cols) {
       const uint32_t ys = tile + (pass % E::kBuffers) * E::kTileBytes, ws = (c0 >> 6) * w_bytes;
-      // the sums start from the base
-      const uint32_t mine = ys + (lane >> 2) * 128 + 4 * (lane & 3);
-      const uint32_t turn = (lane >> 2) << 4;
+      // the sums start from the base, whose 8 x 8 matrices lie in the lanes as the sums do
       float acc[8][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 4; ++i) {
+        uint32_t v[4] = {0, 0, 0, 0};
+        if (from != nullptr) load_matrices(v, ys + y_at[i]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float2 v = make_float2(0.0f, 0.0f);
-          if (from != nullptr) v = unpack2<KIND>(get_shared(mine + ((i << 4) ^ turn) + 1024 * h));
-          acc[i][2 * h] = KIND == OK_F16 ? v.x * unit[h] : v.x;
-          acc[i][2 * h + 1] = KIND == OK_F16 ? v.y * unit[h] : v.y;
+        for (int k = 0; k < 4; ++k) {
+          const float2 f2 = unpack2<KIND>(v[k]);
+          acc[2 * i + k / 2][2 * (k & 1)] = KIND == OK_F16 ? f2.x * unit[k & 1] : f2.x;
+          acc[2 * i + k / 2][2 * (k & 1) + 1] = KIND == OK_F16 ? f2.y * unit[k & 1] : f2.y;
         }
+      }
 #pragma unroll
       for (int s = 0; s < R / 16; ++s) {
         if (!FULL && s * 16 >= rank) break;
@@ -511,11 +513,15 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
           }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 4; ++i) {
+        uint32_t v[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          put_shared(mine + ((i << 4) ^ turn) + 1024 * h,
-                     KIND == OK_F16 ? pack2<KIND>(acc[i][2 * h] * back[h], acc[i][2 * h + 1] * back[h]) : pack2<KIND>(acc[i][2 * h], acc[i][2 * h + 1]));
+        for (int k = 0; k < 4; ++k) {
+          const float* at = &acc[2 * i + k / 2][2 * (k & 1)];
+          v[k] = KIND == OK_F16 ? pack2<KIND>(at[0] * back[k & 1], at[1] * back[k & 1]) : pack2<KIND>(at[0], at[1]);
+        }
+        store_matrices(ys + y_at[i], v[0], v[1], v[2], v[3]);
+      }
       __syncwarp();
       const int c = pass * across * 64 + at_col;
 #pragma unroll
@@ -860,10 +866,18 @@ template <typename F>
 bsgg_status with_half(int format, F&& f) {
   return format == BSGG_OUT_BF16 ? f(std::integral_constant<int, OK_BF16>()) : f(std::integral_constant<int, OK_F16>());
 }
-// Shared memory beyond the default 48 KB has to be asked for.
-template <typename K>
-bool allowed(K kern, int smem) {
-  return succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+// Shared memory beyond the default 48 KB has to be asked for, once for a kernel on a device
+// (half a microsecond of the host's time at each call otherwise).
+template <auto KERNEL>
+bool allowed(int smem) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (!succeeded(cudaGetDevice(&dev))) return false;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (!succeeded(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 // Tiles of `rows` rows that can hold tokens, at the most.
@@ -881,7 +895,7 @@ bsgg_status launch_shrink(int format, ShrinkParams p, cudaStream_t s) {
     return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
       constexpr bool E = decltype(full)::value;
-      if (!allowed(shrink_kernel<K, R, E>, Shrink<R>::kSmem)) return BSGG_ERR_CUDA;
+      if (!allowed<shrink_kernel<K, R, E>>(Shrink<R>::kSmem)) return BSGG_ERR_CUDA;
       const LaunchConfig c(dim3(static_cast<unsigned>(tiles * p.split)), kThreads, Shrink<R>::kSmem, s, p.split);
       return launch_kernel(c, shrink_kernel<K, R, E>, p);
     });
@@ -895,7 +909,7 @@ bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
     return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
       constexpr bool E = decltype(full)::value;
-      if (!allowed(expand_kernel<K, R, E>, Expand<R>::kSmem)) return BSGG_ERR_CUDA;
+      if (!allowed<expand_kernel<K, R, E>>(Expand<R>::kSmem)) return BSGG_ERR_CUDA;
       const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ceil_div(p.width, Expand<R>::kCols)));
       const LaunchConfig c(grid, kThreads, Expand<R>::kSmem, s);
       return launch_kernel(c, expand_kernel<K, R, E>, p);
@@ -934,7 +948,7 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
       if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
       auto launch = [&](auto terms) {
         constexpr int N = decltype(terms)::value;
-        if (!allowed(outer_kernel<K, R, N, E>, Outer<R>::smem(N))) return BSGG_ERR_CUDA;
+        if (!allowed<outer_kernel<K, R, N, E>>(Outer<R>::smem(N))) return BSGG_ERR_CUDA;
         const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, Outer<R>::smem(N), s);
         const bsgg_status st = launch_kernel(c, outer_kernel<K, R, N, E>, p);
         if (st != BSGG_OK) return st;

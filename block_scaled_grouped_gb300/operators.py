@@ -195,6 +195,11 @@ def _empty_on(stream):
     return empty
 
 
+def _ptr(t):
+    """A tensor's address (None passes)."""
+    return None if t is None else t.data_ptr()
+
+
 def _handle(stream, t, *others):
     """The stream's handle; the tensors (None: absent) have to be on the current device."""
     dev = t.get_device()
@@ -536,14 +541,19 @@ def route_groups(logits, topk: int, score: str = "sigmoid", bias=None, groups: i
     desc = RouteGroupsDesc(T, ld, L, k, int(groups), int(topk_groups), int(group_top), _score(score), _format(logits, "logits"),
                            1 if normalize else 0, scale)
     handle = _handle(stream, logits, bias, ids, weights)
-    if ids is None or weights is None:
-        empty, dev = _empty_on(stream), logits.device
-        if ids is None:
-            ids = empty((T, max(k, 0)), dtype=_I32, device=dev)
-        if weights is None:
-            weights = empty((T, max(k, 0)), dtype=_F32, device=dev)
-    _check(lib().bsgg_route_groups(byref(desc), logits.data_ptr(), _flat(bias, "bias", L, _F32), _flat(ids, "ids", T * k, _I32),
-                                   _flat(weights, "weights", T * k, _F32), handle), "bsgg_route_groups")
+    empty, dev = _empty_on(stream), logits.device
+    # what is made here needs no look at its type and shape
+    p_ids = _flat(ids, "ids", T * k, _I32)
+    p_weights = _flat(weights, "weights", T * k, _F32)
+    if ids is None:
+        ids = empty((T, max(k, 0)), dtype=_I32, device=dev)
+        p_ids = ids.data_ptr()
+    if weights is None:
+        weights = empty((T, max(k, 0)), dtype=_F32, device=dev)
+        p_weights = weights.data_ptr()
+    code = lib().bsgg_route_groups(byref(desc), logits.data_ptr(), _flat(bias, "bias", L, _F32), p_ids, p_weights, handle)
+    if code:
+        _check(code, "bsgg_route_groups")
     return ids, weights
 
 
@@ -618,8 +628,10 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out_format: Optio
         rows = max(128, (T + 127) // 128 * 128) if m_pad is None else int(m_pad)
         a, sfa = _row_buffers(max(rows, 0), H, row_format, dev, empty)
     desc = NormDesc(T, H, rows, ldx, ldr, ldh, H, _format(x, "x"), fw, _FORMATS[dt], rf, eps)
-    _check(lib().bsgg_rms_norm(byref(desc), x.data_ptr(), residual.data_ptr() if residual is not None else None, p_w,
-                               *(v.data_ptr() if v is not None else None for v in (h, y, rstd, a, sfa)), handle), "bsgg_rms_norm")
+    code = lib().bsgg_rms_norm(byref(desc), x.data_ptr(), _ptr(residual), p_w, _ptr(h), _ptr(y), _ptr(rstd), _ptr(a), _ptr(sfa),
+                               handle)
+    if code:
+        _check(code, "bsgg_rms_norm")
     return Norm(y, h, rstd, a, sfa)
 
 
@@ -645,9 +657,10 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, want_dweight: bool = True, d
         dw = empty(H, dtype=_F32, device=dev)
         ws = empty(L.bsgg_rms_norm_workspace_bytes(T, H) // 4, dtype=_F32, device=dev)
     desc = NormBwdDesc(T, H, ld_dy, ldh, ld_dh, ld_dx, _format(h, "h"), fw, _format(dy, "dy"), 0)
-    _check(L.bsgg_rms_norm_backward(byref(desc), dy.data_ptr(), h.data_ptr(), p_w, _flat(rstd, "rstd", T, _F32),
-                                    *(v.data_ptr() if v is not None else None for v in (dh, dx, dw, ws)), handle),
-           "bsgg_rms_norm_backward")
+    code = L.bsgg_rms_norm_backward(byref(desc), dy.data_ptr(), h.data_ptr(), p_w, _flat(rstd, "rstd", T, _F32), _ptr(dh),
+                                    dx.data_ptr(), _ptr(dw), _ptr(ws), handle)
+    if code:
+        _check(code, "bsgg_rms_norm_backward")
     return dx, dw
 
 
@@ -679,10 +692,9 @@ def adapters(x, a, b, tokens: TokenMap, scales=None, base=None, out=None, stream
     (tokens, rank) for the backward.  `tokens` is sort_tokens of the tokens' adapters
     (tokens, 1), -1 for none.  y goes into a given out (base will do) or a new tensor."""
     xt = x.dtype
-    ldx = _matrix(x, "x")
-    T = x.shape[0]
     S, r, K, N = _adapter_weights(a, b, xt)
-    _matrix(x, "x", T, K)
+    ldx = _matrix(x, "x", None, K)
+    T = x.shape[0]
     ldb = _matrix(base, "base", T, N, xt) if base is not None else 0
     m_pad, p_off, p_row, p_slot = _adapter_map(tokens, T, S)
     handle = _handle(stream, x, a, b, tokens.padded_offsets, tokens.row_of_slot, tokens.slot_of_row, scales, base, out)
@@ -693,9 +705,10 @@ def adapters(x, a, b, tokens: TokenMap, scales=None, base=None, out=None, stream
         y, ldy = out, _matrix(out, "out", T, N, xt)
     u = empty((T, r), dtype=_F32, device=dev)
     desc = AdaptersDesc(T, K, N, m_pad, ldx, ldb, ldy, S, r, _format(x, "x"), 0)
-    _check(lib().bsgg_adapters(byref(desc), x.data_ptr(), a.data_ptr(), b.data_ptr(), _flat(scales, "scales", S, _F32), p_off,
-                               p_row, p_slot, base.data_ptr() if base is not None else None, u.data_ptr(), y.data_ptr(), handle),
-           "bsgg_adapters")
+    code = lib().bsgg_adapters(byref(desc), x.data_ptr(), a.data_ptr(), b.data_ptr(), _flat(scales, "scales", S, _F32), p_off,
+                               p_row, p_slot, _ptr(base), u.data_ptr(), y.data_ptr(), handle)
+    if code:
+        _check(code, "bsgg_adapters")
     return y, u
 
 
@@ -706,10 +719,9 @@ def adapters_backward(dy, x, u, a, b, tokens: TokenMap, scales=None, base=None, 
     given tensor (base will do) or a new one; da and db, dense like a and b, are in
     grad_format (by default x's type), zeros for an adapter without tokens."""
     t = dy.dtype
-    ld_dy = _matrix(dy, "dy")
-    T = dy.shape[0]
     S, r, K, N = _adapter_weights(a, b, t)
-    _matrix(dy, "dy", T, N)
+    ld_dy = _matrix(dy, "dy", None, N)
+    T = dy.shape[0]
     ldx = _matrix(x, "x", T, K, t)
     ldb = _matrix(base, "base", T, K, t) if base is not None else 0
     m_pad, p_off, p_row, p_slot = _adapter_map(tokens, T, S)
@@ -731,9 +743,10 @@ def adapters_backward(dy, x, u, a, b, tokens: TokenMap, scales=None, base=None, 
     nws = L.bsgg_adapters_workspace_bytes(T, K, N, r) // 4 if want_da or want_db else 0
     ws = empty(nws, dtype=_F32, device=dev) if nws else None
     desc = AdaptersBwdDesc(T, K, N, m_pad, ld_dy, ldx, ldb, ld_dx, S, r, _format(dy, "dy"), _FORMATS[gt])
-    _check(L.bsgg_adapters_backward(byref(desc), dy.data_ptr(), x.data_ptr(), _flat(u, "u", T * r, _F32), a.data_ptr(),
+    code = L.bsgg_adapters_backward(byref(desc), dy.data_ptr(), x.data_ptr(), _flat(u, "u", T * r, _F32), a.data_ptr(),
                                     b.data_ptr(), _flat(scales, "scales", S, _F32), p_off, p_row, p_slot,
-                                    _flat(tokens.rows_used, "rows_used", 1, _I32),
-                                    *(v.data_ptr() if v is not None else None for v in (base, du, dx, da, db, ws)), handle),
-           "bsgg_adapters_backward")
+                                    _flat(tokens.rows_used, "rows_used", 1, _I32), _ptr(base), _ptr(du), _ptr(dx), _ptr(da),
+                                    _ptr(db), _ptr(ws), handle)
+    if code:
+        _check(code, "bsgg_adapters_backward")
     return dx, da, db
