@@ -41,9 +41,6 @@ __device__ __forceinline__ uint4 get_shared4(uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ void put_shared2(uint32_t at, uint32_t x, uint32_t y) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
-}
 __device__ __forceinline__ float4 get_shared4f(uint32_t at) {
   const uint4 v = get_shared4(at);
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
@@ -143,12 +140,13 @@ __device__ __forceinline__ int row_groups(int n) { return n <= 16 ? 1 : n <= 32 
 // that: a decoding batch has a token or two per adapter, and is then a stream of A.
 template <int R>
 struct Shrink {
-  static constexpr int kRows = 64, kStages = 4;
-  // rows of 128 bytes in a stage: 64 of X and R of W, or with few tokens several blocks of
-  // 64 of the reduction
-  static constexpr int kStageRows = R == 16 ? 128 : R == 32 ? 96 : R == 64 ? 160 : 192;
+  static constexpr int kRows = 64, kStages = R == 128 ? 4 : 3;
+  // rows of 128 bytes in a stage: 64 of X and R of W twice (two blocks of 64 of the reduction
+  // between barriers), once at a rank of 128; with few tokens up to four
+  static constexpr int kStageRows = R == 128 ? 192 : 2 * (64 + R);
   static constexpr int kStageBytes = kStageRows * 128;
-  static constexpr int kSmem = kStages * kStageBytes + 128;
+  // 8 rows more: of an odd number of eights of ranks the last matrix load reads 16 rows
+  static constexpr int kSmem = kStages * kStageBytes + 8 * 128 + 128;
 };
 
 struct ShrinkParams {
@@ -245,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 3 : R == 64 ? 2 : 1) shrin
         uint32_t b[R / 16][4];
 #pragma unroll
         for (int i = 0; i < R / 16; ++i)
-          // of an odd number of eights the last pair's second half is what lies behind: inside the stage, and unused
+          // of an odd number of eights the last pair's second half is what lies behind, and unused
           if (FULL || i * 16 < rank) load_matrices(b[i], bs + i * 2048);
 #pragma unroll
         for (int i = 0; i < R / 16; ++i) {
@@ -538,20 +536,20 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
 }
 
 // ---------------------------------------------------------------- outer
-// dA and dB together: a block takes one segment of an adapter's rows (`segment` of them, so
-// that blocks are alike however the tokens are shared out) and COLS columns of x or dy.
-// An adapter of one segment is finished there; the segments' sums of the others meet in a
-// second launch, in order.  The products are (rank x 64 tokens) (64 tokens x columns),
-// both read across their rows.
-template <int R>
+// dA and dB together.  u and du are first written as terms of 16 bits, row by row of the map
+// (every block of columns would do it again).  Then a block takes one segment of an
+// adapter's rows (`segment` of them, so that blocks are alike however the tokens are shared
+// out) and kCols columns of x or dy.  An adapter of one segment is finished there; the
+// segments' sums of the others meet in another launch, in order.  The products are
+// (rank x 64 tokens) (64 tokens x columns), both read across their rows.
+template <int R, int TERMS>
 struct Outer {
   static constexpr int kCols = R == 128 ? 128 : 256, kTokens = 64, kStages = R <= 32 ? 2 : 3;
-  static constexpr int kXBytes = kTokens * kCols * 2, kGBytes = kTokens * R * 4;
-  static constexpr int kStageBytes = kXBytes + kGBytes;
   static constexpr int kTermPitch = 2 * R + 16;         // bytes of a token's ranks: eight rows in different banks
-  static constexpr int kTermBytes = kTokens * kTermPitch;
-  static constexpr int smem(int terms) { return kStages * kStageBytes + terms * kTermBytes + 128; }
-  static_assert(R * kCols * 4 <= kStages * kStageBytes, "the sums reuse the stages");
+  static constexpr int kXBytes = kTokens * kCols * 2, kTermBytes = kTokens * kTermPitch;
+  static constexpr int kStageBytes = kXBytes + TERMS * kTermBytes;
+  static constexpr int kSmem = kStages * kStageBytes;
+  static_assert(R * kCols * 4 <= kSmem, "the sums reuse the stages");
 };
 
 // One of the two gradients: sum over an adapter's tokens of g[t]^T X[t], times f_i.
@@ -561,6 +559,8 @@ struct OuterSide {
   const float* scales;
   void* out;
   float* part;                    // (slots, rank, width) sums of segments
+  uint16_t* terms;                // (TERMS, m_pad, ranks) of g
+  float* units;                   // of each segment's terms
   int64_t ldx;
   int width, blocks;              // blocks of columns; 0: not wanted
 };
@@ -627,16 +627,69 @@ __device__ __forceinline__ Segment find_segment(const OuterParams& p, int64_t wa
   return found;
 }
 
+// g of a segment's rows as terms of 16 bits, zeros for padding rows (up to a multiple of 64)
+// and behind the rank (to a multiple of 16).  float16 keeps them inside its range by the
+// segment's own power of two; its sums are scaled back before they are joined.
+template <int KIND, int TERMS>
+__global__ void __launch_bounds__(kThreads) outer_terms_kernel(const __grid_constant__ OuterParams p) {
+  __shared__ float most_of[kWarps];
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const OuterSide& side = p.side[blockIdx.y];
+  // a block takes 64 rows; the segment's power of two it finds by itself
+  const int chunks = p.segment / 64;
+  const int64_t number = blockIdx.x / chunks;
+  const int chunk = static_cast<int>(blockIdx.x - number * chunks);
+  const Segment seg = find_segment(p, number, 0);
+  if (seg.adapter < 0 || side.blocks == 0) return;
+  const int64_t row0 = adapter_begin(p, seg.adapter) + static_cast<int64_t>(seg.index) * p.segment;
+  const int64_t row1 = min(row0 + p.segment, adapter_end(p, seg.adapter));
+  const int quads = p.rank / 4;
+  float unit = 1.0f;
+  if (KIND == OK_F16) {
+    float most = 0.0f;
+    for (int64_t e = threadIdx.x; e < (row1 - row0) * quads; e += kThreads) {
+      const int64_t r = e / quads;
+      const int32_t t = token_at(p.map, row0 + r);
+      if (t < 0) continue;
+      const float4 v = *reinterpret_cast<const float4*>(side.g + static_cast<int64_t>(t) * p.rank + (e - r * quads) * 4);
+      most = fmaxf(fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    if ((threadIdx.x & 31) == 0) most_of[threadIdx.x >> 5] = most;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) most = fmaxf(most, most_of[w]);
+    unit = unit_of(most);
+    if (threadIdx.x == 0) side.units[number] = unit;             // the same from each of them
+  }
+  const int ranks = (p.rank + 15) & ~15, all = ranks / 4;
+  const int64_t from = row0 + chunk * 64;
+  if (from >= row1) return;
+  for (int e = threadIdx.x; e < 64 * all; e += kThreads) {
+    const int i = e / all, q = e - i * all;
+    const int64_t r = from + i;
+    if (r >= p.map.m_pad) break;
+    const int32_t t = r < row1 ? token_at(p.map, r) : -1;
+    float4 v = make_float4(0, 0, 0, 0);
+    if (t >= 0 && q < quads) v = *reinterpret_cast<const float4*>(side.g + static_cast<int64_t>(t) * p.rank + q * 4);
+    uint32_t lo[TERMS], hi[TERMS];
+    split_terms<KIND, TERMS>(v.x * unit, v.y * unit, lo);
+    split_terms<KIND, TERMS>(v.z * unit, v.w * unit, hi);
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k)
+      *reinterpret_cast<uint2*>(side.terms + (k * p.map.m_pad + r) * ranks + q * 4) = make_uint2(lo[k], hi[k]);
+  }
+}
+
 template <int KIND, int R, int TERMS, bool FULL>
 __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const __grid_constant__ OuterParams p) {
-  using O = Outer<R>;
+  using O = Outer<R, TERMS>;
   constexpr int kTiles = O::kCols / 8 / kWarps;         // of 8 columns, a warp
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int32_t token[O::kStages + 1][O::kTokens];
-  __shared__ float most_of[kWarps];
-  const int rank = FULL ? R : p.rank;
+  const int rank = FULL ? R : p.rank, ranks = FULL ? R : (rank + 15) & ~15;
   const uint32_t base = smem_u32(smem);
-  const uint32_t terms = base + O::kStages * O::kStageBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_segment = p.side[0].blocks + p.side[1].blocks;
   const int64_t number = blockIdx.x / per_segment;
@@ -658,38 +711,18 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
     return r < row1 ? token_at(p.map, r) : -1;
   };
 
-  float unit = 1.0f;
-  if (KIND == OK_F16) {
-    // this block's own power of two: its sums are scaled back before they are joined
-    float most = 0.0f;
-    for (int64_t r = row0 + threadIdx.x; r < row1; r += kThreads) {
-      const int32_t t = token_at(p.map, r);
-      if (t < 0) continue;
-      for (int k = 0; k < rank; k += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(side.g + static_cast<int64_t>(t) * rank + k);
-        most = fmaxf(fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-    if (lane == 0) most_of[warp] = most;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) most = fmaxf(most, most_of[w]);
-    unit = unit_of(most);
-  }
-
   // a thread copies one piece of every kStep-th token's columns, and one of every kGStep-th
-  // token's ranks
-  constexpr int kPieces = O::kCols / 8, kStep = kThreads / kPieces, kQuads = R / 4, kGStep = kThreads / kQuads;
-  static_assert(kStep % 8 == 0 && kGStep <= O::kTokens, "a thread's rows have one swizzle");
+  // row of terms
+  constexpr int kPieces = O::kCols / 8, kStep = kThreads / kPieces, kTermPieces = R / 8, kGStep = kThreads / kTermPieces;
+  static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
   const int piece = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
-  const int quad = threadIdx.x % kQuads, g0 = threadIdx.x / kQuads;
+  const int g_piece = threadIdx.x % kTermPieces, g0 = threadIdx.x / kTermPieces;
   const bool in_cols = col0 + piece * 8 < side.width;
-  const int64_t ldx = side.ldx;
+  const int64_t ldx = side.ldx, term_size = p.map.m_pad * ranks;
   const uint16_t* xp = static_cast<const uint16_t*>(side.x) + (in_cols ? col0 + piece * 8 : 0);
-  const float* gp = side.g + quad * 4;
+  const uint16_t* gp = side.terms + (row0 + g0) * ranks + g_piece * 8;
   const uint32_t x_to = base + (piece >> 3) * (O::kTokens * 128) + swizzled(r0, piece & 7);
-  const uint32_t g_to = base + O::kXBytes + (g0 * R + quad * 4) * 4;
+  const uint32_t g_to = base + O::kXBytes + g0 * O::kTermPitch + g_piece * 16;
   auto load = [&](int c) {
     if (c < chunks) {
       const int32_t* tok = token[c % (O::kStages + 1)];
@@ -699,13 +732,15 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
         const int32_t t = tok[r0 + i * kStep];
         copy16(x_to + stage + i * kStep * 128, xp + (t >= 0 ? t * ldx : 0), t >= 0 && in_cols ? 16 : 0);
       }
-      if (FULL || quad * 4 < rank) {
+      if (FULL || g_piece * 8 < ranks) {
 #pragma unroll
-        for (int i = 0; i < O::kTokens / kGStep; ++i) {
-          const int32_t t = tok[g0 + i * kGStep];
-          copy16(g_to + stage + i * kGStep * R * 4, gp + (t >= 0 ? static_cast<int64_t>(t) * rank : 0), t >= 0 ? 16 : 0);
-        }
+        for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+          for (int i = 0; i < O::kTokens; i += kGStep)
+            if (kGStep <= O::kTokens || g0 < O::kTokens)
+              copy16(g_to + stage + k * O::kTermBytes + i * O::kTermPitch, gp + k * term_size + i * ranks, 16);
       }
+      gp += O::kTokens * ranks;
     }
     copies_commit();
   };
@@ -739,19 +774,6 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
       load(ahead);
       if (threadIdx.x < O::kTokens) next = token_of(ahead + 1, threadIdx.x);
       const uint32_t stage = base + (c % O::kStages) * O::kStageBytes;
-      // g as terms of 16 bits, zeros behind the rank
-#pragma unroll
-      for (int i = 0; i < O::kTokens / kGStep; ++i) {
-        float4 v = make_float4(0, 0, 0, 0);
-        if (FULL || quad * 4 < rank) v = get_shared4f(g_to - base + stage + i * kGStep * R * 4);
-        uint32_t lo[TERMS], hi[TERMS];
-        split_terms<KIND, TERMS>(v.x * unit, v.y * unit, lo);
-        split_terms<KIND, TERMS>(v.z * unit, v.w * unit, hi);
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k)
-          put_shared2(terms + k * O::kTermBytes + (g0 + i * kGStep) * O::kTermPitch + quad * 8, lo[k], hi[k]);
-      }
-      __syncthreads();
 #pragma unroll
       for (int s = 0; s < O::kTokens / 16; ++s) {
         uint32_t b[kTiles / 2][4];
@@ -760,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
           const int tile = warp * kTiles + i;          // of 8 columns; 8 of them share 128 bytes
           load_matrices_t(b[i / 2], stage + (tile >> 3) * (O::kTokens * 128) + swizzled(s * 16 + (lane & 15), (tile & 7) + (lane >> 4)));
         }
-        const uint32_t as = terms + (s * 16 + (lane & 7) + ((lane >> 4) << 3)) * O::kTermPitch + ((lane >> 3) & 1) * 16;
+        const uint32_t as = stage + O::kXBytes + (s * 16 + (lane & 7) + ((lane >> 4) << 3)) * O::kTermPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
         for (int k = 0; k < TERMS; ++k) {
           uint32_t a[R / 16][4];
@@ -790,7 +812,8 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
   const bool alone = seg.count == 1;
-  const float f = (alone && side.scales != nullptr ? side.scales[seg.adapter] : 1.0f), back = 1.0f / unit;
+  const float f = (alone && side.scales != nullptr ? side.scales[seg.adapter] : 1.0f),
+              back = KIND == OK_F16 ? 1.0f / side.units[number] : 1.0f;
 #pragma unroll
   for (int m = 0; m < R / 16; ++m) {
     if (!FULL && m * 16 >= rank) break;
@@ -931,6 +954,33 @@ int64_t outer_slots(int64_t tokens, int64_t k, int64_t n) {
   return tokens > rows ? 2 * ceil_div(tokens, rows) : 0;
 }
 
+// Blocks' worth of segments of a map.
+int64_t outer_segments(int64_t tokens, int64_t m_pad, int64_t adapters, int64_t rows) {
+  // an adapter's rows are its tokens rounded up to 128
+  const int64_t used = tokens < adapters ? tokens : adapters, all = tokens + 128 * used;
+  return used + (all < m_pad ? all : m_pad) / rows;
+}
+
+// What lies where in the workspace, in bytes: both sides' terms (three at the most), their
+// units, and the segments' sums.
+struct OuterSpace {
+  uint64_t terms[2], units[2], part[2], bytes;
+  OuterSpace(int64_t tokens, int64_t k, int64_t n, int64_t m_pad, int64_t adapters, int64_t rank) {
+    uint64_t at = 0;
+    auto take = [&](uint64_t size) {
+      const uint64_t from = at;
+      at += (size + 15) / 16 * 16;
+      return from;
+    };
+    const int64_t segments = outer_segments(tokens, m_pad, adapters, outer_segment(tokens, k, n)), slots = outer_slots(tokens, k, n);
+    for (uint64_t& t : terms) t = take(uint64_t(6) * m_pad * ((rank + 15) / 16 * 16));
+    for (uint64_t& u : units) u = take(uint64_t(4) * segments);
+    part[0] = take(uint64_t(4) * slots * rank * n);
+    part[1] = take(uint64_t(4) * slots * rank * k);
+    bytes = at;
+  }
+};
+
 bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
   return with_half(format, [&](auto kind) {
     return with_rank(p.rank, [&](auto r, auto full) {
@@ -938,19 +988,20 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
       constexpr bool E = decltype(full)::value;
       int64_t most = 0;
       for (OuterSide& side : p.side) {
-        side.blocks = side.out != nullptr ? static_cast<int>(ceil_div(side.width, Outer<R>::kCols)) : 0;
+        side.blocks = side.out != nullptr ? static_cast<int>(ceil_div(side.width, Outer<R, 2>::kCols)) : 0;
         most += side.out != nullptr ? ceil_div(int64_t(p.rank) * side.width, 8 * kThreads) : 0;
       }
-      // an adapter's rows are its tokens rounded up to 128
-      const int64_t used = p.map.tokens < p.map.adapters ? p.map.tokens : p.map.adapters;
-      const int64_t all = p.map.tokens + 128 * used < p.map.m_pad ? p.map.tokens + 128 * used : p.map.m_pad;
-      const int64_t grid = (used + all / p.segment) * (p.side[0].blocks + p.side[1].blocks);
+      const int64_t segments = outer_segments(p.map.tokens, p.map.m_pad, p.map.adapters, p.segment), grid = segments * (p.side[0].blocks + p.side[1].blocks);
       if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
       auto launch = [&](auto terms) {
         constexpr int N = decltype(terms)::value;
-        if (!allowed<outer_kernel<K, R, N, E>>(Outer<R>::smem(N))) return BSGG_ERR_CUDA;
-        const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, Outer<R>::smem(N), s);
-        const bsgg_status st = launch_kernel(c, outer_kernel<K, R, N, E>, p);
+        constexpr int kSmem = Outer<R, N>::kSmem;
+        if (!allowed<outer_kernel<K, R, N, E>>(kSmem)) return BSGG_ERR_CUDA;
+        const LaunchConfig t(dim3(static_cast<unsigned>(segments * (p.segment / 64)), 2), kThreads, 0, s);
+        bsgg_status st = launch_kernel(t, outer_terms_kernel<K, N>, p);
+        if (st != BSGG_OK) return st;
+        const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, kSmem, s);
+        st = launch_kernel(c, outer_kernel<K, R, N, E>, p);
         if (st != BSGG_OK) return st;
         // two rounds of blocks over all adapters
         const int64_t each = 2432 / p.map.adapters < 1 ? 1 : 2432 / p.map.adapters;
@@ -1003,9 +1054,9 @@ bsgg_status bsgg_adapters(const bsgg_adapters_desc* d, const void* x, const void
                                    static_cast<int>(d->n), d->rank}, s);
 }
 
-uint64_t bsgg_adapters_workspace_bytes(int64_t tokens, int64_t k, int64_t n, int32_t rank) {
-  if (check_adapters(tokens, k, n, 128, 1, rank, BSGG_OUT_BF16) != BSGG_OK) return 0;
-  return uint64_t(4) * outer_slots(tokens, k, n) * rank * (k + n);
+uint64_t bsgg_adapters_workspace_bytes(int64_t tokens, int64_t k, int64_t n, int64_t m_pad, int32_t adapters, int32_t rank) {
+  if (check_adapters(tokens, k, n, m_pad, adapters, rank, BSGG_OUT_BF16) != BSGG_OK || tokens == 0) return 0;
+  return OuterSpace(tokens, k, n, m_pad, adapters, rank).bytes;
 }
 
 bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* dy, const void* x, const float* u,
@@ -1037,7 +1088,7 @@ bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* 
   if (!dx && !da && !db) return BSGG_ERR_INVALID_ARG;
   const bool wants_du = dx || da;
   if (!dy || !padded_offsets || !slot_of_row || (wants_du && (!b || !du)) || (dx && (!a || !row_of_slot)) || (da && !x) ||
-      (db && !u) || ((da || db) && !rows_used) || ((da || db) && !workspace && outer_slots(d->tokens, d->k, d->n) > 0))
+      (db && !u) || ((da || db) && !rows_used) || ((da || db) && !workspace))
     return BSGG_ERR_INVALID_ARG;
   const AdapterMap map = {d->tokens, d->m_pad, d->adapters, padded_offsets, row_of_slot, slot_of_row};
   bsgg_status ran = BSGG_OK;
@@ -1047,9 +1098,14 @@ bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* 
     p.map = map; p.rows_used = rows_used; p.rank = d->rank; p.out_kind = d->grad_format;
     p.segment = static_cast<int>(outer_segment(d->tokens, d->k, d->n));
     p.slots = static_cast<int>(outer_slots(d->tokens, d->k, d->n));
-    float* part = static_cast<float*>(workspace);
-    p.side[0] = {u, dy, scales, db, part, d->ld_dy, static_cast<int>(d->n), 0};
-    p.side[1] = {du, x, nullptr, da, part + outer_slots(d->tokens, d->k, d->n) * d->rank * d->n, d->ldx, static_cast<int>(d->k), 0};
+    const OuterSpace space(d->tokens, d->k, d->n, d->m_pad, d->adapters, d->rank);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    auto side = [&](int i, const float* g, const void* in, const float* f, void* out, int64_t ld, int64_t width) {
+      p.side[i] = {g, in, f, out, reinterpret_cast<float*>(ws + space.part[i]), reinterpret_cast<uint16_t*>(ws + space.terms[i]),
+                   reinterpret_cast<float*>(ws + space.units[i]), ld, static_cast<int>(width), 0};
+    };
+    side(0, u, dy, scales, db, d->ld_dy, d->n);
+    side(1, du, x, nullptr, da, d->ldx, d->k);
     ran = launch_outer(d->format, p, s);
   }
   if (ran == BSGG_OK && dx)

@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : NV <= 2 ? 256 : kN
   if (kAhead) row.load(p, row0, first, step);
   for (int64_t t = row0; t < p.tokens; t += gridDim.x * rows, turn ^= 1) {
     if (!kAhead) row.load(p, t, first, step);
+    if (kAhead) next.load(p, t + gridDim.x * rows, first, step);
     const float2 rstd = make_float2(row.rstd, row.rstd);
     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -282,7 +283,6 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : NV <= 2 ? 256 : kN
           sum = __ffma2_rn(q, make_float2(ww[0], ww[1]), sum);
         }
       }
-    if (kAhead) next.load(p, t + gridDim.x * rows, first, step);
     // two buffers: the next row's sums are written while this row's may still be read
     const float mean = row_sum<WARP>(sum.x + sum.y, part[turn]) * p.inv_hidden;
     const float2 minus = make_float2(-mean, -mean);

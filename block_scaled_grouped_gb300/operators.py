@@ -116,7 +116,7 @@ def bind(L) -> None:
     L.bsgg_rms_norm_workspace_bytes.restype, L.bsgg_rms_norm_workspace_bytes.argtypes = ctypes.c_uint64, [i64, i64]
     L.bsgg_rms_norm_backward.argtypes = [ctypes.POINTER(NormBwdDesc)] + [vp] * 9
     L.bsgg_adapters.argtypes = [ctypes.POINTER(AdaptersDesc)] + [vp] * 11
-    L.bsgg_adapters_workspace_bytes.restype, L.bsgg_adapters_workspace_bytes.argtypes = ctypes.c_uint64, [i64, i64, i64, i32]
+    L.bsgg_adapters_workspace_bytes.restype, L.bsgg_adapters_workspace_bytes.argtypes = ctypes.c_uint64, [i64] * 4 + [i32] * 2
     L.bsgg_adapters_backward.argtypes = [ctypes.POINTER(AdaptersBwdDesc)] + [vp] * 17
     for name in ("bsgg_route_groups", "bsgg_route_groups_backward", "bsgg_rms_norm", "bsgg_rms_norm_backward", "bsgg_adapters",
                  "bsgg_adapters_backward",
@@ -740,8 +740,7 @@ def adapters_backward(dy, x, u, a, b, tokens: TokenMap, scales=None, base=None, 
     db = empty((S, r, N), dtype=gt, device=dev) if want_db else None
     du = empty((T, r), dtype=_F32, device=dev) if want_dx or want_da else None
     L = lib()
-    nws = L.bsgg_adapters_workspace_bytes(T, K, N, r) // 4 if want_da or want_db else 0
-    ws = empty(nws, dtype=_F32, device=dev) if nws else None
+    ws = empty(L.bsgg_adapters_workspace_bytes(T, K, N, m_pad, S, r), dtype=_U8, device=dev) if want_da or want_db else None
     desc = AdaptersBwdDesc(T, K, N, m_pad, ld_dy, ldx, ldb, ld_dx, S, r, _format(dy, "dy"), _FORMATS[gt])
     code = L.bsgg_adapters_backward(byref(desc), dy.data_ptr(), x.data_ptr(), _flat(u, "u", T * r, _F32), a.data_ptr(),
                                     b.data_ptr(), _flat(scales, "scales", S, _F32), p_off, p_row, p_slot,

@@ -738,9 +738,9 @@ BSGG_API bsgg_status bsgg_adapters(const bsgg_adapters_desc* desc, const void* x
  * da and db are dense like A and B, in grad_format, zeros for an adapter without tokens.
  * dx, da and db may each be NULL: not wanted (x, u, a are then not read where only they need them).
  * The scales are constants: they get no gradient.  rows_used (1) as bsgg_sort_tokens writes it
- * (da and db only): where the last adapter's rows end.  workspace:
- * bsgg_adapters_workspace_bytes bytes with da or db (0: may be NULL), 16-byte aligned; it is
- * free once the call's work on the stream is done. */
+ * (da and db only): where the last adapter's rows end.  workspace (da and db only):
+ * bsgg_adapters_workspace_bytes bytes, 16-byte aligned; it is free once the call's work on
+ * the stream is done. */
 typedef struct {
   int64_t tokens;
   int64_t k, n;
@@ -752,7 +752,8 @@ typedef struct {
   int32_t grad_format;    /* f: da, db */
 } bsgg_adapters_bwd_desc;
 
-BSGG_API uint64_t bsgg_adapters_workspace_bytes(int64_t tokens, int64_t k, int64_t n, int32_t rank);
+BSGG_API uint64_t bsgg_adapters_workspace_bytes(int64_t tokens, int64_t k, int64_t n, int64_t m_pad, int32_t adapters,
+                                                int32_t rank);
 BSGG_API bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* desc, const void* dy, const void* x,
                                             const float* u, const void* a, const void* b, const float* scales,
                                             const int32_t* padded_offsets, const int32_t* row_of_slot,

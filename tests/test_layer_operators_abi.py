@@ -173,14 +173,16 @@ def test_adapters_backward_refuses(lib, over):
 
 
 def test_adapters_backward_refuses_pointers(lib):
-    for name in ("dy", "x", "u", "a", "b", "off", "row", "slot", "used", "du"):
+    for name in ("dy", "x", "u", "a", "b", "off", "row", "slot", "used", "du", "ws"):
         assert adapt_bwd(lib, {name: None}) == 1, name
     for name in ("dy", "x", "u", "a", "b", "scales", "off", "row", "slot", "used", "base", "du", "dx", "da", "db", "ws"):
         assert adapt_bwd(lib, {name: ODD}) == 1, name
     assert adapt_bwd(lib, dict(dx=None, da=None, db=None)) == 1        # nothing wanted
-    big = dict(tokens=100000, k=4096, n=14336, ld_dy=14336, ldx=4096, ld_base=4096, ld_dx=4096)
-    assert lib.bsgg_adapters_workspace_bytes(100000, 4096, 14336, 16) > 0 and adapt_bwd(lib, dict(ws=None), **big) == 1
-    assert lib.bsgg_adapters_workspace_bytes(100, 4096, 14336, 16) == 0 and lib.bsgg_adapters_workspace_bytes(-1, 8, 8, 8) == 0
+    assert adapt_bwd(lib, dict(ws=None)) == 1 and adapt_bwd(lib, dict(ws=None, da=None)) == 1
+    need = lib.bsgg_adapters_workspace_bytes
+    assert need(4, 64, 32, 128, 3, 16) > 0 and need(0, 64, 32, 128, 3, 16) == 0 and need(-1, 64, 32, 128, 3, 16) == 0
+    # sums of segments on top of the terms, for many tokens
+    assert need(100000, 4096, 14336, 2 ** 17, 3, 16) > 6 * 2 ** 17 * 32 + 4 * 16 * 18432
     assert adapt_bwd(lib, dict(base=P), ld_base=72) == 1               # in place under another pitch
     assert adapt_bwd(lib, dict(dy=None, da=None, db=None), tokens=0) == 0
 
