@@ -67,7 +67,8 @@ CASES = [(1, 1, 8, 8, 8, "bf16", "one"), (1, 4, 16, 2048, 512, "f16", "any"), (3
          (64, 5, 64, 320, 1032, "f16", "any"), (65, 1, 128, 128, 136, "bf16", "one"), (130, 1, 128, 200, 600, "f16", "one"),
          (70, 1, 56, 1000, 264, "bf16", "one"), (100, 2, 72, 88, 520, "bf16", "any"), (128, 64, 16, 512, 640, "bf16", "any"),
          (300, 3, 16, 256, 512, "f16", "runs"), (600, 2, 32, 128, 2056, "bf16", "runs"), (20, 1, 120, 64, 64, "f16", "one"),
-         (9, 3, 16, 64, 64, "bf16", "none"), (50, 1000, 8, 64, 64, "f16", "any"), (120, 1, 112, 640, 1096, "bf16", "one")]
+         (9, 3, 16, 64, 64, "bf16", "none"), (25, 1, 8, 512, 96, "f16", "one"), (90, 1, 24, 1024, 160, "bf16", "one"),
+         (20, 1, 56, 200, 80, "bf16", "one"), (31, 2, 104, 72, 304, "f16", "one"), (50, 1000, 8, 64, 64, "f16", "any"), (120, 1, 112, 640, 1096, "bf16", "one")]
 
 
 @pytest.mark.parametrize("case", CASES)
@@ -178,10 +179,11 @@ def test_gradients_are_those_of_the_forward_by_differences():
         assert abs(float(f(*args[0]) - f(*args[1])) - want) <= tol
 
 
-def test_many_tokens_of_few_adapters():
-    """Several tiles of an adapter, long sums, against the same in 64 bits by products."""
-    T, S, r, K, N = 3000, 3, 32, 1024, 1536
-    p = problem(T, S, r, K, N, "bf16", "runs", 7)
+@pytest.mark.parametrize("T,S,r,K,N,dtype", [(3000, 3, 32, 1024, 1536, "bf16"), (2500, 5, 16, 4096, 2048, "f16"), (1100, 2, 64, 512, 8192, "bf16"),
+                                             (2000, 2, 128, 256, 768, "f16"), (700, 40, 24, 512, 264, "bf16")])
+def test_many_tokens_of_few_adapters(T, S, r, K, N, dtype):
+    """Several tiles and segments of an adapter, long sums, against the same in 64 bits by products."""
+    p = problem(T, S, r, K, N, dtype, "runs", 7)
     t = map_of(p, S)
     x, a, b, base, dy = (p[n].cuda() for n in ("x", "a", "b", "base", "dy"))
     y, u = bsgg.adapters(x, a, b, t, base=base)
@@ -197,7 +199,8 @@ def test_many_tokens_of_few_adapters():
         want_da.append(dui.t() @ x.double())
         want_db.append(ui.t() @ dy.double())
     # 16-bit results carry their own rounding, 2^-9.2 in norm; those in 32 bits the sums' 2^-19
-    assert far(y, want_y) < 2.0 ** -8.5 and far(dx, want_dx) < 2.0 ** -8.5
+    half = 2.0 ** -8.5 if dtype == "bf16" else 2.0 ** -11.5
+    assert far(y, want_y) < half and far(dx, want_dx) < half
     assert far(da, torch.stack(want_da)) < 2.0 ** -19 and far(db, torch.stack(want_db)) < 2.0 ** -19
     for _ in range(2):                                # no order depends on timing
         again = bsgg.adapters_backward(dy, x, u, a, b, t, grad_format="f32")
@@ -260,6 +263,32 @@ def test_streams_and_graph():
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want_q))
+
+
+def test_offsets_past_32_bits():
+    """Rows of x, base and y that lie more than 2^31 elements from the first."""
+    K = N = 16384
+    T = 2 ** 31 // K + 40
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    ids = torch.full((T, 1), -1, dtype=torch.int32)
+    last = [T - 1, T - 2, T - 17, 5]
+    ids[last] = 1
+    g = gen(3)
+    rows = torch.randn(len(last), K, generator=g).bfloat16()
+    x[last] = rows.cuda()
+    a, b = (torch.randn(2, 8, K, generator=g) / K ** 0.5).bfloat16(), torch.randn(2, 8, N, generator=g).bfloat16()
+    t = bsgg.sort_tokens(ids.cuda(), 2)
+    y, u = bsgg.adapters(x, a.cuda(), b.cuda(), t, base=x)
+    want, want_u = R.adapters(rows, a, b, [1] * len(last), None, rows)
+    got = y[last].cpu().double()
+    assert ((got - want).abs() <= 2.0 ** -6 + rounding(want, torch.bfloat16)).all()
+    assert torch.equal(y[:5], x[:5]) and torch.equal(y[T - 16:T - 2], x[T - 16:T - 2]) and (u[:5] == 0).all()
+    dx, da, db = bsgg.adapters_backward(y, x, u, a.cuda(), b.cuda(), t, grad_format="f32")
+    assert (da[0] == 0).all() and (db[0] == 0).all()
+    w = u[last].double().t() @ y[last].double()
+    assert float((db[1].double() - w).norm() / w.norm()) < 2.0 ** -18
+    w = (y[last].double() @ b[1].cuda().double().t()) @ a[1].cuda().double()
+    assert float((dx[last].double() - w).norm() / w.norm()) < 2.0 ** -8.5 and (dx[:5] == 0).all()
 
 
 def test_no_tokens():

@@ -164,6 +164,46 @@ def test_groups_without_a_bias_near_ties(score):
     assert torch.equal(ids.cpu(), want)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_ties_of_logits_of_few_bits(score, dtype):
+    """bfloat16 logits with a bias of zeros, as training starts: equal scores in most rows,
+    of experts and of groups."""
+    T, L = 500, 64
+    l = (torch.randn(T, L, generator=gen(29)) * 0.3).to(DT[dtype])
+    l = torch.round(l.float() * 8).div(8).to(DT[dtype])
+    for bias in (None, torch.zeros(L), torch.full((L,), 0.25)):
+        for groups, kept, top in ((1, 1, 1), (8, 4, 2), (8, 4, 1), (4, 1, 2)):
+            where = dict(score=score, groups=groups, topk_groups=kept, group_top=top)
+            want, _ = R.route_groups(l, 6, bias=bias, **where)
+            ids, _ = bsgg.route_groups(l.cuda(), 6, bias=None if bias is None else bias.cuda(), **where)
+            assert torch.equal(ids.cpu(), want), (groups, top)
+
+
+def test_biases_larger_than_scores():
+    """Groups whose terms cancel: large biases of both signs."""
+    T, L = 64, 32
+    l = torch.randn(T, L, generator=gen(31))
+    bias = torch.randn(L, generator=gen(32)) * 30.0
+    bias[::2] = bias[1::2] * -1.0
+    for top in (1, 2):
+        where = dict(groups=8, topk_groups=3, group_top=top)
+        want, _ = R.route_groups(l, 5, bias=bias, **where)
+        ids, _ = bsgg.route_groups(l.cuda(), 5, bias=bias.cuda(), **where)
+        assert torch.equal(ids.cpu(), want)
+
+
+def test_offsets_past_32_bits():
+    T, L = 2 ** 21 + 3, 1024
+    l = torch.zeros(T, L, dtype=torch.bfloat16, device="cuda")
+    l[-1] = torch.randn(L, generator=gen(33)).bfloat16().cuda()
+    ids, w = bsgg.route_groups(l, 3, score="sigmoid", groups=16, topk_groups=2)
+    want, want_w = R.route_groups(l[-1:].cpu(), 3, groups=16, topk_groups=2)
+    assert torch.equal(ids[-1:].cpu(), want) and (ids[:-1] == torch.arange(3, device="cuda", dtype=torch.int32)).all()
+    dl = bsgg.route_groups_backward(l, ids, w, torch.ones_like(w), normalize=False)
+    assert float(dl[-1, int(want[0, 0])]) != 0.0 and (dl[0, 3:] == 0).all()
+
+
 def test_scores_below_the_smallest_number_keep_their_ratios():
     l = torch.tensor([[-200.0, -201.0, -300.0, -202.0], [90.0, 100.0, 95.0, -95.0], [-88.0, -89.0, -104.0, -87.0]])
     for score in ("sigmoid", "softmax"):
