@@ -98,37 +98,40 @@ __device__ __forceinline__ float unit_of(float largest) {
   return e >= 1u && e <= 253u ? __uint_as_float((254u - e) << 23) : 1.0f;
 }
 
-// The adapter whose rows hold `row`.  All threads call it.
-__device__ __forceinline__ int adapter_of(const AdapterMap& m, int64_t row) {
-  int n = 0;
-  for (int i = 0; i < m.adapters; i += kThreads) {
-    const int at = i + threadIdx.x;
-    n += __syncthreads_count(at < m.adapters && m.offsets[at] <= row);
-  }
-  return min(n, m.adapters - 1);
-}
 __device__ __forceinline__ int32_t token_at(const AdapterMap& m, int64_t row) {
   const int32_t t = row < m.m_pad ? m.slot_of_row[row] : -1;
   return t >= 0 && t < m.tokens ? t : -1;
 }
-// Tokens of ROWS rows from row0 into shared memory; one past the last row that has one.
+// ROWS rows from row0: their tokens into shared memory, one past the last row that has one,
+// and the adapter whose rows they are.  All threads call it: the map and the offsets are
+// read at once.
+struct Tile {
+  int n, adapter;
+};
 template <int ROWS>
-__device__ __forceinline__ int tokens_of(const AdapterMap& m, int64_t row0, int32_t* token) {
-  bool has = false;
-  if (threadIdx.x < ROWS) {
-    const int32_t t = token_at(m, row0 + threadIdx.x);
-    token[threadIdx.x] = t;
-    has = t >= 0;
-  }
+__device__ __forceinline__ Tile tile_at(const AdapterMap& m, int64_t row0, int32_t* token) {
   __shared__ uint32_t mask[ROWS / 32];
-  const uint32_t b = __ballot_sync(0xFFFFFFFFu, has);
-  if ((threadIdx.x & 31) == 0 && threadIdx.x < ROWS) mask[threadIdx.x >> 5] = b;
+  __shared__ int ends[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t t = threadIdx.x < ROWS ? token_at(m, row0 + threadIdx.x) : -1;
+  int before = 0;                                      // adapters whose rows end before these
+  for (int i = threadIdx.x; i < m.adapters; i += kThreads) before += m.offsets[i] <= row0;
+  const uint32_t b = __ballot_sync(0xFFFFFFFFu, t >= 0);
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  if (threadIdx.x < ROWS) token[threadIdx.x] = t;
+  if (lane == 0) {
+    ends[warp] = before;
+    if (warp < ROWS / 32) mask[warp] = b;
+  }
   __syncthreads();
-  int n = 0;
+  Tile tile = {0, 0};
 #pragma unroll
   for (int i = 0; i < ROWS / 32; ++i)
-    if (mask[i] != 0) n = 32 * i + 32 - __clz(mask[i]);
-  return n;
+    if (mask[i] != 0) tile.n = 32 * i + 32 - __clz(mask[i]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) tile.adapter += ends[w];
+  tile.adapter = min(tile.adapter, m.adapters - 1);
+  return tile;
 }
 // Groups of 16 rows, as a power of two, that hold n rows.
 __device__ __forceinline__ int row_groups(int n) { return n <= 16 ? 1 : n <= 32 ? 2 : n <= 64 ? 4 : 8; }
@@ -172,9 +175,9 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 3 : R == 64 ? 2 : 1) shrin
   let_next_kernel_start();
   wait_for_previous_kernel();
   const int64_t row0 = tile * S::kRows;
-  const int n = tokens_of<S::kRows>(p.map, row0, token);
+  const Tile at_tile = tile_at<S::kRows>(p.map, row0, token);
+  const int n = at_tile.n, adapter = at_tile.adapter;
   if (n == 0) return;                                  // for the whole cluster
-  const int adapter = adapter_of(p.map, row0);
   const int groups = row_groups(n), rows = 16 * groups, shares = kWarps / groups;
   const int mw = warp % groups, kw = warp / groups;
   const int blocks = max(1, min(4, S::kStageRows / (rows + p.rank)));   // of 64, a stage
@@ -323,42 +326,54 @@ struct ExpandParams {
   void* y;
   float* zero_u;              // u's rows of tokens without an adapter, where wanted
   int64_t tiles;
-  int ld_base, ldy, width, rank;
+  int ld_base, ldy, width, rank, col_blocks, rest_parts;
 };
 
-// Tokens without an adapter: y = base, u = 0.
-__device__ __noinline__ void expand_rest(const ExpandParams& p, int64_t block, int cols, uint8_t* smem) {
+// Tokens without an adapter: y = base, u = 0.  A block has 32 tokens and one of `rest_parts`
+// parts of the columns.
+constexpr int kRestTokens = 32;
+__device__ __noinline__ void expand_rest(const ExpandParams& p, int64_t number, uint8_t* smem) {
   int32_t* list = reinterpret_cast<int32_t*>(smem);
-  int* count = list + kThreads;
-  const int64_t t = block * kThreads + threadIdx.x;
-  bool none = false;
-  if (t < p.map.tokens) {
-    const int32_t r = p.map.row_of_slot[t];
-    none = r < 0 || r >= p.map.m_pad;
+  int* count = list + kRestTokens;
+  const int64_t block = number / p.rest_parts;
+  const int part = static_cast<int>(number - block * p.rest_parts);
+  if (threadIdx.x < kRestTokens) {
+    const int64_t t = block * kRestTokens + threadIdx.x;
+    bool none = false;
+    if (t < p.map.tokens) {
+      const int32_t r = p.map.row_of_slot[t];
+      none = r < 0 || r >= p.map.m_pad;
+    }
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, none);
+    if (none) list[__popc(b & ((1u << threadIdx.x) - 1u))] = static_cast<int32_t>(t);
+    if (threadIdx.x == 0) *count = __popc(b);
   }
-  const uint32_t b = __ballot_sync(0xFFFFFFFFu, none);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) count[warp] = __popc(b);
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    before += w < warp ? count[w] : 0;
-    all += count[w];
-  }
-  if (none) list[before + __popc(b & ((1u << lane) - 1u))] = static_cast<int32_t>(t);
-  __syncthreads();
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * cols;
+  const int all = *count, eights = p.width / 8;
   if (p.base != p.y) {
-    const int pieces = cols / 8;
-    for (int e = threadIdx.x; e < all * pieces; e += kThreads) {
-      const int64_t tok = list[e / pieces], c = c0 + (e % pieces) * 8;
-      if (c >= p.width) continue;
-      const uint4 v = p.base != nullptr ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + tok * static_cast<int64_t>(p.ld_base) + c)
-                                        : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + tok * static_cast<int64_t>(p.ldy) + c) = v;
+    // four pieces a thread in flight
+    const int c0 = static_cast<int>(static_cast<int64_t>(eights) * part / p.rest_parts);
+    const int pieces = static_cast<int>(static_cast<int64_t>(eights) * (part + 1) / p.rest_parts) - c0;
+    for (int e0 = threadIdx.x; e0 < all * pieces; e0 += 4 * kThreads) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = e0 + k * kThreads;
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (p.base != nullptr && e < all * pieces)
+          v[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) +
+                                                 list[e / pieces] * static_cast<int64_t>(p.ld_base) + (c0 + e % pieces) * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = e0 + k * kThreads;
+        if (e < all * pieces)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + list[e / pieces] * static_cast<int64_t>(p.ldy) +
+                                    (c0 + e % pieces) * 8) = v[k];
+      }
     }
   }
-  if (p.zero_u != nullptr && blockIdx.y == 0) {
+  if (p.zero_u != nullptr && part == 0) {
     const int pieces = p.rank / 4;
     for (int e = threadIdx.x; e < all * pieces; e += kThreads)
       *reinterpret_cast<float4*>(p.zero_u + static_cast<int64_t>(list[e / pieces]) * p.rank + (e % pieces) * 4) = make_float4(0, 0, 0, 0);
@@ -372,38 +387,25 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
   __shared__ int32_t token[E::kRows];
   let_next_kernel_start();
   wait_for_previous_kernel();
-  if (blockIdx.x >= p.tiles) {
-    expand_rest(p, blockIdx.x - p.tiles, E::kCols, smem_raw);
+  const int64_t number = blockIdx.x / p.col_blocks;
+  const int col_at = static_cast<int>(blockIdx.x - number * p.col_blocks);
+  if (number >= p.tiles) {
+    expand_rest(p, blockIdx.x - p.tiles * p.col_blocks, smem_raw);
     return;
   }
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * E::kRows, col0 = static_cast<int64_t>(blockIdx.y) * E::kCols;
-  const int n = tokens_of<E::kRows>(p.map, row0, token);
+  const int64_t row0 = number * E::kRows, col0 = static_cast<int64_t>(col_at) * E::kCols;
+  const Tile at_rows = tile_at<E::kRows>(p.map, row0, token);
+  const int n = at_rows.n, adapter = at_rows.adapter;
   if (n == 0) return;
-  const int adapter = adapter_of(p.map, row0);
   const int groups = row_groups(n), across = min(kWarps / groups, E::kCols / 64 < kWarps ? E::kCols / 64 : kWarps);
   const int mw = warp % groups, cw = warp / groups;
   const int rank = FULL ? R : p.rank, ranks = FULL ? R : (rank + 15) & ~15;   // whole steps of 16, zeros behind the rank
   const int cols = static_cast<int>(min(int64_t(E::kCols), p.width - col0));
   const int passes = (cols + 64 * across - 1) / (64 * across);
   const uint32_t w_bytes = ranks * 128;                 // of 64 columns
-
-  // W: a thread copies one 16-byte piece of every 32nd row of each 64 columns
-  {
-    const int piece = threadIdx.x & 7, r0 = threadIdx.x >> 3;
-    const uint16_t* w = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * rank + r0) * p.width + col0 + piece * 8;
-    uint32_t to = base + swizzled(r0, piece);
-    for (int c = piece * 8; c - piece * 8 < cols; c += 64, to += w_bytes, w += 64) {
-#pragma unroll
-      for (int i = 0; i < (R + 31) / 32; ++i) {
-        const int k = r0 + 32 * i;
-        if (k < ranks) copy16(to + 4096 * i, w + 32 * i * static_cast<int64_t>(p.width), c < cols && (FULL || k < rank) ? 16 : 0);
-      }
-    }
-  }
-  copies_commit();
 
   // this lane's pieces of the warp's rows, of base and y alike
   const uint16_t* from = static_cast<const uint16_t*>(p.base);
@@ -441,6 +443,21 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
   for (int i = 0; i < 4; ++i) y_at[i] = w_at[i] - base;
 #pragma unroll
   for (int i = 0; i < E::kBuffers; ++i) load(i);
+  // W: a thread copies one 16-byte piece of every 32nd row of each 64 columns
+  {
+    const int piece = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+    const uint16_t* w = static_cast<const uint16_t*>(p.w) + (static_cast<int64_t>(adapter) * rank + r0) * p.width + col0 + piece * 8;
+    uint32_t to = base + swizzled(r0, piece);
+    for (int c = piece * 8; c - piece * 8 < cols; c += 64, to += w_bytes, w += 64) {
+#pragma unroll
+      for (int i = 0; i < (R + 31) / 32; ++i) {
+        const int k = r0 + 32 * i;
+        if (k < ranks) copy16(to + 4096 * i, w + 32 * i * static_cast<int64_t>(p.width), c < cols && (FULL || k < rank) ? 16 : 0);
+      }
+    }
+  }
+  copies_commit();
+
 
   // this warp's rows of u, as the products take them
   constexpr int kTerms = 2;
@@ -474,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
       for (int k = 0; k < kTerms; ++k) a[k][i / 2][2 * (i & 1) + h] = term[k];
     }
   }
-  copies_wait<E::kBuffers>();
+  copies_wait<0>();
   __syncthreads();                                     // W is there
 
   for (int pass = 0; pass < passes; ++pass) {
@@ -586,8 +603,13 @@ __device__ __forceinline__ int64_t adapter_begin(const OuterParams& p, int i) {
   return i > 0 ? max(int64_t(0), min(static_cast<int64_t>(p.map.offsets[i - 1]), p.map.m_pad)) : 0;
 }
 // The segment with this number (wanted >= 0), or those of an adapter (index 0).  All
-// threads call it: four adapters each, their counts summed over the block.
+// threads call it: four adapters each, their counts summed over the block.  Where no adapter
+// can have two (slots = 0), the number is the adapter's.
 __device__ __forceinline__ Segment find_segment(const OuterParams& p, int64_t wanted, int of_adapter) {
+  if (p.slots == 0) {
+    const int i = static_cast<int>(wanted);
+    return {i, 0, adapter_end(p, i) > adapter_begin(p, i) ? 1 : 0, 0};
+  }
   __shared__ int sums[2][kWarps];
   __shared__ Segment found;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -703,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
   const Segment seg = find_segment(p, number, 0);
   // more sums than there is room for come of no map that the sort writes
   if (seg.adapter < 0 || (seg.count > 1 && seg.slot + seg.index >= p.slots)) return;
+  // (without tokens, which only a numbering by adapters asks for, the sums are zeros)
   const int64_t row0 = adapter_begin(p, seg.adapter) + static_cast<int64_t>(seg.index) * p.segment;
   const int64_t row1 = min(row0 + p.segment, adapter_end(p, seg.adapter));
   const int chunks = static_cast<int>((row1 - row0 + O::kTokens - 1) / O::kTokens);
@@ -811,9 +834,9 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
   copies_wait<0>();
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
-  const bool alone = seg.count == 1;
-  const float f = (alone && side.scales != nullptr ? side.scales[seg.adapter] : 1.0f),
-              back = KIND == OK_F16 ? 1.0f / side.units[number] : 1.0f;
+  const bool alone = seg.count <= 1;
+  const float f = alone && chunks > 0 && side.scales != nullptr ? side.scales[seg.adapter] : 1.0f,
+              back = KIND == OK_F16 && chunks > 0 ? 1.0f / side.units[number] : 1.0f;
 #pragma unroll
   for (int m = 0; m < R / 16; ++m) {
     if (!FULL && m * 16 >= rank) break;
@@ -927,14 +950,19 @@ bsgg_status launch_shrink(int format, ShrinkParams p, cudaStream_t s) {
 
 bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
   p.tiles = p.map.m_pad / 128;
-  const int64_t blocks = p.tiles + ceil_div(p.map.tokens, kThreads);
+  const int64_t rest = ceil_div(p.map.tokens, kRestTokens);
   return with_half(format, [&](auto kind) {
     return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
       constexpr bool E = decltype(full)::value;
       if (!allowed<expand_kernel<K, R, E>>(Expand<R>::kSmem)) return BSGG_ERR_CUDA;
-      const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ceil_div(p.width, Expand<R>::kCols)));
-      const LaunchConfig c(grid, kThreads, Expand<R>::kSmem, s);
+      p.col_blocks = static_cast<int>(ceil_div(p.width, Expand<R>::kCols));
+      // two blocks an SM for the tokens without an adapter, whose number only the map knows
+      const int64_t parts = ceil_div(304, rest);
+      p.rest_parts = static_cast<int>(parts < p.col_blocks ? parts : p.col_blocks);
+      const int64_t grid = p.tiles * p.col_blocks + rest * p.rest_parts;
+      if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
+      const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, Expand<R>::kSmem, s);
       return launch_kernel(c, expand_kernel<K, R, E>, p);
     });
   });
@@ -954,8 +982,9 @@ int64_t outer_slots(int64_t tokens, int64_t k, int64_t n) {
   return tokens > rows ? 2 * ceil_div(tokens, rows) : 0;
 }
 
-// Blocks' worth of segments of a map.
+// Segments of a map, at the most; where a segment holds all tokens, one for each adapter.
 int64_t outer_segments(int64_t tokens, int64_t m_pad, int64_t adapters, int64_t rows) {
+  if (tokens <= rows) return adapters;
   // an adapter's rows are its tokens rounded up to 128
   const int64_t used = tokens < adapters ? tokens : adapters, all = tokens + 128 * used;
   return used + (all < m_pad ? all : m_pad) / rows;
@@ -1002,7 +1031,7 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
         if (st != BSGG_OK) return st;
         const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, kSmem, s);
         st = launch_kernel(c, outer_kernel<K, R, N, E>, p);
-        if (st != BSGG_OK) return st;
+        if (st != BSGG_OK || p.slots == 0) return st;
         // two rounds of blocks over all adapters
         const int64_t each = 2432 / p.map.adapters < 1 ? 1 : 2432 / p.map.adapters;
         const LaunchConfig j(dim3(static_cast<unsigned>(most < each ? most : each), static_cast<unsigned>(p.map.adapters)), kThreads, 0, s);
