@@ -162,8 +162,8 @@ struct ShrinkParams {
   int depth, rank, split;
 };
 
-template <int KIND, int R, bool FULL>
-__global__ void __launch_bounds__(kThreads, R <= 32 ? 3 : R == 64 ? 2 : 1) shrink_kernel(const __grid_constant__ ShrinkParams p) {
+template <int KIND, int R, bool FULL, bool RUNS>
+__global__ void __launch_bounds__(kThreads, R <= 32 ? 3 : R == 64 || !RUNS ? 2 : 1) shrink_kernel(const __grid_constant__ ShrinkParams p) {
   using S = Shrink<R>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int32_t token[S::kRows];
@@ -218,13 +218,13 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 3 : R == 64 ? 2 : 1) shrin
   };
   const int ar = mw * 16 + (lane & 15), br = (lane & 7) + ((lane >> 4) << 3);
 
-  float acc[R / 8][4], sum[R / 8][4];
+  float acc[R / 8][4], sum[RUNS ? R / 8 : 1][4];
 #pragma unroll
-  for (int i = 0; i < R / 8; ++i)
+  for (int i = 0; i < (RUNS ? R / 8 : 1); ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum[i][k] = 0.0f;
   for (int s = 0; s < S::kStages - 1; ++s) load(s);
-  const int run = kRun / 64 * shares / blocks;          // stages until a warp has summed kRun products
+  const int run = RUNS ? kRun / 64 * shares / blocks : steps;   // stages until a warp has summed kRun products
   for (int s0 = 0; s0 < steps; s0 += run) {
 #pragma unroll
     for (int i = 0; i < R / 8; ++i)
@@ -255,10 +255,12 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 3 : R == 64 ? 2 : 1) shrin
         }
       }
     }
+    if (RUNS) {
 #pragma unroll
-    for (int i = 0; i < R / 8; ++i)
+      for (int i = 0; i < R / 8; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum[i][k] += acc[i][k];
+        for (int k = 0; k < 4; ++k) acc[i][k] = sum[RUNS ? i : 0][k] += acc[i][k];
+    }
   }
   copies_wait<0>();
   __syncthreads();
@@ -270,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 3 : R == 64 ? 2 : 1) shrin
 #pragma unroll
     for (int i = 0; i < R / 8; ++i) {
       if (i * 8 >= rank) break;
-      *reinterpret_cast<float2*>(at + i * 8) = make_float2(sum[i][0], sum[i][1]);
-      *reinterpret_cast<float2*>(at + 8 * rank + i * 8) = make_float2(sum[i][2], sum[i][3]);
+      *reinterpret_cast<float2*>(at + i * 8) = make_float2(acc[i][0], acc[i][1]);
+      *reinterpret_cast<float2*>(at + 8 * rank + i * 8) = make_float2(acc[i][2], acc[i][3]);
     }
   }
   __syncthreads();
@@ -326,7 +328,7 @@ struct ExpandParams {
   void* y;
   float* zero_u;              // u's rows of tokens without an adapter, where wanted
   int64_t tiles;
-  int ld_base, ldy, width, rank, col_blocks, rest_parts;
+  int ld_base, ldy, width, rank, cols, col_blocks, rest_parts;   // cols: of a block, a multiple of 64
 };
 
 // Tokens without an adapter: y = base, u = 0.  A block has 32 tokens and one of `rest_parts`
@@ -396,14 +398,14 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row0 = number * E::kRows, col0 = static_cast<int64_t>(col_at) * E::kCols;
+  const int64_t row0 = number * E::kRows, col0 = static_cast<int64_t>(col_at) * p.cols;
   const Tile at_rows = tile_at<E::kRows>(p.map, row0, token);
   const int n = at_rows.n, adapter = at_rows.adapter;
   if (n == 0) return;
-  const int groups = row_groups(n), across = min(kWarps / groups, E::kCols / 64 < kWarps ? E::kCols / 64 : kWarps);
+  const int groups = row_groups(n), across = min(kWarps / groups, p.cols / 64);
   const int mw = warp % groups, cw = warp / groups;
   const int rank = FULL ? R : p.rank, ranks = FULL ? R : (rank + 15) & ~15;   // whole steps of 16, zeros behind the rank
-  const int cols = static_cast<int>(min(int64_t(E::kCols), p.width - col0));
+  const int cols = static_cast<int>(min(int64_t(p.cols), p.width - col0));
   const int passes = (cols + 64 * across - 1) / (64 * across);
   const uint32_t w_bytes = ranks * 128;                 // of 64 columns
 
@@ -941,9 +943,20 @@ bsgg_status launch_shrink(int format, ShrinkParams p, cudaStream_t s) {
     return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
       constexpr bool E = decltype(full)::value;
-      if (!allowed<shrink_kernel<K, R, E>>(Shrink<R>::kSmem)) return BSGG_ERR_CUDA;
-      const LaunchConfig c(dim3(static_cast<unsigned>(tiles * p.split)), kThreads, Shrink<R>::kSmem, s, p.split);
-      return launch_kernel(c, shrink_kernel<K, R, E>, p);
+      auto launch = [&](auto runs) {
+        constexpr bool N = decltype(runs)::value;
+        if (!allowed<shrink_kernel<K, R, E, N>>(Shrink<R>::kSmem)) return BSGG_ERR_CUDA;
+        const LaunchConfig c(dim3(static_cast<unsigned>(tiles * p.split)), kThreads, Shrink<R>::kSmem, s, p.split);
+        return launch_kernel(c, shrink_kernel<K, R, E, N>, p);
+      };
+      // two warps at least share a part: of up to 1024 each sums a run.  At a rank of 128 the
+      // registers for more leave room for one block on an SM: 3362 tokens, 1952 wide, rank 88,
+      // take 46 us with their expand and 32 without; 904 tokens, 7152 wide, whose blocks have
+      // an SM each anyway, 30 with and 37 without
+      if constexpr (R == 128) {
+        if (ceil_div(nb, p.split) * 64 <= 2 * kRun && busy * p.split > 228) return launch(std::false_type());
+      }
+      return launch(std::true_type());
     });
   });
 }
@@ -956,9 +969,15 @@ bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
       constexpr bool E = decltype(full)::value;
       if (!allowed<expand_kernel<K, R, E>>(Expand<R>::kSmem)) return BSGG_ERR_CUDA;
-      p.col_blocks = static_cast<int>(ceil_div(p.width, Expand<R>::kCols));
-      // two blocks an SM for the tokens without an adapter, whose number only the map knows
-      const int64_t parts = ceil_div(304, rest);
+      // the fewer tiles hold tokens, the fewer columns a block takes, down to a warp's 64: 109
+      // tokens of 13 adapters, 3688 wide, took 14 us in blocks of 1024 columns
+      const int64_t each = ceil_div(p.width, ceil_div(304, busy_tiles(p.map, Expand<R>::kRows)));
+      p.cols = static_cast<int>(ceil_div(each, 64) * 64);
+      if (p.cols > Expand<R>::kCols) p.cols = Expand<R>::kCols;
+      p.col_blocks = static_cast<int>(ceil_div(p.width, p.cols));
+      // six blocks an SM for the tokens without an adapter, whose number only the map knows (4096
+      // tokens, 14336 wide, a fifth of them without: 91 us with two, 79 with six, 81 with sixteen)
+      const int64_t parts = ceil_div(912, rest);
       p.rest_parts = static_cast<int>(parts < p.col_blocks ? parts : p.col_blocks);
       const int64_t grid = p.tiles * p.col_blocks + rest * p.rest_parts;
       if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
