@@ -6,10 +6,12 @@
 //   shrink  u[t]  = f_i X[t] W_i^T        forward u = x A^T; backward du = s dy B^T
 //   expand  Y[t]  = base[t] + f_i u[t] W_i  forward y (B); backward dx (A)
 //   outer   dW_i  = f_i sum_t g[t]^T X[t]   dA from du and x, dB from u and dy
-// Each reads its wide operand once, 2 rank products per value of two bytes: at a rank of 64
-// and the memory's rate that is 435 TFLOP/s, which mma.sync delivers, so memory bounds
-// them and the tensor cores' large tiles (128 rows of one adapter, whatever the batch
-// holds) would only be padding.
+// Each reads its wide operand once, 2 rank products per value of two bytes: 435 TFLOP/s at a
+// rank of 64 and the memory's rate.  That is within mma.sync's 620 (1024 products a cycle
+// and SM), whose tiles of 16 x 8 fit what a batch holds, from one token of an adapter up,
+// where tcgen05's are 128 rows.  What they cost was looked at: expand of 4096 tokens, rank
+// 64, 4096 to 14336, takes as long with half of its products left out, and 11 us less of 87
+// without any.
 #include <atomic>
 
 #include "bsgg_ops.cuh"
@@ -141,6 +143,10 @@ __device__ __forceinline__ int row_groups(int n) { return n <= 16 ? 1 : n <= 32 
 // cluster's blocks join through distributed shared memory, in order.  Its warps are as
 // many groups of 16 rows as there are tokens, and share the reduction's steps of 16 beyond
 // that: a decoding batch has a token or two per adapter, and is then a stream of A.
+//   4096 tokens, rank 64, from 4096: 19 us for 34 MB of x, 1.8 TB/s; rank 32, from 14336: 31 us
+//   for 117 MB, 3.8 TB/s: bound by the chain from stage to stage (barrier, matrix loads,
+//   products) and the cluster's join; with one block of 64 of the reduction between barriers
+//   35.  128 tokens of 64 adapters, rank 16, from 4096: 11 us alone, 7.3 MB of A.
 template <int R>
 struct Shrink {
   static constexpr int kRows = 64, kStages = R == 128 ? 4 : 3;
@@ -311,6 +317,12 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 3 : R == 64 || !RUNS ? 2 :
 // multiplies, and stores rows of 128 bytes.  Eight groups of 16 rows are eight warps that
 // walk the same columns; with fewer tokens the warps lie along the columns too.  The blocks
 // behind the tiles see to the tokens without an adapter.
+//   4096 tokens, rank 64, to 14336: 57 us for 235 MB, 4.1 TB/s: shared memory is busy 60 % of
+//   the time (every warp reads all of W for its 16 rows) and the matrix pipe 45 %; rank 32, to
+//   4096: 19 us for 67 MB with the dx of a fifth of the tokens copied.  128 tokens of 64
+//   adapters, rank 16, to 14336: 15 us for 36 MB (in blocks of 512 columns 22).  Base and W of
+//   128 rows in passes behind a barrier each: 76 us; neighbouring blocks on other rows of the
+//   same columns: 7 more.
 template <int R>
 struct Expand {
   static constexpr int kRows = 128, kCols = R == 16 ? 1024 : R == 128 ? 256 : 512, kBuffers = 2;
@@ -460,7 +472,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
   }
   copies_commit();
 
-
   // this warp's rows of u, as the products take them
   constexpr int kTerms = 2;
   uint32_t a[kTerms][R / 16][4];
@@ -561,6 +572,10 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
 // out) and kCols columns of x or dy.  An adapter of one segment is finished there; the
 // segments' sums of the others meet in another launch, in order.  The products are
 // (rank x 64 tokens) (64 tokens x columns), both read across their rows.
+//   4096 tokens of 4 adapters, rank 32, 4096 and 14336: 54 us for 151 MB, 2.8 TB/s, after 7 us
+//   of terms and before 10 of join (both less behind one another): shared memory is busy half
+//   of the time, the matrix pipe as long, in turns.  With the reduction split over clusters
+//   by adapter, whose shares are unlike, the two took 65 and 37 us.
 template <int R, int TERMS>
 struct Outer {
   static constexpr int kCols = R == 128 ? 128 : 256, kTokens = 64, kStages = R <= 32 ? 2 : 3;
@@ -587,7 +602,7 @@ struct OuterParams {
   AdapterMap map;
   const int32_t* rows_used;       // where the last adapter's rows end
   OuterSide side[2];
-  int rank, segment, slots, out_kind;
+  int rank, segment, term_rows, slots, out_kind;
 };
 
 // Where an adapter's segments are.
@@ -660,8 +675,8 @@ __global__ void __launch_bounds__(kThreads) outer_terms_kernel(const __grid_cons
   let_next_kernel_start();
   wait_for_previous_kernel();
   const OuterSide& side = p.side[blockIdx.y];
-  // a block takes 64 rows; the segment's power of two it finds by itself
-  const int chunks = p.segment / 64;
+  // a block takes term_rows rows (a multiple of 64); the segment's power of two it finds by itself
+  const int chunks = p.segment / p.term_rows;
   const int64_t number = blockIdx.x / chunks;
   const int chunk = static_cast<int>(blockIdx.x - number * chunks);
   const Segment seg = find_segment(p, number, 0);
@@ -688,9 +703,10 @@ __global__ void __launch_bounds__(kThreads) outer_terms_kernel(const __grid_cons
     if (threadIdx.x == 0) side.units[number] = unit;             // the same from each of them
   }
   const int ranks = (p.rank + 15) & ~15, all = ranks / 4;
-  const int64_t from = row0 + chunk * 64;
+  const int64_t from = row0 + static_cast<int64_t>(chunk) * p.term_rows;
   if (from >= row1) return;
-  for (int e = threadIdx.x; e < 64 * all; e += kThreads) {
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.term_rows), (row1 - from + 63) / 64 * 64));
+  for (int e = threadIdx.x; e < rows * all; e += kThreads) {
     const int i = e / all, q = e - i * all;
     const int64_t r = from + i;
     if (r >= p.map.m_pad) break;
@@ -1039,13 +1055,15 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
         side.blocks = side.out != nullptr ? static_cast<int>(ceil_div(side.width, Outer<R, 2>::kCols)) : 0;
         most += side.out != nullptr ? ceil_div(int64_t(p.rank) * side.width, 8 * kThreads) : 0;
       }
+      // float16's blocks each go through their whole segment first: at most eight of them
+      p.term_rows = K == OK_F16 && p.segment > 512 ? p.segment / 8 : 64;
       const int64_t segments = outer_segments(p.map.tokens, p.map.m_pad, p.map.adapters, p.segment), grid = segments * (p.side[0].blocks + p.side[1].blocks);
       if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
       auto launch = [&](auto terms) {
         constexpr int N = decltype(terms)::value;
         constexpr int kSmem = Outer<R, N>::kSmem;
         if (!allowed<outer_kernel<K, R, N, E>>(kSmem)) return BSGG_ERR_CUDA;
-        const LaunchConfig t(dim3(static_cast<unsigned>(segments * (p.segment / 64)), 2), kThreads, 0, s);
+        const LaunchConfig t(dim3(static_cast<unsigned>(segments * (p.segment / p.term_rows)), 2), kThreads, 0, s);
         bsgg_status st = launch_kernel(t, outer_terms_kernel<K, N>, p);
         if (st != BSGG_OK) return st;
         const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, kSmem, s);

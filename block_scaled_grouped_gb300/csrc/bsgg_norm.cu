@@ -64,6 +64,11 @@ __device__ __forceinline__ void store8_as(int kind, void* base, int64_t i, const
 // first load to the last store, so that every tensor is passed over once.  FMT: the
 // quantized rows' format, BSGG_IN_BF16 for none.  The blocks past the tokens write A's
 // padding rows.
+//   8192 x 7168 bfloat16 with a residual, into h, y and E4M3 rows: 530 MB in 89 to 91 us, 5.8
+//     TB/s, 85 % of the copy rate, bound by the loads' latency and the mix of three writes to
+//     two reads (marked as read once 97 us; six blocks an SM with 40 registers 100);
+//   128 x 7168: 4.7 us, 333 x 4104 float16: 4.9, of which the launch and two trips to memory
+//     are most.
 template <int KIND, int FMT, int NV, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : kNormMaxThreads)
     rms_norm_kernel(const __grid_constant__ NormParams p) {
@@ -215,7 +220,10 @@ struct NormRow {
 // A block (or each of its warps) walks rows, gridDim apart, its threads holding the
 // same columns of each, so that the weight's gradient stays in registers until the
 // block's rows are done; the blocks' sums meet in a second launch, in order.  The next
-// row is on its way while this one is reduced and written (AHEAD: where registers hold two).
+// row is on its way while this one is reduced and written (where registers hold two).
+//   8192 x 4096 bfloat16 with dh: 268 MB in 47 to 51 us with that launch, 5.3 TB/s, bound by
+//     the loads' latency (without the next row ahead 71, with its loads after the first half
+//     of the row's arithmetic 56).
 template <int KIND, int YKIND, int NV, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : NV <= 2 ? 256 : kNormMaxThreads, WARP ? 1 : NV <= 2 ? 2 : 1)
     rms_norm_backward_kernel(const __grid_constant__ NormBwdParams p) {
@@ -342,7 +350,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : NV <= 2 ? 256 : kN
 }
 
 // dweight[c] = the sum of the blocks' parts: 32 columns a block, 32 warps that take
-// every 32nd part, joined in order.
+// every 32nd part, joined in order: a chain of ten loads (304 parts of 4096: 6 us alone; eight
+// warps 8).
 constexpr int kNormJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kNormJoinWarps) norm_join_kernel(const float* part, int64_t parts, int hidden, float* dweight) {
   __shared__ float sums[kNormJoinWarps][32];
@@ -366,25 +375,29 @@ __global__ void __launch_bounds__(32 * kNormJoinWarps) norm_join_kernel(const fl
 
 // ---------------------------------------------------------------- host
 constexpr int64_t kNormMaxHidden = 32768;
-// Blocks of the gradient: two on each of the 152 SMs, of rows that are a warp's eight.
-constexpr int64_t kNormBwdBlocks = 304, kNormBwdWarpBlocks = 1216;
+// Blocks of the gradient: two on each of the 152 SMs, or as many of fewer threads as make
+// 512 there.
+constexpr int64_t kNormBwdBlocks = 304, kNormBwdThreads = 512 * 152;
 
-// How rows of `cols` columns lie: a warp each with one or two runs of 16 a lane, or a
-// block each with the fewest runs that 256 threads (512 at the most) hold.
+// How rows of `cols` columns lie: a warp each up to 512, a run of 16 a lane (16384 rows of
+// 512, forward 18 us and back 23; in blocks 22 and 62); wider ones a block each, with the
+// fewest runs a thread that 256 threads (512 at the most) hold: 16384 rows of 1024 take 29
+// and 33 us so, in warps of two runs 31 and 39; 8192 of 7168, forward, 91 us in two runs and
+// 96 in one of 512 threads.
 struct RowShape {
   bool warp;
   int values, threads;
 };
 RowShape row_shape(int64_t cols) {
   const int64_t runs = ceil_div(cols, kNormValues);
-  if (runs <= 64) return {true, runs <= 32 ? 1 : 2, 32 * kNormWarpRows};
+  if (runs <= 32) return {true, 1, 32 * kNormWarpRows};
   const int nv = runs <= 256 ? 1 : runs <= 512 ? 2 : 4;
   return {false, nv, static_cast<int>(ceil_div(ceil_div(runs, nv), 32) * 32)};
 }
 template <typename F>
 bsgg_status with_shape(const RowShape& s, F&& f) {
   using std::integral_constant;
-  if (s.warp) return s.values == 1 ? f(integral_constant<int, 1>(), std::true_type()) : f(integral_constant<int, 2>(), std::true_type());
+  if (s.warp) return f(integral_constant<int, 1>(), std::true_type());
   if (s.values == 1) return f(integral_constant<int, 1>(), std::false_type());
   if (s.values == 2) return f(integral_constant<int, 2>(), std::false_type());
   return f(integral_constant<int, 4>(), std::false_type());
@@ -415,8 +428,9 @@ bsgg_status with_quantized(int fmt, F&& f) {
 }
 
 int64_t norm_bwd_blocks(int64_t tokens, int64_t hidden) {
-  const bool warp = row_shape(hidden).warp;
-  const int64_t rows = warp ? ceil_div(tokens, kNormWarpRows) : tokens, most = warp ? kNormBwdWarpBlocks : kNormBwdBlocks;
+  const RowShape shape = row_shape(hidden);
+  const int64_t rows = shape.warp ? ceil_div(tokens, kNormWarpRows) : tokens;
+  const int64_t most = kNormBwdThreads / shape.threads > kNormBwdBlocks ? kNormBwdThreads / shape.threads : kNormBwdBlocks;
   return rows < most ? rows : most;
 }
 
