@@ -576,9 +576,10 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
 //   of terms and before 10 of join (both less behind one another): shared memory is busy half
 //   of the time, the matrix pipe as long, in turns.  With the reduction split over clusters
 //   by adapter, whose shares are unlike, the two took 65 and 37 us.
-template <int R, int TERMS>
+template <int R, int TERMS, bool RUNS>
 struct Outer {
-  static constexpr int kCols = R == 128 ? 128 : 256, kTokens = 64, kStages = R <= 32 ? 2 : 3;
+  // the room that a single run leaves goes to a second block on an SM
+  static constexpr int kCols = R == 128 ? 128 : 256, kTokens = 64, kStages = R > 32 && RUNS ? 3 : 2;
   static constexpr int kTermPitch = 2 * R + 16;         // bytes of a token's ranks: eight rows in different banks
   static constexpr int kXBytes = kTokens * kCols * 2, kTermBytes = kTokens * kTermPitch;
   static constexpr int kStageBytes = kXBytes + TERMS * kTermBytes;
@@ -722,9 +723,9 @@ __global__ void __launch_bounds__(kThreads) outer_terms_kernel(const __grid_cons
   }
 }
 
-template <int KIND, int R, int TERMS, bool FULL>
-__global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const __grid_constant__ OuterParams p) {
-  using O = Outer<R, TERMS>;
+template <int KIND, int R, int TERMS, bool FULL, bool RUNS>
+__global__ void __launch_bounds__(kThreads, R <= 32 || !RUNS ? 2 : 1) outer_kernel(const __grid_constant__ OuterParams p) {
+  using O = Outer<R, TERMS, RUNS>;
   constexpr int kTiles = O::kCols / 8 / kWarps;         // of 8 columns, a warp
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int32_t token[O::kStages + 1][O::kTokens];
@@ -786,27 +787,30 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
     copies_commit();
   };
 
-  float acc[R / 16][kTiles][4], sum[R / 16][kTiles][4];
+  float acc[R / 16][kTiles][4], sum[RUNS ? R / 16 : 1][kTiles][4];
 #pragma unroll
   for (int m = 0; m < R / 16; ++m)
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum[m][i][k] = 0.0f;
+      for (int k = 0; k < 4; ++k) acc[m][i][k] = sum[RUNS ? m : 0][i][k] = 0.0f;
   for (int c = 0; c < O::kStages - 1; ++c)
     if (threadIdx.x < O::kTokens) token[c][threadIdx.x] = token_of(c, threadIdx.x);
   __syncthreads();
   for (int c = 0; c < O::kStages - 1; ++c) load(c);
   // a chunk's tokens are fetched two rounds before their rows are
   int32_t next = threadIdx.x < O::kTokens ? token_of(O::kStages - 1, threadIdx.x) : -1;
-  for (int c0 = 0; c0 < chunks; c0 += kRun / O::kTokens) {
+  const int run = RUNS ? kRun / O::kTokens : chunks;
+  for (int c0 = 0; c0 < chunks; c0 += run) {
+    if (RUNS) {
 #pragma unroll
-    for (int m = 0; m < R / 16; ++m)
+      for (int m = 0; m < R / 16; ++m)
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
+        for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[m][i][k] = 0.0f;
-    const int c1 = min(c0 + kRun / O::kTokens, chunks);
+          for (int k = 0; k < 4; ++k) acc[m][i][k] = 0.0f;
+    }
+    const int c1 = min(c0 + run, chunks);
     for (int c = c0; c < c1; ++c) {
       const int ahead = c + O::kStages - 1;
       copies_wait<O::kStages - 2>();
@@ -842,12 +846,14 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
         }
       }
     }
+    if (RUNS) {
 #pragma unroll
-    for (int m = 0; m < R / 16; ++m)
+      for (int m = 0; m < R / 16; ++m)
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
+        for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum[m][i][k] += acc[m][i][k];
+          for (int k = 0; k < 4; ++k) acc[m][i][k] = sum[RUNS ? m : 0][i][k] += acc[m][i][k];
+    }
   }
   copies_wait<0>();
   __syncthreads();
@@ -861,8 +867,8 @@ __global__ void __launch_bounds__(kThreads, R <= 32 ? 2 : 1) outer_kernel(const 
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       float* at = sums + (m * 16 + (lane >> 2)) * O::kCols + (warp * kTiles + i) * 8 + 2 * (lane & 3);
-      *reinterpret_cast<float2*>(at) = make_float2(sum[m][i][0] * back * f, sum[m][i][1] * back * f);
-      *reinterpret_cast<float2*>(at + 8 * O::kCols) = make_float2(sum[m][i][2] * back * f, sum[m][i][3] * back * f);
+      *reinterpret_cast<float2*>(at) = make_float2(acc[m][i][0] * back * f, acc[m][i][1] * back * f);
+      *reinterpret_cast<float2*>(at + 8 * O::kCols) = make_float2(acc[m][i][2] * back * f, acc[m][i][3] * back * f);
     }
   }
   __syncthreads();
@@ -1052,32 +1058,39 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
       constexpr bool E = decltype(full)::value;
       int64_t most = 0;
       for (OuterSide& side : p.side) {
-        side.blocks = side.out != nullptr ? static_cast<int>(ceil_div(side.width, Outer<R, 2>::kCols)) : 0;
+        side.blocks = side.out != nullptr ? static_cast<int>(ceil_div(side.width, Outer<R, 2, true>::kCols)) : 0;
         most += side.out != nullptr ? ceil_div(int64_t(p.rank) * side.width, 8 * kThreads) : 0;
       }
       // float16's blocks each go through their whole segment first: at most eight of them
       p.term_rows = K == OK_F16 && p.segment > 512 ? p.segment / 8 : 64;
       const int64_t segments = outer_segments(p.map.tokens, p.map.m_pad, p.map.adapters, p.segment), grid = segments * (p.side[0].blocks + p.side[1].blocks);
       if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
-      auto launch = [&](auto terms) {
+      auto launch = [&](auto terms, auto runs) {
         constexpr int N = decltype(terms)::value;
-        constexpr int kSmem = Outer<R, N>::kSmem;
-        if (!allowed<outer_kernel<K, R, N, E>>(kSmem)) return BSGG_ERR_CUDA;
+        constexpr bool U = decltype(runs)::value;
+        constexpr int kSmem = Outer<R, N, U>::kSmem;
+        if (!allowed<outer_kernel<K, R, N, E, U>>(kSmem)) return BSGG_ERR_CUDA;
         const LaunchConfig t(dim3(static_cast<unsigned>(segments * (p.segment / p.term_rows)), 2), kThreads, 0, s);
         bsgg_status st = launch_kernel(t, outer_terms_kernel<K, N>, p);
         if (st != BSGG_OK) return st;
         const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, kSmem, s);
-        st = launch_kernel(c, outer_kernel<K, R, N, E>, p);
+        st = launch_kernel(c, outer_kernel<K, R, N, E, U>, p);
         if (st != BSGG_OK || p.slots == 0) return st;
         // two rounds of blocks over all adapters
         const int64_t each = 2432 / p.map.adapters < 1 ? 1 : 2432 / p.map.adapters;
         const LaunchConfig j(dim3(static_cast<unsigned>(most < each ? most : each), static_cast<unsigned>(p.map.adapters)), kThreads, 0, s);
         return launch_kernel(j, outer_join_kernel, p);
       };
-      if constexpr (K == OK_BF16) {
-        if (p.out_kind == OK_F32) return launch(std::integral_constant<int, 3>());
+      // What is rounded to 16 bits is summed whole at ranks over 32, up to 32768 rows (3.3e-5 of
+      // the sum): without registers for runs two blocks fit an SM (4096 tokens, rank 64, all of
+      // the gradient 150 us for 167, rank 128 284 for 320; at ranks 16 and 32 no change)
+      if (R > 32 && p.out_kind != OK_F32 && p.segment <= 32768) {
+        if constexpr (R > 32) return launch(std::integral_constant<int, 2>(), std::false_type());
       }
-      return launch(std::integral_constant<int, 2>());
+      if constexpr (K == OK_BF16) {
+        if (p.out_kind == OK_F32) return launch(std::integral_constant<int, 3>(), std::true_type());
+      }
+      return launch(std::integral_constant<int, 2>(), std::true_type());
     });
   });
 }
