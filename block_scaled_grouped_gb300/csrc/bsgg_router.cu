@@ -117,6 +117,30 @@ __device__ __noinline__ uint64_t group64(const RouterParams& p, Row r, uint64_t 
   return p.group_top == 1 || b == 0 ? a : key64(value(a) + value(b));
 }
 
+// Whether the experts in `open` (bits of this lane's, of the groups in doubt) all have one
+// logit and one bias, and each such group two of them: then the groups are equal.  A router
+// that starts from zeros has such rows.  Called by all lanes of the warp.
+__device__ __noinline__ bool all_alike(const RouterParams& p, Row r, uint64_t open) {
+  int count = __popcll(open);
+  for (int o = 1; o < p.per; o <<= 1) count += __shfl_xor_sync(kAll, count, o);
+  uint32_t low[2] = {kAll, kAll}, high[2] = {0, 0};
+  const bool some = open != 0;
+#pragma unroll 1
+  while (open != 0) {
+    const int i = __ffsll(static_cast<long long>(open)) - 1;
+    open &= open - 1;
+    const uint32_t k[2] = {logit_key(row_logit(p, r, i)), logit_key(p.bias[r.first + p.per * i])};
+    for (int j = 0; j < 2; ++j) { low[j] = min(low[j], k[j]); high[j] = max(high[j], k[j]); }
+  }
+  __syncwarp();
+  bool alike = !__any_sync(kAll, some && count < 2);
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t least = __reduce_min_sync(kAll, low[j]), most = __reduce_max_sync(kAll, high[j]);
+    alike = alike && least == most;
+  }
+  return alike;
+}
+
 // Of the experts in `near` (bits of this lane's) the best by c in 64 bits: its index in
 // the lane that has it, kAll in the others.  Called by all lanes of the warp.
 __device__ __noinline__ uint32_t expert64(const RouterParams& p, Row r, uint64_t near) {
@@ -177,7 +201,8 @@ __device__ __forceinline__ void set_key(uint32_t (&key)[NI], const Row& row, int
 // that near are compared in 64 bits.  Equal logits under equal biases are equal, and
 // need none of it.  Groups likewise, but there only the last one kept has to lead.
 //   8192 x 256 bfloat16, top-8 of the best 4 of 8 groups, sigmoid and bias: 20 us (4.2 MB: 0.6
-//   of them the bytes'); 16384 x 128 float32, top-4 of 3 of 8: 17; 128 x 64 top-8: 4.2.  Bound by
+//   of them the bytes'; the plain softmax router 12.5); 16384 x 128 float32, top-4 of 3 of 8: 21; 128
+//   x 64 top-8: 4.2.  8192 x 256 whose every row is in doubt to the last choice: 1150.  Bound by
 //   issue (58 to 67 % of the slots; 1350 instructions a token of 256 experts, half of them the
 //   rounds).  With the near ones looked for in every round 25 and 23 us.
 template <int NI>
@@ -272,11 +297,13 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_groups_kernel(const _
       // have few bits
       const bool same = !biased && a == last_a && b == last_b;
       const bool left_out = __any_sync(kAll, near && g != 0), unlike = __any_sync(kAll, near && !same);
-      if (left_out && unlike) {
-        // all of the groups in 64 bits, from the experts that may be their best two
-        const float least = b > kMaskedKey ? key_logit(b) : -INFINITY;
-        const float under = least - (2.0f * off + 0x1p-21f * fabsf(least));
-        const uint64_t open = keys_from(key, biased && b != kAll ? logit_key(under) : biased ? 0u : p.group_top == 2 ? b : a);
+      // the experts that may be a group's best two
+      const float least = b > kMaskedKey ? key_logit(b) : -INFINITY;
+      const float under = least - (2.0f * off + 0x1p-21f * fabsf(least));
+      const bool doubt = left_out && unlike;
+      const uint64_t open = doubt ? keys_from(key, biased && b != kAll ? logit_key(under) : biased ? 0u : p.group_top == 2 ? b : a) : 0;
+      if (doubt && !(biased && all_alike(p, row, near ? open : 0))) {
+        // all of the groups in 64 bits
         uint64_t k = group64(p, row, g0 != 0 ? open : 0);
         if (g0 == 0) k = 0;
         kept = false;

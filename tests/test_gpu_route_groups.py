@@ -180,6 +180,20 @@ def test_ties_of_logits_of_few_bits(score, dtype):
             assert torch.equal(ids.cpu(), want), (groups, top)
 
 
+def test_a_router_of_zeros():
+    """Logits and biases that are all the same: the first groups, the first experts; and groups
+    of which some have a single expert left."""
+    l = torch.zeros(40, 32)
+    l[10:20, 1:8] = -math.inf
+    l[20:30, ::2] = -math.inf
+    for bias in (torch.zeros(32), torch.full((32,), 0.3)):
+        for top in (1, 2):
+            where = dict(groups=8, topk_groups=3, group_top=top)
+            want, _ = R.route_groups(l, 6, bias=bias, **where)
+            ids, _ = bsgg.route_groups(l.cuda(), 6, bias=bias.cuda(), **where)
+            assert torch.equal(ids.cpu(), want)
+
+
 def test_biases_larger_than_scores():
     """Groups whose terms cancel: large biases of both signs."""
     T, L = 64, 32
