@@ -617,8 +617,9 @@ __device__ __forceinline__ int64_t adapter_end(const OuterParams& p, int i) {
   if (i + 1 == p.map.adapters) end = min(end, static_cast<int64_t>(*p.rows_used));
   return max(int64_t(0), min(end, p.map.m_pad));
 }
+// (rounded down to what the sort writes: chunks of 64 rows of terms end inside m_pad)
 __device__ __forceinline__ int64_t adapter_begin(const OuterParams& p, int i) {
-  return i > 0 ? max(int64_t(0), min(static_cast<int64_t>(p.map.offsets[i - 1]), p.map.m_pad)) : 0;
+  return i > 0 ? max(int64_t(0), min(static_cast<int64_t>(p.map.offsets[i - 1]), p.map.m_pad)) & ~int64_t(127) : 0;
 }
 // The segment with this number (wanted >= 0), or those of an adapter (index 0).  All
 // threads call it: four adapters each, their counts summed over the block.  Where no adapter
@@ -638,7 +639,8 @@ __device__ __forceinline__ Segment find_segment(const OuterParams& p, int64_t wa
     count[k] = 0;
     if (i < p.map.adapters) {
       const int64_t rows = adapter_end(p, i) - adapter_begin(p, i);
-      count[k] = rows > 0 ? static_cast<int>((rows + p.segment - 1) / p.segment) : 0;
+      // (bounded, so that no offsets make the sums overflow: a sorted map has some hundreds)
+      count[k] = rows > 0 ? static_cast<int>(min((rows + p.segment - 1) / p.segment, int64_t(1) << 20)) : 0;
     }
     all += count[k];
     slots += count[k] > 1 ? count[k] : 0;

@@ -299,3 +299,46 @@ def test_no_tokens():
     assert y.shape == (0, 32) and u.shape == (0, 8)
     dx, da, db = bsgg.adapters_backward(y, x, u, a, b, t)
     assert dx.shape == (0, 64) and (da == 0).all() and (db == 0).all()
+
+
+def test_a_map_with_too_few_rows():
+    """Tokens that the sort had no row for are tokens without an adapter, of an adapter cut
+    in the middle and of one that is left out as a whole."""
+    T, S, r, K, N = 1200, 4, 16, 128, 192
+    p = problem(T, S, r, K, N, "bf16", "any", seed=5)
+    t = map_of(p, S, m_pad=384)
+    assert bsgg.operators_status() == 5
+    cut = p["ids"].clone()
+    cut[t.row_of_slot.view(-1).cpu() < 0] = -1
+    sizes = [int((cut == i).sum()) for i in range(S)]
+    assert 128 < sizes[0] <= 256 and sizes[1:] == [128, 0, 0] and int((p["ids"] == 1).sum()) > 128
+    whole = map_of({"ids": cut}, S)
+    dev = {k: p[k].cuda() for k in ("x", "a", "b", "scales", "base", "dy", "basex")}
+    y, u = bsgg.adapters(dev["x"], dev["a"], dev["b"], t, scales=dev["scales"], base=dev["base"])
+    want = bsgg.adapters(dev["x"], dev["a"], dev["b"], whole, scales=dev["scales"], base=dev["base"])
+    assert torch.equal(y, want[0]) and torch.equal(u, want[1])
+    got, want = (bsgg.adapters_backward(dev["dy"], dev["x"], u, dev["a"], dev["b"], m, scales=dev["scales"], base=dev["basex"])
+                 for m in (t, whole))
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+
+
+def test_offsets_that_the_sort_does_not_write():
+    """Offsets out of order, negative, past the map or off the multiples of 128 give some
+    gradient, of no memory but the arguments' own."""
+    T, S, r, K, N = 700, 3, 24, 64, 136
+    p = problem(T, S, r, K, N, "bf16", "any", seed=6)
+    t = map_of(p, S)
+    dev = {k: p[k].cuda() for k in ("x", "a", "b", "base", "dy")}
+    m = t.slot_of_row.numel()
+    for offsets, used in (([5, 261, m - 3], m + 7), ([m, -128, 384], m), ([1 << 30, 1 << 30, 1 << 30], 1 << 30), ([-5, -5, -5], -1)):
+        bad = t._replace(padded_offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                         rows_used=torch.tensor([used], dtype=torch.int32, device="cuda"))
+        y, u = bsgg.adapters(dev["x"], dev["a"], dev["b"], bad, base=dev["base"])
+        for grads in (None, "f32"):
+            bsgg.adapters_backward(dev["dy"], dev["x"], u, dev["a"], dev["b"], bad, grad_format=grads)
+    torch.cuda.synchronize()
+    # what a good map gives is what it gave
+    first = bsgg.adapters_backward(dev["dy"], dev["x"], u, dev["a"], dev["b"], t)
+    again = bsgg.adapters_backward(dev["dy"], dev["x"], u, dev["a"], dev["b"], t)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
