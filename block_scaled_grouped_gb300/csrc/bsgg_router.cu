@@ -434,11 +434,12 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_groups_backward_kerne
     }
   }
   if constexpr (NI == 0) {
-    for (int e = lane; e < p.L; e += 32) store1(p.kind, p.dlogits, at + e, 0.0f);
+    // 1 - s = 1 / (1 + e^l), before the row is filled: dlogits may be the logits
+    const float rest = p.sigmoid && id >= 0 ? sigmoid32(-load1(p.kind, p.logits, at + id)) : 1.0f;
     const float inner = p.normalize ? warp_sum(w * g) / p.scale : 0.0f;
-    float d = w * (g - inner);
-    // 1 - s = 1 / (1 + e^l)
-    if (p.sigmoid && id >= 0) d *= sigmoid32(-load1(p.kind, p.logits, at + id));
+    const float d = w * (g - inner) * rest;
+    __syncwarp();
+    for (int e = lane; e < p.L; e += 32) store1(p.kind, p.dlogits, at + e, 0.0f);
     __syncwarp();
     if (id >= 0) store1(p.kind, p.dlogits, at + id, d);
   } else {

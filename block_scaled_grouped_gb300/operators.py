@@ -561,7 +561,8 @@ def route_groups_backward(logits, ids, weights, dweights, score: str = "sigmoid"
                           row_of_slot=None, dlogits=None, stream=None):
     """Gradient of route_groups with respect to the logits, in their type; score,
     normalize and scale as they were.  dweights is (tokens, topk), or with row_of_slot a
-    per-row gradient (the backward GEMM's dprob)."""
+    per-row gradient (the backward GEMM's dprob).  The result goes into a given dlogits (of
+    the logits' row pitch; the logits will do) or a new tensor."""
     ld = _matrix(logits, "logits")
     T, L = logits.shape
     if ids.dim() != 2 or ids.shape[0] != T:

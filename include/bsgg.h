@@ -652,7 +652,8 @@ BSGG_API bsgg_status bsgg_route_groups(const bsgg_route_groups_desc* desc, const
  *   sigmoid, normalize = 1   dlogits_i = w_i (1 - s_i) (g_i - inner) for the chosen i, 0 elsewhere
  *   sigmoid, normalize = 0   dlogits_i = w_i (1 - s_i) g_i for the chosen i, 0 elsewhere
  * The choice itself (and so the bias) has no gradient.  row_of_slot and m_pad as in
- * bsgg_route_backward; groups, topk_groups and group_top are not read. */
+ * bsgg_route_backward; groups, topk_groups and group_top are not read.  dlogits may be
+ * the logits. */
 BSGG_API bsgg_status bsgg_route_groups_backward(const bsgg_route_groups_desc* desc, const void* logits,
                                                 const int32_t* ids, const float* weights, const float* dweights,
                                                 const int32_t* row_of_slot, int64_t m_pad, void* dlogits, void* stream);

@@ -111,6 +111,8 @@ def test_route_groups_backward(T, L, k, dtype, score, normalize):
     same = bsgg.route_groups_backward(*args, per_row.cuda(), row_of_slot=rows.cuda(), dlogits=out, **how)
     assert same.data_ptr() == out.data_ptr()
     assert torch.equal(same, bsgg.route_groups_backward(*args, g0.cuda(), **how))
+    # where the logits are
+    assert torch.equal(bsgg.route_groups_backward(*args, g.cuda(), dlogits=dev, **how), got) and torch.isnan(dev._base[:, L:].float()).all()
 
 
 def test_gradient_is_that_of_the_formula_by_differences():
