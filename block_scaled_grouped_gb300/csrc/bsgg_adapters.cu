@@ -596,6 +596,7 @@ struct OuterSide {
   float* part;                    // (slots, rank, width) sums of segments
   uint16_t* terms;                // (TERMS, m_pad, ranks) of g
   float* units;                   // of each segment's terms
+  float* most;                    // the largest |g| of every 64 rows (float16)
   int64_t ldx;
   int width, blocks;              // blocks of columns; 0: not wanted
 };
@@ -603,7 +604,7 @@ struct OuterParams {
   AdapterMap map;
   const int32_t* rows_used;       // where the last adapter's rows end
   OuterSide side[2];
-  int rank, segment, term_rows, slots, out_kind;
+  int rank, segment, slots, out_kind;
 };
 
 // Where an adapter's segments are.
@@ -669,17 +670,48 @@ __device__ __forceinline__ Segment find_segment(const OuterParams& p, int64_t wa
   return found;
 }
 
+// The largest of the threads' values, in all of them.
+__device__ __forceinline__ float block_max(float v) {
+  __shared__ float of_warp[kWarps];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) v = fmaxf(v, of_warp[w]);
+  return v;
+}
+
+// The largest |g| of 64 rows of the map, for float16's powers of two (with the terms' blocks
+// going through their segments by themselves 12 us more of a gradient's 108).
+constexpr int kTermRows = 64;
+__global__ void __launch_bounds__(kThreads) outer_most_kernel(const __grid_constant__ OuterParams p) {
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const OuterSide& side = p.side[blockIdx.y];
+  if (side.blocks == 0) return;
+  const int quads = p.rank / 4;
+  float most = 0.0f;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < kTermRows * quads; e += kThreads) {
+    const int i = e / quads;
+    const int32_t t = token_at(p.map, static_cast<int64_t>(blockIdx.x) * kTermRows + i);
+    float4 v = make_float4(0, 0, 0, 0);
+    if (t >= 0) v = *reinterpret_cast<const float4*>(side.g + static_cast<int64_t>(t) * p.rank + (e - i * quads) * 4);
+    most = fmaxf(fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+  }
+  most = block_max(most);
+  if (threadIdx.x == 0) side.most[blockIdx.x] = most;
+}
+
 // g of a segment's rows as terms of 16 bits, zeros for padding rows (up to a multiple of 64)
 // and behind the rank (to a multiple of 16).  float16 keeps them inside its range by the
 // segment's own power of two; its sums are scaled back before they are joined.
 template <int KIND, int TERMS>
 __global__ void __launch_bounds__(kThreads) outer_terms_kernel(const __grid_constant__ OuterParams p) {
-  __shared__ float most_of[kWarps];
   let_next_kernel_start();
   wait_for_previous_kernel();
   const OuterSide& side = p.side[blockIdx.y];
-  // a block takes term_rows rows (a multiple of 64); the segment's power of two it finds by itself
-  const int chunks = p.segment / p.term_rows;
+  const int chunks = p.segment / kTermRows;
   const int64_t number = blockIdx.x / chunks;
   const int chunk = static_cast<int>(blockIdx.x - number * chunks);
   const Segment seg = find_segment(p, number, 0);
@@ -690,26 +722,14 @@ __global__ void __launch_bounds__(kThreads) outer_terms_kernel(const __grid_cons
   float unit = 1.0f;
   if (KIND == OK_F16) {
     float most = 0.0f;
-    for (int64_t e = threadIdx.x; e < (row1 - row0) * quads; e += kThreads) {
-      const int64_t r = e / quads;
-      const int32_t t = token_at(p.map, row0 + r);
-      if (t < 0) continue;
-      const float4 v = *reinterpret_cast<const float4*>(side.g + static_cast<int64_t>(t) * p.rank + (e - r * quads) * 4);
-      most = fmaxf(fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-    if ((threadIdx.x & 31) == 0) most_of[threadIdx.x >> 5] = most;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) most = fmaxf(most, most_of[w]);
-    unit = unit_of(most);
+    for (int64_t r = row0 + threadIdx.x * kTermRows; r < row1; r += kThreads * kTermRows) most = fmaxf(most, side.most[r / kTermRows]);
+    unit = unit_of(block_max(most));
     if (threadIdx.x == 0) side.units[number] = unit;             // the same from each of them
   }
   const int ranks = (p.rank + 15) & ~15, all = ranks / 4;
-  const int64_t from = row0 + static_cast<int64_t>(chunk) * p.term_rows;
+  const int64_t from = row0 + static_cast<int64_t>(chunk) * kTermRows;
   if (from >= row1) return;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(p.term_rows), (row1 - from + 63) / 64 * 64));
-  for (int e = threadIdx.x; e < rows * all; e += kThreads) {
+  for (int e = threadIdx.x; e < kTermRows * all; e += kThreads) {
     const int i = e / all, q = e - i * all;
     const int64_t r = from + i;
     if (r >= p.map.m_pad) break;
@@ -1016,7 +1036,7 @@ bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
 int64_t outer_segment(int64_t tokens, int64_t k, int64_t n) {
   const int64_t blocks = ceil_div(k, 256) + ceil_div(n, 256);
   int64_t rows = 128;
-  while (ceil_div(tokens, rows) * blocks > 608) rows *= 2;
+  while (ceil_div(tokens, rows) * blocks > 456) rows *= 2;
   return rows;
 }
 // Sums of segments that can be needed at once: only adapters of several segments have any.
@@ -1034,9 +1054,9 @@ int64_t outer_segments(int64_t tokens, int64_t m_pad, int64_t adapters, int64_t 
 }
 
 // What lies where in the workspace, in bytes: both sides' terms (three at the most), their
-// units, and the segments' sums.
+// units and largest values, and the segments' sums.
 struct OuterSpace {
-  uint64_t terms[2], units[2], part[2], bytes;
+  uint64_t terms[2], units[2], most[2], part[2], bytes;
   OuterSpace(int64_t tokens, int64_t k, int64_t n, int64_t m_pad, int64_t adapters, int64_t rank) {
     uint64_t at = 0;
     auto take = [&](uint64_t size) {
@@ -1047,6 +1067,7 @@ struct OuterSpace {
     const int64_t segments = outer_segments(tokens, m_pad, adapters, outer_segment(tokens, k, n)), slots = outer_slots(tokens, k, n);
     for (uint64_t& t : terms) t = take(uint64_t(6) * m_pad * ((rank + 15) / 16 * 16));
     for (uint64_t& u : units) u = take(uint64_t(4) * segments);
+    for (uint64_t& v : most) v = take(uint64_t(4) * (m_pad / kTermRows));
     part[0] = take(uint64_t(4) * slots * rank * n);
     part[1] = take(uint64_t(4) * slots * rank * k);
     bytes = at;
@@ -1063,8 +1084,6 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
         side.blocks = side.out != nullptr ? static_cast<int>(ceil_div(side.width, Outer<R, 2, true>::kCols)) : 0;
         most += side.out != nullptr ? ceil_div(int64_t(p.rank) * side.width, 8 * kThreads) : 0;
       }
-      // float16's blocks each go through their whole segment first: at most eight of them
-      p.term_rows = K == OK_F16 && p.segment > 512 ? p.segment / 8 : 64;
       const int64_t segments = outer_segments(p.map.tokens, p.map.m_pad, p.map.adapters, p.segment), grid = segments * (p.side[0].blocks + p.side[1].blocks);
       if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
       auto launch = [&](auto terms, auto runs) {
@@ -1072,8 +1091,14 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
         constexpr bool U = decltype(runs)::value;
         constexpr int kSmem = Outer<R, N, U>::kSmem;
         if (!allowed<outer_kernel<K, R, N, E, U>>(kSmem)) return BSGG_ERR_CUDA;
-        const LaunchConfig t(dim3(static_cast<unsigned>(segments * (p.segment / p.term_rows)), 2), kThreads, 0, s);
-        bsgg_status st = launch_kernel(t, outer_terms_kernel<K, N>, p);
+        bsgg_status st = BSGG_OK;
+        if (K == OK_F16) {
+          const LaunchConfig v(dim3(static_cast<unsigned>(p.map.m_pad / kTermRows), 2), kThreads, 0, s);
+          st = launch_kernel(v, outer_most_kernel, p);
+          if (st != BSGG_OK) return st;
+        }
+        const LaunchConfig t(dim3(static_cast<unsigned>(segments * (p.segment / kTermRows)), 2), kThreads, 0, s);
+        st = launch_kernel(t, outer_terms_kernel<K, N>, p);
         if (st != BSGG_OK) return st;
         const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, kSmem, s);
         st = launch_kernel(c, outer_kernel<K, R, N, E, U>, p);
@@ -1183,7 +1208,7 @@ bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     auto side = [&](int i, const float* g, const void* in, const float* f, void* out, int64_t ld, int64_t width) {
       p.side[i] = {g, in, f, out, reinterpret_cast<float*>(ws + space.part[i]), reinterpret_cast<uint16_t*>(ws + space.terms[i]),
-                   reinterpret_cast<float*>(ws + space.units[i]), ld, static_cast<int>(width), 0};
+                   reinterpret_cast<float*>(ws + space.units[i]), reinterpret_cast<float*>(ws + space.most[i]), ld, static_cast<int>(width), 0};
     };
     side(0, u, dy, scales, db, d->ld_dy, d->n);
     side(1, du, x, nullptr, da, d->ldx, d->k);
