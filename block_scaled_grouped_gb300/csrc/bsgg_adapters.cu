@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 3 : 2) expand_kernel(const
 // out) and kCols columns of x or dy.  An adapter of one segment is finished there; the
 // segments' sums of the others meet in another launch, in order.  The products are
 // (rank x 64 tokens) (64 tokens x columns), both read across their rows.
-//   4096 tokens of 4 adapters, rank 32, 4096 and 14336: 54 us for 151 MB, 2.8 TB/s, after 7 us
+//   4096 tokens of 4 adapters, rank 32, 4096 and 14336: 47 us for 151 MB, 3.2 TB/s, after 8 us
 //   of terms and before 10 of join (both less behind one another): shared memory is busy half
 //   of the time, the matrix pipe as long, in turns.  With the reduction split over clusters
 //   by adapter, whose shares are unlike, the two took 65 and 37 us.
@@ -681,8 +681,9 @@ __device__ __forceinline__ float block_max(float v) {
   return v;
 }
 
-// The largest |g| of 64 rows of the map, for float16's powers of two (with the terms' blocks
-// going through their segments by themselves 12 us more of a gradient's 108).
+// The largest |g| of 64 rows of the map, for float16's powers of two (4096 tokens, rank 32, all
+// of the gradient 111 us; with the terms' blocks going through their segments by themselves
+// 139).
 constexpr int kTermRows = 64;
 __global__ void __launch_bounds__(kThreads) outer_most_kernel(const __grid_constant__ OuterParams p) {
   let_next_kernel_start();
@@ -1031,8 +1032,10 @@ bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
   });
 }
 
-// Rows of a segment: 64 to 512 (or more, where the blocks would be more than a few rounds),
-// until two blocks an SM have work.
+// Rows of a segment: 128, or as many more as make the blocks one or two rounds of two an SM.
+// 4096 tokens of 4 adapters, rank 32, 4096 and 14336, all of the gradient: 107 us (1024 rows; with
+// half as many 112, twice as many 114); rank 128 268 (286); 8192 tokens, rank 64, 1024 wide, 75
+// (92); 16384 tokens of 8 adapters, rank 16, 4096 wide, 158 (157, and 181 with twice as many).
 int64_t outer_segment(int64_t tokens, int64_t k, int64_t n) {
   const int64_t blocks = ceil_div(k, 256) + ceil_div(n, 256);
   int64_t rows = 128;
@@ -1109,8 +1112,8 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
         return launch_kernel(j, outer_join_kernel, p);
       };
       // What is rounded to 16 bits is summed whole at ranks over 32, up to 32768 rows (3.3e-5 of
-      // the sum): without registers for runs two blocks fit an SM (4096 tokens, rank 64, all of
-      // the gradient 150 us for 167, rank 128 284 for 320; at ranks 16 and 32 no change)
+      // the sum): without registers for runs two blocks fit an SM (4096 tokens in segments of 512,
+      // rank 64, all of the gradient 150 us for 167, rank 128 284 for 320; at ranks 16 and 32 no change)
       if (R > 32 && p.out_kind != OK_F32 && p.segment <= 32768) {
         if constexpr (R > 32) return launch(std::integral_constant<int, 2>(), std::false_type());
       }
