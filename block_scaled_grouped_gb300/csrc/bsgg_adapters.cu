@@ -1036,10 +1036,11 @@ bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
 // 4096 tokens of 4 adapters, rank 32, 4096 and 14336, all of the gradient: 107 us (1024 rows; with
 // half as many 112, twice as many 114); rank 128 268 (286); 8192 tokens, rank 64, 1024 wide, 75
 // (92); 16384 tokens of 8 adapters, rank 16, 4096 wide, 158 (157, and 181 with twice as many).
+// Layers so wide that one segment of all tokens has more blocks than that stay with one.
 int64_t outer_segment(int64_t tokens, int64_t k, int64_t n) {
   const int64_t blocks = ceil_div(k, 256) + ceil_div(n, 256);
   int64_t rows = 128;
-  while (ceil_div(tokens, rows) * blocks > 456) rows *= 2;
+  while (rows < tokens && ceil_div(tokens, rows) * blocks > 456) rows *= 2;
   return rows;
 }
 // Sums of segments that can be needed at once: only adapters of several segments have any.

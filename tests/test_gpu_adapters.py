@@ -342,3 +342,35 @@ def test_offsets_that_the_sort_does_not_write():
     first = bsgg.adapters_backward(dev["dy"], dev["x"], u, dev["a"], dev["b"], t)
     again = bsgg.adapters_backward(dev["dy"], dev["x"], u, dev["a"], dev["b"], t)
     assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("grads", [None, "f32"])
+@pytest.mark.parametrize("T,S,r,K,N,dtype", [(16, 1, 8, 64, 128256, "bf16"), (1, 2, 16, 64, 128256, "bf16"), (40, 3, 24, 128256, 72, "f16"),
+                                             (300, 2, 72, 64, 128256, "bf16"), (500, 1, 40, 151936, 136, "f16")])
+def test_gradients_of_wide_layers(T, S, r, K, N, dtype, grads):
+    """Beside an output head: so wide that a segment of all tokens has more blocks than fill the
+    chip, from one token up, several chunks of an adapter's rows among them."""
+    p = problem(T, S, r, K, N, dtype, "any" if S > 1 else "one", seed=T + r)
+    p["ids"][0] = S - 1                                  # a token, where there is one
+    t = map_of(p, S)
+    dt, gt = DT[dtype], DT[dtype] if grads is None else torch.float32
+    x, a, b, s, dy, base = (p[n].cuda() for n in ("x", "a", "b", "scales", "dy", "basex"))
+    u = torch.randn(T, r, generator=gen(r)).cuda()
+    dx, da, db = bsgg.adapters_backward(dy, x, u, a, b, t, scales=s, base=base, grad_format=grads)
+    ids = p["ids"].cuda()
+    want_dx, tol_dx = base.double(), torch.zeros(T, K, dtype=torch.float64, device="cuda")
+    terms = 2.0 ** -23 if gt == torch.float32 and dt == torch.bfloat16 else TERMS[dt]
+    for i in range(S):
+        m, f = (ids == i).double()[:, None], float(s[i])
+        dui, ui = f * m * (dy.double() @ b[i].double().t()), f * m * u.double()
+        err = f * m * (dy.double().abs() @ b[i].double().abs().t()) * product_error(N)
+        # float16's terms are of the largest: of the row for dx, of the segment for the gradients
+        size = dui.abs().amax(1, keepdim=True) if dt == torch.float16 else dui.abs()
+        want_dx = want_dx + dui @ a[i].double()
+        tol_dx += (err + size * TERMS[dt] + dui.abs() * product_error(2 * r)) @ a[i].double().abs()
+        for got, g, e, v in ((da[i], dui, err, x), (db[i], ui, torch.zeros_like(err), dy)):
+            want = g.t() @ v.double()
+            size = g.abs().max() if dt == torch.float16 else g.abs()
+            tol = (e + size * terms * m + g.abs() * product_error(3 * T)).t() @ v.double().abs()
+            assert ((got.double() - want).abs() <= tol + want.abs() * 2.0 ** -23 + rounding(want, gt)).all()
+    assert ((dx.double() - want_dx).abs() <= tol_dx + want_dx.abs() * 2.0 ** -23 + rounding(want_dx, dt)).all()

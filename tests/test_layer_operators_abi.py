@@ -310,3 +310,20 @@ def test_reference_adapters_gradient_against_differences():
             args = [[x, a, b], [x, a, b]]
             args[0][i], args[1][i] = v + s.view_as(v), v - s.view_as(v)
             assert abs(float(f(*args[0]) - f(*args[1])) / 2e-6 - float(d.reshape(-1)[at])) < 1e-7
+
+
+# ------------------------------------------------------------------ wide layers
+@pytest.mark.parametrize("k,n", [(4096, 14336), (4096, 105904), (4096, 112648), (4096, 128256), (8192, 151936), (2 ** 24, 2 ** 24)])
+@pytest.mark.parametrize("tokens", [1, 2, 16, 4096, 65536])
+def test_workspace_of_wide_layers(lib, tokens, k, n):
+    """Beside an output head a single segment has more blocks than fill the chip.  The terms, in
+    six bytes at the most, are there for any width; sums of segments only where there are several,
+    of blocks that are 456 together at the most."""
+    m_pad, adapters, rank = bsgg.sort_rows(tokens, 4), 4, 16
+    need = lib.bsgg_adapters_workspace_bytes(tokens, k, n, m_pad, adapters, rank)
+    terms = 2 * 6 * m_pad * 16
+    assert terms <= need
+    if tokens <= 128 or 2 * (-(-k // 256) - (-n // 256)) > 456:
+        assert need <= terms + 2 * 4 * (adapters + m_pad // 64) + 6 * 16
+    else:
+        assert need >= terms + 2 * 4 * rank * (k + n)
