@@ -12,8 +12,6 @@
 // where tcgen05's are 128 rows.  What they cost was looked at: expand of 4096 tokens, rank
 // 64, 4096 to 14336, takes as long with half of its products left out, and 11 us less of 87
 // without any.
-#include <atomic>
-
 #include "bsgg_ops.cuh"
 
 namespace {
@@ -959,20 +957,6 @@ template <typename F>
 bsgg_status with_half(int format, F&& f) {
   return format == BSGG_OUT_BF16 ? f(std::integral_constant<int, OK_BF16>()) : f(std::integral_constant<int, OK_F16>());
 }
-// Shared memory beyond the default 48 KB has to be asked for, once for a kernel on a device
-// (half a microsecond of the host's time at each call otherwise).
-template <auto KERNEL>
-bool allowed(int smem) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  if (!succeeded(cudaGetDevice(&dev))) return false;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return true;
-  if (!succeeded(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return false;
-  done.fetch_or(bit, std::memory_order_relaxed);
-  return true;
-}
-
 // Tiles of `rows` rows that can hold tokens, at the most.
 int64_t busy_tiles(const AdapterMap& m, int rows) {
   const int64_t most = (m.tokens < m.adapters ? m.tokens : m.adapters) + m.tokens / rows;

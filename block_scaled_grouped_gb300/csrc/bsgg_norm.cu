@@ -520,9 +520,7 @@ bsgg_status bsgg_rms_norm_backward(const bsgg_norm_bwd_desc* d, const void* dy, 
         constexpr int K = decltype(kind)::value, Y = decltype(ykind)::value, N = decltype(nv)::value;
         constexpr auto kernel = rms_norm_backward_kernel<K, Y, N, decltype(warp)::value>;
         const size_t smem = N == 4 ? sizeof(float) * kNormValues * N * shape.threads : 0;       // 128 KB at the most
-        if (smem > 0 &&
-            !succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))))
-          return BSGG_ERR_CUDA;
+        if (N == 4 && !allowed<kernel>(static_cast<int>(sizeof(float)) * kNormValues * N * kNormMaxThreads)) return BSGG_ERR_CUDA;
         const LaunchConfig c(dim3(static_cast<unsigned>(blocks)), shape.threads, smem, s);
         return launch_kernel(c, kernel, p);
       });

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -51,6 +52,22 @@ inline bool succeeded(cudaError_t e) {
 template <typename... P, typename... A>
 bsgg_status launch_kernel(const LaunchConfig& c, void (*kern)(P...), A... args) {
   return succeeded(cudaLaunchKernelEx(&c.cfg, kern, P(args)...)) ? BSGG_OK : BSGG_ERR_CUDA;
+}
+
+// Shared memory beyond the default 48 KB has to be asked for, once for a kernel on a device
+// (half a microsecond of the host's time at each call otherwise).  `smem` is the most that
+// any launch of the kernel takes: the limit is the process's, and a smaller one that another
+// thread set in between would refuse this one's launch.
+template <auto KERNEL>
+inline bool allowed(int smem) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (!succeeded(cudaGetDevice(&dev))) return false;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (!succeeded(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

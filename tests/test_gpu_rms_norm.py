@@ -1,7 +1,9 @@
 """The RMS norm with the residual's addition and its gradient on the GPU against 64-bit
 references: every pair of types, every row format, widths from 8 to the largest,
 one token and many, pitches wider than the rows, sums in place."""
+import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -217,3 +219,28 @@ def test_many_rows_and_long_offsets():
     want, _ = R.rms_norm(2 * x[-2:].cpu(), None, 0.0)
     assert ((n.y[-2:].cpu().double() - want).abs() <= want.abs() * (RSTD + 2.0 ** -23) + rounding(want, torch.bfloat16)).all()
     assert torch.equal(n.a[T - 2].cpu(), n.a[0].cpu()) and (n.a[T:] == 0).all()
+
+
+def test_widths_in_two_threads():
+    """Rows above 8192 columns keep sums in shared memory, more of it the wider they are: calls of
+    two widths from two host threads, on streams of their own."""
+    lib, codes = bsgg.lib(), [[], []]
+    torch.cuda.synchronize()
+
+    def calls(i, H):
+        s = torch.cuda.Stream()
+        h = torch.ones(1, H, dtype=torch.bfloat16, device="cuda")
+        rstd, dx = torch.ones(1, device="cuda"), torch.empty(1, H, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        d = bsgg.operators.NormBwdDesc(1, H, H, H, H, H, 0, 0, 0, 0)
+        args = (ctypes.byref(d), h.data_ptr(), h.data_ptr(), None, rstd.data_ptr(), None, dx.data_ptr(), None, None, s.cuda_stream)
+        codes[i] = [lib.bsgg_rms_norm_backward(*args) for _ in range(60000)]
+        s.synchronize()
+        assert (dx == 0).all()                       # g - n mean(g n) of ones
+
+    threads = [threading.Thread(target=calls, args=a) for a in enumerate((16384, 32768))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert [(len(c), sum(c)) for c in codes] == [(60000, 0)] * 2
