@@ -183,6 +183,7 @@ struct SortShared {
       : mine(sm), total(sm + L), before(sm + 2 * L), first(sm + 3 * L), scan(sm + 4 * L + 1),
         warp_count(sm + 4 * L + 1 + kSortWarps) {}
 };
+constexpr int kSortMaxExperts = 1024;
 constexpr size_t sort_shared_bytes(int L) { return 4 * (4 * size_t(L) + 1 + kSortWarps + size_t(L) * kSortWarps); }
 
 __device__ __forceinline__ int sort_id(const SortParams& p, int64_t s) {
@@ -672,13 +673,6 @@ void sort_shape(int64_t slots, int64_t* blocks, int64_t* steps) {
   }
 }
 
-// Shared memory beyond the default 48 KB has to be asked for.
-template <typename K>
-bool sort_allowed(K kern, size_t smem) {
-  return smem <= 48 * 1024 ||
-         succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-}
-
 }  // namespace
 
 extern "C" {
@@ -718,7 +712,7 @@ bsgg_status bsgg_route_backward(const bsgg_route_desc* d, const void* logits, co
 }
 
 int64_t bsgg_sort_rows(int64_t slots, int32_t num_experts) {
-  if (slots < 0 || slots >= (int64_t(1) << 31) || num_experts < 1 || num_experts > 1024) return -1;
+  if (slots < 0 || slots >= (int64_t(1) << 31) || num_experts < 1 || num_experts > kSortMaxExperts) return -1;
   // the most that sizes adding up to `slots` can need: as many experts as can
   // be, each one slot past a multiple of 128 (one block of rows for no slots)
   const int64_t some = slots < num_experts ? slots : num_experts;
@@ -758,13 +752,14 @@ bsgg_status bsgg_sort_tokens(int64_t slots, int32_t num_experts, int64_t m_pad, 
   p.ids = ids; p.weights = weights; p.offsets = padded_offsets; p.row_of_slot = row_of_slot; p.slot_of_row = slot_of_row;
   p.rows_used = rows_used; p.prob = prob; p.counts = static_cast<int32_t*>(workspace); p.status = status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t smem = sort_shared_bytes(p.L);                // 82 KB at the most: 1024 experts
+  const size_t smem = sort_shared_bytes(p.L);
+  constexpr int kMost = static_cast<int>(sort_shared_bytes(kSortMaxExperts));   // 82 KB
   if (one_cluster) {
-    if (!sort_allowed(sort_cluster_kernel, smem)) return BSGG_ERR_CUDA;
+    if (!allowed<sort_cluster_kernel>(kMost)) return BSGG_ERR_CUDA;
     const LaunchConfig c(dim3(static_cast<unsigned>(p.blocks)), kSortThreads, smem, s, p.blocks);
     return launch_kernel(c, sort_cluster_kernel, p);
   }
-  if (!sort_allowed(sort_count_kernel, smem) || !sort_allowed(sort_place_kernel, smem)) return BSGG_ERR_CUDA;
+  if (!allowed<sort_count_kernel>(kMost) || !allowed<sort_place_kernel>(kMost)) return BSGG_ERR_CUDA;
   const LaunchConfig c(dim3(static_cast<unsigned>(p.blocks)), kSortThreads, smem, s);
   const bsgg_status st = launch_kernel(c, sort_count_kernel, p);
   return st == BSGG_OK ? launch_kernel(c, sort_place_kernel, p) : st;
