@@ -19,8 +19,9 @@ namespace {
 using namespace bsgg;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-// Sums of more than this many products are added up in registers in runs of this length
-// (the matrix instruction cuts what an addition drops, 1e-9 of the sum per element).
+// Sums of more than this many products are added up in registers in runs of this length: the
+// matrix instruction cuts what an addition drops, and a sum of one sign comes out small by
+// 3.5e-9 of it per product (float16, 32768 rows in two terms 2.3e-4; in runs of 512 3.1e-6).
 constexpr int kRun = 512;
 constexpr int kMaxCluster = 8;
 
@@ -1096,10 +1097,13 @@ bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
         const LaunchConfig j(dim3(static_cast<unsigned>(most < each ? most : each), static_cast<unsigned>(p.map.adapters)), kThreads, 0, s);
         return launch_kernel(j, outer_join_kernel, p);
       };
-      // What is rounded to 16 bits is summed whole at ranks over 32, up to 32768 rows (3.3e-5 of
-      // the sum): without registers for runs two blocks fit an SM (4096 tokens in segments of 512,
-      // rank 64, all of the gradient 150 us for 167, rank 128 284 for 320; at ranks 16 and 32 no change)
-      if (R > 32 && p.out_kind != OK_F32 && p.segment <= 32768) {
+      // What is rounded to 16 bits is summed whole at ranks over 32, as long as what the additions
+      // drop is under an eighth of the rounding where all products have one sign: into bfloat16
+      // up to 32768 rows (2.3e-4 of 3.9e-3), into float16 up to 8192 (5.9e-5 of 4.9e-4).  Without
+      // registers for runs two blocks fit an SM (4096 tokens in segments of 512, rank 64, all of the
+      // gradient 150 us for 167, rank 128 284 for 320; db alone of 8192 tokens in one segment, 45056
+      // wide, rank 64, 377 for 445; at ranks 16 and 32 no change)
+      if (R > 32 && p.out_kind != OK_F32 && p.segment <= (p.out_kind == OK_F16 ? 8192 : 32768)) {
         if constexpr (R > 32) return launch(std::integral_constant<int, 2>(), std::false_type());
       }
       if constexpr (K == OK_BF16) {

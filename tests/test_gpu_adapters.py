@@ -374,3 +374,73 @@ def test_gradients_of_wide_layers(T, S, r, K, N, dtype, grads):
             tol = (e + size * terms * m + g.abs() * product_error(3 * T)).t() @ v.double().abs()
             assert ((got.double() - want).abs() <= tol + want.abs() * 2.0 ** -23 + rounding(want, gt)).all()
     assert ((dx.double() - want_dx).abs() <= tol_dx + want_dx.abs() * 2.0 ** -23 + rounding(want_dx, dt)).all()
+
+
+def gradients_in_64_bits(p, u, S):
+    """(du, da, db) by products in 64 bits on the GPU, scales none."""
+    ids, x, b, dy = (p[n].cuda() for n in ("ids", "x", "b", "dy"))
+    da, db, du = [], [], torch.zeros(u.shape, dtype=torch.float64, device="cuda")
+    for i in range(S):
+        m = (ids == i).double()[:, None]
+        di = m * (dy.double() @ b[i].double().t())
+        du += di
+        da.append(di.t() @ x.double())
+        db.append((m * u.double()).t() @ dy.double())
+    return du, da, db
+
+
+@pytest.mark.parametrize("T,S,r,K,N,dtype", [(3000, 3, 64, 1024, 1536, "bf16"), (2000, 2, 128, 256, 768, "f16"), (1100, 2, 64, 512, 8192, "f16"),
+                                             (3000, 3, 32, 1024, 1536, "bf16"), (2500, 5, 16, 4096, 2048, "f16"), (2600, 2, 88, 1032, 520, "bf16"),
+                                             (4100, 1, 128, 2048, 264, "bf16"), (1900, 3, 40, 4096, 8192, "f16")])
+def test_gradients_into_16_bits_of_several_segments(T, S, r, K, N, dtype):
+    """da and db in the tokens' own type, of adapters whose tokens lie in several segments."""
+    p = problem(T, S, r, K, N, dtype, "runs" if S > 1 else "one", 11)
+    t = map_of(p, S)
+    x, a, b, dy = (p[n].cuda() for n in ("x", "a", "b", "dy"))
+    u = torch.randn(T, r, generator=gen(r)).cuda()
+    dt = DT[dtype]
+    _, da, db = bsgg.adapters_backward(dy, x, u, a, b, t, want_dx=False)
+    assert da.dtype == dt and db.dtype == dt
+    du, want_da, want_db = gradients_in_64_bits(p, u, S)
+    ids = p["ids"].cuda()
+    for i in range(S):
+        m = (ids == i).double()[:, None]
+        err = m * (dy.double().abs() @ b[i].double().abs().t()) * product_error(N)
+        for got, g, e, v, want in ((da[i], m * du, err, x, want_da[i]), (db[i], m * u.double(), 0 * err, dy, want_db[i])):
+            # bfloat16's two terms are of each value, float16's of the largest
+            size = g.abs() if dt == torch.bfloat16 else g.abs().max() * m
+            tol = (e + size * TERMS[dt] + g.abs() * product_error(3 * T)).t() @ v.double().abs()
+            assert ((got.double() - want).abs() <= tol + rounding(want, dt)).all()
+    for _ in range(2):                                # no order depends on timing
+        again = bsgg.adapters_backward(dy, x, u, a, b, t, want_dx=False)
+        assert torch.equal(again[1], da) and torch.equal(again[2], db)
+
+
+@pytest.mark.parametrize("T,r,dtype,grads", [(32768, 64, "bf16", "bf16"), (32768, 64, "f16", "f16"), (32768, 40, "f16", "f16"), (8192, 128, "f16", "f16"),
+                                             (32768, 128, "bf16", "bf16"), (16384, 64, "bf16", "f16"), (32768, 32, "f16", "f16")])
+def test_long_sums_of_one_sign_into_16_bits(T, r, dtype, grads):
+    """A segment of 8192 to 32768 tokens of one adapter, all products of one sign: what the additions
+    drop adds up, and stays under an eighth of the rounding to 16 bits."""
+    K, N = 16384, 45056                                # 240 blocks of columns: one segment
+    dt, gt = DT[dtype], DT[grads]
+    g = torch.Generator(device="cuda").manual_seed(r)
+    some = lambda *s: torch.rand(*s, generator=g, device="cuda")  # noqa: E731
+    x, dy = (some(T, K) + 0.25).to(dt), (some(T, N) + 0.25).to(dt)
+    u = some(T, r) + 0.25
+    a = torch.zeros(1, r, K, dtype=dt, device="cuda")
+    b = (some(1, r, N) / N).to(dt)
+    t = bsgg.sort_tokens(torch.zeros(T, 1, dtype=torch.int32, device="cuda"), 1)
+    _, da, db = bsgg.adapters_backward(dy, x, u, a, b, t, want_dx=False, grad_format=grads)
+    # (columns of the first and the last blocks)
+    at_k, at_n = (torch.cat([torch.arange(300), torch.arange(w - 300, w)]).cuda() for w in (K, N))
+    du = torch.cat([part.double() @ b[0].double().t() for part in dy.split(4096)])
+    for got, g, v in ((da[0][:, at_k], du, x[:, at_k]), (db[0][:, at_n], u.double(), dy[:, at_n])):
+        want = g.t() @ v.double()
+        off = (got.double() - want) / want
+        # du's own sums are in runs, a rounding for each; float16's terms are of the largest, up to 8
+        # times the value
+        terms = TERMS[dt] * (8 if dt == torch.float16 else 1) + product_error(512) + N / 512 * 2.0 ** -24
+        assert (off.abs() <= 1.125 * ROUND[gt] + terms).all()
+        # roundings to 16 bits are of either sign: their mean over n values is within 6 of their
+        # own standard errors
+        assert abs(float(off.mean())) <= 0.125 * ROUND[gt] + terms + 6 * ROUND[gt] / off.numel() ** 0.5
