@@ -991,26 +991,37 @@ bsgg_status launch_shrink(int format, ShrinkParams p, cudaStream_t s) {
   });
 }
 
-bsgg_status launch_expand(int format, ExpandParams p, cudaStream_t s) {
+// A launch has less than 2^31 blocks; the calls refuse sizes that want more before anything runs.
+bool fits_grid(int64_t blocks) { return blocks < (int64_t(1) << 31); }
+
+// Sets how the tiles and columns are shared out; the number of blocks.
+int64_t plan_expand(ExpandParams& p) {
   p.tiles = p.map.m_pad / 128;
   const int64_t rest = ceil_div(p.map.tokens, kRestTokens);
+  int most = 0;
+  with_rank(p.rank, [&](auto r, auto) {
+    most = Expand<decltype(r)::value>::kCols;
+    return BSGG_OK;
+  });
+  // the fewer tiles hold tokens, the fewer columns a block takes, down to a warp's 64: 109
+  // tokens of 13 adapters, 3688 wide, took 14 us in blocks of 1024 columns
+  const int64_t each = ceil_div(p.width, ceil_div(304, busy_tiles(p.map, 128)));
+  p.cols = static_cast<int>(ceil_div(each, 64) * 64);
+  if (p.cols > most) p.cols = most;
+  p.col_blocks = static_cast<int>(ceil_div(p.width, p.cols));
+  // six blocks an SM for the tokens without an adapter, whose number only the map knows (4096
+  // tokens, 14336 wide, a fifth of them without: 91 us with two, 79 with six, 81 with sixteen)
+  const int64_t parts = ceil_div(912, rest);
+  p.rest_parts = static_cast<int>(parts < p.col_blocks ? parts : p.col_blocks);
+  return p.tiles * p.col_blocks + rest * p.rest_parts;
+}
+
+bsgg_status launch_expand(int format, const ExpandParams& p, int64_t grid, cudaStream_t s) {
   return with_half(format, [&](auto kind) {
     return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
       constexpr bool E = decltype(full)::value;
       if (!allowed<expand_kernel<K, R, E>>(Expand<R>::kSmem)) return BSGG_ERR_CUDA;
-      // the fewer tiles hold tokens, the fewer columns a block takes, down to a warp's 64: 109
-      // tokens of 13 adapters, 3688 wide, took 14 us in blocks of 1024 columns
-      const int64_t each = ceil_div(p.width, ceil_div(304, busy_tiles(p.map, Expand<R>::kRows)));
-      p.cols = static_cast<int>(ceil_div(each, 64) * 64);
-      if (p.cols > Expand<R>::kCols) p.cols = Expand<R>::kCols;
-      p.col_blocks = static_cast<int>(ceil_div(p.width, p.cols));
-      // six blocks an SM for the tokens without an adapter, whose number only the map knows (4096
-      // tokens, 14336 wide, a fifth of them without: 91 us with two, 79 with six, 81 with sixteen)
-      const int64_t parts = ceil_div(912, rest);
-      p.rest_parts = static_cast<int>(parts < p.col_blocks ? parts : p.col_blocks);
-      const int64_t grid = p.tiles * p.col_blocks + rest * p.rest_parts;
-      if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
       const LaunchConfig c(dim3(static_cast<unsigned>(grid)), kThreads, Expand<R>::kSmem, s);
       return launch_kernel(c, expand_kernel<K, R, E>, p);
     });
@@ -1063,18 +1074,26 @@ struct OuterSpace {
   }
 };
 
-bsgg_status launch_outer(int format, OuterParams p, cudaStream_t s) {
+// Sets the blocks of columns; the most blocks that a launch of the gradient has.
+int64_t plan_outer(OuterParams& p) {
+  with_rank(p.rank, [&](auto r, auto) {
+    for (OuterSide& side : p.side)
+      side.blocks = side.out != nullptr ? static_cast<int>(ceil_div(side.width, Outer<decltype(r)::value, 2, true>::kCols)) : 0;
+    return BSGG_OK;
+  });
+  const int64_t segments = outer_segments(p.map.tokens, p.map.m_pad, p.map.adapters, p.segment);
+  const int64_t products = segments * (p.side[0].blocks + p.side[1].blocks), terms = segments * (p.segment / kTermRows);
+  return products > terms ? products : terms;
+}
+
+bsgg_status launch_outer(int format, const OuterParams& p, cudaStream_t s) {
   return with_half(format, [&](auto kind) {
     return with_rank(p.rank, [&](auto r, auto full) {
       constexpr int K = decltype(kind)::value, R = decltype(r)::value;
       constexpr bool E = decltype(full)::value;
       int64_t most = 0;
-      for (OuterSide& side : p.side) {
-        side.blocks = side.out != nullptr ? static_cast<int>(ceil_div(side.width, Outer<R, 2, true>::kCols)) : 0;
-        most += side.out != nullptr ? ceil_div(int64_t(p.rank) * side.width, 8 * kThreads) : 0;
-      }
+      for (const OuterSide& side : p.side) most += side.out != nullptr ? ceil_div(int64_t(p.rank) * side.width, 8 * kThreads) : 0;
       const int64_t segments = outer_segments(p.map.tokens, p.map.m_pad, p.map.adapters, p.segment), grid = segments * (p.side[0].blocks + p.side[1].blocks);
-      if (grid >= (int64_t(1) << 31)) return BSGG_ERR_UNSUPPORTED;
       auto launch = [&](auto terms, auto runs) {
         constexpr int N = decltype(terms)::value;
         constexpr bool U = decltype(runs)::value;
@@ -1146,10 +1165,12 @@ bsgg_status bsgg_adapters(const bsgg_adapters_desc* d, const void* x, const void
     return BSGG_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const AdapterMap map = {d->tokens, d->m_pad, d->adapters, padded_offsets, row_of_slot, slot_of_row};
+  ExpandParams e = {map, u, b, scales, base, y, u, 0, base ? static_cast<int>(d->ld_base) : 0, static_cast<int>(d->ldy),
+                    static_cast<int>(d->n), d->rank};
+  const int64_t grid = plan_expand(e);
+  if (!fits_grid(grid)) return BSGG_ERR_UNSUPPORTED;
   const bsgg_status ran = launch_shrink(d->format, {map, x, a, nullptr, u, d->ldx, static_cast<int>(d->k), d->rank, 1}, s);
-  if (ran != BSGG_OK) return ran;
-  return launch_expand(d->format, {map, u, b, scales, base, y, u, 0, base ? static_cast<int>(d->ld_base) : 0, static_cast<int>(d->ldy),
-                                   static_cast<int>(d->n), d->rank}, s);
+  return ran == BSGG_OK ? launch_expand(d->format, e, grid, s) : ran;
 }
 
 uint64_t bsgg_adapters_workspace_bytes(int64_t tokens, int64_t k, int64_t n, int64_t m_pad, int32_t adapters, int32_t rank) {
@@ -1189,10 +1210,12 @@ bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* 
       (db && !u) || ((da || db) && !rows_used) || ((da || db) && !workspace))
     return BSGG_ERR_INVALID_ARG;
   const AdapterMap map = {d->tokens, d->m_pad, d->adapters, padded_offsets, row_of_slot, slot_of_row};
-  bsgg_status ran = BSGG_OK;
-  if (wants_du) ran = launch_shrink(d->format, {map, dy, b, scales, du, d->ld_dy, static_cast<int>(d->n), d->rank, 1}, s);
-  if (ran == BSGG_OK && (da || db)) {
-    OuterParams p = {};
+  ExpandParams e = {map, du, a, nullptr, base, dx, nullptr, 0, base ? static_cast<int>(d->ld_base) : 0, static_cast<int>(d->ld_dx),
+                    static_cast<int>(d->k), d->rank};
+  const int64_t grid = dx ? plan_expand(e) : 0;
+  if (!fits_grid(grid)) return BSGG_ERR_UNSUPPORTED;
+  OuterParams p = {};
+  if (da || db) {
     p.map = map; p.rows_used = rows_used; p.rank = d->rank; p.out_kind = d->grad_format;
     p.segment = static_cast<int>(outer_segment(d->tokens, d->k, d->n));
     p.slots = static_cast<int>(outer_slots(d->tokens, d->k, d->n));
@@ -1204,11 +1227,12 @@ bsgg_status bsgg_adapters_backward(const bsgg_adapters_bwd_desc* d, const void* 
     };
     side(0, u, dy, scales, db, d->ld_dy, d->n);
     side(1, du, x, nullptr, da, d->ldx, d->k);
-    ran = launch_outer(d->format, p, s);
+    if (!fits_grid(plan_outer(p))) return BSGG_ERR_UNSUPPORTED;
   }
-  if (ran == BSGG_OK && dx)
-    ran = launch_expand(d->format, {map, du, a, nullptr, base, dx, nullptr, 0, base ? static_cast<int>(d->ld_base) : 0,
-                                   static_cast<int>(d->ld_dx), static_cast<int>(d->k), d->rank}, s);
+  bsgg_status ran = BSGG_OK;
+  if (wants_du) ran = launch_shrink(d->format, {map, dy, b, scales, du, d->ld_dy, static_cast<int>(d->n), d->rank, 1}, s);
+  if (ran == BSGG_OK && (da || db)) ran = launch_outer(d->format, p, s);
+  if (ran == BSGG_OK && dx) ran = launch_expand(d->format, e, grid, s);
   return ran;
 }
 

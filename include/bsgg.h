@@ -716,7 +716,9 @@ BSGG_API bsgg_status bsgg_rms_norm_backward(const bsgg_norm_bwd_desc* desc, cons
  * The tokens' adapters come as bsgg_sort_tokens writes them for ids (tokens, 1), -1 for
  * none: padded_offsets (adapters), row_of_slot (tokens), slot_of_row (m_pad); one sort
  * serves all layers of a step.  k, n multiples of 8, rank a multiple of 8 up to 128; all
- * of x, A, B, base, y and u 16-byte aligned with pitches that are multiples of 8. */
+ * of x, A, B, base, y and u 16-byte aligned with pitches that are multiples of 8.  Sizes that
+ * need 2^31 blocks or more of a launch are BSGG_ERR_UNSUPPORTED before anything runs, here and
+ * in the backward. */
 typedef struct {
   int64_t tokens;         /* 0..2^30 */
   int64_t k, n;           /* 8..2^24 */

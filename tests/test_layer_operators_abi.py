@@ -327,3 +327,12 @@ def test_workspace_of_wide_layers(lib, tokens, k, n):
         assert need <= terms + 2 * 4 * (adapters + m_pad // 64) + 6 * 16
     else:
         assert need >= terms + 2 * 4 * rank * (k + n)
+
+
+def test_grids_past_31_bits_are_refused_before_anything_runs(lib):
+    """(No GPU here: a launch would give another status.)"""
+    wide = dict(tokens=2 ** 30, m_pad=2 ** 30)
+    assert adapt(lib, n=2 ** 24, ld_base=2 ** 24, ldy=2 ** 24, **wide) == 2
+    assert adapt_bwd(lib, dict(da=None, db=None), k=2 ** 24, ldx=2 ** 24, ld_base=2 ** 24, ld_dx=2 ** 24, **wide) == 2
+    # one segment of 2^30 rows for each of the adapters
+    assert adapt_bwd(lib, k=65536, n=65536, ld_dy=65536, ldx=65536, ld_base=65536, ld_dx=65536, adapters=1024, **wide) == 2
