@@ -375,9 +375,12 @@ __global__ void __launch_bounds__(32 * kNormJoinWarps) norm_join_kernel(const fl
 
 // ---------------------------------------------------------------- host
 constexpr int64_t kNormMaxHidden = 32768;
-// Blocks of the gradient: two on each of the 152 SMs, or as many of fewer threads as make
-// 512 there.
-constexpr int64_t kNormBwdBlocks = 304, kNormBwdThreads = 512 * 152;
+// Blocks of the gradient on each of the 152 SMs: two, or as many of fewer threads as 512 hold
+// (at 128 registers a thread no more are there at once).  They walk the rows until there are
+// none, so that a few more blocks than fit would wait for the first to end and double the time:
+// 8192 rows of 7168 took 194 us in 347 blocks and take 129 in 304, 16384 of 1536 55 in 810 and
+// 40 in 760.
+constexpr int64_t kNormSms = 152, kNormSmThreads = 512;
 
 // How rows of `cols` columns lie: a warp each up to 512, a run of 16 a lane (16384 rows of
 // 512, forward 18 us and back 23; in blocks 22 and 62); wider ones a block each, with the
@@ -430,7 +433,7 @@ bsgg_status with_quantized(int fmt, F&& f) {
 int64_t norm_bwd_blocks(int64_t tokens, int64_t hidden) {
   const RowShape shape = row_shape(hidden);
   const int64_t rows = shape.warp ? ceil_div(tokens, kNormWarpRows) : tokens;
-  const int64_t most = kNormBwdThreads / shape.threads > kNormBwdBlocks ? kNormBwdThreads / shape.threads : kNormBwdBlocks;
+  const int64_t each = kNormSmThreads / shape.threads, most = kNormSms * (each < 2 ? 2 : each);
   return rows < most ? rows : most;
 }
 

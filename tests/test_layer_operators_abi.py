@@ -336,3 +336,10 @@ def test_grids_past_31_bits_are_refused_before_anything_runs(lib):
     assert adapt_bwd(lib, dict(da=None, db=None), k=2 ** 24, ldx=2 ** 24, ld_base=2 ** 24, ld_dx=2 ** 24, **wide) == 2
     # one segment of 2^30 rows for each of the adapters
     assert adapt_bwd(lib, k=65536, n=65536, ld_dy=65536, ldx=65536, ld_base=65536, ld_dx=65536, adapters=1024, **wide) == 2
+
+# ------------------------------------------------------------------ the norm's gradient
+@pytest.mark.parametrize("hidden", [64, 512, 520, 1024, 1536, 2048, 4096, 4104, 5120, 7168, 8192, 8200, 12288, 16384, 32768])
+def test_norm_gradient_has_as_many_blocks_on_each_sm(lib, hidden):
+    """Its blocks walk rows until there are none: one more than fit at once would double the time."""
+    parts = lib.bsgg_rms_norm_workspace_bytes(2 ** 20, hidden) // (4 * hidden)
+    assert parts % 152 == 0 and parts >= 2 * 152
