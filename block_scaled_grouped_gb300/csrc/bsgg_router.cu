@@ -30,7 +30,8 @@ __device__ __forceinline__ float sigmoid32(float l) {
 }
 // The same for the choice, with the hardware's exponential and quotient: off by 2^-21 at most
 // (e^-l by (2 + 1.2 |l|) 2^-23 of itself, which moves the score by its slope, the quotient by
-// 2^-22), and by 2^-15 of itself down to l = -88, below which it is 0.
+// 2^-22), and by 2^-15 of itself down to l = -87.3.  There the denominator passes 2^126 and the
+// quotient is 0: off by 2^-126, which is less than the least that two scores have to differ.
 __device__ __forceinline__ float sigmoid_choice(float l) { return __fdividef(1.0f, 1.0f + __expf(-l)); }
 __device__ __forceinline__ double sigmoid64(double l) {
   const double e = exp(-fabs(l));
@@ -287,8 +288,10 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_groups_kernel(const _
     }
     const uint32_t rest = __reduce_max_sync(kAll, g);
     if ((biased || p.group_top == 2) && last != 0 && rest != 0) {
-      // with a bias two scores of `off` each and roundings; without one each is positive and
-      // off by 2^-15 of itself at most
+      // with a bias two scores of `off` each and roundings; without one each is positive and off
+      // by 2^-15 of itself at most, or by 2^-126.  (Of the largest group: more than the last one
+      // kept needs, so that rows of a few large scores are compared in 64 bits oftener than they
+      // have to be.)
       const float most = warp_max(size);
       const float slack = biased ? 4.0f * off + 0x1p-20f * most : 0x1p-13f * most + 0x1p-120f;
       const uint32_t last_a = __shfl_sync(kAll, a, who), last_b = __shfl_sync(kAll, b, who);

@@ -286,3 +286,17 @@ def test_no_tokens():
     ids, w = bsgg.route_groups(l, 3)
     assert ids.shape == (0, 3) and w.shape == (0, 3)
     assert bsgg.route_groups_backward(l, ids, w, w).shape == (0, 16)
+
+
+@pytest.mark.parametrize("L,groups,kept", [(32, 8, 3), (256, 8, 4), (60, 5, 2)])
+def test_sigmoids_at_the_end_of_the_range(L, groups, kept):
+    """Scores near the smallest normal number, where the quotient of the choice's sigmoid is
+    already 0: groups of them are in the order of their sums all the same."""
+    T = 64
+    l = -88.0 + torch.rand(T, L, generator=gen(41)) * 1.5                  # -88 to -86.5
+    l[1::4, : L // 2] = -87.9 + torch.rand(T // 4, L // 2, generator=gen(42)) * 0.5
+    l[2::4, -(L // groups):] -= 30.0                                       # a group that is 0 in 32 bits
+    l[3::4] = torch.round(l[3::4] * 64) / 64
+    want, _ = R.route_groups(l, 4, groups=groups, topk_groups=kept, group_top=2)
+    ids, w = bsgg.route_groups(l.cuda(), 4, groups=groups, topk_groups=kept, group_top=2)
+    assert torch.equal(ids.cpu(), want) and torch.isfinite(w).all()
