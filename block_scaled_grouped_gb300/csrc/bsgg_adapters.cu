@@ -79,7 +79,7 @@ __device__ __forceinline__ uint32_t swizzled(int row, int piece) {
 }
 
 // A pair of 32-bit values as a sum of TERMS pairs of 16-bit ones: the products take them one
-// after the other, so that u and du enter unrounded (two terms: to 2^-17 of the value in
+// after the other, so that u and du enter nearly as they are (two terms: to 2^-17 of the value in
 // bfloat16, to 2^-22 in float16; three of bfloat16: 2^-24).
 template <int KIND, int TERMS>
 __device__ __forceinline__ void split_terms(float x, float y, uint32_t (&t)[TERMS]) {

@@ -68,7 +68,8 @@ __device__ __forceinline__ void store8_as(int kind, void* base, int64_t i, const
 //     TB/s, 85 % of the copy rate, bound by the loads' latency and the mix of three writes to
 //     two reads (marked as read once 97 us; six blocks an SM with 40 registers 100);
 //   128 x 7168: 4.7 us, 333 x 4104 float16: 4.9, of which the launch and two trips to memory
-//     are most.
+//     are most;
+//   8192 x 7168 into y and MXFP4 92 us, NVFP4 105 (4.8 TB/s; without y 95): a division a value.
 template <int KIND, int FMT, int NV, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : kNormMaxThreads)
     rms_norm_kernel(const __grid_constant__ NormParams p) {
@@ -223,7 +224,10 @@ struct NormRow {
 // row is on its way while this one is reduced and written (where registers hold two).
 //   8192 x 4096 bfloat16 with dh: 268 MB in 47 to 51 us with that launch, 5.3 TB/s, bound by
 //     the loads' latency (without the next row ahead 71, with its loads after the first half
-//     of the row's arithmetic 56).
+//     of the row's arithmetic 56); float32 99, with 36 to 96 bytes of spills a thread.
+//   Above 4096 columns registers hold no row ahead: 8192 x 7168 129 us, 3.6 TB/s, 8192 x 8192 136,
+//     float32 7168 228 (up to 116 bytes of spills).  Above 8192 four runs a thread spill up to 600
+//     bytes: 4096 x 12288 296 us, 1.4 TB/s, 2048 x 32768 359.
 template <int KIND, int YKIND, int NV, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : NV <= 2 ? 256 : kNormMaxThreads, WARP ? 1 : NV <= 2 ? 2 : 1)
     rms_norm_backward_kernel(const __grid_constant__ NormBwdParams p) {

@@ -203,7 +203,9 @@ __device__ __forceinline__ void set_key(uint32_t (&key)[NI], const Row& row, int
 // need none of it.  Groups likewise, but there only the last one kept has to lead.
 //   8192 x 256 bfloat16, top-8 of the best 4 of 8 groups, sigmoid and bias: 20 us (4.2 MB: 0.6
 //   of them the bytes'; the plain softmax router 12.5); 16384 x 128 float32, top-4 of 3 of 8: 21; 128
-//   x 64 top-8: 4.2.  8192 x 256 whose every row is in doubt to the last choice: 1150.  Bound by
+//   x 64 top-8: 4.2.  8192 x 256 whose every row is in doubt to the last choice: 1150.  Without a
+//   bias 16; normal logits times 8, groups of two large scores: softmax 19, sigmoid 41 (sums near 2
+//   that 32 bits do not tell apart), times 16 softmax 34.  Bound by
 //   issue (58 to 67 % of the slots; 1350 instructions a token of 256 experts, half of them the
 //   rounds).  With the near ones looked for in every round 25 and 23 us.
 template <int NI>

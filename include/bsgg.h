@@ -712,7 +712,9 @@ BSGG_API bsgg_status bsgg_rms_norm_backward(const bsgg_norm_bwd_desc* desc, cons
  * and without an adapter u[t] = 0, y[t] = base[t].  A is (adapters, rank, k) and B is
  * (adapters, rank, n), both dense: B's rows lie along n, the transpose of an (n, rank)
  * weight, so that both products and all gradients read rows.  x, A, B, base and y are in
- * `format` (bfloat16 or float16); u is rounded nowhere, y once.  base may be y.
+ * `format` (bfloat16 or float16).  u is kept in float; the product with B takes scales[i] * u
+ * as the sum of two values of `format` (bfloat16: to 2^-17 of each, float16: to 2^-22 of the
+ * token's largest), and y is rounded once.  base may be y.
  * The tokens' adapters come as bsgg_sort_tokens writes them for ids (tokens, 1), -1 for
  * none: padded_offsets (adapters), row_of_slot (tokens), slot_of_row (m_pad); one sort
  * serves all layers of a step.  k, n multiples of 8, rank a multiple of 8 up to 128; all
@@ -739,6 +741,9 @@ BSGG_API bsgg_status bsgg_adapters(const bsgg_adapters_desc* desc, const void* x
  *   dx[t] = base[t] + du[t] A_i         base: the dense layer's own dx (NULL: zeros); may be dx
  *   da_i  = sum over its tokens of du[t]^T x[t],   db_i = sum of (scales[i] u[t])^T dy[t]
  * da and db are dense like A and B, in grad_format, zeros for an adapter without tokens.
+ * du and u enter the products as two values of `format` too (float16: to 2^-22 of the largest
+ * of a token for dx, of a run of the adapter's tokens for da and db), as three (to 2^-24)
+ * where bfloat16 tensors have float gradients.
  * dx, da and db may each be NULL: not wanted (x, u, a are then not read where only they need them).
  * The scales are constants: they get no gradient.  rows_used (1) as bsgg_sort_tokens writes it
  * (da and db only): where the last adapter's rows end.  workspace (da and db only):
